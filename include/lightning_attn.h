@@ -339,6 +339,188 @@ la_status lightning_attn_mixed_step(const void *q, const void *k, const void *v,
                                     const int32_t *cu_seqlens_host, void *prefill_stream,
                                     void *decode_stream);
 
+/* ------------------------------------------------------------------------
+ * Softmax layers of a hybrid stack (one such layer after every seven lightning
+ * layers in MiniMax-01): the operators a serving step needs around their paged
+ * key-value cache, and the per-head norm with the position rotation that
+ * precedes either kind of attention, with its gradients.
+ *
+ * Common to these calls
+ *   - Row strides (q_stride, ...) are in ELEMENTS, from one token's heads to
+ *     the next; a token's [heads, head_dim] block is contiguous.  Slices of one
+ *     fused projection output are therefore taken as they are.  Strides and
+ *     pointers of floating-point arrays are multiples of 16 bytes; int32 and
+ *     byte arrays need their natural alignment only.
+ *   - rotary  [rotary_rows, rotary_dim] fp32: row p holds the rotary_dim / 2
+ *             cosines and then the rotary_dim / 2 sines of position p.
+ *             rotary_dim is a multiple of 16 up to head_dim; 0 (rotary and
+ *             positions NULL) means no rotation.
+ *   - interleaved  0: element i is rotated with element i + rotary_dim / 2;
+ *             1: element 2 i with element 2 i + 1.  Elements from rotary_dim on
+ *             are not rotated.
+ *   - positions [num_tokens] int32; values outside the table are clamped to it.
+ *   - q_weight, k_weight [head_dim] fp32, shared by the heads; both NULL: no norm.
+ *   - A key-value cache is two arrays [num_pages, num_kv_heads, page_size,
+ *             head_dim]; k_page_stride and v_page_stride are the elements from
+ *             one page to the next (>= num_kv_heads * page_size * head_dim), so
+ *             the two may be halves of one array.  Slot s is row s % page_size
+ *             of page s / page_size; num_pages * page_size < 2^31.  page_size
+ *             is any number >= 1.
+ *   - dtype of q, k, v, the cache and the outputs is LA_DTYPE_BF16 or
+ *             LA_DTYPE_FP32; head_dim 64 or 128.  Arithmetic is fp32
+ *             throughout (bf16 products exact, fp32 sums), rounded once into
+ *             an output.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * RMS norm over each query and key head and the position rotation, in one pass:
+ *     n = x (mean(x^2) + eps)^-1/2 weight,   y = R(position) n
+ *
+ * q [num_tokens, num_heads, head_dim], k [num_tokens, num_kv_heads, head_dim];
+ * q_out, k_out likewise (contiguous, or strided).  q_out may be q and k_out may
+ * be k (with the same stride); no other overlap is allowed.  num_kv_heads = 0
+ * (k and k_out NULL) processes the queries alone.
+ */
+la_status lightning_attn_qk_norm_rope(
+    const void *q, int64_t q_stride, const void *k, int64_t k_stride, const int32_t *positions,
+    const float *rotary, int32_t rotary_rows, int32_t rotary_dim, int32_t interleaved,
+    const float *q_weight, const float *k_weight, float eps, int32_t num_tokens,
+    int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, la_dtype dtype, void *q_out,
+    int64_t q_out_stride, void *k_out, int64_t k_out_stride, void *stream);
+
+/*
+ * Gradients of lightning_attn_qk_norm_rope: given d_q_out and d_k_out (gradients
+ * of its outputs) and its inputs, with g = R^T dy and r = (mean(x^2) + eps)^-1/2
+ *     dx = r (weight g - x r mean(weight g x r)),   d_weight = sum_rows g x r
+ * d_q and d_k (dtype `dtype`) may be the arrays of d_q_out and d_k_out.
+ * d_q_weight, d_k_weight [head_dim] fp32 (overwritten; NULL when there are no
+ * weights).  workspace: lightning_attn_qk_norm_rope_workspace_bytes(head_dim)
+ * bytes, 16-byte aligned, not shared by calls that may overlap (not used, and may
+ * be NULL, without weights).  The sums are taken in a fixed order: the same
+ * call gives the same bits.
+ */
+la_status lightning_attn_qk_norm_rope_backward(
+    const void *q, int64_t q_stride, const void *k, int64_t k_stride, const int32_t *positions,
+    const float *rotary, int32_t rotary_rows, int32_t rotary_dim, int32_t interleaved,
+    const float *q_weight, const float *k_weight, float eps, int32_t num_tokens,
+    int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, la_dtype dtype,
+    const void *d_q_out, int64_t d_q_out_stride, const void *d_k_out, int64_t d_k_out_stride,
+    void *d_q, int64_t d_q_stride, void *d_k, int64_t d_k_stride, float *d_q_weight,
+    float *d_k_weight, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of lightning_attn_qk_norm_rope_backward; -1 for an
+ * invalid head_dim. */
+int64_t lightning_attn_qk_norm_rope_workspace_bytes(int32_t head_dim);
+
+/*
+ * lightning_attn_qk_norm_rope whose keys, and the values as they are, go into
+ * the cache: row t of k (normed and rotated) and v into slot slots[t].  A slot
+ * outside [0, num_pages * page_size) (e.g. -1, a padding token) writes no
+ * cache row; the slots of one call are otherwise distinct.
+ */
+la_status lightning_attn_paged_append(
+    const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+    int64_t v_stride, const int32_t *positions, const float *rotary, int32_t rotary_rows,
+    int32_t rotary_dim, int32_t interleaved, const float *q_weight, const float *k_weight,
+    float eps, int32_t num_tokens, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+    la_dtype dtype, void *q_out, int64_t q_out_stride, void *k_cache, int64_t k_page_stride,
+    void *v_cache, int64_t v_page_stride, const int32_t *slots, int32_t num_pages,
+    int32_t page_size, void *stream);
+
+/*
+ * Softmax attention of one new token per request over the paged cache:
+ *     out[b][h] = sum_t p_t v_t,  p = softmax_t(scale q[b][h] . k_t),
+ * over the first seq_lens[b] tokens of request b (its new token among them), keys
+ * and values of head h / (num_heads / num_kv_heads).
+ *
+ * q            [batch, num_heads, head_dim] (row stride q_stride).
+ * block_table  [batch, table_width] int32, table_stride elements a row: token t of
+ *              request b is row t % page_size of page block_table[b][t / page_size].
+ *              Entries past a request's last block are not read; a page outside
+ *              [0, num_pages) leaves its tokens out of the softmax.
+ * seq_lens     [batch] int32; negative counts as 0, more than table_width *
+ *              page_size as that.  A request with no token (or none left) gets
+ *              zeros, and -infinity as its lse.
+ * scale        softmax scale (e.g. head_dim^-1/2).
+ * out          [batch, num_heads, head_dim], contiguous.
+ * lse          nullable; [batch, num_heads] fp32: log sum_t e^(scale q . k_t).
+ * workspace    lightning_attn_paged_decode_workspace_bytes(head_dim) bytes,
+ *              16-byte aligned; scratch, not shared by calls that may overlap
+ *              (two captured graphs that may run at once need one each).
+ * num_heads is a multiple of num_kv_heads.  What lies in the cache past a
+ * request's last token is not used, whatever it holds.
+ */
+la_status lightning_attn_paged_decode(
+    const void *q, int64_t q_stride, const void *k_cache, int64_t k_page_stride,
+    const void *v_cache, int64_t v_page_stride, const int32_t *block_table, int32_t table_stride,
+    int32_t table_width, const int32_t *seq_lens, int32_t num_pages, int32_t page_size,
+    int32_t batch, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, la_dtype dtype,
+    float scale, void *out, float *lse, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of lightning_attn_paged_decode; -1 for an invalid
+ * head_dim. */
+int64_t lightning_attn_paged_decode_workspace_bytes(int32_t head_dim);
+
+/*
+ * One serving step of a softmax layer: lightning_attn_paged_append of each
+ * request's new token (row b of q, k, v), then lightning_attn_paged_decode over
+ * the cache that now holds it.  The normed and rotated queries stay fp32
+ * between the two (in the workspace), so out is rounded once.  seq_lens counts the
+ * new tokens.  workspace: lightning_attn_paged_step_workspace_bytes(...) bytes,
+ * 16-byte aligned.
+ */
+la_status lightning_attn_paged_step(
+    const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+    int64_t v_stride, const int32_t *positions, const float *rotary, int32_t rotary_rows,
+    int32_t rotary_dim, int32_t interleaved, const float *q_weight, const float *k_weight,
+    float eps, void *k_cache, int64_t k_page_stride, void *v_cache, int64_t v_page_stride,
+    const int32_t *slots, const int32_t *block_table, int32_t table_stride, int32_t table_width,
+    const int32_t *seq_lens, int32_t num_pages, int32_t page_size, int32_t batch,
+    int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, la_dtype dtype, float scale,
+    void *out, float *lse, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of lightning_attn_paged_step; -1 for invalid sizes. */
+int64_t lightning_attn_paged_step_workspace_bytes(int32_t batch, int32_t num_heads,
+                                                  int32_t head_dim);
+
+/*
+ * Page bookkeeping of one serving step, from the requests' lengths, on the GPU.
+ * In this order:
+ *   1. A finished request (finished[b] != 0; finished may be NULL) pushes the
+ *      pages of its ceil(seq_lens[b] / page_size) first blocks onto the free
+ *      stack, requests and blocks in ascending order, and has length 0 from there on.
+ *   2. Request b asks for the pages that new_lens[b] more tokens need beyond
+ *      those it has.  Requests are served in ascending order: b is served if its
+ *      tokens fit its table row, and if it needs no page or the pages needed by
+ *      the requests up to b (those that do not fit their row left out) are on the stack.
+ *      A served request's new blocks get the pages popped from the top, one
+ *      after the other.
+ *   3. The new tokens are numbered in the order of the requests, served or not.
+ *
+ * block_table  [batch, table_width] int32 (table_stride elements a row), updated:
+ *              new blocks of served requests.
+ * seq_lens     [batch] int32, new_lens [batch] int32 (negative counts as 0).
+ * free_pages   [num_pages] int32 stack, free_count [1] its height (entries below
+ *              it are free pages); entries pushed in step 1 are written, popped
+ *              ones left in place.
+ * slots, positions [num_tokens] int32: slot and position (length so far + index)
+ *              of every new token; slot -1, position 0 for tokens of requests
+ *              not served and for entries past the last new token.  num_tokens is
+ *              the arrays' size: tokens past it are not written.
+ * cu_seqlens   [batch + 1] int32: first new token of every request, and the total.
+ * served       [batch] bytes, 1 or 0.
+ * seq_lens_out [batch], free_count_out [1] int32: lengths after the step (a request
+ *              not served keeps its length, 0 if it finished) and the stack's
+ *              height.  They may be seq_lens and free_count.
+ * batch <= 8192 (LA_ERR_UNSUPPORTED above).  Other overlaps are not allowed.
+ */
+la_status lightning_attn_paged_reserve(
+    int32_t *block_table, int32_t table_stride, int32_t table_width, const int32_t *seq_lens,
+    const int32_t *new_lens, const uint8_t *finished, int32_t batch, int32_t *free_pages,
+    const int32_t *free_count, int32_t num_pages, int32_t page_size, int32_t num_tokens,
+    int32_t *slots, int32_t *positions, int32_t *cu_seqlens, uint8_t *served,
+    int32_t *seq_lens_out, int32_t *free_count_out, void *stream);
+
 /*
  * Synchronises `stream`, then reports whether a kernel of this library raised
  * its device error word since the last call (and clears it).  The

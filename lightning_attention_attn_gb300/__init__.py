@@ -22,7 +22,12 @@ import weakref
 
 import torch
 
+from . import softmax_layer
 from . import workloads  # noqa: F401  (seeded input recipes)
+from .softmax_layer import (paged_append, paged_decode,  # noqa: F401
+                            paged_decode_workspace_bytes, paged_reserve, paged_step,
+                            paged_step_workspace_bytes, qk_norm_rope, qk_norm_rope_backward,
+                            rotary_table)
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "liblightning_attn.so")
@@ -123,6 +128,7 @@ def load(path: str = LIB_PATH):
             lib.lightning_attn_version.restype = ctypes.c_int32
             lib.lightning_attn_device_status.argtypes = [vp]
             lib.lightning_attn_device_status.restype = ctypes.c_int
+            softmax_layer.declare(lib)
             _lib = lib
     return _lib
 

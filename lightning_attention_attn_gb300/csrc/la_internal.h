@@ -125,4 +125,85 @@ void set_last_error(const char *fmt, ...) __attribute__((format(printf, 1, 2)));
 cudaError_t decode_f32(const DecodeArgs &a);
 cudaError_t decode_bf16(const DecodeArgs &a);
 
+// ------------------------------------------- softmax layers (paged cache)
+// One kind of rows (query, key or value heads) of the norm + rotation pass.
+// Strides are in bytes: from one token's rows to the next, or, with `cache`,
+// from one page to the next.
+struct NormRopeRows {
+    const void *x = nullptr;
+    size_t x_stride = 0;
+    const void *dy = nullptr;      // backward: gradient of the rotated rows
+    size_t dy_stride = 0;
+    void *out = nullptr;           // rotated rows, or (backward) the gradient of x
+    size_t out_stride = 0;
+    const float *weight = nullptr; // [D]; nullptr: no norm
+    int heads = 0;
+    bool cache = false;            // out is a paged cache, written at `slots`
+    bool out_f32 = false;          // out is contiguous fp32 [T, heads, D]
+};
+
+struct NormRopeArgs {
+    NormRopeRows set[3];           // queries, keys, values (copied)
+    const float *rotary = nullptr; // [rotary_rows, rotary_dim]: cosines, then sines
+    const int32_t *positions = nullptr;
+    int rotary_rows = 0, rotary_dim = 0;
+    bool interleaved = false;
+    float eps = 0.f;
+    int num_tokens = 0, head_dim = 0;
+    const int32_t *slots = nullptr;
+    int num_slots = 0, page_size = 1;
+    float *partial = nullptr;      // backward: [kNormBackwardBlocks][2][D]
+    float *dq_weight = nullptr, *dk_weight = nullptr;
+    cudaStream_t stream = nullptr;
+};
+
+// Blocks of the backward pass, each leaving one partial weight gradient.
+constexpr int kNormBackwardBlocks = 152 * 8;
+
+cudaError_t qk_norm_rope(const NormRopeArgs &a, bool bf16);
+cudaError_t qk_norm_rope_backward(const NormRopeArgs &a, bool bf16);
+
+struct PagedDecodeArgs {
+    const void *q;                 // [B, H, D] (fp32 where q_f32), q_stride elements a request
+    int64_t q_stride;
+    const void *k, *v;             // [pages, Hkv, page_size, D]
+    int64_t k_page_stride, v_page_stride;  // elements
+    const int32_t *block_table;    // [B, table_stride]
+    const int32_t *seq_lens;       // [B]
+    int table_stride, max_tokens;  // max_tokens: capacity of a table row in tokens
+    int num_pages, page_size;
+    int batch, num_heads, num_kv_heads, group, head_dim;
+    float scale_log2;              // softmax scale times log2(e)
+    void *out;                     // [B, H, D]
+    float *lse;                    // [B, H] or nullptr
+    float *workspace;              // [kPagedCtas][2][rows][D + 2]
+    cudaStream_t stream;
+    int head_groups = 1;           // units a key-value head is cut into (set by the launcher)
+};
+
+// CTAs the work of the paged attention is divided among (two per SM), and
+// the most query heads of one unit.
+constexpr int kPagedCtas = 152 * 2;
+constexpr int kPagedMaxRows = 16;
+
+cudaError_t paged_decode(const PagedDecodeArgs &a, bool bf16, bool q_f32);
+
+struct PagedReserveArgs {
+    int32_t *block_table;          // [B, table_stride]
+    int table_stride, table_width, batch;
+    const int32_t *seq_lens, *new_lens;
+    const uint8_t *finished;       // [B] or nullptr
+    int32_t *free_pages;
+    const int32_t *free_count;
+    int num_pages, page_size, num_tokens;
+    int32_t *slots, *positions, *cu_seqlens;
+    uint8_t *served;
+    int32_t *seq_lens_out, *free_count_out;
+    cudaStream_t stream;
+};
+
+constexpr int kReserveMaxBatch = 8192;
+
+cudaError_t paged_reserve(const PagedReserveArgs &a);
+
 }  // namespace la

@@ -1,0 +1,864 @@
+// Softmax attention of one new token per request over a paged key-value
+// cache, the work split over the cache's length and joined.
+//
+// For request b with len tokens in the cache, query head h and its key-value
+// head (h / G, G = num_heads / num_kv_heads):
+//     s_t = scale q_h . k_t,   out_h = sum_t e^(s_t - m) v_t / sum_t e^(s_t - m)
+// in one pass with the running maximum m and sum l of a softmax, in fp32.
+//
+// Bound: every key and value is read once, 2 G flops a byte of bf16 cache, so
+// the kernel is a stream over HBM and its layout serves the loads.
+//
+// Split.  The work is cut into tiles of kTile tokens of one unit (a request's
+// key-value head, or 16 query heads of one).  The tiles of all units, one after the other,
+// are divided evenly among a fixed number of CTAs, whatever the lengths are: no
+// host copy of the lengths, no plan, the same launch for one long request and
+// for many ragged ones.  A unit that lies inside one CTA's range is finished
+// there; a piece of a unit leaves its unnormalised sums, maxima and
+// exponential sums in the workspace (a CTA has at most two such pieces: the
+// end of one unit and the start of another), and a second kernel joins the
+// pieces of each unit in the order of their tokens.
+//
+// Inside a CTA each warp streams its own token groups through its own ring
+// of shared-memory stages (cp.async, 16 bytes a lane) with its own running
+// maximum, so the main loop has no block-wide barrier; the warps' results are
+// joined once per piece.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <math_constants.h>
+
+#include "la_internal.h"
+#include "sm100_ptx.cuh"
+
+namespace la {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kGroup = 16;              // tokens of one warp step
+constexpr int kTile = kWarps * kGroup;  // tokens of one tile of the work split
+constexpr int kStages = 3;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+    // an invalid row is filled with zeros, nothing is read
+    const int n = valid ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+// The value of each half of a packed pair, exactly.
+__device__ __forceinline__ float lo_of(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ float hi_of(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
+
+// ------------------------------------------------------------ work split
+// Length of request b as the kernels use it: inside [0, table capacity].
+__device__ __forceinline__ int request_len(const PagedDecodeArgs &a, int b) {
+    return min(max(__ldg(a.seq_lens + b), 0), a.max_tokens);
+}
+__device__ __forceinline__ int request_tiles(const PagedDecodeArgs &a, int b) {
+    return (request_len(a, b) + kTile - 1) / kTile;
+}
+
+// Tiles of the requests before `b` and of all requests (per unit of a
+// request), by the whole block.  red: kWarpsIn + ... words of shared memory.
+template <int kThr>
+__device__ __forceinline__ void count_tiles(const PagedDecodeArgs &a, int b, long long &before,
+                                            long long &all, long long *red) {
+    long long sb = 0, sa = 0;
+    for (int i = threadIdx.x; i < a.batch; i += kThr) {
+        const int t = request_tiles(a, i);
+        sa += t;
+        if (i < b) sb += t;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        sa += __shfl_xor_sync(0xffffffffu, sa, o);
+        sb += __shfl_xor_sync(0xffffffffu, sb, o);
+    }
+    if ((threadIdx.x & 31) == 0) {
+        red[threadIdx.x >> 5] = sa;
+        red[kThr / 32 + (threadIdx.x >> 5)] = sb;
+    }
+    __syncthreads();
+    all = before = 0;
+#pragma unroll
+    for (int w = 0; w < kThr / 32; ++w) all += red[w], before += red[kThr / 32 + w];
+}
+
+// First tile of CTA c's range when `all` tiles are divided among n CTAs.
+__device__ __forceinline__ long long range_begin(long long all, int n, int c) {
+    return all * c / n;
+}
+
+// Finds the request that tile `w` (of all units) lies in: its index, and the
+// tiles of the requests before it.  Whole block; walks the lengths in order,
+// kThreads at a time.
+__device__ __forceinline__ void find_request(const PagedDecodeArgs &a, long long w, int units,
+                                             int &b, long long &before, long long *scan) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long base = 0;
+    for (int b0 = 0;; b0 += kThreads) {
+        const int i = b0 + threadIdx.x;
+        const int t = i < a.batch ? request_tiles(a, i) : 0;
+        long long s = t;  // inclusive scan
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += v;
+        }
+        __syncthreads();
+        if (lane == 31) scan[warp] = s;
+        if (threadIdx.x == 0) scan[kWarps] = -1;
+        __syncthreads();
+        long long upto = base;
+        for (int v = 0; v < warp; ++v) upto += scan[v];
+        upto += s;
+        // exactly one request holds w: the first whose inclusive count passes it
+        if (t > 0 && w >= (upto - t) * units && w < upto * units) {
+            scan[kWarps] = i;
+            scan[kWarps + 1] = s - t;
+        }
+        __syncthreads();
+        if (scan[kWarps] >= 0) {
+            b = (int)scan[kWarps];
+            before = base + scan[kWarps + 1];
+            for (int v = 0; v < (b - b0) / 32; ++v) before += scan[v];
+            return;
+        }
+        for (int v = 0; v < kWarps; ++v) base += scan[v];
+        if (b0 + kThreads >= a.batch) {  // w is past the last tile: not reached
+            b = a.batch;
+            before = base;
+            return;
+        }
+    }
+}
+
+// Where piece `first` (of a unit that CTA c does not hold whole) of CTA c
+// lives in the workspace: rows of kMaxGroup heads x D sums, then maxima and
+// exponential sums.
+template <int D>
+__device__ __forceinline__ float *piece_at(const PagedDecodeArgs &a, int c, bool first, int rows) {
+    return a.workspace + ((size_t)c * 2 + (first ? 0 : 1)) * rows * (D + 2);
+}
+
+// --------------------------------------------------------- bf16 main kernel
+// Heads of the query in the columns of the products (N = 8, NT such tiles):
+//     S^T [16 tokens x 8] = K [16 x D] Q^T,   O^T [D x 8] += V^T [D x 16] P^T
+// K and V are the A operands straight from shared memory (V transposed by
+// ldmatrix), so up to 8 (16) query heads share one read of the cache and no
+// row of an MMA is padding when G is 8 (16).  P^T is S^T's accumulator
+// rounded to bf16 with the remainder as a second bf16 operand (P = hi + lo,
+// 2^-17 relative): the tensor pipe is idle most of the time and the second
+// product keeps the result at fp32 accuracy.
+template <int D, int NT>
+struct Bf16Core {
+    static constexpr int kRow = D * 2;              // bytes of a token row
+    static constexpr int kMat = kGroup * kRow;      // bytes of K (V) of a stage
+    static constexpr int kStageBytes = 2 * kMat;
+    static constexpr int kSmem = kWarps * kStages * kStageBytes;
+};
+
+template <int D, int NT, bool QF32>
+__global__ void __launch_bounds__(kThreads)
+paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
+    using C = Bf16Core<D, NT>;
+    constexpr int KS = D / 16;   // k steps of S, row tiles of O^T
+    constexpr int CH = D / 8;    // 16-byte chunks of a row
+    constexpr int RPI = 32 / CH; // rows one warp-wide copy covers
+    constexpr int kRows = 8 * NT;
+
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ long long red[2 * kWarps];
+    __shared__ long long scan[kWarps + 2];
+
+    // launched as a dependent launch: the lengths, the table and the cache
+    // may have been written by the kernel before
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, c2 = (lane & 3) * 2;
+    const int units = a.num_kv_heads * a.head_groups;
+
+    long long unused, all;
+    count_tiles<kThreads>(a, 0, unused, all, red);
+    all *= units;
+    const int n = (int)min(all, (long long)gridDim.x);
+    if ((int)blockIdx.x >= n) return;
+    long long w0 = range_begin(all, n, blockIdx.x);
+    const long long w1 = range_begin(all, n, blockIdx.x + 1);
+    int b;
+    long long before;
+    find_request(a, w0, units, b, before, scan);
+
+    const uint32_t ring = ptx::smem_u32(smem) + warp * kStages * C::kStageBytes;
+    const int crow = lane / CH, cch = lane % CH;
+    // ldmatrix row addresses: K as rows, V transposed
+    const int krow = lane & 15, kchunk = lane >> 4;
+    const int vrow = (lane & 7) + ((lane >> 4) << 3), vchunk = (lane >> 3) & 1;
+
+    bool first = true;
+    long long unit0 = before * units;  // first tile of request b
+    for (; w0 < w1; ) {
+        if (b >= a.batch) return;
+        const int len = request_len(a, b);
+        const int tiles = (len + kTile - 1) / kTile;
+        if (w0 >= unit0 + (long long)tiles * units) {  // next request (empty ones pass)
+            unit0 += (long long)tiles * units;
+            ++b;
+            continue;
+        }
+        const int unit = (int)((w0 - unit0) / tiles);
+        const int tile0 = (int)((w0 - unit0) % tiles);
+        const int tile1 = (int)min((long long)tiles, tile0 + (w1 - w0));
+        const int kvh = unit / a.head_groups, hg = unit % a.head_groups;
+        const int head0 = kvh * a.group + hg * kRows;
+        const int heads = min(kRows, a.group - hg * kRows);
+        const int t0 = tile0 * kTile, t1 = min(len, tile1 * kTile);
+
+        // queries as B operands, scaled after the product
+        uint32_t qb[NT][KS][2], ql[QF32 ? NT : 1][QF32 ? KS : 1][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int h = nt * 8 + g;
+            const bool has = h < heads;
+            if (QF32) {
+                const float *qp = static_cast<const float *>(a.q) +
+                                  (size_t)b * a.q_stride + (size_t)(head0 + h) * D + c2;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float2 x = make_float2(0.f, 0.f);
+                        if (has) x = *reinterpret_cast<const float2 *>(qp + ks * 16 + i * 8);
+                        const uint32_t p = pack2(x.x, x.y);
+                        qb[nt][ks][i] = p;
+                        ql[nt][ks][i] = pack2(x.x - lo_of(p), x.y - hi_of(p));
+                    }
+            } else {
+                const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q) +
+                                          (size_t)b * a.q_stride + (size_t)(head0 + h) * D + c2;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        qb[nt][ks][i] =
+                            has ? *reinterpret_cast<const uint32_t *>(qp + ks * 16 + i * 8) : 0u;
+            }
+        }
+        float o[NT][KS][4];
+        float mx[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            mx[nt][0] = mx[nt][1] = -CUDART_INF_F;
+            l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+                o[nt][ks][0] = o[nt][ks][1] = o[nt][ks][2] = o[nt][ks][3] = 0.f;
+        }
+
+        const int32_t *pages = a.block_table + (size_t)b * a.table_stride;
+        const int groups = (t1 - t0 + kGroup - 1) / kGroup;  // of the whole piece
+        // This warp's groups: warp, warp + kWarps, ...; lane r < 16 finds row
+        // r of a group: its offset inside a key (value) head's page, or -1.
+        auto locate = [&](int grp, int &page, int &row) {
+            const int t = t0 + grp * kGroup + (lane & 15);
+            page = -1;
+            row = 0;
+            if (t < t1) {
+                const int blk = t / a.page_size;
+                row = t - blk * a.page_size;
+                page = __ldg(pages + blk);
+                if (page >= a.num_pages) page = -1;
+            }
+        };
+        // Issues the copies of one group; returns the mask of its present rows.
+        auto issue = [&](int stage, int page, int row) -> uint32_t {
+            const uint32_t have = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
+            const uint32_t dk = ring + stage * C::kStageBytes, dv = dk + C::kMat;
+#pragma unroll
+            for (int i = 0; i < kGroup / RPI; ++i) {
+                const int r = i * RPI + crow;
+                const int pg = __shfl_sync(0xffffffffu, page, r);
+                const int rw = __shfl_sync(0xffffffffu, row, r);
+                const bool ok = pg >= 0;
+                const size_t in = ((size_t)kvh * a.page_size + rw) * D + cch * 8;
+                const size_t p = ok ? pg : 0;
+                const uint32_t off = r * C::kRow + ((cch ^ (r & 7)) << 4);
+                cp_async16(dk + off, static_cast<const __nv_bfloat16 *>(a.k) + p * a.k_page_stride + in, ok);
+                cp_async16(dv + off, static_cast<const __nv_bfloat16 *>(a.v) + p * a.v_page_stride + in, ok);
+            }
+            return have;
+        };
+
+        uint32_t have[kStages];
+#pragma unroll
+        for (int s = 0; s < kStages - 1; ++s) {
+            const int grp = warp + s * kWarps;
+            have[s] = 0;
+            if (grp < groups) {
+                int page, row;
+                locate(grp, page, row);
+                have[s] = issue(s, page, row);
+            }
+            cp_commit();
+        }
+        int npage, nrow;  // of the group that is issued next
+        locate(warp + (kStages - 1) * kWarps, npage, nrow);
+
+        int stage = 0;
+        for (int grp = warp; grp < groups; grp += kWarps) {
+            // refill the stage that was read last (its readers are this warp)
+            {
+                const int nx = grp + (kStages - 1) * kWarps;
+                const int ns = stage == 0 ? kStages - 1 : stage - 1;
+                __syncwarp();
+                have[kStages - 1] = 0;
+                if (nx < groups) have[kStages - 1] = issue(ns, npage, nrow);
+                cp_commit();
+                locate(nx + kWarps, npage, nrow);
+            }
+            cp_wait<kStages - 1>();
+            __syncwarp();
+            const uint32_t kb = ring + stage * C::kStageBytes, vb = kb + C::kMat;
+
+            float s[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                uint32_t ka[4];
+                ldsm4(ka, kb + krow * C::kRow + (((2 * ks + kchunk) ^ (krow & 7)) << 4));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma16816(s[nt], ka, qb[nt][ks][0], qb[nt][ks][1]);
+                    if (QF32) mma16816(s[nt], ka, ql[nt][ks][0], ql[nt][ks][1]);
+                }
+            }
+            const bool v0 = (have[0] >> g) & 1, v1 = (have[0] >> (g + 8)) & 1;
+            uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {  // this lane's two heads
+                    s[nt][j] = v0 ? s[nt][j] * a.scale_log2 : -CUDART_INF_F;
+                    s[nt][2 + j] = v1 ? s[nt][2 + j] * a.scale_log2 : -CUDART_INF_F;
+                }
+                float t0m = fmaxf(s[nt][0], s[nt][2]), t1m = fmaxf(s[nt][1], s[nt][3]);
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) {
+                    t0m = fmaxf(t0m, __shfl_xor_sync(0xffffffffu, t0m, d));
+                    t1m = fmaxf(t1m, __shfl_xor_sync(0xffffffffu, t1m, d));
+                }
+                // a maximum that rose rescales what was summed
+                if (__any_sync(0xffffffffu, t0m > mx[nt][0] || t1m > mx[nt][1])) {
+                    const float n0 = fmaxf(mx[nt][0], t0m), n1 = fmaxf(mx[nt][1], t1m);
+                    const float f0 = n0 == -CUDART_INF_F ? 1.f : exp2f(mx[nt][0] - n0);
+                    const float f1 = n1 == -CUDART_INF_F ? 1.f : exp2f(mx[nt][1] - n1);
+                    mx[nt][0] = n0;
+                    mx[nt][1] = n1;
+                    l[nt][0] *= f0;
+                    l[nt][1] *= f1;
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        o[nt][ks][0] *= f0;
+                        o[nt][ks][1] *= f1;
+                        o[nt][ks][2] *= f0;
+                        o[nt][ks][3] *= f1;
+                    }
+                }
+                const float b0 = mx[nt][0] == -CUDART_INF_F ? 0.f : mx[nt][0];
+                const float b1 = mx[nt][1] == -CUDART_INF_F ? 0.f : mx[nt][1];
+                const float p0 = exp2f(s[nt][0] - b0), p1 = exp2f(s[nt][1] - b1);
+                const float p2 = exp2f(s[nt][2] - b0), p3 = exp2f(s[nt][3] - b1);
+                l[nt][0] += p0 + p2;
+                l[nt][1] += p1 + p3;
+                const uint32_t h0 = pack2(p0, p1), h1 = pack2(p2, p3);
+                ph[nt][0] = transpose8x8(h0);
+                ph[nt][1] = transpose8x8(h1);
+                pl[nt][0] = transpose8x8(pack2(p0 - lo_of(h0), p1 - hi_of(h0)));
+                pl[nt][1] = transpose8x8(pack2(p2 - lo_of(h1), p3 - hi_of(h1)));
+            }
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                uint32_t va[4];
+                ldsm4_t(va, vb + vrow * C::kRow + (((2 * ks + vchunk) ^ (vrow & 7)) << 4));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma16816(o[nt][ks], va, ph[nt][0], ph[nt][1]);
+                    mma16816(o[nt][ks], va, pl[nt][0], pl[nt][1]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kStages - 1; ++i) have[i] = have[i + 1];
+            stage = stage == kStages - 1 ? 0 : stage + 1;
+        }
+        cp_wait<0>();
+
+        // ---- join the warps: each leaves maxima, sums and O^T in shared memory
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1)
+                    l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], d);
+        float *ow = reinterpret_cast<float *>(smem);            // [warp][head][D]
+        float *ml = ow + kWarps * kRows * D;                    // [warp][head][2]
+        __syncthreads();  // every warp has read its stages
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            if (g == 0) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int h = nt * 8 + c2 + j;
+                    ml[(warp * kRows + h) * 2] = mx[nt][j];
+                    ml[(warp * kRows + h) * 2 + 1] = l[nt][j];
+                }
+            }
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    ow[(warp * kRows + nt * 8 + c2 + (i & 1)) * D + ks * 16 + g + (i >> 1) * 8] =
+                        o[nt][ks][i];
+        }
+        __syncthreads();
+        const bool whole = tile0 == 0 && tile1 == tiles;
+        float *ws = whole ? nullptr : piece_at<D>(a, blockIdx.x, first, kRows);
+        for (int i = threadIdx.x; i < heads * (D / 4); i += kThreads) {
+            const int h = i / (D / 4), d = (i % (D / 4)) * 4;
+            float m = -CUDART_INF_F;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[(w * kRows + h) * 2]);
+            const float mb = m == -CUDART_INF_F ? 0.f : m;
+            float sum = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = exp2f(ml[(w * kRows + h) * 2] - mb);
+                const float4 x = *reinterpret_cast<const float4 *>(ow + (w * kRows + h) * D + d);
+                sum += f * ml[(w * kRows + h) * 2 + 1];
+                acc.x += f * x.x;
+                acc.y += f * x.y;
+                acc.z += f * x.z;
+                acc.w += f * x.w;
+            }
+            if (whole) {
+                const float r = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays NaN
+                const size_t row = (size_t)b * a.num_heads + head0 + h;
+                uint2 y = make_uint2(pack2(acc.x * r, acc.y * r), pack2(acc.z * r, acc.w * r));
+                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + d) = y;
+                if (a.lse && d == 0)
+                    a.lse[row] = sum != 0.f ? (m + log2f(sum)) * (1.f / kLog2e) : -CUDART_INF_F;
+            } else {
+                *reinterpret_cast<float4 *>(ws + h * D + d) = acc;
+                if (d == 0) {
+                    ws[kRows * D + 2 * h] = m;
+                    ws[kRows * D + 2 * h + 1] = sum;
+                }
+            }
+        }
+        __syncthreads();  // shared memory is the ring again
+        first = false;
+        w0 += tile1 - tile0;
+    }
+}
+
+// -------------------------------------------------------------- fp32 kernel
+// The same split and rings on the CUDA cores (fp32 products, as the library's
+// other fp32 paths): a lane takes one token's half row for the scores, then
+// D / 32 columns of the values; queries and probabilities are broadcast from
+// shared memory.
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads)
+paged_decode_f32_kernel(const __grid_constant__ PagedDecodeArgs a) {
+    constexpr int kRows = 8 * NT;
+    constexpr int CH = D / 4;     // 16-byte chunks of a row
+    constexpr int CPL = CH / 16;  // chunks a copying lane takes of each row pair
+    constexpr int VEC = D / 32;   // value columns of a lane
+    constexpr int kMat = kGroup * D;  // floats
+    constexpr int kSt = D == 128 ? 2 : 3;
+
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ long long red[2 * kWarps];
+    __shared__ long long scan[kWarps + 2];
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int units = a.num_kv_heads * a.head_groups;
+    long long unused, all;
+    count_tiles<kThreads>(a, 0, unused, all, red);
+    all *= units;
+    const int n = (int)min(all, (long long)gridDim.x);
+    if ((int)blockIdx.x >= n) return;
+    long long w0 = range_begin(all, n, blockIdx.x);
+    const long long w1 = range_begin(all, n, blockIdx.x + 1);
+    int b;
+    long long before;
+    find_request(a, w0, units, b, before, scan);
+
+    float *qs = reinterpret_cast<float *>(smem);                  // [kRows][D]
+    float *pw = qs + kRows * D + warp * kGroup * kRows;           // [16][kRows] of this warp
+    float *ring = qs + kRows * D + kWarps * kGroup * kRows + warp * kSt * 2 * kMat;
+    const uint32_t ring_u = ptx::smem_u32(ring);
+
+    bool first = true;
+    long long unit0 = before * units;
+    for (; w0 < w1; ) {
+        if (b >= a.batch) return;
+        const int len = request_len(a, b);
+        const int tiles = (len + kTile - 1) / kTile;
+        if (w0 >= unit0 + (long long)tiles * units) {
+            unit0 += (long long)tiles * units;
+            ++b;
+            continue;
+        }
+        const int unit = (int)((w0 - unit0) / tiles);
+        const int tile0 = (int)((w0 - unit0) % tiles);
+        const int tile1 = (int)min((long long)tiles, tile0 + (w1 - w0));
+        const int kvh = unit / a.head_groups, hg = unit % a.head_groups;
+        const int head0 = kvh * a.group + hg * kRows;
+        const int heads = min(kRows, a.group - hg * kRows);
+        const int t0 = tile0 * kTile, t1 = min(len, tile1 * kTile);
+
+        for (int i = threadIdx.x; i < kRows * D; i += kThreads) {
+            const int h = i / D;
+            qs[i] = h < heads ? static_cast<const float *>(a.q)[(size_t)b * a.q_stride +
+                                                                (size_t)(head0 + h) * D + i % D]
+                              : 0.f;
+        }
+        __syncthreads();
+
+        float o[kRows][VEC], mx[kRows], l[kRows];
+#pragma unroll
+        for (int h = 0; h < kRows; ++h) {
+            mx[h] = -CUDART_INF_F;
+            l[h] = 0.f;
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) o[h][c] = 0.f;
+        }
+        const int32_t *pages = a.block_table + (size_t)b * a.table_stride;
+        const int groups = (t1 - t0 + kGroup - 1) / kGroup;
+        auto issue = [&](int stage, int grp) -> uint32_t {
+            const int t = t0 + grp * kGroup + (lane & 15);
+            int page = -1, row = 0;
+            if (t < t1) {
+                const int blk = t / a.page_size;
+                row = t - blk * a.page_size;
+                page = __ldg(pages + blk);
+                if (page >= a.num_pages) page = -1;
+            }
+            const uint32_t have = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
+            const uint32_t dk = ring_u + stage * 2 * kMat * 4, dv = dk + kMat * 4;
+#pragma unroll
+            for (int i = 0; i < kGroup / 2; ++i) {
+                const int r = i * 2 + (lane >> 4);
+                const int pg = __shfl_sync(0xffffffffu, page, r);
+                const int rw = __shfl_sync(0xffffffffu, row, r);
+                const bool ok = pg >= 0;
+                const size_t p = ok ? pg : 0;
+#pragma unroll
+                for (int j = 0; j < CPL; ++j) {
+                    const int ch = (lane & 15) + 16 * j;
+                    const size_t in = ((size_t)kvh * a.page_size + rw) * D + ch * 4;
+                    const uint32_t off = r * D * 4 + ((ch ^ (r & 7)) << 4);
+                    cp_async16(dk + off, static_cast<const float *>(a.k) + p * a.k_page_stride + in, ok);
+                    cp_async16(dv + off, static_cast<const float *>(a.v) + p * a.v_page_stride + in, ok);
+                }
+            }
+            return have;
+        };
+        uint32_t have[kSt];
+#pragma unroll
+        for (int s = 0; s < kSt - 1; ++s) {
+            const int grp = warp + s * kWarps;
+            have[s] = grp < groups ? issue(s, grp) : 0;
+            cp_commit();
+        }
+        int stage = 0;
+        for (int grp = warp; grp < groups; grp += kWarps) {
+            const int nx = grp + (kSt - 1) * kWarps;
+            const int ns = stage == 0 ? kSt - 1 : stage - 1;
+            __syncwarp();
+            have[kSt - 1] = nx < groups ? issue(ns, nx) : 0;
+            cp_commit();
+            cp_wait<kSt - 1>();
+            __syncwarp();
+            const float *kb = ring + stage * 2 * kMat, *vb = kb + kMat;
+
+            // scores: token lane & 15, half of the row each
+            const int r = lane & 15, hf = lane >> 4;
+            float s[kRows];
+#pragma unroll
+            for (int h = 0; h < kRows; ++h) s[h] = 0.f;
+#pragma unroll 4
+            for (int c = 0; c < CH / 2; ++c) {
+                const int ch = hf * (CH / 2) + c;
+                const float4 k4 = *reinterpret_cast<const float4 *>(kb + r * D + ((ch ^ (r & 7)) << 2));
+#pragma unroll
+                for (int h = 0; h < kRows; ++h) {
+                    const float4 q4 = *reinterpret_cast<const float4 *>(qs + h * D + ch * 4);
+                    s[h] = fmaf(k4.x, q4.x, fmaf(k4.y, q4.y, fmaf(k4.z, q4.z, fmaf(k4.w, q4.w, s[h]))));
+                }
+            }
+            const bool ok = (have[0] >> r) & 1;
+            bool rose = false;
+            float top[kRows];
+#pragma unroll
+            for (int h = 0; h < kRows; ++h) {
+                s[h] += __shfl_xor_sync(0xffffffffu, s[h], 16);
+                s[h] = ok ? s[h] * a.scale_log2 : -CUDART_INF_F;
+                float t = s[h];
+#pragma unroll
+                for (int d = 1; d < 16; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+                top[h] = t;
+                rose |= t > mx[h];
+            }
+            if (rose) {  // the same in every lane
+#pragma unroll
+                for (int h = 0; h < kRows; ++h) {
+                    const float nm = fmaxf(mx[h], top[h]);
+                    const float f = nm == -CUDART_INF_F ? 1.f : exp2f(mx[h] - nm);
+                    mx[h] = nm;
+                    l[h] *= f;
+#pragma unroll
+                    for (int c = 0; c < VEC; ++c) o[h][c] *= f;
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < kRows; ++h) {
+                const float p = exp2f(s[h] - (mx[h] == -CUDART_INF_F ? 0.f : mx[h]));
+                l[h] += p;  // per token lane: summed over the lanes at the end
+                if (hf == 0) pw[r * kRows + h] = p;
+            }
+            __syncwarp();
+#pragma unroll 4
+            for (int t = 0; t < kGroup; ++t) {
+                float v[VEC];
+                const int ch = lane * VEC / 4, in = lane * VEC % 4;
+                const float *vp = vb + t * D + ((ch ^ (t & 7)) << 2) + in;
+                if constexpr (VEC == 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(vp);
+                    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2 *>(vp);
+                    v[0] = x.x, v[1] = x.y;
+                }
+#pragma unroll
+                for (int h = 0; h < kRows; h += 4) {
+                    const float4 p4 = *reinterpret_cast<const float4 *>(pw + t * kRows + h);
+#pragma unroll
+                    for (int c = 0; c < VEC; ++c) {
+                        o[h][c] = fmaf(p4.x, v[c], o[h][c]);
+                        o[h + 1][c] = fmaf(p4.y, v[c], o[h + 1][c]);
+                        o[h + 2][c] = fmaf(p4.z, v[c], o[h + 2][c]);
+                        o[h + 3][c] = fmaf(p4.w, v[c], o[h + 3][c]);
+                    }
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < kSt - 1; ++i) have[i] = have[i + 1];
+            stage = stage == kSt - 1 ? 0 : stage + 1;
+        }
+        cp_wait<0>();
+#pragma unroll
+        for (int h = 0; h < kRows; ++h)
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], d);
+
+        float *ow = qs + kRows * D + kWarps * kGroup * kRows;  // [warp][head][D], over the rings
+        float *ml = qs + kRows * D;                            // [warp][head][2], over P
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < kRows; ++h) {
+            if (lane == 0) {
+                ml[(warp * kRows + h) * 2] = mx[h];
+                ml[(warp * kRows + h) * 2 + 1] = l[h];
+            }
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) ow[(warp * kRows + h) * D + lane * VEC + c] = o[h][c];
+        }
+        __syncthreads();
+        const bool whole = tile0 == 0 && tile1 == tiles;
+        float *ws = whole ? nullptr : piece_at<D>(a, blockIdx.x, first, kRows);
+        for (int i = threadIdx.x; i < heads * D; i += kThreads) {
+            const int h = i / D, d = i % D;
+            float m = -CUDART_INF_F;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[(w * kRows + h) * 2]);
+            const float mb = m == -CUDART_INF_F ? 0.f : m;
+            float sum = 0.f, acc = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = exp2f(ml[(w * kRows + h) * 2] - mb);
+                sum += f * ml[(w * kRows + h) * 2 + 1];
+                acc += f * ow[(w * kRows + h) * D + d];
+            }
+            if (whole) {
+                const size_t row = (size_t)b * a.num_heads + head0 + h;
+                static_cast<float *>(a.out)[row * D + d] = sum != 0.f ? acc / sum : 0.f;
+                if (a.lse && d == 0)
+                    a.lse[row] = sum != 0.f ? (m + log2f(sum)) * (1.f / kLog2e) : -CUDART_INF_F;
+            } else {
+                ws[h * D + d] = acc;
+                if (d == 0) {
+                    ws[kRows * D + 2 * h] = m;
+                    ws[kRows * D + 2 * h + 1] = sum;
+                }
+            }
+        }
+        __syncthreads();
+        first = false;
+        w0 += tile1 - tile0;
+    }
+}
+
+// -------------------------------------------------------------------- join
+// One block per unit: adds the pieces of a unit that several CTAs hold, in
+// the order of their tokens, and writes the rows of requests without tokens.
+template <typename T, int D>
+__global__ void __launch_bounds__(128)
+paged_join_kernel(const __grid_constant__ PagedDecodeArgs a, int ctas, int rows) {
+    __shared__ long long red[8];
+    const int units = a.num_kv_heads * a.head_groups;
+    const int b = blockIdx.x / units, unit = blockIdx.x % units;
+    // The lengths were complete before the main kernel let this one be
+    // scheduled; the pieces are read after the wait.
+    long long before, all;
+    count_tiles<128>(a, b, before, all, red);
+    all *= units;
+    const int tiles = request_tiles(a, b);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const int kvh = unit / a.head_groups, hg = unit % a.head_groups;
+    const int head0 = kvh * a.group + hg * rows;
+    const int heads = min(rows, a.group - hg * rows);
+    const size_t row0 = (size_t)b * a.num_heads + head0;
+    if (tiles == 0) {
+        for (int i = threadIdx.x; i < heads * D; i += 128)
+            static_cast<T *>(a.out)[row0 * D + i] = T(0.f);
+        if (a.lse && threadIdx.x < heads) a.lse[row0 + threadIdx.x] = -CUDART_INF_F;
+        return;
+    }
+    const int n = (int)min(all, (long long)ctas);
+    const long long u0 = before * units + (long long)unit * tiles, u1 = u0 + tiles;
+    // CTA of a tile: the last one whose range begins at or before it
+    auto cta_of = [&](long long w) {
+        int c = (int)(w * n / all);
+        while (range_begin(all, n, c + 1) <= w) ++c;
+        return c;
+    };
+    const int c0 = cta_of(u0), c1 = cta_of(u1 - 1);
+    if (c0 == c1) return;  // finished by the main kernel
+
+    for (int i = threadIdx.x; i < heads * D; i += 128) {
+        const int h = i / D, d = i % D;
+        float m = -CUDART_INF_F, sum = 0.f, acc = 0.f;
+        for (int c = c0; c <= c1; ++c) {
+            const float *p = piece_at<D>(a, c, range_begin(all, n, c) >= u0, rows);
+            const float pm = p[rows * D + 2 * h], ps = p[rows * D + 2 * h + 1];
+            const float x = p[h * D + d];
+            const float nm = fmaxf(m, pm);
+            const float base = nm == -CUDART_INF_F ? 0.f : nm;
+            const float f = exp2f(m - base), e = exp2f(pm - base);
+            sum = sum * f + ps * e;
+            acc = acc * f + x * e;
+            m = nm;
+        }
+        static_cast<T *>(a.out)[(row0 + h) * D + d] = T(sum != 0.f ? acc / sum : 0.f);
+        if (a.lse && d == 0)
+            a.lse[row0 + h] = sum != 0.f ? (m + log2f(sum)) * (1.f / kLog2e) : -CUDART_INF_F;
+    }
+}
+
+// Opts `kern` into `smem` bytes of dynamic shared memory on every device it
+// is launched on (the call is cheap and idempotent).
+template <typename K> cudaError_t allow_smem(K kern, size_t smem) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+}
+
+template <typename T, int D>
+cudaError_t join(const PagedDecodeArgs &a, int rows) {
+    return launch_dependent(paged_join_kernel<T, D>,
+                            (unsigned)(a.batch * a.num_kv_heads * a.head_groups), 128, 0, a.stream,
+                            a, (int)kPagedCtas, rows);
+}
+
+template <int D, int NT, bool QF32>
+cudaError_t launch_bf16(PagedDecodeArgs a) {
+    a.head_groups = (a.group + 8 * NT - 1) / (8 * NT);
+    auto kern = paged_decode_kernel<D, NT, QF32>;
+    constexpr size_t kSmem = Bf16Core<D, NT>::kSmem;
+    cudaError_t e = allow_smem(kern, kSmem);
+    if (e == cudaSuccess) e = launch_dependent(kern, kPagedCtas, kThreads, kSmem, a.stream, a);
+    if (e == cudaSuccess) e = join<__nv_bfloat16, D>(a, 8 * NT);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int D, int NT>
+cudaError_t launch_f32(PagedDecodeArgs a) {
+    a.head_groups = (a.group + 8 * NT - 1) / (8 * NT);
+    auto kern = paged_decode_f32_kernel<D, NT>;
+    constexpr int kSt = D == 128 ? 2 : 3;
+    constexpr size_t kSmem =
+        sizeof(float) * (8 * NT * D + kWarps * kGroup * 8 * NT + kWarps * kSt * 2 * kGroup * D);
+    cudaError_t e = allow_smem(kern, kSmem);
+    if (e == cudaSuccess) e = launch_dependent(kern, kPagedCtas, kThreads, kSmem, a.stream, a);
+    if (e == cudaSuccess) e = join<float, D>(a, 8 * NT);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Up to 8 query heads share a key-value head: one column tile; more: two
+// (and a further unit for every 16).
+template <int D>
+cudaError_t dispatch(const PagedDecodeArgs &a, bool bf16, bool q_f32) {
+    if (!bf16) return a.group <= 8 ? launch_f32<D, 1>(a) : launch_f32<D, 2>(a);
+    if (q_f32) return a.group <= 8 ? launch_bf16<D, 1, true>(a) : launch_bf16<D, 2, true>(a);
+    return a.group <= 8 ? launch_bf16<D, 1, false>(a) : launch_bf16<D, 2, false>(a);
+}
+
+}  // namespace
+
+cudaError_t paged_decode(const PagedDecodeArgs &a, bool bf16, bool q_f32) {
+    if (a.head_dim == 128) return dispatch<128>(a, bf16, q_f32);
+    if (a.head_dim == 64) return dispatch<64>(a, bf16, q_f32);
+    return cudaErrorNotSupported;
+}
+
+}  // namespace la
