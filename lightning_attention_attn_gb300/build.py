@@ -1,10 +1,13 @@
-"""Builds liblightning_attn.so in-tree with nvcc for sm_103a.
+"""Builds liblightning_attn.so (and the Python binding of the softmax layers'
+operators) in-tree with nvcc for sm_103a.
 
 Every ``csrc/*.cu`` is compiled in parallel to an object file, then linked
 into one shared library (CUDA runtime linked statically, so loading the
 library needs no GPU driver; the driver is only touched by the first CUDA
-call).  A content hash of the sources and flags skips rebuilds that would
-produce the same library.
+call).  ``csrc/binding.cpp`` is compiled against the installed torch into
+_lightning_binding.so, which is linked to the library beside it.  A content
+hash of the sources, flags and versions skips rebuilds that would produce the
+same files.
 """
 from __future__ import annotations
 
@@ -14,6 +17,8 @@ import hashlib
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +27,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "liblightning_attn.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
+BINDING_PATH = os.path.join(BUILD_DIR, "_lightning_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
@@ -42,14 +48,41 @@ def _sources():
 def _fingerprint(extra):
     h = hashlib.sha256()
     files = _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
+        sorted(glob.glob(os.path.join(CSRC, "*.cpp"))) + \
         sorted(glob.glob(os.path.join(CSRC, "*.h"))) + \
         sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
     for f in files:
         h.update(f.encode())
         with open(f, "rb") as fh:
             h.update(fh.read())
-    h.update(" ".join(ARCH + NVCC_FLAGS + list(extra)).encode())
+    import torch
+    h.update(" ".join(ARCH + NVCC_FLAGS + list(extra) + [torch.__version__, sys.version]).encode())
     return h.hexdigest()
+
+
+def _binding_commands(obj: str, out: str) -> list[list[str]]:
+    """Compile and link commands of the binding (host code only)."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cxx = shutil.which("c++") or shutil.which("g++") or "g++"
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [INCLUDE, os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    lib = os.path.join(root, "lib")
+    return [[cxx, "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
+             *[f"-I{i}" for i in inc], "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj],
+            [cxx, "-shared", "-o", out, obj, f"-L{BUILD_DIR}", "-l:" + LIB_NAME,
+             "-Wl,-rpath,$ORIGIN", f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10",
+             "-lc10_cuda", f"-Wl,-rpath,{lib}"]]
+
+
+def _run(cmd: list[str], what: str) -> str:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    return r.stdout + r.stderr
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(),
@@ -58,8 +91,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(),
     os.makedirs(BUILD_DIR, exist_ok=True)
     stamp = os.path.join(BUILD_DIR, "fingerprint.txt")
     fp = _fingerprint(extra_flags)
-    if (not force and os.path.exists(LIB_PATH) and os.path.exists(stamp)
-            and open(stamp).read().strip() == fp):
+    if (not force and os.path.exists(LIB_PATH) and os.path.exists(BINDING_PATH)
+            and os.path.exists(stamp) and open(stamp).read().strip() == fp):
         return LIB_PATH
     cc = nvcc()
 
@@ -68,29 +101,29 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(),
         cmd = [cc, *ARCH, *NVCC_FLAGS, *extra_flags, "-c", src, "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
-        return obj, (r.stdout + r.stderr)
+        return obj, _run(cmd, f"nvcc for {src}")
 
+    binding_obj = os.path.join(BUILD_DIR, "binding.o")
+    binding_cc, binding_ld = _binding_commands(binding_obj, BINDING_PATH + ".tmp")
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=jobs or min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=jobs or min(8, len(srcs) + 1)) as ex:
+        binding = ex.submit(_run, binding_cc, "binding")
         results = list(ex.map(compile_one, srcs))
+        binding.result()
     if verbose:
         for _, log in results:
             if log.strip():
                 print(log)
     tmp = LIB_PATH + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp] + [o for o, _ in results]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run(cmd, "link")
     os.replace(tmp, LIB_PATH)
+    _run(binding_ld, "binding link")
+    os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
     with open(stamp, "w") as f:
         f.write(fp)
     return LIB_PATH
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))

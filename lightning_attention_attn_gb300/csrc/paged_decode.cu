@@ -89,78 +89,90 @@ __device__ __forceinline__ int request_tiles(const PagedDecodeArgs &a, int b) {
     return (request_len(a, b) + kTile - 1) / kTile;
 }
 
-// Tiles of the requests before `b` and of all requests (per unit of a
-// request), by the whole block.  red: kWarpsIn + ... words of shared memory.
+// The tile that CTA `cta`'s range begins with.  All tiles (of all units, request
+// by request) are cut into ranges of `chunk`, CTA c taking [c chunk, (c + 1) chunk).
+struct Place {
+    long long all, chunk, w;  // tiles of all units, of a range, first of this one
+    long long unit0;          // first tile of request b
+    int b;
+};
+
+// Whole block (kThr threads): false where the CTA has no tile.  The lengths are
+// read once for up to kThr requests.
 template <int kThr>
-__device__ __forceinline__ void count_tiles(const PagedDecodeArgs &a, int b, long long &before,
-                                            long long &all, long long *red) {
-    long long sb = 0, sa = 0;
-    for (int i = threadIdx.x; i < a.batch; i += kThr) {
-        const int t = request_tiles(a, i);
-        sa += t;
-        if (i < b) sb += t;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        sa += __shfl_xor_sync(0xffffffffu, sa, o);
-        sb += __shfl_xor_sync(0xffffffffu, sb, o);
-    }
-    if ((threadIdx.x & 31) == 0) {
-        red[threadIdx.x >> 5] = sa;
-        red[kThr / 32 + (threadIdx.x >> 5)] = sb;
-    }
-    __syncthreads();
-    all = before = 0;
-#pragma unroll
-    for (int w = 0; w < kThr / 32; ++w) all += red[w], before += red[kThr / 32 + w];
-}
-
-// First tile of CTA c's range when `all` tiles are divided among n CTAs.
-__device__ __forceinline__ long long range_begin(long long all, int n, int c) {
-    return all * c / n;
-}
-
-// Finds the request that tile `w` (of all units) lies in: its index, and the
-// tiles of the requests before it.  Whole block; walks the lengths in order,
-// kThreads at a time.
-__device__ __forceinline__ void find_request(const PagedDecodeArgs &a, long long w, int units,
-                                             int &b, long long &before, long long *scan) {
+__device__ __forceinline__ bool find_place(const PagedDecodeArgs &a, int units, int cta, Place &p) {
+    constexpr int kW = kThr / 32;
+    __shared__ long long sums[kW];
+    __shared__ long long found[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long base = 0;
-    for (int b0 = 0;; b0 += kThreads) {
+    long long total;
+    // inclusive prefix sum of the tiles of requests b0 .. b0 + kThr - 1
+    auto scan = [&](int b0, int &t) {
         const int i = b0 + threadIdx.x;
-        const int t = i < a.batch ? request_tiles(a, i) : 0;
-        long long s = t;  // inclusive scan
+        t = i < a.batch ? request_tiles(a, i) : 0;
+        long long s = t;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long v = __shfl_up_sync(0xffffffffu, s, o);
             if (lane >= o) s += v;
         }
         __syncthreads();
-        if (lane == 31) scan[warp] = s;
-        if (threadIdx.x == 0) scan[kWarps] = -1;
+        if (lane == 31) sums[warp] = s;
+        if (threadIdx.x == 0) found[0] = -1;
         __syncthreads();
-        long long upto = base;
-        for (int v = 0; v < warp; ++v) upto += scan[v];
-        upto += s;
-        // exactly one request holds w: the first whose inclusive count passes it
-        if (t > 0 && w >= (upto - t) * units && w < upto * units) {
-            scan[kWarps] = i;
-            scan[kWarps + 1] = s - t;
+        long long below = 0;
+        total = 0;
+#pragma unroll
+        for (int v = 0; v < kW; ++v) {
+            if (v < warp) below += sums[v];
+            total += sums[v];
+        }
+        return s + below;
+    };
+    int t;
+    long long upto = scan(0, t), sum = total;
+    for (int b0 = kThr; b0 < a.batch; b0 += kThr) {
+        int unused;
+        scan(b0, unused);
+        sum += total;
+    }
+    p.all = sum * units;
+    p.chunk = max((p.all + kPagedCtas - 1) / kPagedCtas, 1LL);
+    p.w = cta * p.chunk;
+    if (p.w >= p.all) return false;
+    long long base = 0;
+    for (int b0 = 0;; b0 += kThr) {
+        if (b0 > 0 || a.batch > kThr) upto = scan(b0, t);
+        // one request holds w: the first whose inclusive count passes it
+        if (t > 0 && p.w >= (base + upto - t) * units && p.w < (base + upto) * units) {
+            found[0] = b0 + threadIdx.x;
+            found[1] = base + upto - t;
         }
         __syncthreads();
-        if (scan[kWarps] >= 0) {
-            b = (int)scan[kWarps];
-            before = base + scan[kWarps + 1];
-            for (int v = 0; v < (b - b0) / 32; ++v) before += scan[v];
-            return;
-        }
-        for (int v = 0; v < kWarps; ++v) base += scan[v];
-        if (b0 + kThreads >= a.batch) {  // w is past the last tile: not reached
-            b = a.batch;
-            before = base;
-            return;
-        }
+        if (found[0] >= 0 || b0 + kThr >= a.batch) break;
+        base += total;
+    }
+    p.b = (int)found[0];
+    p.unit0 = found[1] * units;
+    return p.b >= 0;
+}
+
+// n / d for a count of tiles: 32-bit where it fits.
+__device__ __forceinline__ int tiles_div(long long n, int d) {
+    return (n >> 32) == 0 ? (int)((uint32_t)n / (uint32_t)d) : (int)(n / d);
+}
+
+// Zeros for the requests without tokens, which are nobody's tiles.
+template <typename T>
+__device__ __forceinline__ void write_empty(const PagedDecodeArgs &a) {
+    const int row = a.num_heads * a.head_dim;
+    for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+        if (request_len(a, b) != 0) continue;
+        for (int i = threadIdx.x; i < row; i += blockDim.x)
+            static_cast<T *>(a.out)[(size_t)b * row + i] = T(0.f);
+        if (a.lse)
+            for (int i = threadIdx.x; i < a.num_heads; i += blockDim.x)
+                a.lse[(size_t)b * a.num_heads + i] = -CUDART_INF_F;
     }
 }
 
@@ -199,8 +211,6 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     constexpr int kRows = 8 * NT;
 
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long red[2 * kWarps];
-    __shared__ long long scan[kWarps + 2];
 
     // launched as a dependent launch: the lengths, the table and the cache
     // may have been written by the kernel before
@@ -211,16 +221,12 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     const int g = lane >> 2, c2 = (lane & 3) * 2;
     const int units = a.num_kv_heads * a.head_groups;
 
-    long long unused, all;
-    count_tiles<kThreads>(a, 0, unused, all, red);
-    all *= units;
-    const int n = (int)min(all, (long long)gridDim.x);
-    if ((int)blockIdx.x >= n) return;
-    long long w0 = range_begin(all, n, blockIdx.x);
-    const long long w1 = range_begin(all, n, blockIdx.x + 1);
-    int b;
-    long long before;
-    find_request(a, w0, units, b, before, scan);
+    write_empty<__nv_bfloat16>(a);
+    Place at;
+    if (!find_place<kThreads>(a, units, blockIdx.x, at)) return;
+    long long w0 = at.w;
+    const long long w1 = min(at.all, w0 + at.chunk);
+    int b = at.b;
 
     const uint32_t ring = ptx::smem_u32(smem) + warp * kStages * C::kStageBytes;
     const int crow = lane / CH, cch = lane % CH;
@@ -229,7 +235,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     const int vrow = (lane & 7) + ((lane >> 4) << 3), vchunk = (lane >> 3) & 1;
 
     bool first = true;
-    long long unit0 = before * units;  // first tile of request b
+    long long unit0 = at.unit0;  // first tile of request b
     for (; w0 < w1; ) {
         if (b >= a.batch) return;
         const int len = request_len(a, b);
@@ -239,8 +245,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
             ++b;
             continue;
         }
-        const int unit = (int)((w0 - unit0) / tiles);
-        const int tile0 = (int)((w0 - unit0) % tiles);
+        const int unit = tiles_div(w0 - unit0, tiles);
+        const int tile0 = (int)(w0 - unit0 - (long long)unit * tiles);
         const int tile1 = (int)min((long long)tiles, tile0 + (w1 - w0));
         const int kvh = unit / a.head_groups, hg = unit % a.head_groups;
         const int head0 = kvh * a.group + hg * kRows;
@@ -512,24 +518,18 @@ paged_decode_f32_kernel(const __grid_constant__ PagedDecodeArgs a) {
     constexpr int kSt = D == 128 ? 2 : 3;
 
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long red[2 * kWarps];
-    __shared__ long long scan[kWarps + 2];
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int units = a.num_kv_heads * a.head_groups;
-    long long unused, all;
-    count_tiles<kThreads>(a, 0, unused, all, red);
-    all *= units;
-    const int n = (int)min(all, (long long)gridDim.x);
-    if ((int)blockIdx.x >= n) return;
-    long long w0 = range_begin(all, n, blockIdx.x);
-    const long long w1 = range_begin(all, n, blockIdx.x + 1);
-    int b;
-    long long before;
-    find_request(a, w0, units, b, before, scan);
+    write_empty<float>(a);
+    Place at;
+    if (!find_place<kThreads>(a, units, blockIdx.x, at)) return;
+    long long w0 = at.w;
+    const long long w1 = min(at.all, w0 + at.chunk);
+    int b = at.b;
 
     float *qs = reinterpret_cast<float *>(smem);                  // [kRows][D]
     float *pw = qs + kRows * D + warp * kGroup * kRows;           // [16][kRows] of this warp
@@ -537,7 +537,7 @@ paged_decode_f32_kernel(const __grid_constant__ PagedDecodeArgs a) {
     const uint32_t ring_u = ptx::smem_u32(ring);
 
     bool first = true;
-    long long unit0 = before * units;
+    long long unit0 = at.unit0;
     for (; w0 < w1; ) {
         if (b >= a.batch) return;
         const int len = request_len(a, b);
@@ -547,8 +547,8 @@ paged_decode_f32_kernel(const __grid_constant__ PagedDecodeArgs a) {
             ++b;
             continue;
         }
-        const int unit = (int)((w0 - unit0) / tiles);
-        const int tile0 = (int)((w0 - unit0) % tiles);
+        const int unit = tiles_div(w0 - unit0, tiles);
+        const int tile0 = (int)(w0 - unit0 - (long long)unit * tiles);
         const int tile1 = (int)min((long long)tiles, tile0 + (w1 - w0));
         const int kvh = unit / a.head_groups, hg = unit % a.head_groups;
         const int head0 = kvh * a.group + hg * kRows;
@@ -749,62 +749,97 @@ paged_decode_f32_kernel(const __grid_constant__ PagedDecodeArgs a) {
 }
 
 // -------------------------------------------------------------------- join
-// One block per unit: adds the pieces of a unit that several CTAs hold, in
-// the order of their tokens, and writes the rows of requests without tokens.
-template <typename T, int D>
-__global__ void __launch_bounds__(128)
-paged_join_kernel(const __grid_constant__ PagedDecodeArgs a, int ctas, int rows) {
-    __shared__ long long red[8];
+// Adds the pieces of the units that several CTAs hold, in the order of their
+// tokens.  Block c - 1 looks at the start of CTA c's range: if it is the first such
+// start inside a unit, the block joins that unit (at most kPagedCtas - 1 units are
+// cut, whatever the batch).  A unit's maxima come first, all pieces at once,
+// then its columns, four a thread, the pieces in kJoin / columns slices.
+constexpr int kJoin = 512;
+
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(kJoin)
+paged_join_kernel(const __grid_constant__ PagedDecodeArgs a) {
+    __shared__ float wgt[kPagedCtas][ROWS];
+    __shared__ float4 part[kJoin];
     const int units = a.num_kv_heads * a.head_groups;
-    const int b = blockIdx.x / units, unit = blockIdx.x % units;
     // The lengths were complete before the main kernel let this one be
     // scheduled; the pieces are read after the wait.
-    long long before, all;
-    count_tiles<128>(a, b, before, all, red);
-    all *= units;
-    const int tiles = request_tiles(a, b);
+    Place at;
+    const int c = blockIdx.x + 1;
+    const bool any = find_place<kJoin>(a, units, c, at);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (!any) return;
+    const int tiles = request_tiles(a, at.b);
+    const int unit = tiles_div(at.w - at.unit0, tiles);
+    const long long u0 = at.unit0 + (long long)unit * tiles;
+    if (at.w == u0 || at.w - at.chunk > u0) return;  // no cut here, or not a unit's first
+    const int pieces = (int)((u0 + tiles - 1) / at.chunk) - c + 2;
+    // the first piece ends CTA c - 1's range (and is all of it if it began there),
+    // the others begin theirs
+    const float *first = piece_at<D>(a, c - 1, at.w - at.chunk == u0, ROWS);
+    auto piece = [&](int i) { return i == 0 ? first : piece_at<D>(a, c - 1 + i, true, ROWS); };
 
     const int kvh = unit / a.head_groups, hg = unit % a.head_groups;
-    const int head0 = kvh * a.group + hg * rows;
-    const int heads = min(rows, a.group - hg * rows);
-    const size_t row0 = (size_t)b * a.num_heads + head0;
-    if (tiles == 0) {
-        for (int i = threadIdx.x; i < heads * D; i += 128)
-            static_cast<T *>(a.out)[row0 * D + i] = T(0.f);
-        if (a.lse && threadIdx.x < heads) a.lse[row0 + threadIdx.x] = -CUDART_INF_F;
-        return;
-    }
-    const int n = (int)min(all, (long long)ctas);
-    const long long u0 = before * units + (long long)unit * tiles, u1 = u0 + tiles;
-    // CTA of a tile: the last one whose range begins at or before it
-    auto cta_of = [&](long long w) {
-        int c = (int)(w * n / all);
-        while (range_begin(all, n, c + 1) <= w) ++c;
-        return c;
-    };
-    const int c0 = cta_of(u0), c1 = cta_of(u1 - 1);
-    if (c0 == c1) return;  // finished by the main kernel
-
-    for (int i = threadIdx.x; i < heads * D; i += 128) {
-        const int h = i / D, d = i % D;
-        float m = -CUDART_INF_F, sum = 0.f, acc = 0.f;
-        for (int c = c0; c <= c1; ++c) {
-            const float *p = piece_at<D>(a, c, range_begin(all, n, c) >= u0, rows);
-            const float pm = p[rows * D + 2 * h], ps = p[rows * D + 2 * h + 1];
-            const float x = p[h * D + d];
-            const float nm = fmaxf(m, pm);
-            const float base = nm == -CUDART_INF_F ? 0.f : nm;
-            const float f = exp2f(m - base), e = exp2f(pm - base);
-            sum = sum * f + ps * e;
-            acc = acc * f + x * e;
-            m = nm;
+    const int head0 = kvh * a.group + hg * ROWS;
+    const int heads = min(ROWS, a.group - hg * ROWS);
+    const size_t row0 = (size_t)at.b * a.num_heads + head0;
+    const int lane = threadIdx.x & 31;
+    for (int h = threadIdx.x >> 5; h < heads; h += kJoin / 32) {
+        float m = -CUDART_INF_F, sum = 0.f;
+        for (int i = lane; i < pieces; i += 32) {
+            const float pm = piece(i)[ROWS * D + 2 * h];
+            wgt[i][h] = pm;
+            m = fmaxf(m, pm);
         }
-        static_cast<T *>(a.out)[(row0 + h) * D + d] = T(sum != 0.f ? acc / sum : 0.f);
-        if (a.lse && d == 0)
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float base = m == -CUDART_INF_F ? 0.f : m;
+        for (int i = lane; i < pieces; i += 32) {
+            const float f = exp2f(wgt[i][h] - base);
+            sum += f * piece(i)[ROWS * D + 2 * h + 1];
+            wgt[i][h] = f;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float r = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays NaN
+        for (int i = lane; i < pieces; i += 32) wgt[i][h] *= r;
+        if (a.lse && lane == 0)
             a.lse[row0 + h] = sum != 0.f ? (m + log2f(sum)) * (1.f / kLog2e) : -CUDART_INF_F;
     }
+    __syncthreads();
+
+    const int cols = heads * (D / 4);  // at most kJoin
+    const int slices = kJoin / cols;
+    const int slice = threadIdx.x / cols, col = threadIdx.x - slice * cols;
+    const int h = col / (D / 4), d = (col % (D / 4)) * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (slice < slices) {
+#pragma unroll 8
+        for (int i = slice; i < pieces; i += slices) {
+            const float4 x = *reinterpret_cast<const float4 *>(piece(i) + h * D + d);
+            const float f = wgt[i][h];
+            acc.x += f * x.x;
+            acc.y += f * x.y;
+            acc.z += f * x.z;
+            acc.w += f * x.w;
+        }
+    }
+    part[threadIdx.x] = acc;
+    __syncthreads();
+    if (slice > 0) return;
+    for (int i = 1; i < slices; ++i) {
+        const float4 x = part[threadIdx.x + i * cols];
+        acc.x += x.x;
+        acc.y += x.y;
+        acc.z += x.z;
+        acc.w += x.w;
+    }
+    T *o = static_cast<T *>(a.out) + (row0 + h) * D + d;
+    if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<uint2 *>(o) = make_uint2(pack2(acc.x, acc.y), pack2(acc.z, acc.w));
+    else
+        *reinterpret_cast<float4 *>(o) = acc;
 }
 
 // Opts `kern` into `smem` bytes of dynamic shared memory on every device it
@@ -813,11 +848,9 @@ template <typename K> cudaError_t allow_smem(K kern, size_t smem) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
 
-template <typename T, int D>
-cudaError_t join(const PagedDecodeArgs &a, int rows) {
-    return launch_dependent(paged_join_kernel<T, D>,
-                            (unsigned)(a.batch * a.num_kv_heads * a.head_groups), 128, 0, a.stream,
-                            a, (int)kPagedCtas, rows);
+template <typename T, int D, int ROWS>
+cudaError_t join(const PagedDecodeArgs &a) {
+    return launch_dependent(paged_join_kernel<T, D, ROWS>, kPagedCtas - 1, kJoin, 0, a.stream, a);
 }
 
 template <int D, int NT, bool QF32>
@@ -827,7 +860,7 @@ cudaError_t launch_bf16(PagedDecodeArgs a) {
     constexpr size_t kSmem = Bf16Core<D, NT>::kSmem;
     cudaError_t e = allow_smem(kern, kSmem);
     if (e == cudaSuccess) e = launch_dependent(kern, kPagedCtas, kThreads, kSmem, a.stream, a);
-    if (e == cudaSuccess) e = join<__nv_bfloat16, D>(a, 8 * NT);
+    if (e == cudaSuccess) e = join<__nv_bfloat16, D, 8 * NT>(a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -840,7 +873,7 @@ cudaError_t launch_f32(PagedDecodeArgs a) {
         sizeof(float) * (8 * NT * D + kWarps * kGroup * 8 * NT + kWarps * kSt * 2 * kGroup * D);
     cudaError_t e = allow_smem(kern, kSmem);
     if (e == cudaSuccess) e = launch_dependent(kern, kPagedCtas, kThreads, kSmem, a.stream, a);
-    if (e == cudaSuccess) e = join<float, D>(a, 8 * NT);
+    if (e == cudaSuccess) e = join<float, D, 8 * NT>(a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

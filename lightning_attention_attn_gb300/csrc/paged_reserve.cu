@@ -9,14 +9,15 @@
 //     served iff want fits the table row and (need_b = 0 or upto_b <= free)
 // and page i of its need comes from the free stack's entry
 // free - 1 - (upto_b - need_b) - i.  Prefix sums only, so the result does not
-// depend on the order in which threads run.
+// depend on the order in which threads run; the requests served with a need
+// are the first ones that have one.
 //
-// Latency-bound: a few kilobytes of lengths, then one slot and one position a
-// token.  One launch of one cluster: every CTA computes the prefix sums for
-// itself (a few hundred lengths) and takes a share of the tokens; the
-// cluster's barrier separates the pushes and all reads of the lengths from
-// the pops and the updates, so lengths and count may be updated in place.
-// One CTA up to kSmallTokens tokens, else eight (the portable cluster size).
+// Latency-bound: a few kilobytes of lengths, then a slot and a position a
+// token.  One CTA computes the prefix sums; up to kSmallTokens tokens it writes
+// the slots too (one launch).  For more (prompts) a second kernel, over all
+// SMs, reads the lengths after the step and the offsets that the first has
+// written and fills slots, positions and table, so lengths and count may be
+// updated in place.
 #include <cuda_runtime.h>
 
 #include "la_internal.h"
@@ -24,201 +25,250 @@
 namespace la {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxThreads = 1024;
+constexpr int kFillThreads = 256;
+constexpr int kFillBlocks = 152 * 2;
 constexpr int kSmallTokens = 4096;
-constexpr int kCluster = 8;
 
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ int cluster_rank() {
-    int r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
+struct Pair {
+    long long x, y;
+};
 
-// Inclusive prefix sum over the block's threads; *all is the block's sum.
-__device__ __forceinline__ long long block_scan(long long x, long long *warp_sums, long long *all) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Inclusive prefix sums of two values over the block's threads, and the
+// block's totals.  sums: two rows of 32.
+__device__ __forceinline__ Pair block_scan(long long x, long long y, long long (*sums)[32], Pair *all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += v;
+        const long long u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) x += u, y += v;
     }
     __syncthreads();  // the previous scan's readers are done
-    if (lane == 31) warp_sums[warp] = x;
+    if (lane == 31) sums[0][warp] = x, sums[1][warp] = y;
     __syncthreads();
-    long long w = warp_sums[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += v;
+    Pair below = {0, 0};
+    *all = {0, 0};
+    for (int w = 0; w < warps; ++w) {
+        const long long u = sums[0][w], v = sums[1][w];
+        if (w < warp) below.x += u, below.y += v;
+        all->x += u, all->y += v;
     }
-    *all = __shfl_sync(0xffffffffu, w, 31);
-    const long long below = __shfl_sync(0xffffffffu, w, warp == 0 ? 0 : warp - 1);
-    return x + (warp == 0 ? 0 : below);
+    return {x + below.x, y + below.y};
 }
 
 __device__ __forceinline__ int blocks_of(long long tokens, int page) {
     return (int)((tokens + page - 1) / page);
 }
 
-__global__ void __launch_bounds__(kThreads)
-paged_reserve_kernel(const PagedReserveArgs a, int ctas) {
-    extern __shared__ int smem[];
-    __shared__ long long warp_sums[32];
-    int *cu = smem;                  // [B + 1] first new token of a request
-    int *old = cu + a.batch + 1;     // [B] tokens before the step; ~tokens if not served
-    int *top = old + a.batch;        // [B] stack entry of a request's first new page
-
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-    const int rank = ctas > 1 ? cluster_rank() : 0;
-    const int lane = threadIdx.x & 31, warp = rank * kWarps + (threadIdx.x >> 5);
-    const int warps = ctas * kWarps;
-    const long long capacity = min((long long)a.table_width * a.page_size, 0x7fffffffLL);
-    long long count = min(max(__ldcg(a.free_count), 0), a.num_pages);
-
-    // pages that finished requests return, in the order of requests and blocks
-    if (a.finished) {
-        long long base = 0;
-        for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
-            const int b = b0 + threadIdx.x;
-            int n = 0;
-            if (b < a.batch && a.finished[b])
-                n = blocks_of(min((long long)max(__ldcg(a.seq_lens + b), 0), capacity), a.page_size);
-            long long all;
-            const long long upto = block_scan(n, warp_sums, &all) + base;
-            if (b < a.batch) {
-                top[b] = (int)min(count + upto - n, (long long)a.num_pages);
-                old[b] = n;
-            }
-            base += all;
-        }
-        __syncthreads();
-        for (int b = warp; b < a.batch; b += warps)
-            for (int i = lane; i < old[b]; i += 32)
-                if (top[b] + i < a.num_pages)
-                    a.free_pages[top[b] + i] = __ldcg(a.block_table + (size_t)b * a.table_stride + i);
-        count = min(count + base, (long long)a.num_pages);
-        __syncthreads();
+// The last entry of the ascending at[0 .. n) that is <= v (at[0] is).
+__device__ __forceinline__ int last_at(const int *at, int n, int v) {
+    int lo = 0;
+    while (n - lo > 1) {
+        const int mid = (lo + n) >> 1;
+        if (at[mid] <= v) lo = mid; else n = mid;
     }
+    return lo;
+}
 
-    // pages and offsets of the new tokens
-    long long tokens = 0, taken = 0, left = count;
-    for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
-        const int b = b0 + threadIdx.x;
-        long long was = 0, add = 0;
-        int need = 0;
-        bool fits = true;
-        if (b < a.batch) {
-            was = max(__ldcg(a.seq_lens + b), 0);
-            if (a.finished && a.finished[b]) was = 0;
-            add = max(__ldcg(a.new_lens + b), 0);
-            fits = was + add <= capacity;
-            if (fits) need = blocks_of(was + add, a.page_size) - blocks_of(was, a.page_size);
-        }
-        long long all, all_need;
-        const long long upto = block_scan(add, warp_sums, &all) + tokens;
-        const long long upto_need = block_scan(need, warp_sums, &all_need) + taken;
-        if (b < a.batch) {
-            const bool ok = fits && (need == 0 || upto_need <= count);
-            cu[b] = (int)min(upto - add, 0x7fffffffLL);
-            old[b] = ok ? (int)was : ~(int)was;
-            top[b] = (int)(count - 1 - (upto_need - need));  // used by served requests only
-            if (ok && need > 0) left = min(left, count - upto_need);
-        }
-        tokens += all;
-        taken += all_need;
-    }
-    if (threadIdx.x == 0) cu[a.batch] = (int)min(tokens, 0x7fffffffLL);
-    // the stack after the step: the smallest remainder that a served request left
-    {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) left = min(left, __shfl_xor_sync(0xffffffffu, left, o));
-        __syncthreads();
-        if (lane == 0) warp_sums[threadIdx.x >> 5] = left;
-        __syncthreads();
-        left = warp_sums[lane];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) left = min(left, __shfl_xor_sync(0xffffffffu, left, o));
-    }
+// Arrays of the step in shared memory.
+struct Step {
+    int *cu;     // [B + 1] first new token of a request
+    int *old;    // [B] tokens before the step; ~tokens if it is not served
+    int *taken;  // [B + 1] pages taken by the requests before
+};
+__device__ __forceinline__ Step step_arrays(int *smem, int batch) {
+    return {smem, smem + batch + 1, smem + 2 * batch + 1};
+}
 
-    // every read of the lengths, the count and finished rows is done, every
-    // push is visible
-    if (ctas > 1) cluster_barrier(); else __syncthreads();
-
-    const int end = cu[a.batch];
-    for (int t = rank * kThreads + threadIdx.x; t < a.num_tokens; t += ctas * kThreads) {
+// Slots and positions of the new tokens, and the table's new blocks; thread
+// `i` of `n`.  top: the stack entry of the first page taken; pages: how many are.
+__device__ __forceinline__ void fill(const PagedReserveArgs &a, const Step &s, int top, int pages, int i,
+                                     int n) {
+    const int end = s.cu[a.batch];
+    for (int t = i; t < a.num_tokens; t += n) {
         int slot = -1, position = 0;
         if (t < end) {
-            int lo = 0, hi = a.batch;  // the last request with cu[b] <= t
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (cu[mid] <= t) lo = mid; else hi = mid;
-            }
-            const int was = old[lo];
+            const int b = last_at(s.cu, a.batch, t);
+            const int was = s.old[b];
             if (was >= 0) {
-                position = was + (t - cu[lo]);
+                position = was + (t - s.cu[b]);
                 const int blk = position / a.page_size;
                 const int have = blocks_of(was, a.page_size);
+                // new blocks from the stack: the table may not hold them yet
                 const int page = blk < have
-                                     ? __ldcg(a.block_table + (size_t)lo * a.table_stride + blk)
-                                     : __ldcg(a.free_pages + (top[lo] - (blk - have)));
-                slot = page < 0 || page >= a.num_pages ? -1 : page * a.page_size + (position - blk * a.page_size);
+                                     ? __ldcg(a.block_table + (size_t)b * a.table_stride + blk)
+                                     : __ldcg(a.free_pages + (top - s.taken[b] - (blk - have)));
+                slot = page < 0 || page >= a.num_pages
+                           ? -1 : page * a.page_size + (position - blk * a.page_size);
             }
         }
         a.slots[t] = slot;
         a.positions[t] = position;
     }
-    for (int b = warp; b < a.batch; b += warps) {
-        const int was = old[b];
-        if (was < 0) continue;
-        const int have = blocks_of(was, a.page_size);
-        const int want = blocks_of((long long)was + (cu[b + 1] - cu[b]), a.page_size);
-        for (int i = have + lane; i < want; i += 32)
-            a.block_table[(size_t)b * a.table_stride + i] = __ldcg(a.free_pages + (top[b] - (i - have)));
+    for (int j = i; j < pages; j += n) {
+        const int b = last_at(s.taken, a.batch, j);
+        const int blk = blocks_of(s.old[b], a.page_size) + (j - s.taken[b]);
+        a.block_table[(size_t)b * a.table_stride + blk] = __ldcg(a.free_pages + (top - j));
     }
-    for (int b = rank * kThreads + threadIdx.x; b < a.batch; b += ctas * kThreads) {
-        const int was = old[b];
-        a.cu_seqlens[b + 1] = cu[b + 1];
-        a.served[b] = was >= 0;
-        a.seq_lens_out[b] = was >= 0 ? was + (cu[b + 1] - cu[b]) : ~was;
+}
+
+template <bool FILL>
+__global__ void __launch_bounds__(kMaxThreads)
+paged_reserve_kernel(const __grid_constant__ PagedReserveArgs a) {
+    extern __shared__ int smem[];
+    __shared__ long long sums[2][32];
+    const Step s = step_arrays(smem, a.batch);
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const int threads = blockDim.x;
+    const long long capacity = min((long long)a.table_width * a.page_size, 0x7fffffffLL);
+    long long count = min(max(__ldcg(a.free_count), 0), a.num_pages);
+
+    // a request's length, finish mark and new tokens; those of the first
+    // `threads` requests are loaded once
+    int len = 0, add = 0;
+    bool ended = false;
+    auto load = [&](int b) {
+        len = add = 0;
+        ended = false;
+        if (b < a.batch) {
+            len = max(__ldcg(a.seq_lens + b), 0);
+            add = max(__ldcg(a.new_lens + b), 0);
+            ended = a.finished && a.finished[b] != 0;
+        }
+    };
+    load(threadIdx.x);
+
+    // pages that finished requests return, in the order of requests and blocks
+    if (a.finished) {
+        long long base = 0;
+        for (int b0 = 0; b0 < a.batch; b0 += threads) {
+            const int b = b0 + threadIdx.x;
+            if (b0 > 0) load(b);
+            const int n = ended ? blocks_of(min((long long)len, capacity), a.page_size) : 0;
+            Pair all;
+            const Pair upto = block_scan(n, 0, sums, &all);
+            if (b < a.batch) s.taken[b] = (int)min(count + base + upto.x - n, (long long)a.num_pages);
+            base += all.x;
+        }
+        __syncthreads();
+        // entry j of the push: block j - (entries before) of the request that holds it
+        const int top = (int)count, most = (int)min(count + base, (long long)a.num_pages);
+        for (int j = top + threadIdx.x; j < most; j += threads) {
+            const int b = last_at(s.taken, a.batch, j);
+            a.free_pages[j] = __ldcg(a.block_table + (size_t)b * a.table_stride + (j - s.taken[b]));
+        }
+        count = min(count + base, (long long)a.num_pages);
+        if (a.batch > threads) load(threadIdx.x);
+        __syncthreads();
     }
-    if (rank == 0 && threadIdx.x == 0) {
+
+    // offsets of the new tokens, pages for them
+    Pair base = {0, 0};
+    long long left = count;
+    for (int b0 = 0; b0 < a.batch; b0 += threads) {
+        const int b = b0 + threadIdx.x;
+        if (b0 > 0) load(b);
+        const long long was = ended ? 0 : len;
+        const bool fits = was + add <= capacity;
+        const int need =
+            fits ? blocks_of(was + add, a.page_size) - blocks_of(was, a.page_size) : 0;
+        Pair all;
+        Pair upto = block_scan(add, need, sums, &all);
+        upto.x += base.x, upto.y += base.y;
+        if (b < a.batch) {
+            const bool ok = fits && (need == 0 || upto.y <= count);
+            s.cu[b] = (int)min(upto.x - add, 0x7fffffffLL);
+            s.old[b] = ok ? (int)was : ~(int)was;
+            s.taken[b] = (int)min(upto.y - need, 0x7fffffffLL);
+            if (ok && need > 0) left = min(left, count - upto.y);
+            a.cu_seqlens[b + 1] = (int)min(upto.x, 0x7fffffffLL);
+            a.served[b] = ok;
+            a.seq_lens_out[b] = (int)(ok ? was + add : was);
+        }
+        base.x += all.x, base.y += all.y;
+    }
+    if (threadIdx.x == 0) {
+        s.cu[a.batch] = (int)min(base.x, 0x7fffffffLL);
         a.cu_seqlens[0] = 0;
-        a.free_count_out[0] = (int)left;
     }
+    // the stack after the step: below the last page that a served request took
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) left = min(left, __shfl_xor_sync(0xffffffffu, left, o));
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sums[0][threadIdx.x >> 5] = left;
+    __syncthreads();
+    for (int w = 0; w < threads >> 5; ++w) left = min(left, sums[0][w]);
+    if (threadIdx.x == 0) a.free_count_out[0] = (int)left;
+    if (FILL) fill(a, s, (int)count - 1, (int)(count - left), threadIdx.x, threads);
+}
+
+// The second kernel of a long step: every CTA takes the step's arrays from the
+// first one's results.
+__global__ void __launch_bounds__(kFillThreads)
+paged_fill_kernel(const __grid_constant__ PagedReserveArgs a) {
+    extern __shared__ int smem[];
+    __shared__ long long sums[2][32];
+    const Step s = step_arrays(smem, a.batch);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    long long base = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kFillThreads) {
+        const int b = b0 + threadIdx.x;
+        int need = 0, was = 0, from = 0;
+        bool ok = false;
+        if (b < a.batch) {
+            from = __ldcg(a.cu_seqlens + b);
+            const int len = __ldcg(a.seq_lens_out + b);
+            ok = __ldcg(a.served + b) != 0;
+            was = ok ? len - (__ldcg(a.cu_seqlens + b + 1) - from) : len;
+            if (ok) need = blocks_of(len, a.page_size) - blocks_of(was, a.page_size);
+        }
+        Pair all;
+        const Pair upto = block_scan(need, 0, sums, &all);
+        if (b < a.batch) {
+            s.cu[b] = from;
+            s.old[b] = ok ? was : ~was;
+            s.taken[b] = (int)(base + upto.x - need);
+        }
+        base += all.x;
+    }
+    if (threadIdx.x == 0) s.cu[a.batch] = __ldcg(a.cu_seqlens + a.batch);
+    __syncthreads();
+    const int pages = (int)base;
+    fill(a, s, __ldcg(a.free_count_out) + pages - 1, pages, blockIdx.x * kFillThreads + threadIdx.x,
+         gridDim.x * kFillThreads);
 }
 
 }  // namespace
 
 cudaError_t paged_reserve(const PagedReserveArgs &a) {
-    const size_t smem = sizeof(int) * (3 * (size_t)a.batch + 1);
+    const size_t smem = sizeof(int) * (3 * (size_t)a.batch + 2);
+    const size_t most = sizeof(int) * (3 * (size_t)kReserveMaxBatch + 2);
+    const bool small = a.num_tokens <= kSmallTokens;
+    auto kern = small ? paged_reserve_kernel<true> : paged_reserve_kernel<false>;
+    cudaError_t e = cudaSuccess;
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            paged_reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-            (int)(sizeof(int) * (3 * (size_t)kReserveMaxBatch + 1)));
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+        if (e == cudaSuccess && !small)
+            e = cudaFuncSetAttribute(paged_fill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)most);
         if (e != cudaSuccess) return e;
     }
-    const int ctas = a.num_tokens > kSmallTokens ? kCluster : 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = a.stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_reserve_kernel, a, ctas);
+    // a thread per request (and, where it writes them, per token); all for the
+    // pages of finished requests, hundreds each
+    int threads = small && a.num_tokens > a.batch ? a.num_tokens : a.batch;
+    threads = threads > kMaxThreads || a.finished ? kMaxThreads
+              : threads < 128 ? 128 : (threads + 31) / 32 * 32;
+    e = launch_dependent(kern, 1, threads, smem, a.stream, a);
+    if (e == cudaSuccess && !small) {
+        const int blocks = (a.num_tokens + kFillThreads - 1) / kFillThreads;
+        e = launch_dependent(paged_fill_kernel, blocks < kFillBlocks ? blocks : kFillBlocks,
+                             kFillThreads, smem, a.stream, a);
+    }
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -12,57 +12,95 @@
 // once.
 //
 // Memory-bound: a row is read once and written once (backward: two reads, one
-// write), so the layout serves the loads.  A row is held by L = 16 B-vectors
-// lanes (8 to 32), 32 / L rows a warp instruction; a warp takes U such passes
-// of one token and one kind (query, key or value heads), so the token's
-// cosines and sines and the weights stay in registers for all its rows, and
-// U 16-byte loads a lane are in flight at once.
+// write), so the layout serves the loads.  A row is held by L = 8 to 32 lanes
+// of 16 bytes, 32 / L rows a warp instruction.  A warp takes one token's rows
+// of one kind (query, key or value heads), U passes at a time with the next U
+// already in flight, so the token's cosines and sines and the weights are
+// loaded once for all of them.  They are folded into two coefficients an
+// element, y = r (x A + partner(x) B) with A = w cos, B = +-w' sin, applied with
+// packed fp32 pairs; the partner's element crosses lanes in its stored type
+// (half the shuffles of an fp32 one in bf16).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "la_internal.h"
+#include "sm100_ptx.cuh"
 
 namespace la {
 namespace {
 
 constexpr int kWarps = 4;
 
-__device__ __forceinline__ void unpack(const uint4 &v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// 16 stored bytes as fp32 pairs.
+template <typename T> struct Vec;
+template <> struct Vec<__nv_bfloat16> {
+    static constexpr int P = 4;  // pairs
+    static __device__ __forceinline__ void unpack(const uint4 &v, float2 (&x)[4]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        for (int i = 0; i < 4; ++i)
+            x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    }
+    static __device__ __forceinline__ uint4 pack(const float2 (&x)[4]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(x[i].x, x[i].y);
+            w[i] = *reinterpret_cast<const uint32_t *>(&p);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <> struct Vec<float> {
+    static constexpr int P = 2;
+    static __device__ __forceinline__ void unpack(const uint4 &v, float2 (&x)[2]) {
+        x[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+        x[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+    }
+    static __device__ __forceinline__ uint4 pack(const float2 (&x)[2]) {
+        return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x),
+                          __float_as_uint(x[1].y));
+    }
+};
+
+template <int P> __device__ __forceinline__ void load_pairs(const float *p, float2 (&x)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; i += 2) {
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(p + 2 * i));
+        x[i] = make_float2(v.x, v.y);
+        x[i + 1] = make_float2(v.z, v.w);
     }
 }
-__device__ __forceinline__ void unpack(const uint4 &v, float (&x)[4]) {
-    x[0] = __uint_as_float(v.x);
-    x[1] = __uint_as_float(v.y);
-    x[2] = __uint_as_float(v.z);
-    x[3] = __uint_as_float(v.w);
-}
-__device__ __forceinline__ uint4 pack(const float (&x)[8]) {
-    uint32_t w[4];
+__device__ __forceinline__ float2 swapped(float2 x) { return make_float2(x.y, x.x); }
+__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
+
+// The rotated partner of every element of a lane's 16 bytes: in the lane that
+// holds the row's other half, or the other element of a pair; zero past
+// rotary_dim (where its coefficient is zero too).
+template <typename T>
+__device__ __forceinline__ void partner(const uint4 &v, const float2 (&x)[Vec<T>::P],
+                                        bool interleaved, bool rotated, int src,
+                                        float2 (&y)[Vec<T>::P]) {
+    if (interleaved) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&p);
+        for (int i = 0; i < Vec<T>::P; ++i) y[i] = rotated ? swapped(x[i]) : twice(0.f);
+    } else {
+        uint4 w;
+        w.x = __shfl_sync(0xffffffffu, v.x, src);
+        w.y = __shfl_sync(0xffffffffu, v.y, src);
+        w.z = __shfl_sync(0xffffffffu, v.z, src);
+        w.w = __shfl_sync(0xffffffffu, v.w, src);
+        Vec<T>::unpack(rotated ? w : make_uint4(0, 0, 0, 0), y);
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ uint4 pack(const float (&x)[4]) {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                      __float_as_uint(x[3]));
 }
 
-// One lane's coefficients of its token's rotation: y[e] = n[e] cs[e] +
-// partner(n)[e] sn[e], the sign of the partner's term inside sn; the identity
-// past rotary_dim.  The transposed rotation has sn negated.
-template <int E>
+// A lane's coefficients of its token's rotation, y = x cs + partner(x) sn; the
+// transposed rotation (sign -1) has sn negated.
+template <int P>
 __device__ __forceinline__ void load_rotation(const NormRopeArgs &a, int token, int j0, float sign,
-                                              float (&cs)[E], float (&sn)[E]) {
+                                              float2 (&cs)[P], float2 (&sn)[P]) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) cs[e] = 1.f, sn[e] = 0.f;
+    for (int i = 0; i < P; ++i) cs[i] = twice(1.f), sn[i] = twice(0.f);
     if (j0 >= a.rotary_dim) return;
     // positions are checked nowhere on the host: clamped, so every read stays
     // inside the table
@@ -71,45 +109,19 @@ __device__ __forceinline__ void load_rotation(const NormRopeArgs &a, int token, 
     const int half = a.rotary_dim >> 1;
     if (a.interleaved) {
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-            const int i = (j0 + e) >> 1;
-            const float c = __ldg(row + i), s = sign * __ldg(row + half + i);
-            cs[e] = cs[e + 1] = c;
-            sn[e] = -s;
-            sn[e + 1] = s;
+        for (int i = 0; i < P; ++i) {
+            const float c = __ldg(row + (j0 >> 1) + i), s = sign * __ldg(row + half + (j0 >> 1) + i);
+            cs[i] = twice(c);
+            sn[i] = make_float2(-s, s);
         }
     } else {
         const bool low = j0 < half;
         const float *c = row + (low ? j0 : j0 - half);
-        const float sg = low ? -sign : sign;
+        load_pairs<P>(c, cs);
+        load_pairs<P>(c + half, sn);
+        const float2 sg = twice(low ? -sign : sign);
 #pragma unroll
-        for (int e = 0; e < E; e += 4) {
-            const float4 cv = __ldg(reinterpret_cast<const float4 *>(c + e));
-            const float4 sv = __ldg(reinterpret_cast<const float4 *>(c + half + e));
-            cs[e] = cv.x, cs[e + 1] = cv.y, cs[e + 2] = cv.z, cs[e + 3] = cv.w;
-            sn[e] = sg * sv.x, sn[e + 1] = sg * sv.y, sn[e + 2] = sg * sv.z,
-            sn[e + 3] = sg * sv.w;
-        }
-    }
-}
-
-// x <- rotated x; `src` is the lane that holds the other half's elements.
-template <int E>
-__device__ __forceinline__ void rotate(float (&x)[E], const float (&cs)[E], const float (&sn)[E],
-                                       bool interleaved, int src) {
-    if (interleaved) {
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-            const float u = x[e], v = x[e + 1];
-            x[e] = fmaf(u, cs[e], v * sn[e]);
-            x[e + 1] = fmaf(v, cs[e + 1], u * sn[e + 1]);
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float p = __shfl_sync(0xffffffffu, x[e], src);
-            x[e] = fmaf(x[e], cs[e], p * sn[e]);
-        }
+        for (int i = 0; i < P; ++i) sn[i] = ptx::f2_mul(sn[i], sg);
     }
 }
 
@@ -121,141 +133,172 @@ template <int L> __device__ __forceinline__ float row_sum(float s) {
 
 template <typename T, int D, int U, bool BACK>
 __global__ void __launch_bounds__(32 * kWarps)
-qk_norm_rope_kernel(const NormRopeArgs a) {
-    constexpr int E = 16 / (int)sizeof(T);  // elements per lane
-    constexpr int L = D / E;                // lanes per row
+qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int batches) {
+    using V = Vec<T>;
+    constexpr int P = V::P;                 // fp32 pairs per lane
+    constexpr int L = D / (2 * P);          // lanes per row
     constexpr int R = 32 / L;               // rows per pass
-    constexpr int kRows = R * U;            // rows per work item
+    constexpr int kRows = R * U;            // rows in flight
+    constexpr size_t kRowBytes = D * sizeof(T);
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int sub = lane / L, col = lane % L, j0 = col * E;
+    const int sub = lane / L, j0 = (lane % L) * 2 * P;
     const int half = a.rotary_dim >> 1;
-    // lane of the other half of a rotated pair (itself past rotary_dim)
-    const int src = a.interleaved || j0 >= a.rotary_dim ? lane
-                    : j0 < half ? lane + half / E : lane - half / E;
+    const bool rotated = j0 < a.rotary_dim;
+    // first element of the rotated partners, and the lane that holds it
+    const int jp = a.interleaved || !rotated ? j0 : j0 < half ? j0 + half : j0 - half;
+    const int src = lane + (jp - j0) / (2 * P);
 
-    const int nq = (a.set[0].heads + kRows - 1) / kRows, nk = (a.set[1].heads + kRows - 1) / kRows;
-    const int nv = (a.set[2].heads + kRows - 1) / kRows;
+    const int per_item = kRows * batches;
+    const int nq = (a.set[0].heads + per_item - 1) / per_item;
+    const int nk = (a.set[1].heads + per_item - 1) / per_item;
+    const int nv = (a.set[2].heads + per_item - 1) / per_item;
     const int per = nq + nk + nv;
     const int items = a.num_tokens * per;  // fits: the caller bounds the number of rows
 
-    float dw[2][E];  // this lane's columns of the weights' gradients
+    float2 dw[2][P];  // this lane's columns of the weights' gradients
     if (BACK) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) dw[0][e] = dw[1][e] = 0.f;
+        for (int i = 0; i < P; ++i) dw[0][i] = dw[1][i] = twice(0.f);
     }
 
     for (int item = blockIdx.x * kWarps + warp; item < items; item += gridDim.x * kWarps) {
         const int token = item / per, c = item - token * per;
         const int kind = c < nq ? 0 : c < nq + nk ? 1 : 2;
-        const NormRopeRows s = a.set[kind];
-        const int row0 = (kind == 0 ? c : kind == 1 ? c - nq : c - nq - nk) * kRows + sub;
+        const NormRopeRows &s = a.set[kind];
+        int row = (kind == 0 ? c : kind == 1 ? c - nq : c - nq - nk) * per_item;
+        const int end = min(s.heads, row + per_item);
+        row += sub;
 
-        // every load of the item first, so that they overlap
-        uint4 xv[U], gv[U];
-        const char *xp = static_cast<const char *>(s.x) + (size_t)token * s.x_stride + (size_t)j0 * sizeof(T);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            xv[u] = make_uint4(0, 0, 0, 0);
-            if (row0 + u * R < s.heads)
-                xv[u] = *reinterpret_cast<const uint4 *>(xp + (size_t)(row0 + u * R) * D * sizeof(T));
-        }
-        if (BACK) {
-            const char *gp = static_cast<const char *>(s.dy) + (size_t)token * s.dy_stride +
-                             (size_t)j0 * sizeof(T);
+        const char *xp = static_cast<const char *>(s.x) + (size_t)token * s.x_stride + j0 * sizeof(T);
+        const char *gp = BACK ? static_cast<const char *>(s.dy) + (size_t)token * s.dy_stride +
+                                    j0 * sizeof(T)
+                              : nullptr;
+        uint4 xv[U], gv[BACK ? U : 1];
+        auto load = [&](int first, uint4 (&x)[U], uint4 (&g)[BACK ? U : 1]) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                gv[u] = make_uint4(0, 0, 0, 0);
-                if (row0 + u * R < s.heads)
-                    gv[u] = *reinterpret_cast<const uint4 *>(gp + (size_t)(row0 + u * R) * D * sizeof(T));
+                const int r = first + u * R;
+                x[u] = r < end ? *reinterpret_cast<const uint4 *>(xp + r * kRowBytes)
+                               : make_uint4(0, 0, 0, 0);
+                if (BACK)
+                    g[u] = r < end ? *reinterpret_cast<const uint4 *>(gp + r * kRowBytes)
+                                   : make_uint4(0, 0, 0, 0);
             }
-        }
+        };
+        load(row, xv, gv);
+
         // destination of the token's rows: its row of the output, or its slot
         // of the cache (a slot outside the pool is skipped)
         char *out = static_cast<char *>(s.out);
-        size_t head_bytes = D * sizeof(T);
+        size_t head_bytes = kRowBytes;
         if (s.cache) {
             const int slot = __ldg(a.slots + token);
             if (slot < 0 || slot >= a.num_slots) continue;
             const int page = slot / a.page_size;
-            out += (size_t)page * s.out_stride + (size_t)(slot - page * a.page_size) * D * sizeof(T);
+            out += (size_t)page * s.out_stride + (size_t)(slot - page * a.page_size) * kRowBytes;
             head_bytes *= a.page_size;
         } else {
             out += (size_t)token * s.out_stride;
         }
-        out += (size_t)j0 * sizeof(T);
+        out += j0 * sizeof(T);
 
-        if (!BACK && kind == 2) {  // values: copied
+        float2 ca[P], cb[P], w[P];
+        const bool norm = s.weight != nullptr;
+        if (kind != 2) {
+            load_rotation<P>(a, token, j0, BACK ? -1.f : 1.f, ca, cb);
+            if (norm) {
+                load_pairs<P>(s.weight + j0, w);
+                if (!BACK) {  // forward: the weights go into the coefficients
+                    float2 wp[P];
+                    load_pairs<P>(s.weight + jp, wp);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (row0 + u * R < s.heads)
-                    *reinterpret_cast<uint4 *>(out + (size_t)(row0 + u * R) * head_bytes) = xv[u];
-            continue;
-        }
-
-        float cs[E], sn[E], w[E];
-        load_rotation<E>(a, token, j0, BACK ? -1.f : 1.f, cs, sn);
-        if (s.weight) {
-#pragma unroll
-            for (int e = 0; e < E; e += 4) {
-                const float4 t = __ldg(reinterpret_cast<const float4 *>(s.weight + j0 + e));
-                w[e] = t.x, w[e + 1] = t.y, w[e + 2] = t.z, w[e + 3] = t.w;
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float x[E];
-            unpack(xv[u], x);
-            float r = 0.f;
-            if (s.weight) {
-                float ss = 0.f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) ss = fmaf(x[e], x[e], ss);
-                ss = row_sum<L>(ss);
-                // a row past the last head stays zero also where eps is 0
-                r = row0 + u * R < s.heads ? rsqrtf(ss * (1.f / D) + a.eps) : 0.f;
-            }
-            if (BACK) {
-                float g[E];
-                unpack(gv[u], g);
-                rotate<E>(g, cs, sn, a.interleaved, src);
-                if (s.weight) {
-                    float dot = 0.f;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        x[e] *= r;
-                        const float p = g[e] * x[e];
-                        if (kind == 0) dw[0][e] += p; else dw[1][e] += p;
-                        g[e] *= w[e];
-                        dot = fmaf(w[e], p, dot);
+                    for (int i = 0; i < P; ++i) {
+                        ca[i] = ptx::f2_mul(ca[i], w[i]);
+                        cb[i] = ptx::f2_mul(cb[i], a.interleaved ? swapped(wp[i]) : wp[i]);
                     }
-                    dot = row_sum<L>(dot) * (1.f / D);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) g[e] = r * fmaf(-x[e], dot, g[e]);
                 }
-                if (row0 + u * R < s.heads)
-                    *reinterpret_cast<uint4 *>(out + (size_t)(row0 + u * R) * head_bytes) = pack(g);
+            }
+        }
+        for (;; row += kRows) {
+            uint4 nx[U], ng[BACK ? U : 1];
+            const bool more = row - sub + kRows < end;  // the same in the whole warp
+            if (more) load(row + kRows, nx, ng);
+            if (!BACK && kind == 2) {  // values: copied
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (row + u * R < end)
+                        *reinterpret_cast<uint4 *>(out + (row + u * R) * head_bytes) = xv[u];
             } else {
-                if (s.weight) {
 #pragma unroll
-                    for (int e = 0; e < E; ++e) x[e] *= r * w[e];
-                }
-                rotate<E>(x, cs, sn, a.interleaved, src);
-                if (row0 + u * R < s.heads) {
-                    if (s.out_f32) {  // unrounded rows (the queries of a fused step)
-                        float *o = reinterpret_cast<float *>(s.out) +
-                                   ((size_t)token * s.heads + row0 + u * R) * D + j0;
+                for (int u = 0; u < U; ++u) {
+                    const bool in = row + u * R < end;
+                    float2 x[P], y[P];
+                    V::unpack(xv[u], x);
+                    float r = 1.f;
+                    if (norm) {
+                        float2 ss = twice(0.f);
 #pragma unroll
-                        for (int e = 0; e < E; e += 4)
-                            *reinterpret_cast<float4 *>(o + e) =
-                                make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                        for (int i = 0; i < P; ++i) ss = ptx::f2_fma(x[i], x[i], ss);
+                        // a row past the last head stays zero also where eps is 0
+                        r = row_sum<L>(ss.x + ss.y) * (1.f / D) + a.eps;
+                        r = in ? rsqrtf(r) : 0.f;
+                    }
+                    if (BACK) {
+                        float2 g[P];
+                        V::unpack(gv[u], g);
+                        partner<T>(gv[u], g, a.interleaved, rotated, src, y);
+                        float2 dot = twice(0.f);
+                        const float2 rr = twice(r);
+#pragma unroll
+                        for (int i = 0; i < P; ++i) {
+                            g[i] = ptx::f2_fma(g[i], ca[i], ptx::f2_mul(y[i], cb[i]));
+                            if (norm) {
+                                x[i] = ptx::f2_mul(x[i], rr);
+                                const float2 p = ptx::f2_mul(g[i], x[i]);
+                                if (kind == 0) dw[0][i] = ptx::f2_add(dw[0][i], p);
+                                else dw[1][i] = ptx::f2_add(dw[1][i], p);
+                                dot = ptx::f2_fma(w[i], p, dot);
+                                g[i] = ptx::f2_mul(g[i], w[i]);
+                            }
+                        }
+                        if (norm) {
+                            const float2 m = twice(row_sum<L>(dot.x + dot.y) * (-1.f / D));
+#pragma unroll
+                            for (int i = 0; i < P; ++i)
+                                g[i] = ptx::f2_mul(rr, ptx::f2_fma(x[i], m, g[i]));
+                        }
+                        if (in)
+                            *reinterpret_cast<uint4 *>(out + (row + u * R) * head_bytes) = V::pack(g);
                     } else {
-                        *reinterpret_cast<uint4 *>(out + (size_t)(row0 + u * R) * head_bytes) = pack(x);
+                        partner<T>(xv[u], x, a.interleaved, rotated, src, y);
+                        const float2 rr = twice(r);
+#pragma unroll
+                        for (int i = 0; i < P; ++i) {
+                            y[i] = ptx::f2_fma(x[i], ca[i], ptx::f2_mul(y[i], cb[i]));
+                            if (norm) y[i] = ptx::f2_mul(y[i], rr);
+                        }
+                        if (in && s.out_f32) {  // unrounded rows (the queries of a fused step)
+                            float *o = static_cast<float *>(s.out) +
+                                       ((size_t)token * s.heads + row + u * R) * D + j0;
+#pragma unroll
+                            for (int i = 0; i < P; i += 2)
+                                *reinterpret_cast<float4 *>(o + 2 * i) =
+                                    make_float4(y[i].x, y[i].y, y[i + 1].x, y[i + 1].y);
+                        } else if (in) {
+                            *reinterpret_cast<uint4 *>(out + (row + u * R) * head_bytes) = V::pack(y);
+                        }
                     }
                 }
+            }
+            if (!more) break;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                xv[u] = nx[u];
+                if (BACK) gv[u] = ng[u];
             }
         }
     }
@@ -266,11 +309,11 @@ qk_norm_rope_kernel(const NormRopeArgs a) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                float t = dw[k][e];
+            for (int i = 0; i < 2 * P; ++i) {
+                float t = i & 1 ? dw[k][i / 2].y : dw[k][i / 2].x;
 #pragma unroll
                 for (int o = 16; o >= L; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-                if (sub == 0) red[warp][k][j0 + e] = t;
+                if (sub == 0) red[warp][k][j0 + i] = t;
             }
         __syncthreads();
         for (int i = threadIdx.x; i < 2 * D; i += 32 * kWarps) {
@@ -305,17 +348,17 @@ norm_weight_sum_kernel(const float *__restrict__ partial, int blocks, int D, flo
 }
 
 template <typename T, int D, int U, bool BACK>
-cudaError_t launch_u(const NormRopeArgs &a) {
-    constexpr int kRows = 32 / (D / (16 / (int)sizeof(T))) * U;
+cudaError_t launch_u(const NormRopeArgs &a, int batches) {
+    constexpr int kRows = 32 / (D / (2 * Vec<T>::P)) * U;
     long per = 0;
-    for (const NormRopeRows &s : a.set) per += (s.heads + kRows - 1) / kRows;
+    for (const NormRopeRows &s : a.set) per += (s.heads + kRows * batches - 1) / (kRows * batches);
     long grid = (a.num_tokens * per + kWarps - 1) / kWarps;
     // the backward pass keeps its weight sums in registers over a fixed
     // number of blocks, one partial result each
     const long most = BACK ? kNormBackwardBlocks : 0x7fffffffL;
     if (grid > most) grid = most;
     cudaError_t e = launch_dependent(qk_norm_rope_kernel<T, D, U, BACK>, (unsigned)grid,
-                                     32 * kWarps, 0, a.stream, a);
+                                     32 * kWarps, 0, a.stream, a, batches);
     if (e == cudaSuccess && BACK && a.set[0].weight)
         e = launch_dependent(norm_weight_sum_kernel, (a.dk_weight ? 2 : 1) * D / 32, 1024, 0, a.stream,
                              static_cast<const float *>(a.partial), (int)grid, D, a.dq_weight,
@@ -325,12 +368,13 @@ cudaError_t launch_u(const NormRopeArgs &a) {
 
 template <typename T, int D, bool BACK>
 cudaError_t launch(const NormRopeArgs &a) {
-    // One pass a warp spreads a few rows over many SMs; four amortise the
-    // token's cosines and sines over its rows.
-    constexpr int kRows = 32 / (D / (16 / (int)sizeof(T)));
+    // Few rows: one pass a warp spreads them over many SMs.  Many: the token's
+    // cosines, sines and weights are loaded once for up to kBatches * U passes.
+    constexpr int kRows = 32 / (D / (2 * Vec<T>::P));
+    constexpr int U = BACK ? 2 : 4, kBatches = 4;
     const long rows = (long)a.num_tokens * (a.set[0].heads + a.set[1].heads + a.set[2].heads);
-    if (rows <= 152L * 16 * kRows) return launch_u<T, D, 1, BACK>(a);
-    return launch_u<T, D, 4, BACK>(a);
+    if (rows <= 152L * 16 * kRows) return launch_u<T, D, 1, BACK>(a, 1);
+    return launch_u<T, D, U, BACK>(a, rows <= 152L * 16 * kRows * U * kBatches ? 1 : kBatches);
 }
 
 template <typename T>

@@ -12,8 +12,8 @@ beside :func:`decode` of the lightning layers; a prompt enters the cache through
 :func:`prefill` and follow :func:`backward` in training.
 
 As in the rest of the package, nothing is computed here and there is no
-fallback: arguments are checked, turned into pointers, sizes and strides, and
-the library's kernels are launched on ``stream`` (default: the current stream
+fallback: a native binding (``csrc/binding.cpp``) checks the arguments and
+launches the library's kernels on ``stream`` (default: the current stream
 of the tensors' device, whichever device is current).  Scratch memory and
 outputs that a call allocates come from that stream's pool, so they are safe
 on any stream and inside a CUDA graph.
@@ -21,11 +21,11 @@ on any stream and inside a CUDA graph.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
+import os
 
 import torch
-
-_CODES = {torch.bfloat16: 0, torch.float32: 1}
-_INT32 = torch.int32
 
 
 def declare(lib) -> None:
@@ -51,116 +51,28 @@ def declare(lib) -> None:
         fn.argtypes, fn.restype = args, ctypes.c_int64
 
 
-class _Call:
-    """Device and stream of one call: every tensor is on the device of the
-    first; the call runs with that device current."""
+BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build",
+                            "_lightning_binding.so")
+_binding = None
 
-    __slots__ = ("device", "stream", "handle", "given")
 
-    def __init__(self, first, name, stream):
-        if not isinstance(first, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if not first.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor (got {first.device})")
-        self.device, self.given = first.device, stream is not None
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        elif stream.device != self.device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {self.device}")
-        self.stream, self.handle = stream, stream.cuda_stream
-
-    def here(self, t, name):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.device != self.device:
-            raise ValueError(f"{name} must be on {self.device} (got {t.device})")
-
-    def empty(self, shape, dtype):
-        if self.given:  # from the pool of the stream that will write it
-            with torch.cuda.stream(self.stream):
-                return torch.empty(shape, dtype=dtype, device=self.device)
-        return torch.empty(shape, dtype=dtype, device=self.device)
-
-    def workspace(self, workspace, need):
-        """(pointer, bytes) of the scratch memory, and its tensor."""
-        if workspace is None:
-            workspace = self.empty(need, torch.uint8)
-        else:
-            self.here(workspace, "workspace")
-            if not workspace.is_contiguous():
-                raise ValueError("workspace must be contiguous")
-        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-
-    def rows(self, t, name, tokens, heads, d, dtype):
-        """(pointer, row stride) of a [tokens, heads, d] array whose tokens are
-        contiguous blocks."""
-        self.here(t, name)
-        if t.dtype != dtype or tuple(t.shape) != (tokens, heads, d):
-            raise ValueError(f"{name} must be {dtype} of shape {(tokens, heads, d)}, got {t.dtype} "
-                             f"{tuple(t.shape)}")
-        s0, s1, s2 = t.stride()
-        if s2 != 1 or (heads > 1 and s1 != d):
-            raise ValueError(f"{name}: the heads of a token must be contiguous")
-        return t.data_ptr(), s0 if tokens > 1 else heads * d
-
-    def ints(self, t, name, n):
-        self.here(t, name)
-        if t.dtype != _INT32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor of {n} elements")
-        return t.data_ptr()
-
-    def weight(self, t, name, d):
-        if t is None:
-            return None
-        self.here(t, name)
-        if t.dtype != torch.float32 or tuple(t.shape) != (d,) or not t.is_contiguous():
-            raise ValueError(f"{name} must be fp32 [{d}]")
-        return t.data_ptr()
-
-    def rotary(self, positions, table, tokens):
-        """positions, table pointer, rows and rotary_dim."""
-        if table is None:
-            if positions is not None:
-                raise ValueError("positions without a rotary table")
-            return None, None, 0, 0
-        self.here(table, "table")
-        if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous():
-            raise ValueError("table must be a contiguous fp32 [positions, rotary_dim] tensor")
-        return (self.ints(positions, "positions", tokens), table.data_ptr(), table.shape[0],
-                table.shape[1])
-
-    def cache(self, t, name, hk, d, dtype):
-        """(pointer, page stride) of one half of the cache."""
-        self.here(t, name)
-        pages, h, page, dim = t.shape if t.dim() == 4 else (0, 0, 0, 0)
-        if t.dtype != dtype or t.dim() != 4 or h != hk or dim != d:
-            raise ValueError(f"{name} must be {dtype} [pages, {hk}, page_size, {d}], got {t.dtype} "
-                             f"{tuple(t.shape)}")
-        s0, s1, s2, s3 = t.stride()
-        if s3 != 1 or (page > 1 and s2 != d) or (h > 1 and s1 != page * d):
-            raise ValueError(f"{name}: a page must be contiguous")
-        return t.data_ptr(), s0 if pages > 1 else h * page * d
-
-    def table(self, t, batch):
-        """(pointer, row stride, width) of the block table."""
-        self.here(t, "block_table")
-        if t.dtype != _INT32 or t.dim() != 2 or t.shape[0] != batch:
-            raise ValueError(f"block_table must be int32 [{batch}, blocks]")
-        s0, s1 = t.stride()
-        if t.shape[1] > 1 and s1 != 1:
-            raise ValueError("a row of block_table must be contiguous")
-        return t.data_ptr(), s0 if batch > 1 else max(t.shape[1], 1), t.shape[1]
-
-    def run(self, name, *args):
-        from . import _check, load
-        fn = getattr(load(), name)
-        if self.device.index == torch.cuda.current_device():
-            status = fn(*args, self.handle)
-        else:
-            with torch.cuda.device(self.device):
-                status = fn(*args, self.handle)
-        if status:
-            _check(status, name)
+def _calls():
+    """The native binding (``csrc/binding.cpp``), which checks a call's tensors
+    and makes the library call; raises if it has not been built."""
+    global _binding
+    if _binding is None:
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"binding not found at {BINDING_PATH}; build it with "
+                               "`python -m lightning_attention_attn_gb300.build`")
+        from . import load
+        load()
+        name = "_lightning_binding"
+        spec = importlib.util.spec_from_file_location(
+            name, BINDING_PATH, loader=importlib.machinery.ExtensionFileLoader(name, BINDING_PATH))
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _binding = module
+    return _binding
 
 
 def _bytes(name, *args) -> int:
@@ -169,23 +81,6 @@ def _bytes(name, *args) -> int:
     if n < 0:
         raise ValueError("invalid sizes for the workspace")
     return n
-
-
-def _dtype(t) -> int:
-    code = _CODES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {t.dtype} (bf16 or fp32)")
-    return code
-
-
-def _shape(q, k):
-    """(tokens, heads, kv heads, head_dim) of q and k (k may be None)."""
-    if q.dim() != 3:
-        raise ValueError("q must be [T, H, d]")
-    if k is not None and (not isinstance(k, torch.Tensor) or k.dim() != 3):
-        raise ValueError("k must be [T, Hkv, d]")
-    t, h, d = q.shape
-    return t, h, 0 if k is None else k.shape[1], d
 
 
 def rotary_table(max_position: int, rotary_dim: int, *, base: float = 10000.0,
@@ -216,21 +111,8 @@ def qk_norm_rope(q, k, positions=None, table=None, *, q_weight=None, k_weight=No
     are rotated together, instead of i and i + rotary_dim / 2.  ``q_out=q,
     k_out=k`` works in place.
     """
-    call = _Call(q, "q", stream)
-    t, h, hk, d = _shape(q, k)
-    code = _dtype(q)
-    q_in = call.rows(q, "q", t, h, d, q.dtype)
-    k_in = (None, 0) if k is None else call.rows(k, "k", t, hk, d, q.dtype)
-    rot = call.rotary(positions, table, t)
-    w = call.weight(q_weight, "q_weight", d), call.weight(k_weight, "k_weight", d)
-    if q_out is None:
-        q_out = call.empty((t, h, d), q.dtype)
-    if k is not None and k_out is None:
-        k_out = call.empty((t, hk, d), q.dtype)
-    call.run("lightning_attn_qk_norm_rope", *q_in, *k_in, *rot, int(interleaved), *w, eps,
-             t, h, hk, d, code, *call.rows(q_out, "q_out", t, h, d, q.dtype),
-             *((None, 0) if k is None else call.rows(k_out, "k_out", t, hk, d, q.dtype)))
-    return q_out, (None if k is None else k_out)
+    return (_binding or _calls()).qk_norm_rope(q, k, positions, table, q_weight, k_weight, eps,
+                                               interleaved, q_out, k_out, stream)
 
 
 def qk_norm_rope_backward(q, k, positions, table, dq_out, dk_out, *, q_weight=None, k_weight=None,
@@ -241,51 +123,9 @@ def qk_norm_rope_backward(q, k, positions, table, dq_out, dk_out, *, q_weight=No
     (``dq=dq_out`` works in place; strided outputs, e.g. slices of a fused
     gradient, are taken too); the weights' gradients are fp32 [d], or None
     without weights, and the same bits on every call."""
-    call = _Call(q, "q", stream)
-    t, h, hk, d = _shape(q, k)
-    code = _dtype(q)
-    q_in = call.rows(q, "q", t, h, d, q.dtype)
-    dq_in = call.rows(dq_out, "dq_out", t, h, d, q.dtype)
-    k_in = dk_in = (None, 0)
-    if k is not None:
-        k_in = call.rows(k, "k", t, hk, d, q.dtype)
-        dk_in = call.rows(dk_out, "dk_out", t, hk, d, q.dtype)
-    rot = call.rotary(positions, table, t)
-    w = call.weight(q_weight, "q_weight", d), call.weight(k_weight, "k_weight", d)
-    if dq is None:
-        dq = call.empty((t, h, d), q.dtype)
-    if k is not None and dk is None:
-        dk = call.empty((t, hk, d), q.dtype)
-    dqw = dkw = None
-    ws = (None, 0)
-    if q_weight is not None:
-        dqw = call.empty((d,), torch.float32)
-        dkw = None if k is None else call.empty((d,), torch.float32)
-        *ws, workspace = call.workspace(
-            workspace, _bytes("lightning_attn_qk_norm_rope_workspace_bytes", d))
-    call.run("lightning_attn_qk_norm_rope_backward", *q_in, *k_in, *rot, int(interleaved), *w, eps,
-             t, h, hk, d, code, *dq_in, *dk_in, *call.rows(dq, "dq", t, h, d, q.dtype),
-             *((None, 0) if k is None else call.rows(dk, "dk", t, hk, d, q.dtype)),
-             None if dqw is None else dqw.data_ptr(), None if dkw is None else dkw.data_ptr(), *ws)
-    return dq, (None if k is None else dk), dqw, dkw
-
-
-def _qkv(call, q, k, v):
-    t, h, hk, d = _shape(q, k)
-    if k is None:
-        raise ValueError("k must be [T, Hkv, d]")
-    return (t, h, hk, d), (*call.rows(q, "q", t, h, d, q.dtype),
-                           *call.rows(k, "k", t, hk, d, q.dtype),
-                           *call.rows(v, "v", t, hk, d, q.dtype))
-
-
-def _caches(call, k_cache, v_cache, hk, d, dtype):
-    """Pointers and strides of both halves; pages and page size."""
-    both = (*call.cache(k_cache, "k_cache", hk, d, dtype),
-            *call.cache(v_cache, "v_cache", hk, d, dtype))
-    if k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache must have one shape")
-    return both, k_cache.shape[0], k_cache.shape[2]
+    return (_binding or _calls()).qk_norm_rope_backward(
+        q, k, positions, table, dq_out, dk_out, q_weight, k_weight, eps, interleaved, dq, dk,
+        workspace, stream)
 
 
 def paged_append(q, k, v, positions, table, k_cache, v_cache, slots, *, q_weight=None,
@@ -299,32 +139,8 @@ def paged_append(q, k, v, positions, table, k_cache, v_cache, slots, *, q_weight
     into row slots[t] % page_size of page slots[t] // page_size.  A slot outside the
     pool (-1: padding) is skipped; the others are distinct.
     """
-    call = _Call(q, "q", stream)
-    code = _dtype(q)
-    (t, h, hk, d), qkv = _qkv(call, q, k, v)
-    rot = call.rotary(positions, table, t)
-    caches, pages, page = _caches(call, k_cache, v_cache, hk, d, q.dtype)
-    at = call.ints(slots, "slots", t)
-    w = call.weight(q_weight, "q_weight", d), call.weight(k_weight, "k_weight", d)
-    if q_out is None:
-        q_out = call.empty((t, h, d), q.dtype)
-    call.run("lightning_attn_paged_append", *qkv, *rot, int(interleaved), *w, eps, t, h, hk, d,
-             code, *call.rows(q_out, "q_out", t, h, d, q.dtype), *caches, at, pages, page)
-    return q_out
-
-
-def _attention_outputs(call, out, lse, b, h, d, dtype):
-    if out is None:
-        out = call.empty((b, h, d), dtype)
-    else:
-        call.here(out, "out")
-        if out.dtype != dtype or tuple(out.shape) != (b, h, d) or not out.is_contiguous():
-            raise ValueError(f"out must be a contiguous {dtype} [{b}, {h}, {d}]")
-    if lse is not None:
-        call.here(lse, "lse")
-        if lse.dtype != torch.float32 or tuple(lse.shape) != (b, h) or not lse.is_contiguous():
-            raise ValueError(f"lse must be a contiguous fp32 [{b}, {h}]")
-    return out, None if lse is None else lse.data_ptr()
+    return (_binding or _calls()).paged_append(q, k, v, positions, table, k_cache, v_cache, slots,
+                                               q_weight, k_weight, eps, interleaved, q_out, stream)
 
 
 def paged_decode_workspace_bytes(head_dim: int) -> int:
@@ -349,23 +165,8 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, *, scale: float | N
     of the softmax sums; workspace: optional uint8 tensor of
     :func:`paged_decode_workspace_bytes` (a stream's calls may share one).
     """
-    call = _Call(q, "q", stream)
-    code = _dtype(q)
-    if q.dim() != 3:
-        raise ValueError("q must be [B, H, d]")
-    b, h, d = q.shape
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache must be [pages, Hkv, page_size, d]")
-    hk = k_cache.shape[1]
-    q_in = call.rows(q, "q", b, h, d, q.dtype)
-    caches, pages, page = _caches(call, k_cache, v_cache, hk, d, q.dtype)
-    bt = call.table(block_table, b)
-    lens = call.ints(seq_lens, "seq_lens", b)
-    out, lse_ptr = _attention_outputs(call, out, lse, b, h, d, q.dtype)
-    *ws, workspace = call.workspace(workspace, paged_decode_workspace_bytes(d))
-    call.run("lightning_attn_paged_decode", *q_in, *caches, *bt, lens, pages, page, b, h, hk, d,
-             code, d ** -0.5 if scale is None else scale, out.data_ptr(), lse_ptr, *ws)
-    return out
+    return (_binding or _calls()).paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, out,
+                                               lse, workspace, stream)
 
 
 def paged_step(q, k, v, positions, table, k_cache, v_cache, slots, block_table, seq_lens, *,
@@ -375,21 +176,9 @@ def paged_step(q, k, v, positions, table, k_cache, v_cache, slots, block_table, 
     new token, then :func:`paged_decode` over the cache that now holds it (the
     queries stay fp32 in between, so out is rounded once).  q: [B, H, d], k, v:
     [B, Hkv, d]; ``seq_lens`` counts the new tokens.  Returns out [B, H, d]."""
-    call = _Call(q, "q", stream)
-    code = _dtype(q)
-    (b, h, hk, d), qkv = _qkv(call, q, k, v)
-    rot = call.rotary(positions, table, b)
-    caches, pages, page = _caches(call, k_cache, v_cache, hk, d, q.dtype)
-    at = call.ints(slots, "slots", b)
-    bt = call.table(block_table, b)
-    lens = call.ints(seq_lens, "seq_lens", b)
-    w = call.weight(q_weight, "q_weight", d), call.weight(k_weight, "k_weight", d)
-    out, lse_ptr = _attention_outputs(call, out, lse, b, h, d, q.dtype)
-    *ws, workspace = call.workspace(workspace, paged_step_workspace_bytes(b, h, d))
-    call.run("lightning_attn_paged_step", *qkv, *rot, int(interleaved), *w, eps, *caches, at, *bt,
-             lens, pages, page, b, h, hk, d, code, d ** -0.5 if scale is None else scale,
-             out.data_ptr(), lse_ptr, *ws)
-    return out
+    return (_binding or _calls()).paged_step(
+        q, k, v, positions, table, k_cache, v_cache, slots, block_table, seq_lens, q_weight,
+        k_weight, eps, interleaved, scale, out, lse, workspace, stream)
 
 
 def paged_reserve(block_table, seq_lens, new_lens, free_pages, free_count, page_size: int,
@@ -407,33 +196,6 @@ def paged_reserve(block_table, seq_lens, new_lens, free_pages, free_count, page_
     and 0); cu_seqlens: int32 [B + 1]; served: bool [B].  The new lengths and the
     stack's height go to seq_lens_out and free_count_out: by default in place.
     """
-    call = _Call(block_table, "block_table", stream)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be int32 [B, blocks]")
-    b = block_table.shape[0]
-    if free_pages.dim() != 1:
-        raise ValueError("free_pages must be an int32 [pages] tensor")
-    pages = free_pages.shape[0]
-    bt = call.table(block_table, b)
-    lens, new = call.ints(seq_lens, "seq_lens", b), call.ints(new_lens, "new_lens", b)
-    stack = call.ints(free_pages, "free_pages", pages)
-    count = call.ints(free_count, "free_count", 1)
-    done = None
-    if finished is not None:
-        call.here(finished, "finished")
-        if finished.dtype not in (torch.bool, torch.uint8) or tuple(finished.shape) != (b,) or \
-                not finished.is_contiguous():
-            raise ValueError(f"finished must be a contiguous bool tensor of {b} elements")
-        done = finished.data_ptr()
-    lens_to = lens if seq_lens_out is None else call.ints(seq_lens_out, "seq_lens_out", b)
-    count_to = count if free_count_out is None else call.ints(free_count_out, "free_count_out", 1)
-    # one allocation for the three int32 outputs, each on a 16-byte boundary
-    # (cu_seqlens goes on to prefill(), which asks for one)
-    n = (num_tokens + 3) // 4 * 4
-    ints = call.empty((2 * n + b + 1,), _INT32)
-    served = call.empty((b,), torch.bool)
-    base = ints.data_ptr()
-    call.run("lightning_attn_paged_reserve", *bt, lens, new, done, b, stack, count, pages,
-             page_size, num_tokens, base, base + 4 * n, base + 8 * n, served.data_ptr(), lens_to,
-             count_to)
-    return ints[:num_tokens], ints[n:n + num_tokens], ints[2 * n:], served
+    return (_binding or _calls()).paged_reserve(
+        block_table, seq_lens, new_lens, free_pages, free_count, page_size, num_tokens, finished,
+        seq_lens_out, free_count_out, stream)
