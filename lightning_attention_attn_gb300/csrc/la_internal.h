@@ -158,7 +158,7 @@ struct NormRopeArgs {
 };
 
 // Blocks of the backward pass, each leaving one partial weight gradient.
-constexpr int kNormBackwardBlocks = 152 * 8;
+constexpr int kNormBackwardBlocks = 152 * 5;
 
 cudaError_t qk_norm_rope(const NormRopeArgs &a, bool bf16);
 cudaError_t qk_norm_rope_backward(const NormRopeArgs &a, bool bf16);

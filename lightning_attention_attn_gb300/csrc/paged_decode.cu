@@ -61,16 +61,20 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
     return r;
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));  // 2 ulp; 0 below 2^-126
+    return y;
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
@@ -209,6 +213,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     constexpr int CH = D / 8;    // 16-byte chunks of a row
     constexpr int RPI = 32 / CH; // rows one warp-wide copy covers
     constexpr int kRows = 8 * NT;
+    constexpr int kAhead = NT == 1 ? 4 : 2;  // fragments loaded ahead (registers)
 
     extern __shared__ __align__(128) unsigned char smem[];
 
@@ -359,19 +364,45 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
             __syncwarp();
             const uint32_t kb = ring + stage * C::kStageBytes, vb = kb + C::kMat;
 
-            float s[NT][4];
+            // Few warps share an SM, so a warp's own latencies count: the
+            // fragments are loaded ahead of their products, and the scores are summed in
+            // two (with split queries four) independent chains.
+            float s[NT][4], s2[NT][4], s3[QF32 ? NT : 1][4], s4[QF32 ? NT : 1][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                uint32_t ka[4];
-                ldsm4(ka, kb + krow * C::kRow + (((2 * ks + kchunk) ^ (krow & 7)) << 4));
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma16816(s[nt], ka, qb[nt][ks][0], qb[nt][ks][1]);
-                    if (QF32) mma16816(s[nt], ka, ql[nt][ks][0], ql[nt][ks][1]);
+                for (int i = 0; i < 4; ++i) {
+                    s[nt][i] = s2[nt][i] = 0.f;
+                    if (QF32) s3[nt][i] = s4[nt][i] = 0.f;
                 }
+#pragma unroll
+            for (int k0 = 0; k0 < KS; k0 += kAhead) {
+                uint32_t ka[kAhead][4];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+                    ldsm4(ka[i], kb + krow * C::kRow +
+                                     (((2 * (k0 + i) + kchunk) ^ (krow & 7)) << 4));
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const int ks = k0 + i;
+                        mma16816(i & 1 ? s2[nt] : s[nt], ka[i], qb[nt][ks][0], qb[nt][ks][1]);
+                        if (QF32)
+                            mma16816(i & 1 ? s4[nt] : s3[nt], ka[i], ql[nt][ks][0], ql[nt][ks][1]);
+                    }
             }
+            uint32_t va[kAhead][4];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                ldsm4_t(va[i], vb + vrow * C::kRow + (((2 * i + vchunk) ^ (vrow & 7)) << 4));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[nt][i] += s2[nt][i];
+                    if (QF32) s[nt][i] += s3[nt][i] + s4[nt][i];
+                }
             const bool v0 = (have[0] >> g) & 1, v1 = (have[0] >> (g + 8)) & 1;
             uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
@@ -390,8 +421,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
                 // a maximum that rose rescales what was summed
                 if (__any_sync(0xffffffffu, t0m > mx[nt][0] || t1m > mx[nt][1])) {
                     const float n0 = fmaxf(mx[nt][0], t0m), n1 = fmaxf(mx[nt][1], t1m);
-                    const float f0 = n0 == -CUDART_INF_F ? 1.f : exp2f(mx[nt][0] - n0);
-                    const float f1 = n1 == -CUDART_INF_F ? 1.f : exp2f(mx[nt][1] - n1);
+                    const float f0 = n0 == -CUDART_INF_F ? 1.f : ex2(mx[nt][0] - n0);
+                    const float f1 = n1 == -CUDART_INF_F ? 1.f : ex2(mx[nt][1] - n1);
                     mx[nt][0] = n0;
                     mx[nt][1] = n1;
                     l[nt][0] *= f0;
@@ -406,8 +437,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
                 }
                 const float b0 = mx[nt][0] == -CUDART_INF_F ? 0.f : mx[nt][0];
                 const float b1 = mx[nt][1] == -CUDART_INF_F ? 0.f : mx[nt][1];
-                const float p0 = exp2f(s[nt][0] - b0), p1 = exp2f(s[nt][1] - b1);
-                const float p2 = exp2f(s[nt][2] - b0), p3 = exp2f(s[nt][3] - b1);
+                const float p0 = ex2(s[nt][0] - b0), p1 = ex2(s[nt][1] - b1);
+                const float p2 = ex2(s[nt][2] - b0), p3 = ex2(s[nt][3] - b1);
                 l[nt][0] += p0 + p2;
                 l[nt][1] += p1 + p3;
                 const uint32_t h0 = pack2(p0, p1), h1 = pack2(p2, p3);
@@ -417,14 +448,21 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
                 pl[nt][1] = transpose8x8(pack2(p2 - lo_of(h1), p3 - hi_of(h1)));
             }
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                uint32_t va[4];
-                ldsm4_t(va, vb + vrow * C::kRow + (((2 * ks + vchunk) ^ (vrow & 7)) << 4));
+            for (int k0 = 0; k0 < KS; k0 += kAhead) {
+                if (k0 > 0) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma16816(o[nt][ks], va, ph[nt][0], ph[nt][1]);
-                    mma16816(o[nt][ks], va, pl[nt][0], pl[nt][1]);
+                    for (int i = 0; i < kAhead; ++i)
+                        ldsm4_t(va[i], vb + vrow * C::kRow +
+                                           (((2 * (k0 + i) + vchunk) ^ (vrow & 7)) << 4));
                 }
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][k0 + i], va[i], ph[nt][0], ph[nt][1]);
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][k0 + i], va[i], pl[nt][0], pl[nt][1]);
             }
 #pragma unroll
             for (int i = 0; i < kStages - 1; ++i) have[i] = have[i + 1];
@@ -473,7 +511,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float f = exp2f(ml[(w * kRows + h) * 2] - mb);
+                const float f = ex2(ml[(w * kRows + h) * 2] - mb);
                 const float4 x = *reinterpret_cast<const float4 *>(ow + (w * kRows + h) * D + d);
                 sum += f * ml[(w * kRows + h) * 2 + 1];
                 acc.x += f * x.x;
@@ -504,18 +542,34 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
 
 // -------------------------------------------------------------- fp32 kernel
 // The same split and rings on the CUDA cores (fp32 products, as the library's
-// other fp32 paths): a lane takes one token's half row for the scores, then
-// D / 32 columns of the values; queries and probabilities are broadcast from
-// shared memory.
-template <int D, int NT>
+// other fp32 paths).  ROWS (4, 8 or 16) query heads of a unit.
+//   scores   LPT lanes share a token; each keeps DPL dimensions of all queries in
+//            registers, and a transposing reduction over the LPT lanes leaves one
+//            head's score in each
+//   softmax  over the group's scores in shared memory, lane = (head, token), so
+//            every exponential is taken once
+//   values   a lane owns four columns of all heads (of every other token where 16
+//            lanes cover a row)
+// A group is 16 tokens of 64 dimensions or 8 of 128: 8 KB a stage, as in bf16.
+template <int D, int ROWS>
+struct F32Core {
+    static constexpr int kGrp = 1024 / D;             // tokens of a group
+    static constexpr int kDpl = ROWS == 16 ? 4 : 8;   // dimensions of a lane's scores
+    static constexpr int kLpt = D / kDpl;             // lanes of a token
+    static constexpr int kMat = kGrp * D;             // floats of K (V) of a stage
+    static constexpr int kScores = kWarps * kGrp * ROWS;
+    static constexpr size_t kSmem = sizeof(float) * (kScores + kWarps * kStages * 2 * kMat);
+};
+
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kThreads)
 paged_decode_f32_kernel(const __grid_constant__ PagedDecodeArgs a) {
-    constexpr int kRows = 8 * NT;
-    constexpr int CH = D / 4;     // 16-byte chunks of a row
-    constexpr int CPL = CH / 16;  // chunks a copying lane takes of each row pair
-    constexpr int VEC = D / 32;   // value columns of a lane
-    constexpr int kMat = kGroup * D;  // floats
-    constexpr int kSt = D == 128 ? 2 : 3;
+    using C = F32Core<D, ROWS>;
+    constexpr int kGrp = C::kGrp, DPL = C::kDpl, LPT = C::kLpt, kMat = C::kMat;
+    constexpr int TPP = 32 / LPT;    // tokens whose scores a pass computes
+    constexpr int TS = 32 / ROWS;    // tokens of a softmax step
+    constexpr int CH = D / 4;        // 16-byte chunks of a row
+    constexpr int RPI = 32 / CH;     // rows of a warp-wide copy, tokens of a value step
 
     extern __shared__ __align__(128) unsigned char smem[];
 
@@ -531,10 +585,22 @@ paged_decode_f32_kernel(const __grid_constant__ PagedDecodeArgs a) {
     const long long w1 = min(at.all, w0 + at.chunk);
     int b = at.b;
 
-    float *qs = reinterpret_cast<float *>(smem);                  // [kRows][D]
-    float *pw = qs + kRows * D + warp * kGroup * kRows;           // [16][kRows] of this warp
-    float *ring = qs + kRows * D + kWarps * kGroup * kRows + warp * kSt * 2 * kMat;
+    float *base = reinterpret_cast<float *>(smem);
+    float *pw = base + warp * kGrp * ROWS;  // [kGrp][ROWS] of this warp
+    float *ring = base + C::kScores + warp * kStages * 2 * kMat;
     const uint32_t ring_u = ptx::smem_u32(ring);
+    const int sub = lane % LPT, sh = lane % ROWS;
+    // the head whose score the reduction leaves in this lane
+    int my_head = 0;
+    {
+        int n = ROWS;
+#pragma unroll
+        for (int o = LPT / 2; o > 0; o >>= 1)
+            if (n > 1) {
+                n >>= 1;
+                if (lane & o) my_head += n;
+            }
+    }
 
     bool first = true;
     long long unit0 = at.unit0;
@@ -551,194 +617,228 @@ paged_decode_f32_kernel(const __grid_constant__ PagedDecodeArgs a) {
         const int tile0 = (int)(w0 - unit0 - (long long)unit * tiles);
         const int tile1 = (int)min((long long)tiles, tile0 + (w1 - w0));
         const int kvh = unit / a.head_groups, hg = unit % a.head_groups;
-        const int head0 = kvh * a.group + hg * kRows;
-        const int heads = min(kRows, a.group - hg * kRows);
+        const int head0 = kvh * a.group + hg * ROWS;
+        const int heads = min(ROWS, a.group - hg * ROWS);
         const int t0 = tile0 * kTile, t1 = min(len, tile1 * kTile);
 
-        for (int i = threadIdx.x; i < kRows * D; i += kThreads) {
-            const int h = i / D;
-            qs[i] = h < heads ? static_cast<const float *>(a.q)[(size_t)b * a.q_stride +
-                                                                (size_t)(head0 + h) * D + i % D]
-                              : 0.f;
-        }
-        __syncthreads();
-
-        float o[kRows][VEC], mx[kRows], l[kRows];
-#pragma unroll
-        for (int h = 0; h < kRows; ++h) {
-            mx[h] = -CUDART_INF_F;
-            l[h] = 0.f;
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) o[h][c] = 0.f;
-        }
         const int32_t *pages = a.block_table + (size_t)b * a.table_stride;
-        const int groups = (t1 - t0 + kGroup - 1) / kGroup;
-        auto issue = [&](int stage, int grp) -> uint32_t {
-            const int t = t0 + grp * kGroup + (lane & 15);
-            int page = -1, row = 0;
+        const int groups = (t1 - t0 + kGrp - 1) / kGrp;
+        auto locate = [&](int grp, int &page, int &row) {
+            const int t = t0 + grp * kGrp + lane % kGrp;
+            page = -1;
+            row = 0;
             if (t < t1) {
                 const int blk = t / a.page_size;
                 row = t - blk * a.page_size;
                 page = __ldg(pages + blk);
                 if (page >= a.num_pages) page = -1;
             }
-            const uint32_t have = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
+        };
+        auto issue = [&](int stage, int page, int row) -> uint32_t {
+            const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
             const uint32_t dk = ring_u + stage * 2 * kMat * 4, dv = dk + kMat * 4;
+            const int ch = lane % CH;
 #pragma unroll
-            for (int i = 0; i < kGroup / 2; ++i) {
-                const int r = i * 2 + (lane >> 4);
+            for (int i = 0; i < kGrp / RPI; ++i) {
+                const int r = i * RPI + lane / CH;
                 const int pg = __shfl_sync(0xffffffffu, page, r);
                 const int rw = __shfl_sync(0xffffffffu, row, r);
                 const bool ok = pg >= 0;
                 const size_t p = ok ? pg : 0;
-#pragma unroll
-                for (int j = 0; j < CPL; ++j) {
-                    const int ch = (lane & 15) + 16 * j;
-                    const size_t in = ((size_t)kvh * a.page_size + rw) * D + ch * 4;
-                    const uint32_t off = r * D * 4 + ((ch ^ (r & 7)) << 4);
-                    cp_async16(dk + off, static_cast<const float *>(a.k) + p * a.k_page_stride + in, ok);
-                    cp_async16(dv + off, static_cast<const float *>(a.v) + p * a.v_page_stride + in, ok);
-                }
+                const size_t in = ((size_t)kvh * a.page_size + rw) * D + ch * 4;
+                const uint32_t off = r * D * 4 + ((ch ^ (r & 7)) << 4);
+                cp_async16(dk + off, static_cast<const float *>(a.k) + p * a.k_page_stride + in, ok);
+                cp_async16(dv + off, static_cast<const float *>(a.v) + p * a.v_page_stride + in, ok);
             }
             return have;
         };
-        uint32_t have[kSt];
+        uint32_t have[kStages];
 #pragma unroll
-        for (int s = 0; s < kSt - 1; ++s) {
-            const int grp = warp + s * kWarps;
-            have[s] = grp < groups ? issue(s, grp) : 0;
+        for (int s = 0; s < kStages - 1; ++s) {
+            int page, row;
+            locate(warp + s * kWarps, page, row);
+            have[s] = issue(s, page, row);
             cp_commit();
         }
+        int npage, nrow;  // of the group that is issued next
+        locate(warp + (kStages - 1) * kWarps, npage, nrow);
+
+        // chunk sub + i LPT of every query row
+        float2 q[ROWS][DPL / 2];
+#pragma unroll
+        for (int h = 0; h < ROWS; ++h)
+#pragma unroll
+            for (int i = 0; i < DPL / 4; ++i) {
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (h < heads)
+                    x = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) +
+                                                          (size_t)b * a.q_stride +
+                                                          (size_t)(head0 + h) * D +
+                                                          (sub + i * LPT) * 4);
+                q[h][2 * i] = make_float2(x.x, x.y);
+                q[h][2 * i + 1] = make_float2(x.z, x.w);
+            }
+        float2 o[ROWS][2];
+        float mx = -CUDART_INF_F, l = 0.f;  // of head sh (l: this lane's tokens)
+#pragma unroll
+        for (int h = 0; h < ROWS; ++h) o[h][0] = o[h][1] = make_float2(0.f, 0.f);
+
         int stage = 0;
         for (int grp = warp; grp < groups; grp += kWarps) {
-            const int nx = grp + (kSt - 1) * kWarps;
-            const int ns = stage == 0 ? kSt - 1 : stage - 1;
-            __syncwarp();
-            have[kSt - 1] = nx < groups ? issue(ns, nx) : 0;
-            cp_commit();
-            cp_wait<kSt - 1>();
+            {
+                const int ns = stage == 0 ? kStages - 1 : stage - 1;
+                __syncwarp();
+                have[kStages - 1] = issue(ns, npage, nrow);  // copies nothing past the end
+                cp_commit();
+                locate(grp + kStages * kWarps, npage, nrow);
+            }
+            cp_wait<kStages - 1>();
             __syncwarp();
             const float *kb = ring + stage * 2 * kMat, *vb = kb + kMat;
 
-            // scores: token lane & 15, half of the row each
-            const int r = lane & 15, hf = lane >> 4;
-            float s[kRows];
 #pragma unroll
-            for (int h = 0; h < kRows; ++h) s[h] = 0.f;
-#pragma unroll 4
-            for (int c = 0; c < CH / 2; ++c) {
-                const int ch = hf * (CH / 2) + c;
-                const float4 k4 = *reinterpret_cast<const float4 *>(kb + r * D + ((ch ^ (r & 7)) << 2));
+            for (int t = 0; t < kGrp; t += TPP) {
+                const int r = t + lane / LPT;
+                float2 acc[ROWS];
 #pragma unroll
-                for (int h = 0; h < kRows; ++h) {
-                    const float4 q4 = *reinterpret_cast<const float4 *>(qs + h * D + ch * 4);
-                    s[h] = fmaf(k4.x, q4.x, fmaf(k4.y, q4.y, fmaf(k4.z, q4.z, fmaf(k4.w, q4.w, s[h]))));
+                for (int i = 0; i < DPL / 4; ++i) {
+                    const float4 k4 = *reinterpret_cast<const float4 *>(
+                        kb + r * D + (((sub + i * LPT) ^ (r & 7)) << 2));
+#pragma unroll
+                    for (int h = 0; h < ROWS; ++h) {
+                        const float2 lo = make_float2(k4.x, k4.y), hi = make_float2(k4.z, k4.w);
+                        acc[h] = i == 0 ? ptx::f2_mul(lo, q[h][0]) : ptx::f2_fma(lo, q[h][2 * i], acc[h]);
+                        acc[h] = ptx::f2_fma(hi, q[h][2 * i + 1], acc[h]);
+                    }
                 }
-            }
-            const bool ok = (have[0] >> r) & 1;
-            bool rose = false;
-            float top[kRows];
+                float v[ROWS];
 #pragma unroll
-            for (int h = 0; h < kRows; ++h) {
-                s[h] += __shfl_xor_sync(0xffffffffu, s[h], 16);
-                s[h] = ok ? s[h] * a.scale_log2 : -CUDART_INF_F;
-                float t = s[h];
+                for (int h = 0; h < ROWS; ++h) v[h] = acc[h].x + acc[h].y;
+                int n = ROWS;
 #pragma unroll
-                for (int d = 1; d < 16; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
-                top[h] = t;
-                rose |= t > mx[h];
-            }
-            if (rose) {  // the same in every lane
+                for (int d = LPT / 2; d > 0; d >>= 1) {
+                    if (n > 1) {
+                        n >>= 1;
+                        const bool up = lane & d;
 #pragma unroll
-                for (int h = 0; h < kRows; ++h) {
-                    const float nm = fmaxf(mx[h], top[h]);
-                    const float f = nm == -CUDART_INF_F ? 1.f : exp2f(mx[h] - nm);
-                    mx[h] = nm;
-                    l[h] *= f;
-#pragma unroll
-                    for (int c = 0; c < VEC; ++c) o[h][c] *= f;
+                        for (int i = 0; i < ROWS / 2; ++i)
+                            if (i < n) {
+                                const float keep = up ? v[i + n] : v[i], give = up ? v[i] : v[i + n];
+                                v[i] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+                            }
+                    } else {
+                        v[0] += __shfl_xor_sync(0xffffffffu, v[0], d);
+                    }
                 }
-            }
-#pragma unroll
-            for (int h = 0; h < kRows; ++h) {
-                const float p = exp2f(s[h] - (mx[h] == -CUDART_INF_F ? 0.f : mx[h]));
-                l[h] += p;  // per token lane: summed over the lanes at the end
-                if (hf == 0) pw[r * kRows + h] = p;
+                pw[r * ROWS + my_head] = v[0];  // lanes of one head write the same sum
             }
             __syncwarp();
-#pragma unroll 4
-            for (int t = 0; t < kGroup; ++t) {
-                float v[VEC];
-                const int ch = lane * VEC / 4, in = lane * VEC % 4;
-                const float *vp = vb + t * D + ((ch ^ (t & 7)) << 2) + in;
-                if constexpr (VEC == 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(vp);
-                    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-                } else {
-                    const float2 x = *reinterpret_cast<const float2 *>(vp);
-                    v[0] = x.x, v[1] = x.y;
+            float p[kGrp / TS];
+            float top = -CUDART_INF_F;
+#pragma unroll
+            for (int i = 0; i < kGrp / TS; ++i) {
+                const int t = i * TS + lane / ROWS;
+                p[i] = (have[0] >> t) & 1 ? pw[t * ROWS + sh] * a.scale_log2 : -CUDART_INF_F;
+                top = fmaxf(top, p[i]);
+            }
+#pragma unroll
+            for (int d = ROWS; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            if (__any_sync(0xffffffffu, top > mx)) {
+                const float nm = fmaxf(mx, top);
+                const float f = nm == -CUDART_INF_F ? 1.f : ex2(mx - nm);
+                mx = nm;
+                l *= f;
+#pragma unroll
+                for (int h = 0; h < ROWS; ++h) {
+                    const float fh = __shfl_sync(0xffffffffu, f, h);
+                    o[h][0] = ptx::f2_mul(o[h][0], make_float2(fh, fh));
+                    o[h][1] = ptx::f2_mul(o[h][1], make_float2(fh, fh));
                 }
+            }
+            const float mb = mx == -CUDART_INF_F ? 0.f : mx;
 #pragma unroll
-                for (int h = 0; h < kRows; h += 4) {
-                    const float4 p4 = *reinterpret_cast<const float4 *>(pw + t * kRows + h);
+            for (int i = 0; i < kGrp / TS; ++i) {
+                p[i] = ex2(p[i] - mb);
+                l += p[i];
+                pw[(i * TS + lane / ROWS) * ROWS + sh] = p[i];
+            }
+            __syncwarp();
 #pragma unroll
-                    for (int c = 0; c < VEC; ++c) {
-                        o[h][c] = fmaf(p4.x, v[c], o[h][c]);
-                        o[h + 1][c] = fmaf(p4.y, v[c], o[h + 1][c]);
-                        o[h + 2][c] = fmaf(p4.z, v[c], o[h + 2][c]);
-                        o[h + 3][c] = fmaf(p4.w, v[c], o[h + 3][c]);
+            for (int t = 0; t < kGrp; t += RPI) {
+                const int r = t + lane / CH;
+                const float4 v4 = *reinterpret_cast<const float4 *>(vb + r * D + (((lane % CH) ^ (r & 7)) << 2));
+                const float2 lo = make_float2(v4.x, v4.y), hi = make_float2(v4.z, v4.w);
+#pragma unroll
+                for (int h = 0; h < ROWS; h += 4) {
+                    const float4 p4 = *reinterpret_cast<const float4 *>(pw + r * ROWS + h);
+                    const float pp[4] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        o[h + j][0] = ptx::f2_fma(lo, make_float2(pp[j], pp[j]), o[h + j][0]);
+                        o[h + j][1] = ptx::f2_fma(hi, make_float2(pp[j], pp[j]), o[h + j][1]);
                     }
                 }
             }
-            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < kSt - 1; ++i) have[i] = have[i + 1];
-            stage = stage == kSt - 1 ? 0 : stage + 1;
+            for (int i = 0; i < kStages - 1; ++i) have[i] = have[i + 1];
+            stage = stage == kStages - 1 ? 0 : stage + 1;
         }
         cp_wait<0>();
 #pragma unroll
-        for (int h = 0; h < kRows; ++h)
-#pragma unroll
-            for (int d = 1; d < 16; d <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], d);
+        for (int d = ROWS; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
 
-        float *ow = qs + kRows * D + kWarps * kGroup * kRows;  // [warp][head][D], over the rings
-        float *ml = qs + kRows * D;                            // [warp][head][2], over P
+        float *ow = base + C::kScores;  // [warp][head][D], over the rings
+        float *ml = base;               // [warp][head][2], over the scores
         __syncthreads();
+        if (lane < ROWS) {
+            ml[(warp * ROWS + lane) * 2] = mx;
+            ml[(warp * ROWS + lane) * 2 + 1] = l;
+        }
 #pragma unroll
-        for (int h = 0; h < kRows; ++h) {
-            if (lane == 0) {
-                ml[(warp * kRows + h) * 2] = mx[h];
-                ml[(warp * kRows + h) * 2 + 1] = l[h];
+        for (int h = 0; h < ROWS; ++h) {
+            float4 x = make_float4(o[h][0].x, o[h][0].y, o[h][1].x, o[h][1].y);
+            if (RPI == 2) {  // the other half's tokens
+                x.x += __shfl_xor_sync(0xffffffffu, x.x, 16);
+                x.y += __shfl_xor_sync(0xffffffffu, x.y, 16);
+                x.z += __shfl_xor_sync(0xffffffffu, x.z, 16);
+                x.w += __shfl_xor_sync(0xffffffffu, x.w, 16);
             }
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) ow[(warp * kRows + h) * D + lane * VEC + c] = o[h][c];
+            if (lane < CH)
+                *reinterpret_cast<float4 *>(ow + (warp * ROWS + h) * D + lane * 4) = x;
         }
         __syncthreads();
         const bool whole = tile0 == 0 && tile1 == tiles;
-        float *ws = whole ? nullptr : piece_at<D>(a, blockIdx.x, first, kRows);
-        for (int i = threadIdx.x; i < heads * D; i += kThreads) {
-            const int h = i / D, d = i % D;
+        float *ws = whole ? nullptr : piece_at<D>(a, blockIdx.x, first, ROWS);
+        for (int i = threadIdx.x; i < heads * CH; i += kThreads) {
+            const int h = i / CH, d = (i % CH) * 4;
             float m = -CUDART_INF_F;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[(w * kRows + h) * 2]);
+            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[(w * ROWS + h) * 2]);
             const float mb = m == -CUDART_INF_F ? 0.f : m;
-            float sum = 0.f, acc = 0.f;
+            float sum = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float f = exp2f(ml[(w * kRows + h) * 2] - mb);
-                sum += f * ml[(w * kRows + h) * 2 + 1];
-                acc += f * ow[(w * kRows + h) * D + d];
+                const float f = ex2(ml[(w * ROWS + h) * 2] - mb);
+                const float4 x = *reinterpret_cast<const float4 *>(ow + (w * ROWS + h) * D + d);
+                sum += f * ml[(w * ROWS + h) * 2 + 1];
+                acc.x += f * x.x;
+                acc.y += f * x.y;
+                acc.z += f * x.z;
+                acc.w += f * x.w;
             }
             if (whole) {
                 const size_t row = (size_t)b * a.num_heads + head0 + h;
-                static_cast<float *>(a.out)[row * D + d] = sum != 0.f ? acc / sum : 0.f;
+                const float r = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays NaN
+                *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * D + d) =
+                    make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r);
                 if (a.lse && d == 0)
                     a.lse[row] = sum != 0.f ? (m + log2f(sum)) * (1.f / kLog2e) : -CUDART_INF_F;
             } else {
-                ws[h * D + d] = acc;
+                *reinterpret_cast<float4 *>(ws + h * D + d) = acc;
                 if (d == 0) {
-                    ws[kRows * D + 2 * h] = m;
-                    ws[kRows * D + 2 * h + 1] = sum;
+                    ws[ROWS * D + 2 * h] = m;
+                    ws[ROWS * D + 2 * h + 1] = sum;
                 }
             }
         }
@@ -796,7 +896,7 @@ paged_join_kernel(const __grid_constant__ PagedDecodeArgs a) {
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float base = m == -CUDART_INF_F ? 0.f : m;
         for (int i = lane; i < pieces; i += 32) {
-            const float f = exp2f(wgt[i][h] - base);
+            const float f = ex2(wgt[i][h] - base);
             sum += f * piece(i)[ROWS * D + 2 * h + 1];
             wgt[i][h] = f;
         }
@@ -864,24 +964,24 @@ cudaError_t launch_bf16(PagedDecodeArgs a) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int D, int NT>
+template <int D, int ROWS>
 cudaError_t launch_f32(PagedDecodeArgs a) {
-    a.head_groups = (a.group + 8 * NT - 1) / (8 * NT);
-    auto kern = paged_decode_f32_kernel<D, NT>;
-    constexpr int kSt = D == 128 ? 2 : 3;
-    constexpr size_t kSmem =
-        sizeof(float) * (8 * NT * D + kWarps * kGroup * 8 * NT + kWarps * kSt * 2 * kGroup * D);
+    a.head_groups = (a.group + ROWS - 1) / ROWS;
+    auto kern = paged_decode_f32_kernel<D, ROWS>;
+    constexpr size_t kSmem = F32Core<D, ROWS>::kSmem;
     cudaError_t e = allow_smem(kern, kSmem);
     if (e == cudaSuccess) e = launch_dependent(kern, kPagedCtas, kThreads, kSmem, a.stream, a);
-    if (e == cudaSuccess) e = join<float, D, 8 * NT>(a);
+    if (e == cudaSuccess) e = join<float, D, ROWS>(a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Up to 8 query heads share a key-value head: one column tile; more: two
-// (and a further unit for every 16).
+// Query heads of a unit: as many as share a key-value head, up to 16 (a
+// further unit for every 16).
 template <int D>
 cudaError_t dispatch(const PagedDecodeArgs &a, bool bf16, bool q_f32) {
-    if (!bf16) return a.group <= 8 ? launch_f32<D, 1>(a) : launch_f32<D, 2>(a);
+    if (!bf16)
+        return a.group <= 4 ? launch_f32<D, 4>(a) : a.group <= 8 ? launch_f32<D, 8>(a)
+                                                                 : launch_f32<D, 16>(a);
     if (q_f32) return a.group <= 8 ? launch_bf16<D, 1, true>(a) : launch_bf16<D, 2, true>(a);
     return a.group <= 8 ? launch_bf16<D, 1, false>(a) : launch_bf16<D, 2, false>(a);
 }

@@ -13,13 +13,14 @@
 //
 // Memory-bound: a row is read once and written once (backward: two reads, one
 // write), so the layout serves the loads.  A row is held by L = 8 to 32 lanes
-// of 16 bytes, 32 / L rows a warp instruction.  A warp takes one token's rows
-// of one kind (query, key or value heads), U passes at a time with the next U
-// already in flight, so the token's cosines and sines and the weights are
-// loaded once for all of them.  They are folded into two coefficients an
-// element, y = r (x A + partner(x) B) with A = w cos, B = +-w' sin, applied with
-// packed fp32 pairs; the partner's element crosses lanes in its stored type
-// (half the shuffles of an fp32 one in bf16).
+// of 16 bytes, 32 / L rows (a pass) a warp instruction.  A warp takes up to
+// U * G passes of one token and one kind (query, key or value heads) and
+// issues all their loads first, asynchronously into shared memory where each lane
+// reads back its own 16 bytes: 8 KB a warp in flight without registers or
+// barriers, while the token's cosines and sines and the weights arrive.  Those are
+// folded into two coefficients an element, y = r (x A + partner(x) B) with
+// A = w cos, B = +-w' sin, applied with packed fp32 pairs; the partner's element
+// crosses lanes in its stored type (half the shuffles of an fp32 one in bf16).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -70,6 +71,22 @@ template <int P> __device__ __forceinline__ void load_pairs(const float *p, floa
         x[i] = make_float2(v.x, v.y);
         x[i + 1] = make_float2(v.z, v.w);
     }
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+    const int n = valid ? 16 : 0;  // otherwise zeros, nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Waits until group g of n has arrived.
+template <int N> __device__ __forceinline__ void cp_wait_group(int g) {
+    if (g == 0) cp_wait<N - 1>();
+    else if (N > 1 && g == 1) cp_wait<(N > 1 ? N - 2 : 0)>();
+    else if (N > 2 && g == 2) cp_wait<(N > 2 ? N - 3 : 0)>();
+    else cp_wait<0>();
 }
 __device__ __forceinline__ float2 swapped(float2 x) { return make_float2(x.y, x.x); }
 __device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
@@ -131,15 +148,17 @@ template <int L> __device__ __forceinline__ float row_sum(float s) {
     return s;
 }
 
-template <typename T, int D, int U, bool BACK>
+template <typename T, int D, int U, int G, bool BACK>
 __global__ void __launch_bounds__(32 * kWarps)
-qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int batches) {
+qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
     using V = Vec<T>;
     constexpr int P = V::P;                 // fp32 pairs per lane
     constexpr int L = D / (2 * P);          // lanes per row
     constexpr int R = 32 / L;               // rows per pass
-    constexpr int kRows = R * U;            // rows in flight
+    constexpr int kRows = R * U * G;        // rows of an item
     constexpr size_t kRowBytes = D * sizeof(T);
+    constexpr int kArrays = BACK ? 2 : 1;
+    __shared__ uint4 stage[kWarps][kArrays][U * G][32];
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -152,10 +171,9 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int batches) {
     const int jp = a.interleaved || !rotated ? j0 : j0 < half ? j0 + half : j0 - half;
     const int src = lane + (jp - j0) / (2 * P);
 
-    const int per_item = kRows * batches;
-    const int nq = (a.set[0].heads + per_item - 1) / per_item;
-    const int nk = (a.set[1].heads + per_item - 1) / per_item;
-    const int nv = (a.set[2].heads + per_item - 1) / per_item;
+    const int nq = (a.set[0].heads + kRows - 1) / kRows;
+    const int nk = (a.set[1].heads + kRows - 1) / kRows;
+    const int nv = (a.set[2].heads + kRows - 1) / kRows;
     const int per = nq + nk + nv;
     const int items = a.num_tokens * per;  // fits: the caller bounds the number of rows
 
@@ -169,27 +187,26 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int batches) {
         const int token = item / per, c = item - token * per;
         const int kind = c < nq ? 0 : c < nq + nk ? 1 : 2;
         const NormRopeRows &s = a.set[kind];
-        int row = (kind == 0 ? c : kind == 1 ? c - nq : c - nq - nk) * per_item;
-        const int end = min(s.heads, row + per_item);
-        row += sub;
+        const int first = (kind == 0 ? c : kind == 1 ? c - nq : c - nq - nk) * kRows;
+        const int end = s.heads;
+        const int row0 = first + sub;
 
         const char *xp = static_cast<const char *>(s.x) + (size_t)token * s.x_stride + j0 * sizeof(T);
         const char *gp = BACK ? static_cast<const char *>(s.dy) + (size_t)token * s.dy_stride +
                                     j0 * sizeof(T)
                               : nullptr;
-        uint4 xv[U], gv[BACK ? U : 1];
-        auto load = [&](int first, uint4 (&x)[U], uint4 (&g)[BACK ? U : 1]) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int r = first + u * R;
-                x[u] = r < end ? *reinterpret_cast<const uint4 *>(xp + r * kRowBytes)
-                               : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < U * G; ++i) {
+            if (first + i * R < end) {  // the same in the whole warp
+                const int r = row0 + i * R;
+                const bool in = r < end;
+                cp_async16(ptx::smem_u32(&stage[warp][0][i][lane]), xp + (in ? r : 0) * kRowBytes, in);
                 if (BACK)
-                    g[u] = r < end ? *reinterpret_cast<const uint4 *>(gp + r * kRowBytes)
-                                   : make_uint4(0, 0, 0, 0);
+                    cp_async16(ptx::smem_u32(&stage[warp][kArrays - 1][i][lane]),
+                               gp + (in ? r : 0) * kRowBytes, in);
             }
-        };
-        load(row, xv, gv);
+            if (i % U == U - 1) cp_commit();
+        }
 
         // destination of the token's rows: its row of the output, or its slot
         // of the cache (a slot outside the pool is skipped)
@@ -197,7 +214,10 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int batches) {
         size_t head_bytes = kRowBytes;
         if (s.cache) {
             const int slot = __ldg(a.slots + token);
-            if (slot < 0 || slot >= a.num_slots) continue;
+            if (slot < 0 || slot >= a.num_slots) {
+                cp_wait<0>();  // the stage is filled anew
+                continue;
+            }
             const int page = slot / a.page_size;
             out += (size_t)page * s.out_stride + (size_t)(slot - page * a.page_size) * kRowBytes;
             head_bytes *= a.page_size;
@@ -223,84 +243,78 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int batches) {
                 }
             }
         }
-        for (;; row += kRows) {
-            uint4 nx[U], ng[BACK ? U : 1];
-            const bool more = row - sub + kRows < end;  // the same in the whole warp
-            if (more) load(row + kRows, nx, ng);
-            if (!BACK && kind == 2) {  // values: copied
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (row + u * R < end)
-                        *reinterpret_cast<uint4 *>(out + (row + u * R) * head_bytes) = xv[u];
-            } else {
+        for (int g = 0; g < G; ++g) {
+            if (first + g * U * R >= end) break;
+            cp_wait_group<G>(g);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const bool in = row + u * R < end;
-                    float2 x[P], y[P];
-                    V::unpack(xv[u], x);
-                    float r = 1.f;
-                    if (norm) {
-                        float2 ss = twice(0.f);
+            for (int u = 0; u < U; ++u) {
+                const int row = row0 + (g * U + u) * R;
+                if (U > 1 && row - sub >= end) break;
+                const bool in = row < end;
+                const uint4 xv = stage[warp][0][g * U + u][lane];
+                if (!BACK && kind == 2) {  // values: copied
+                    if (in) *reinterpret_cast<uint4 *>(out + row * head_bytes) = xv;
+                    continue;
+                }
+                float2 x[P], y[P];
+                V::unpack(xv, x);
+                float r = 1.f;
+                if (norm) {
+                    float2 ss = twice(0.f);
 #pragma unroll
-                        for (int i = 0; i < P; ++i) ss = ptx::f2_fma(x[i], x[i], ss);
-                        // a row past the last head stays zero also where eps is 0
-                        r = row_sum<L>(ss.x + ss.y) * (1.f / D) + a.eps;
-                        r = in ? rsqrtf(r) : 0.f;
-                    }
-                    if (BACK) {
-                        float2 g[P];
-                        V::unpack(gv[u], g);
-                        partner<T>(gv[u], g, a.interleaved, rotated, src, y);
-                        float2 dot = twice(0.f);
-                        const float2 rr = twice(r);
+                    for (int i = 0; i < P; ++i) ss = ptx::f2_fma(x[i], x[i], ss);
+                    // a row past the last head stays zero also where eps is 0
+                    r = row_sum<L>(ss.x + ss.y) * (1.f / D) + a.eps;
+                    r = in ? rsqrtf(r) : 0.f;
+                }
+                const float2 rr = twice(r);
+                if (BACK) {
+                    const uint4 gv = stage[warp][kArrays - 1][g * U + u][lane];
+                    float2 dy[P];
+                    V::unpack(gv, dy);
+                    partner<T>(gv, dy, a.interleaved, rotated, src, y);
+                    float2 dot = twice(0.f);
 #pragma unroll
-                        for (int i = 0; i < P; ++i) {
-                            g[i] = ptx::f2_fma(g[i], ca[i], ptx::f2_mul(y[i], cb[i]));
-                            if (norm) {
-                                x[i] = ptx::f2_mul(x[i], rr);
-                                const float2 p = ptx::f2_mul(g[i], x[i]);
-                                if (kind == 0) dw[0][i] = ptx::f2_add(dw[0][i], p);
-                                else dw[1][i] = ptx::f2_add(dw[1][i], p);
-                                dot = ptx::f2_fma(w[i], p, dot);
-                                g[i] = ptx::f2_mul(g[i], w[i]);
-                            }
-                        }
+                    for (int i = 0; i < P; ++i) {
+                        dy[i] = ptx::f2_fma(dy[i], ca[i], ptx::f2_mul(y[i], cb[i]));
                         if (norm) {
-                            const float2 m = twice(row_sum<L>(dot.x + dot.y) * (-1.f / D));
-#pragma unroll
-                            for (int i = 0; i < P; ++i)
-                                g[i] = ptx::f2_mul(rr, ptx::f2_fma(x[i], m, g[i]));
+                            x[i] = ptx::f2_mul(x[i], rr);
+                            const float2 p = ptx::f2_mul(dy[i], x[i]);
+                            if (kind == 0) dw[0][i] = ptx::f2_add(dw[0][i], p);
+                            else dw[1][i] = ptx::f2_add(dw[1][i], p);
+                            dot = ptx::f2_fma(w[i], p, dot);
+                            dy[i] = ptx::f2_mul(dy[i], w[i]);
                         }
-                        if (in)
-                            *reinterpret_cast<uint4 *>(out + (row + u * R) * head_bytes) = V::pack(g);
-                    } else {
-                        partner<T>(xv[u], x, a.interleaved, rotated, src, y);
-                        const float2 rr = twice(r);
+                    }
+                    if (norm) {
+                        const float2 m = twice(row_sum<L>(dot.x + dot.y) * (-1.f / D));
 #pragma unroll
-                        for (int i = 0; i < P; ++i) {
-                            y[i] = ptx::f2_fma(x[i], ca[i], ptx::f2_mul(y[i], cb[i]));
-                            if (norm) y[i] = ptx::f2_mul(y[i], rr);
-                        }
-                        if (in && s.out_f32) {  // unrounded rows (the queries of a fused step)
-                            float *o = static_cast<float *>(s.out) +
-                                       ((size_t)token * s.heads + row + u * R) * D + j0;
+                        for (int i = 0; i < P; ++i)
+                            dy[i] = ptx::f2_mul(rr, ptx::f2_fma(x[i], m, dy[i]));
+                    }
+                    if (in) *reinterpret_cast<uint4 *>(out + row * head_bytes) = V::pack(dy);
+                } else {
+                    partner<T>(xv, x, a.interleaved, rotated, src, y);
 #pragma unroll
-                            for (int i = 0; i < P; i += 2)
-                                *reinterpret_cast<float4 *>(o + 2 * i) =
-                                    make_float4(y[i].x, y[i].y, y[i + 1].x, y[i + 1].y);
-                        } else if (in) {
-                            *reinterpret_cast<uint4 *>(out + (row + u * R) * head_bytes) = V::pack(y);
-                        }
+                    for (int i = 0; i < P; ++i) {
+                        y[i] = ptx::f2_fma(x[i], ca[i], ptx::f2_mul(y[i], cb[i]));
+                        if (norm) y[i] = ptx::f2_mul(y[i], rr);
+                    }
+                    if (in && s.out_f32) {  // unrounded rows (the queries of a fused step)
+                        float *o = static_cast<float *>(s.out) +
+                                   ((size_t)token * s.heads + row) * D + j0;
+#pragma unroll
+                        for (int i = 0; i < P; i += 2)
+                            *reinterpret_cast<float4 *>(o + 2 * i) =
+                                make_float4(y[i].x, y[i].y, y[i + 1].x, y[i + 1].y);
+                    } else if (in) {
+                        *reinterpret_cast<uint4 *>(out + row * head_bytes) = V::pack(y);
                     }
                 }
             }
-            if (!more) break;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                xv[u] = nx[u];
-                if (BACK) gv[u] = ng[u];
-            }
         }
+        cp_wait<0>();  // also the groups of rows past the last head: none in flight
     }
 
     if (BACK && a.set[0].weight) {
@@ -325,42 +339,49 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int batches) {
     }
 }
 
-// dw[c] = sum over blocks of partial[block][c], in a fixed order: 32 columns
-// a block, 32 slices of the blocks' axis.
-__global__ void __launch_bounds__(1024)
+// dw[c] = sum over blocks of partial[block][c], in a fixed order: 8 columns (one
+// 32-byte sector of a partial result) a block, 128 slices of the blocks' axis.
+constexpr int kSumCols = 8, kSumSlices = 128;
+__global__ void __launch_bounds__(kSumCols *kSumSlices)
 norm_weight_sum_kernel(const float *__restrict__ partial, int blocks, int D, float *dwq, float *dwk) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __shared__ float red[32][33];
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + x;
+    __shared__ float red[kSumSlices][kSumCols + 1];
+    const int x = threadIdx.x % kSumCols, y = threadIdx.x / kSumCols;
+    const int c = blockIdx.x * kSumCols + x;
     float t = 0.f;
-    for (int b = y; b < blocks; b += 32) t += partial[(size_t)b * 2 * D + c];
+#pragma unroll 8
+    for (int b = y; b < blocks; b += kSumSlices) t += partial[(size_t)b * 2 * D + c];
     red[y][x] = t;
     __syncthreads();
-    t = red[x][y];
+    const int lane = threadIdx.x & 31, col = threadIdx.x >> 5;
+    if (col >= kSumCols) return;
+    t = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSumSlices; i += 32) t += red[i + lane][col];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    if (x == 0) {
-        const int col = blockIdx.x * 32 + y;
-        if (col < D) dwq[col] = t; else dwk[col - D] = t;
+    if (lane == 0) {
+        const int at = blockIdx.x * kSumCols + col;
+        if (at < D) dwq[at] = t; else dwk[at - D] = t;
     }
 }
 
-template <typename T, int D, int U, bool BACK>
-cudaError_t launch_u(const NormRopeArgs &a, int batches) {
-    constexpr int kRows = 32 / (D / (2 * Vec<T>::P)) * U;
+template <typename T, int D, int U, int G, bool BACK>
+cudaError_t launch_u(const NormRopeArgs &a) {
+    constexpr int kRows = 32 / (D / (2 * Vec<T>::P)) * U * G;
     long per = 0;
-    for (const NormRopeRows &s : a.set) per += (s.heads + kRows * batches - 1) / (kRows * batches);
+    for (const NormRopeRows &s : a.set) per += (s.heads + kRows - 1) / kRows;
     long grid = (a.num_tokens * per + kWarps - 1) / kWarps;
     // the backward pass keeps its weight sums in registers over a fixed
     // number of blocks, one partial result each
     const long most = BACK ? kNormBackwardBlocks : 0x7fffffffL;
     if (grid > most) grid = most;
-    cudaError_t e = launch_dependent(qk_norm_rope_kernel<T, D, U, BACK>, (unsigned)grid,
-                                     32 * kWarps, 0, a.stream, a, batches);
+    cudaError_t e = launch_dependent(qk_norm_rope_kernel<T, D, U, G, BACK>, (unsigned)grid,
+                                     32 * kWarps, 0, a.stream, a);
     if (e == cudaSuccess && BACK && a.set[0].weight)
-        e = launch_dependent(norm_weight_sum_kernel, (a.dk_weight ? 2 : 1) * D / 32, 1024, 0, a.stream,
+        e = launch_dependent(norm_weight_sum_kernel, (a.dk_weight ? 2 : 1) * D / kSumCols,
+                             kSumCols * kSumSlices, 0, a.stream,
                              static_cast<const float *>(a.partial), (int)grid, D, a.dq_weight,
                              a.dk_weight);
     return e != cudaSuccess ? e : cudaGetLastError();
@@ -369,12 +390,12 @@ cudaError_t launch_u(const NormRopeArgs &a, int batches) {
 template <typename T, int D, bool BACK>
 cudaError_t launch(const NormRopeArgs &a) {
     // Few rows: one pass a warp spreads them over many SMs.  Many: the token's
-    // cosines, sines and weights are loaded once for up to kBatches * U passes.
+    // cosines, sines and weights are loaded once for up to U * G passes.
     constexpr int kRows = 32 / (D / (2 * Vec<T>::P));
-    constexpr int U = BACK ? 2 : 4, kBatches = 4;
+    constexpr int U = BACK ? 2 : 4;
     const long rows = (long)a.num_tokens * (a.set[0].heads + a.set[1].heads + a.set[2].heads);
-    if (rows <= 152L * 16 * kRows) return launch_u<T, D, 1, BACK>(a, 1);
-    return launch_u<T, D, U, BACK>(a, rows <= 152L * 16 * kRows * U * kBatches ? 1 : kBatches);
+    if (rows <= 152L * 16 * kRows) return launch_u<T, D, 1, 1, BACK>(a);
+    return launch_u<T, D, U, 4, BACK>(a);
 }
 
 template <typename T>
