@@ -326,6 +326,16 @@ int64_t need_of(int64_t n) {
     return n;
 }
 
+// `n` elements of a one-dimensional tensor from `at` on, sharing its storage.
+Tensor part_of(const Tensor &t, int64_t at, int64_t n) {
+    Tensor p = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW,
+                                                        c10::Storage(t.storage()), t.key_set(),
+                                                        t.dtype());
+    p.unsafeGetTensorImpl()->set_storage_offset(at);
+    p.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+    return p;
+}
+
 PyObject *wrap(const Tensor &t) {
     if (!t.defined()) Py_RETURN_NONE;
     return THPVariable_Wrap(t);
@@ -503,8 +513,7 @@ PyObject *paged_reserve(PyObject *const *a) {
             base, base + n, base + 2 * n, static_cast<uint8_t *>(served.data_ptr()), lens_out,
             count_out, call.stream());
     });
-    return tuple(all.narrow(0, 0, tokens), all.narrow(0, n, tokens), all.narrow(0, 2 * n, b + 1),
-                 served);
+    return tuple(part_of(all, 0, tokens), part_of(all, n, tokens), part_of(all, 2 * n, b + 1), served);
 }
 
 template <PyObject *(*F)(PyObject *const *), int N>

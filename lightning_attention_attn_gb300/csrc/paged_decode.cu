@@ -38,6 +38,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kGroup = 16;              // tokens of one warp step
 constexpr int kTile = kWarps * kGroup;  // tokens of one tile of the work split
+constexpr int kOverhead = 3;            // tiles that starting a unit costs
 constexpr int kStages = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -89,19 +90,23 @@ __device__ __forceinline__ float hi_of(uint32_t p) { return __uint_as_float(p & 
 __device__ __forceinline__ int request_len(const PagedDecodeArgs &a, int b) {
     return min(max(__ldg(a.seq_lens + b), 0), a.max_tokens);
 }
-__device__ __forceinline__ int request_tiles(const PagedDecodeArgs &a, int b) {
-    return (request_len(a, b) + kTile - 1) / kTile;
+// Cost of a unit of `len` tokens, in tiles: starting a unit (its page table, queries
+// and first loads one after the other, then the warps' join) takes a CTA about
+// as long as streaming kOverhead tiles.  A unit's cost range is the overhead, then
+// its tiles; a cut inside the overhead is a cut before the first tile.
+__device__ __forceinline__ int unit_cost(int len) {
+    return len > 0 ? kOverhead + (len + kTile - 1) / kTile : 0;
 }
 
-// The tile that CTA `cta`'s range begins with.  All tiles (of all units, request
-// by request) are cut into ranges of `chunk`, CTA c taking [c chunk, (c + 1) chunk).
+// Where CTA `cta`'s range begins.  The costs of all units, request by request,
+// are cut into ranges of `chunk`, CTA c taking [c chunk, (c + 1) chunk).
 struct Place {
-    long long all, chunk, w;  // tiles of all units, of a range, first of this one
-    long long unit0;          // first tile of request b
+    long long all, chunk, w;  // cost of all units, of a range, start of this one
+    long long unit0;          // start of request b's units
     int b;
 };
 
-// Whole block (kThr threads): false where the CTA has no tile.  The lengths are
+// Whole block (kThr threads): false where the CTA has no range.  The lengths are
 // read once for up to kThr requests.
 template <int kThr>
 __device__ __forceinline__ bool find_place(const PagedDecodeArgs &a, int units, int cta, Place &p) {
@@ -110,10 +115,10 @@ __device__ __forceinline__ bool find_place(const PagedDecodeArgs &a, int units, 
     __shared__ long long found[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long total;
-    // inclusive prefix sum of the tiles of requests b0 .. b0 + kThr - 1
+    // inclusive prefix sum of the costs of requests b0 .. b0 + kThr - 1
     auto scan = [&](int b0, int &t) {
         const int i = b0 + threadIdx.x;
-        t = i < a.batch ? request_tiles(a, i) : 0;
+        t = i < a.batch ? unit_cost(request_len(a, i)) : 0;
         long long s = t;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -161,7 +166,7 @@ __device__ __forceinline__ bool find_place(const PagedDecodeArgs &a, int units, 
     return p.b >= 0;
 }
 
-// n / d for a count of tiles: 32-bit where it fits.
+// n / d of two costs: 32-bit where it fits.
 __device__ __forceinline__ int tiles_div(long long n, int d) {
     return (n >> 32) == 0 ? (int)((uint32_t)n / (uint32_t)d) : (int)(n / d);
 }
@@ -244,15 +249,18 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     for (; w0 < w1; ) {
         if (b >= a.batch) return;
         const int len = request_len(a, b);
-        const int tiles = (len + kTile - 1) / kTile;
-        if (w0 >= unit0 + (long long)tiles * units) {  // next request (empty ones pass)
-            unit0 += (long long)tiles * units;
+        const int tiles = (len + kTile - 1) / kTile, cost = unit_cost(len);
+        if (w0 >= unit0 + (long long)cost * units) {  // next request (empty ones pass)
+            unit0 += (long long)cost * units;
             ++b;
             continue;
         }
-        const int unit = tiles_div(w0 - unit0, tiles);
-        const int tile0 = (int)(w0 - unit0 - (long long)unit * tiles);
-        const int tile1 = (int)min((long long)tiles, tile0 + (w1 - w0));
+        const int unit = tiles_div(w0 - unit0, cost);
+        const int at0 = (int)(w0 - unit0 - (long long)unit * cost);
+        const int at1 = (int)min((long long)cost, at0 + (w1 - w0));
+        const int tile0 = max(at0 - kOverhead, 0), tile1 = at1 - kOverhead;
+        w0 += at1 - at0;
+        if (tile1 <= 0) continue;  // only overhead: the next CTA starts the unit
         const int kvh = unit / a.head_groups, hg = unit % a.head_groups;
         const int head0 = kvh * a.group + hg * kRows;
         const int heads = min(kRows, a.group - hg * kRows);
@@ -536,7 +544,6 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
         }
         __syncthreads();  // shared memory is the ring again
         first = false;
-        w0 += tile1 - tile0;
     }
 }
 
@@ -607,15 +614,18 @@ paged_decode_f32_kernel(const __grid_constant__ PagedDecodeArgs a) {
     for (; w0 < w1; ) {
         if (b >= a.batch) return;
         const int len = request_len(a, b);
-        const int tiles = (len + kTile - 1) / kTile;
-        if (w0 >= unit0 + (long long)tiles * units) {
-            unit0 += (long long)tiles * units;
+        const int tiles = (len + kTile - 1) / kTile, cost = unit_cost(len);
+        if (w0 >= unit0 + (long long)cost * units) {  // next request (empty ones pass)
+            unit0 += (long long)cost * units;
             ++b;
             continue;
         }
-        const int unit = tiles_div(w0 - unit0, tiles);
-        const int tile0 = (int)(w0 - unit0 - (long long)unit * tiles);
-        const int tile1 = (int)min((long long)tiles, tile0 + (w1 - w0));
+        const int unit = tiles_div(w0 - unit0, cost);
+        const int at0 = (int)(w0 - unit0 - (long long)unit * cost);
+        const int at1 = (int)min((long long)cost, at0 + (w1 - w0));
+        const int tile0 = max(at0 - kOverhead, 0), tile1 = at1 - kOverhead;
+        w0 += at1 - at0;
+        if (tile1 <= 0) continue;  // only overhead: the next CTA starts the unit
         const int kvh = unit / a.head_groups, hg = unit % a.head_groups;
         const int head0 = kvh * a.group + hg * ROWS;
         const int heads = min(ROWS, a.group - hg * ROWS);
@@ -844,102 +854,125 @@ paged_decode_f32_kernel(const __grid_constant__ PagedDecodeArgs a) {
         }
         __syncthreads();
         first = false;
-        w0 += tile1 - tile0;
     }
 }
 
 // -------------------------------------------------------------------- join
 // Adds the pieces of the units that several CTAs hold, in the order of their
-// tokens.  Block c - 1 looks at the start of CTA c's range: if it is the first such
-// start inside a unit, the block joins that unit (at most kPagedCtas - 1 units are
-// cut, whatever the batch).  A unit's maxima come first, all pieces at once,
-// then its columns, four a thread, the pieces in kJoin / columns slices.
+// tokens.  Block c - 1 looks at the start of CTA c's range: where it lies inside a
+// unit, the block joins a share of that unit's heads (each of the unit's k cuts
+// has a block; block j of them takes the heads j, j + k, ...).  At most
+// kPagedCtas - 1 units are cut, whatever the batch.  A thread takes four columns of
+// every slices-th piece with a running maximum, its loads in flight together; the
+// slices are added in order.
 constexpr int kJoin = 512;
 
 template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(kJoin)
 paged_join_kernel(const __grid_constant__ PagedDecodeArgs a) {
-    __shared__ float wgt[kPagedCtas][ROWS];
     __shared__ float4 part[kJoin];
+    __shared__ float2 stat[kJoin];
     const int units = a.num_kv_heads * a.head_groups;
     // The lengths were complete before the main kernel let this one be
     // scheduled; the pieces are read after the wait.
     Place at;
     const int c = blockIdx.x + 1;
     const bool any = find_place<kJoin>(a, units, c, at);
+    int unit = 0, c0 = 0, c1 = 0;
+    long long u0 = 0;
+    if (any) {
+        const int cost = unit_cost(request_len(a, at.b));
+        unit = tiles_div(at.w - at.unit0, cost);
+        u0 = at.unit0 + (long long)unit * cost;
+        // the CTAs of the unit's first tile (behind its overhead) and of its last
+        c0 = (int)((u0 + kOverhead) / at.chunk);
+        c1 = (int)((u0 + cost - 1) / at.chunk);
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (!any) return;
-    const int tiles = request_tiles(a, at.b);
-    const int unit = tiles_div(at.w - at.unit0, tiles);
-    const long long u0 = at.unit0 + (long long)unit * tiles;
-    if (at.w == u0 || at.w - at.chunk > u0) return;  // no cut here, or not a unit's first
-    const int pieces = (int)((u0 + tiles - 1) / at.chunk) - c + 2;
-    // the first piece ends CTA c - 1's range (and is all of it if it began there),
-    // the others begin theirs
-    const float *first = piece_at<D>(a, c - 1, at.w - at.chunk == u0, ROWS);
-    auto piece = [&](int i) { return i == 0 ? first : piece_at<D>(a, c - 1 + i, true, ROWS); };
+    if (!any || c <= c0) return;  // no cut here
+    const int pieces = c1 - c0 + 1, cuts = c1 - c0;
 
     const int kvh = unit / a.head_groups, hg = unit % a.head_groups;
     const int head0 = kvh * a.group + hg * ROWS;
     const int heads = min(ROWS, a.group - hg * ROWS);
-    const size_t row0 = (size_t)at.b * a.num_heads + head0;
-    const int lane = threadIdx.x & 31;
-    for (int h = threadIdx.x >> 5; h < heads; h += kJoin / 32) {
-        float m = -CUDART_INF_F, sum = 0.f;
-        for (int i = lane; i < pieces; i += 32) {
-            const float pm = piece(i)[ROWS * D + 2 * h];
-            wgt[i][h] = pm;
-            m = fmaxf(m, pm);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float base = m == -CUDART_INF_F ? 0.f : m;
-        for (int i = lane; i < pieces; i += 32) {
-            const float f = ex2(wgt[i][h] - base);
-            sum += f * piece(i)[ROWS * D + 2 * h + 1];
-            wgt[i][h] = f;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float r = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays NaN
-        for (int i = lane; i < pieces; i += 32) wgt[i][h] *= r;
-        if (a.lse && lane == 0)
-            a.lse[row0 + h] = sum != 0.f ? (m + log2f(sum)) * (1.f / kLog2e) : -CUDART_INF_F;
-    }
-    __syncthreads();
+    const int mine = c - c0 - 1;  // this block among the unit's
+    if (mine >= heads) return;
+    const int n = (heads - mine + cuts - 1) / cuts;  // its heads: mine, mine + cuts, ...
 
-    const int cols = heads * (D / 4);  // at most kJoin
+    const int cols = n * (D / 4);  // at most kJoin
     const int slices = kJoin / cols;
     const int slice = threadIdx.x / cols, col = threadIdx.x - slice * cols;
-    const int h = col / (D / 4), d = (col % (D / 4)) * 4;
+    const int h = mine + (col / (D / 4)) * cuts, d = (col % (D / 4)) * 4;
+    float m = -CUDART_INF_F, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (slice < slices) {
-#pragma unroll 8
-        for (int i = slice; i < pieces; i += slices) {
-            const float4 x = *reinterpret_cast<const float4 *>(piece(i) + h * D + d);
-            const float f = wgt[i][h];
-            acc.x += f * x.x;
-            acc.y += f * x.y;
-            acc.z += f * x.z;
-            acc.w += f * x.w;
+        // the first piece ends CTA c0's range (and is all of it if it began
+        // there), the others begin theirs
+        const bool whole = c0 * at.chunk >= u0;
+        constexpr int kFlight = 4;
+        for (int i0 = slice; i0 < pieces; i0 += kFlight * slices) {
+            float4 x[kFlight];
+            float2 ms[kFlight];
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f) {
+                const int i = i0 + f * slices;
+                x[f] = make_float4(0.f, 0.f, 0.f, 0.f);
+                ms[f] = make_float2(-CUDART_INF_F, 0.f);
+                if (i < pieces) {
+                    const float *p = piece_at<D>(a, c0 + i, i > 0 || whole, ROWS);
+                    x[f] = __ldcg(reinterpret_cast<const float4 *>(p + h * D + d));
+                    ms[f] = __ldcg(reinterpret_cast<const float2 *>(p + ROWS * D + 2 * h));
+                }
+            }
+            float top = m;
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f) top = fmaxf(top, ms[f].x);
+            const float base = top == -CUDART_INF_F ? 0.f : top;
+            const float k = ex2(m - base);
+            m = top;
+            sum *= k;
+            acc.x *= k, acc.y *= k, acc.z *= k, acc.w *= k;
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f) {
+                const float e = ex2(ms[f].x - base);
+                sum = fmaf(ms[f].y, e, sum);
+                acc.x = fmaf(x[f].x, e, acc.x);
+                acc.y = fmaf(x[f].y, e, acc.y);
+                acc.z = fmaf(x[f].z, e, acc.z);
+                acc.w = fmaf(x[f].w, e, acc.w);
+            }
         }
     }
     part[threadIdx.x] = acc;
+    stat[threadIdx.x] = make_float2(m, sum);
     __syncthreads();
     if (slice > 0) return;
+    float top = m;
+    for (int i = 1; i < slices; ++i) top = fmaxf(top, stat[threadIdx.x + i * cols].x);
+    const float base = top == -CUDART_INF_F ? 0.f : top;
+    const float k = ex2(m - base);
+    sum *= k;
+    acc.x *= k, acc.y *= k, acc.z *= k, acc.w *= k;
     for (int i = 1; i < slices; ++i) {
         const float4 x = part[threadIdx.x + i * cols];
-        acc.x += x.x;
-        acc.y += x.y;
-        acc.z += x.z;
-        acc.w += x.w;
+        const float2 ms = stat[threadIdx.x + i * cols];
+        const float e = ex2(ms.x - base);
+        sum = fmaf(ms.y, e, sum);
+        acc.x = fmaf(x.x, e, acc.x);
+        acc.y = fmaf(x.y, e, acc.y);
+        acc.z = fmaf(x.z, e, acc.z);
+        acc.w = fmaf(x.w, e, acc.w);
     }
-    T *o = static_cast<T *>(a.out) + (row0 + h) * D + d;
+    const float r = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays NaN
+    const size_t row = (size_t)at.b * a.num_heads + head0 + h;
+    T *o = static_cast<T *>(a.out) + row * D + d;
     if constexpr (sizeof(T) == 2)
-        *reinterpret_cast<uint2 *>(o) = make_uint2(pack2(acc.x, acc.y), pack2(acc.z, acc.w));
+        *reinterpret_cast<uint2 *>(o) = make_uint2(pack2(acc.x * r, acc.y * r), pack2(acc.z * r, acc.w * r));
     else
-        *reinterpret_cast<float4 *>(o) = acc;
+        *reinterpret_cast<float4 *>(o) = make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r);
+    if (a.lse && d == 0)
+        a.lse[row] = sum != 0.f ? (top + log2f(sum)) * (1.f / kLog2e) : -CUDART_INF_F;
 }
 
 // Opts `kern` into `smem` bytes of dynamic shared memory on every device it

@@ -29,6 +29,7 @@ constexpr int kMaxThreads = 1024;
 constexpr int kFillThreads = 256;
 constexpr int kFillBlocks = 152 * 2;
 constexpr int kSmallTokens = 4096;
+constexpr int kFlight = 4;  // dependent loads a thread keeps in flight
 
 struct Pair {
     long long x, y;
@@ -46,18 +47,24 @@ __device__ __forceinline__ Pair block_scan(long long x, long long y, long long (
     __syncthreads();  // the previous scan's readers are done
     if (lane == 31) sums[0][warp] = x, sums[1][warp] = y;
     __syncthreads();
-    Pair below = {0, 0};
-    *all = {0, 0};
-    for (int w = 0; w < warps; ++w) {
-        const long long u = sums[0][w], v = sums[1][w];
-        if (w < warp) below.x += u, below.y += v;
-        all->x += u, all->y += v;
+    // the warps' sums, scanned by every warp
+    long long u = lane < warps ? sums[0][lane] : 0, v = lane < warps ? sums[1][lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long p = __shfl_up_sync(0xffffffffu, u, o), q = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) u += p, v += q;
     }
-    return {x + below.x, y + below.y};
+    all->x = __shfl_sync(0xffffffffu, u, 31);
+    all->y = __shfl_sync(0xffffffffu, v, 31);
+    const long long below_x = __shfl_sync(0xffffffffu, u, warp > 0 ? warp - 1 : 0);
+    const long long below_y = __shfl_sync(0xffffffffu, v, warp > 0 ? warp - 1 : 0);
+    return {x + (warp > 0 ? below_x : 0), y + (warp > 0 ? below_y : 0)};
 }
 
 __device__ __forceinline__ int blocks_of(long long tokens, int page) {
-    return (int)((tokens + page - 1) / page);
+    // 32-bit where it fits (a 64-bit division is many times the work)
+    return tokens < 0x7fffffffLL - page ? ((int)tokens + page - 1) / page
+                                        : (int)((tokens + page - 1) / page);
 }
 
 // The last entry of the ascending at[0 .. n) that is <= v (at[0] is).
@@ -85,25 +92,32 @@ __device__ __forceinline__ Step step_arrays(int *smem, int batch) {
 __device__ __forceinline__ void fill(const PagedReserveArgs &a, const Step &s, int top, int pages, int i,
                                      int n) {
     const int end = s.cu[a.batch];
-    for (int t = i; t < a.num_tokens; t += n) {
-        int slot = -1, position = 0;
-        if (t < end) {
+    for (int t0 = i; t0 < a.num_tokens; t0 += kFlight * n) {
+        int page[kFlight], position[kFlight], row[kFlight];
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+            const int t = t0 + f * n;
+            page[f] = -1;
+            position[f] = row[f] = 0;
+            if (t >= min(end, a.num_tokens)) continue;
             const int b = last_at(s.cu, a.batch, t);
             const int was = s.old[b];
-            if (was >= 0) {
-                position = was + (t - s.cu[b]);
-                const int blk = position / a.page_size;
-                const int have = blocks_of(was, a.page_size);
-                // new blocks from the stack: the table may not hold them yet
-                const int page = blk < have
-                                     ? __ldcg(a.block_table + (size_t)b * a.table_stride + blk)
-                                     : __ldcg(a.free_pages + (top - s.taken[b] - (blk - have)));
-                slot = page < 0 || page >= a.num_pages
-                           ? -1 : page * a.page_size + (position - blk * a.page_size);
-            }
+            if (was < 0) continue;
+            position[f] = was + (t - s.cu[b]);
+            const int blk = position[f] / a.page_size;
+            row[f] = position[f] - blk * a.page_size;
+            const int have = blocks_of(was, a.page_size);
+            // new blocks from the stack: the table may not hold them yet
+            page[f] = blk < have ? __ldcg(a.block_table + (size_t)b * a.table_stride + blk)
+                                 : __ldcg(a.free_pages + (top - s.taken[b] - (blk - have)));
         }
-        a.slots[t] = slot;
-        a.positions[t] = position;
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+            const int t = t0 + f * n;
+            if (t >= a.num_tokens) break;
+            a.slots[t] = page[f] < 0 || page[f] >= a.num_pages ? -1 : page[f] * a.page_size + row[f];
+            a.positions[t] = position[f];
+        }
     }
     for (int j = i; j < pages; j += n) {
         const int b = last_at(s.taken, a.batch, j);
@@ -156,9 +170,18 @@ paged_reserve_kernel(const __grid_constant__ PagedReserveArgs a) {
         __syncthreads();
         // entry j of the push: block j - (entries before) of the request that holds it
         const int top = (int)count, most = (int)min(count + base, (long long)a.num_pages);
-        for (int j = top + threadIdx.x; j < most; j += threads) {
-            const int b = last_at(s.taken, a.batch, j);
-            a.free_pages[j] = __ldcg(a.block_table + (size_t)b * a.table_stride + (j - s.taken[b]));
+        for (int j0 = top + threadIdx.x; j0 < most; j0 += kFlight * threads) {
+            int page[kFlight];
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                const int j = j0 + i * threads;
+                if (j >= most) break;
+                const int b = last_at(s.taken, a.batch, j);
+                page[i] = __ldcg(a.block_table + (size_t)b * a.table_stride + (j - s.taken[b]));
+            }
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i)
+                if (j0 + i * threads < most) a.free_pages[j0 + i * threads] = page[i];
         }
         count = min(count + base, (long long)a.num_pages);
         if (a.batch > threads) load(threadIdx.x);
