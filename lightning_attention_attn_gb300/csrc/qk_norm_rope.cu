@@ -19,7 +19,7 @@
 // no element crosses lanes; D / 8 lanes share a row, 32 / (D / 8) rows (a pass) a
 // warp instruction.  A warp takes up to U * G passes of one token and one kind
 // (query, key or value heads) and issues all their loads first, asynchronously
-// into shared memory: 8 KB a warp (bf16) in flight without registers or block-wide
+// into shared memory: 4 KB a warp (backward 8) in flight without registers or block-wide
 // barriers, while the token's cosines and sines and the weights arrive.  Those are
 // folded into two coefficients an element, y = r (x A + partner(x) B) with
 // A = w cos, B = +-w' sin, applied with packed fp32 pairs.
@@ -124,7 +124,7 @@ template <int L> __device__ __forceinline__ float row_sum(float s) {
 }
 
 template <typename T, int D, int U, int G, bool BACK, bool INTER>
-__global__ void __launch_bounds__(32 * kWarps, U * G == 1 ? 8 : BACK ? 5 : 6)
+__global__ void __launch_bounds__(32 * kWarps, BACK && U * G > 1 ? 5 : 8)
 qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
     constexpr int L = D / 8;            // lanes per row
     constexpr int R = 32 / L;           // rows per pass
@@ -381,13 +381,15 @@ cudaError_t launch_u(const NormRopeArgs &a) {
 template <typename T, int D, bool BACK>
 cudaError_t launch(const NormRopeArgs &a) {
     // Few rows: one pass a warp spreads them over many SMs.  Many: the token's
-    // cosines, sines and weights are loaded once for up to U * G passes (8 KB a
-    // warp in flight).
+    // cosines, sines and weights are loaded once for up to U * G passes.  8192
+    // tokens of 64 + 64 bf16 heads, forward: G = 1, 2, 4 take 103, 90, 97 us (8
+    // blocks an SM fit at G = 2; 7 or 10 take 93, 94); gradients, where the sums over a
+    // block's rows come on top: 183, 144, 134 us.
     constexpr int R = 32 / (D / 8);
     constexpr int U = 8 / (int)sizeof(T) / (BACK ? 2 : 1);
     const long rows = (long)a.num_tokens * (a.set[0].heads + a.set[1].heads + a.set[2].heads);
     if (rows <= 152L * 16 * R) return launch_u<T, D, 1, 1, BACK>(a);
-    return launch_u<T, D, U, 4, BACK>(a);
+    return launch_u<T, D, U, BACK ? 4 : 2, BACK>(a);
 }
 
 template <typename T>
