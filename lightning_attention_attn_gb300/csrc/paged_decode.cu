@@ -23,10 +23,10 @@
 // of shared-memory stages (cp.async, 16 bytes a lane) with its own running
 // maximum, so the main loop has no block-wide barrier; the warps' results are
 // joined once per piece.
+#include <atomic>
+
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
-
-#include <math_constants.h>
 
 #include "la_internal.h"
 #include "sm100_ptx.cuh"
@@ -34,13 +34,11 @@
 namespace la {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kGroup = 16;              // tokens of one warp step
-constexpr int kTile = kWarps * kGroup;  // tokens of one tile of the work split
-constexpr int kOverhead = 3;            // tiles that starting a unit costs
-constexpr int kStages = 3;
+constexpr int kTile = 64;     // tokens of one tile of the work split
+constexpr int kOverhead = 3;  // tiles that starting a unit costs
+constexpr int kStages = 3;    // of a warp's ring: two in flight, one read
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kInf = __builtin_huge_valf();
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
     // an invalid row is filled with zeros, nothing is read
@@ -181,19 +179,83 @@ __device__ __forceinline__ void write_empty(const PagedDecodeArgs &a) {
             static_cast<T *>(a.out)[(size_t)b * row + i] = T(0.f);
         if (a.lse)
             for (int i = threadIdx.x; i < a.num_heads; i += blockDim.x)
-                a.lse[(size_t)b * a.num_heads + i] = -CUDART_INF_F;
+                a.lse[(size_t)b * a.num_heads + i] = -kInf;
     }
 }
 
-// Where piece `first` (of a unit that CTA c does not hold whole) of CTA c
-// lives in the workspace: rows of kMaxGroup heads x D sums, then maxima and
-// exponential sums.
+// Where piece `first` (of a unit that CTA c does not hold whole) of CTA c lives in
+// the workspace: sums of `rows` heads x D, then their maxima and exponential
+// sums.
 template <int D>
 __device__ __forceinline__ float *piece_at(const PagedDecodeArgs &a, int c, bool first, int rows) {
     return a.workspace + ((size_t)c * 2 + (first ? 0 : 1)) * rows * (D + 2);
 }
 
-// --------------------------------------------------------- bf16 main kernel
+// Four columns of one head's softmax in the making: maximum, exponential sum,
+// unnormalised values.
+struct Partial {
+    float m, sum;
+    float4 acc;
+
+    __device__ Partial() : m(-kInf), sum(0.f), acc(make_float4(0.f, 0.f, 0.f, 0.f)) {}
+
+    // Adds N others: their maxima and sums in ms, values in x.
+    template <int N>
+    __device__ __forceinline__ void add(const float2 (&ms)[N], const float4 (&x)[N]) {
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < N; ++i) top = fmaxf(top, ms[i].x);
+        const float base = top == -kInf ? 0.f : top;
+        const float k = ex2(m - base);
+        m = top;
+        sum *= k;
+        acc.x *= k, acc.y *= k, acc.z *= k, acc.w *= k;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float e = ex2(ms[i].x - base);
+            sum = fmaf(ms[i].y, e, sum);
+            acc.x = fmaf(x[i].x, e, acc.x);
+            acc.y = fmaf(x[i].y, e, acc.y);
+            acc.z = fmaf(x[i].z, e, acc.z);
+            acc.w = fmaf(x[i].w, e, acc.w);
+        }
+    }
+    // Writes columns d .. d + 3 of the output's row (and its lse).
+    template <typename T>
+    __device__ __forceinline__ void write(const PagedDecodeArgs &a, size_t row, int d) const {
+        const float r = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays NaN
+        T *o = static_cast<T *>(a.out) + row * a.head_dim + d;
+        if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<uint2 *>(o) = make_uint2(pack2(acc.x * r, acc.y * r), pack2(acc.z * r, acc.w * r));
+        else
+            *reinterpret_cast<float4 *>(o) = make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r);
+        if (a.lse && d == 0)
+            a.lse[row] = sum != 0.f ? (m + log2f(sum)) * (1.f / kLog2e) : -kInf;
+    }
+};
+
+// What a core leaves in shared memory, and its sum over the warps.
+template <typename Core>
+__device__ __forceinline__ Partial warps_sum(const unsigned char *smem, int h, int d) {
+    const float *ow = reinterpret_cast<const float *>(smem);
+    const float2 *ml = reinterpret_cast<const float2 *>(ow + Core::W * Core::ROWS * Core::D);
+    float2 ms[Core::W];
+    float4 x[Core::W];
+#pragma unroll
+    for (int w = 0; w < Core::W; ++w) {
+        ms[w] = ml[w * Core::ROWS + h];
+        x[w] = *reinterpret_cast<const float4 *>(ow + (w * Core::ROWS + h) * Core::D + d);
+    }
+    Partial p;
+    p.add<Core::W>(ms, x);
+    return p;
+}
+
+// --------------------------------------------------------------- bf16 core
+// A core streams tokens [t0, t1) of one unit through the block and leaves, per
+// warp and head, the sums [W][ROWS][D] and (maximum, exponential sum) [W][ROWS] in shared
+// memory (every warp has written when the block next synchronises).
+//
 // Heads of the query in the columns of the products (N = 8, NT such tiles):
 //     S^T [16 tokens x 8] = K [16 x D] Q^T,   O^T [D x 8] += V^T [D x 16] P^T
 // K and V are the A operands straight from shared memory (V transposed by
@@ -201,70 +263,35 @@ __device__ __forceinline__ float *piece_at(const PagedDecodeArgs &a, int c, bool
 // row of an MMA is padding when G is 8 (16).  P^T is S^T's accumulator
 // rounded to bf16 with the remainder as a second bf16 operand (P = hi + lo,
 // 2^-17 relative): the tensor pipe is idle most of the time and the second
-// product keeps the result at fp32 accuracy.
-template <int D, int NT>
+// product keeps the result at fp32 accuracy.  fp32 queries are split alike.
+// mma.sync rather than tcgen05: with 8 or 16 columns the products take a few percent
+// of the tensor pipe, and accumulators in registers feed the softmax without a
+// trip through tensor memory.
+// Four warps of a 16-token, 8 KB stage (D = 128) or eight of 4 KB (D = 64): two CTAs
+// an SM either way, 128 KB in flight.
+template <int D_, int NT, bool QF32>
 struct Bf16Core {
+    using T = __nv_bfloat16;
+    static constexpr int D = D_, ROWS = 8 * NT, W = D == 128 ? 4 : 8, kThreads = 32 * W;
+    static constexpr int kGroup = 16;               // tokens of one warp step
     static constexpr int kRow = D * 2;              // bytes of a token row
     static constexpr int kMat = kGroup * kRow;      // bytes of K (V) of a stage
     static constexpr int kStageBytes = 2 * kMat;
-    static constexpr int kSmem = kWarps * kStages * kStageBytes;
-};
+    static constexpr int kSmem = W * kStages * kStageBytes;
 
-template <int D, int NT, bool QF32>
-__global__ void __launch_bounds__(kThreads)
-paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
-    using C = Bf16Core<D, NT>;
-    constexpr int KS = D / 16;   // k steps of S, row tiles of O^T
-    constexpr int CH = D / 8;    // 16-byte chunks of a row
-    constexpr int RPI = 32 / CH; // rows one warp-wide copy covers
-    constexpr int kRows = 8 * NT;
-    constexpr int kAhead = NT == 1 ? 4 : 2;  // fragments loaded ahead (registers)
-
-    extern __shared__ __align__(128) unsigned char smem[];
-
-    // launched as a dependent launch: the lengths, the table and the cache
-    // may have been written by the kernel before
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int g = lane >> 2, c2 = (lane & 3) * 2;
-    const int units = a.num_kv_heads * a.head_groups;
-
-    write_empty<__nv_bfloat16>(a);
-    Place at;
-    if (!find_place<kThreads>(a, units, blockIdx.x, at)) return;
-    long long w0 = at.w;
-    const long long w1 = min(at.all, w0 + at.chunk);
-    int b = at.b;
-
-    const uint32_t ring = ptx::smem_u32(smem) + warp * kStages * C::kStageBytes;
-    const int crow = lane / CH, cch = lane % CH;
-    // ldmatrix row addresses: K as rows, V transposed
-    const int krow = lane & 15, kchunk = lane >> 4;
-    const int vrow = (lane & 7) + ((lane >> 4) << 3), vchunk = (lane >> 3) & 1;
-
-    bool first = true;
-    long long unit0 = at.unit0;  // first tile of request b
-    for (; w0 < w1; ) {
-        if (b >= a.batch) return;
-        const int len = request_len(a, b);
-        const int tiles = (len + kTile - 1) / kTile, cost = unit_cost(len);
-        if (w0 >= unit0 + (long long)cost * units) {  // next request (empty ones pass)
-            unit0 += (long long)cost * units;
-            ++b;
-            continue;
-        }
-        const int unit = tiles_div(w0 - unit0, cost);
-        const int at0 = (int)(w0 - unit0 - (long long)unit * cost);
-        const int at1 = (int)min((long long)cost, at0 + (w1 - w0));
-        const int tile0 = max(at0 - kOverhead, 0), tile1 = at1 - kOverhead;
-        w0 += at1 - at0;
-        if (tile1 <= 0) continue;  // only overhead: the next CTA starts the unit
-        const int kvh = unit / a.head_groups, hg = unit % a.head_groups;
-        const int head0 = kvh * a.group + hg * kRows;
-        const int heads = min(kRows, a.group - hg * kRows);
-        const int t0 = tile0 * kTile, t1 = min(len, tile1 * kTile);
+    static __device__ __forceinline__ void stream(const PagedDecodeArgs &a, unsigned char *smem, int b,
+                                                  int kvh, int head0, int heads, int t0, int t1) {
+        constexpr int KS = D / 16;   // k steps of S, row tiles of O^T
+        constexpr int CH = D / 8;    // 16-byte chunks of a row
+        constexpr int RPI = 32 / CH; // rows one warp-wide copy covers
+        constexpr int kAhead = NT == 1 ? 4 : 2;  // fragments loaded ahead (registers)
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int g = lane >> 2, c2 = (lane & 3) * 2;
+        const uint32_t ring = ptx::smem_u32(smem) + warp * kStages * kStageBytes;
+        const int crow = lane / CH, cch = lane % CH;
+        // ldmatrix row addresses: K as rows, V transposed
+        const int krow = lane & 15, kchunk = lane >> 4;
+        const int vrow = (lane & 7) + ((lane >> 4) << 3), vchunk = (lane >> 3) & 1;
 
         // queries as B operands, scaled after the product
         uint32_t qb[NT][KS][2], ql[QF32 ? NT : 1][QF32 ? KS : 1][2];
@@ -300,7 +327,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
         float mx[NT][2], l[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            mx[nt][0] = mx[nt][1] = -CUDART_INF_F;
+            mx[nt][0] = mx[nt][1] = -kInf;
             l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
@@ -309,7 +336,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
 
         const int32_t *pages = a.block_table + (size_t)b * a.table_stride;
         const int groups = (t1 - t0 + kGroup - 1) / kGroup;  // of the whole piece
-        // This warp's groups: warp, warp + kWarps, ...; lane r < 16 finds row
+        // This warp's groups: warp, warp + W, ...; lane r < 16 finds row
         // r of a group: its offset inside a key (value) head's page, or -1.
         auto locate = [&](int grp, int &page, int &row) {
             const int t = t0 + grp * kGroup + (lane & 15);
@@ -325,7 +352,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
         // Issues the copies of one group; returns the mask of its present rows.
         auto issue = [&](int stage, int page, int row) -> uint32_t {
             const uint32_t have = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
-            const uint32_t dk = ring + stage * C::kStageBytes, dv = dk + C::kMat;
+            const uint32_t dk = ring + stage * kStageBytes, dv = dk + kMat;
 #pragma unroll
             for (int i = 0; i < kGroup / RPI; ++i) {
                 const int r = i * RPI + crow;
@@ -334,7 +361,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
                 const bool ok = pg >= 0;
                 const size_t in = ((size_t)kvh * a.page_size + rw) * D + cch * 8;
                 const size_t p = ok ? pg : 0;
-                const uint32_t off = r * C::kRow + ((cch ^ (r & 7)) << 4);
+                const uint32_t off = r * kRow + ((cch ^ (r & 7)) << 4);
                 cp_async16(dk + off, static_cast<const __nv_bfloat16 *>(a.k) + p * a.k_page_stride + in, ok);
                 cp_async16(dv + off, static_cast<const __nv_bfloat16 *>(a.v) + p * a.v_page_stride + in, ok);
             }
@@ -344,7 +371,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
         uint32_t have[kStages];
 #pragma unroll
         for (int s = 0; s < kStages - 1; ++s) {
-            const int grp = warp + s * kWarps;
+            const int grp = warp + s * W;
             have[s] = 0;
             if (grp < groups) {
                 int page, row;
@@ -354,23 +381,23 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
             cp_commit();
         }
         int npage, nrow;  // of the group that is issued next
-        locate(warp + (kStages - 1) * kWarps, npage, nrow);
+        locate(warp + (kStages - 1) * W, npage, nrow);
 
         int stage = 0;
-        for (int grp = warp; grp < groups; grp += kWarps) {
+        for (int grp = warp; grp < groups; grp += W) {
             // refill the stage that was read last (its readers are this warp)
             {
-                const int nx = grp + (kStages - 1) * kWarps;
+                const int nx = grp + (kStages - 1) * W;
                 const int ns = stage == 0 ? kStages - 1 : stage - 1;
                 __syncwarp();
                 have[kStages - 1] = 0;
                 if (nx < groups) have[kStages - 1] = issue(ns, npage, nrow);
                 cp_commit();
-                locate(nx + kWarps, npage, nrow);
+                locate(nx + W, npage, nrow);
             }
             cp_wait<kStages - 1>();
             __syncwarp();
-            const uint32_t kb = ring + stage * C::kStageBytes, vb = kb + C::kMat;
+            const uint32_t kb = ring + stage * kStageBytes, vb = kb + kMat;
 
             // Few warps share an SM, so a warp's own latencies count: the
             // fragments are loaded ahead of their products, and the scores are summed in
@@ -388,7 +415,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
                 uint32_t ka[kAhead][4];
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i)
-                    ldsm4(ka[i], kb + krow * C::kRow +
+                    ldsm4(ka[i], kb + krow * kRow +
                                      (((2 * (k0 + i) + kchunk) ^ (krow & 7)) << 4));
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i)
@@ -403,7 +430,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
             uint32_t va[kAhead][4];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i)
-                ldsm4_t(va[i], vb + vrow * C::kRow + (((2 * i + vchunk) ^ (vrow & 7)) << 4));
+                ldsm4_t(va[i], vb + vrow * kRow + (((2 * i + vchunk) ^ (vrow & 7)) << 4));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -417,8 +444,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {  // this lane's two heads
-                    s[nt][j] = v0 ? s[nt][j] * a.scale_log2 : -CUDART_INF_F;
-                    s[nt][2 + j] = v1 ? s[nt][2 + j] * a.scale_log2 : -CUDART_INF_F;
+                    s[nt][j] = v0 ? s[nt][j] * a.scale_log2 : -kInf;
+                    s[nt][2 + j] = v1 ? s[nt][2 + j] * a.scale_log2 : -kInf;
                 }
                 float t0m = fmaxf(s[nt][0], s[nt][2]), t1m = fmaxf(s[nt][1], s[nt][3]);
 #pragma unroll
@@ -429,8 +456,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
                 // a maximum that rose rescales what was summed
                 if (__any_sync(0xffffffffu, t0m > mx[nt][0] || t1m > mx[nt][1])) {
                     const float n0 = fmaxf(mx[nt][0], t0m), n1 = fmaxf(mx[nt][1], t1m);
-                    const float f0 = n0 == -CUDART_INF_F ? 1.f : ex2(mx[nt][0] - n0);
-                    const float f1 = n1 == -CUDART_INF_F ? 1.f : ex2(mx[nt][1] - n1);
+                    const float f0 = n0 == -kInf ? 1.f : ex2(mx[nt][0] - n0);
+                    const float f1 = n1 == -kInf ? 1.f : ex2(mx[nt][1] - n1);
                     mx[nt][0] = n0;
                     mx[nt][1] = n1;
                     l[nt][0] *= f0;
@@ -443,8 +470,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
                         o[nt][ks][3] *= f1;
                     }
                 }
-                const float b0 = mx[nt][0] == -CUDART_INF_F ? 0.f : mx[nt][0];
-                const float b1 = mx[nt][1] == -CUDART_INF_F ? 0.f : mx[nt][1];
+                const float b0 = mx[nt][0] == -kInf ? 0.f : mx[nt][0];
+                const float b1 = mx[nt][1] == -kInf ? 0.f : mx[nt][1];
                 const float p0 = ex2(s[nt][0] - b0), p1 = ex2(s[nt][1] - b1);
                 const float p2 = ex2(s[nt][2] - b0), p3 = ex2(s[nt][3] - b1);
                 l[nt][0] += p0 + p2;
@@ -460,7 +487,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
                 if (k0 > 0) {
 #pragma unroll
                     for (int i = 0; i < kAhead; ++i)
-                        ldsm4_t(va[i], vb + vrow * C::kRow +
+                        ldsm4_t(va[i], vb + vrow * kRow +
                                            (((2 * (k0 + i) + vchunk) ^ (vrow & 7)) << 4));
                 }
 #pragma unroll
@@ -478,7 +505,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
         }
         cp_wait<0>();
 
-        // ---- join the warps: each leaves maxima, sums and O^T in shared memory
+
+        // the warps' results
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -486,70 +514,29 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1)
                     l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], d);
-        float *ow = reinterpret_cast<float *>(smem);            // [warp][head][D]
-        float *ml = ow + kWarps * kRows * D;                    // [warp][head][2]
+        float *ow = reinterpret_cast<float *>(smem);
+        float2 *ml = reinterpret_cast<float2 *>(ow + W * ROWS * D);
         __syncthreads();  // every warp has read its stages
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             if (g == 0) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int h = nt * 8 + c2 + j;
-                    ml[(warp * kRows + h) * 2] = mx[nt][j];
-                    ml[(warp * kRows + h) * 2 + 1] = l[nt][j];
-                }
+                for (int j = 0; j < 2; ++j)
+                    ml[warp * ROWS + nt * 8 + c2 + j] = make_float2(mx[nt][j], l[nt][j]);
             }
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    ow[(warp * kRows + nt * 8 + c2 + (i & 1)) * D + ks * 16 + g + (i >> 1) * 8] =
+                    ow[(warp * ROWS + nt * 8 + c2 + (i & 1)) * D + ks * 16 + g + (i >> 1) * 8] =
                         o[nt][ks][i];
         }
-        __syncthreads();
-        const bool whole = tile0 == 0 && tile1 == tiles;
-        float *ws = whole ? nullptr : piece_at<D>(a, blockIdx.x, first, kRows);
-        for (int i = threadIdx.x; i < heads * (D / 4); i += kThreads) {
-            const int h = i / (D / 4), d = (i % (D / 4)) * 4;
-            float m = -CUDART_INF_F;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[(w * kRows + h) * 2]);
-            const float mb = m == -CUDART_INF_F ? 0.f : m;
-            float sum = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = ex2(ml[(w * kRows + h) * 2] - mb);
-                const float4 x = *reinterpret_cast<const float4 *>(ow + (w * kRows + h) * D + d);
-                sum += f * ml[(w * kRows + h) * 2 + 1];
-                acc.x += f * x.x;
-                acc.y += f * x.y;
-                acc.z += f * x.z;
-                acc.w += f * x.w;
-            }
-            if (whole) {
-                const float r = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays NaN
-                const size_t row = (size_t)b * a.num_heads + head0 + h;
-                uint2 y = make_uint2(pack2(acc.x * r, acc.y * r), pack2(acc.z * r, acc.w * r));
-                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + d) = y;
-                if (a.lse && d == 0)
-                    a.lse[row] = sum != 0.f ? (m + log2f(sum)) * (1.f / kLog2e) : -CUDART_INF_F;
-            } else {
-                *reinterpret_cast<float4 *>(ws + h * D + d) = acc;
-                if (d == 0) {
-                    ws[kRows * D + 2 * h] = m;
-                    ws[kRows * D + 2 * h + 1] = sum;
-                }
-            }
-        }
-        __syncthreads();  // shared memory is the ring again
-        first = false;
     }
-}
+};
 
-// -------------------------------------------------------------- fp32 kernel
-// The same split and rings on the CUDA cores (fp32 products, as the library's
-// other fp32 paths).  ROWS (4, 8 or 16) query heads of a unit.
+// --------------------------------------------------------------- fp32 core
+// The CUDA cores (fp32 products, as the library's other fp32 paths).  ROWS (4, 8 or
+// 16) query heads of a unit.
 //   scores   LPT lanes share a token; each keeps DPL dimensions of all queries in
 //            registers, and a transposing reduction over the LPT lanes leaves one
 //            head's score in each
@@ -558,78 +545,40 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
 //   values   a lane owns four columns of all heads (of every other token where 16
 //            lanes cover a row)
 // A group is 16 tokens of 64 dimensions or 8 of 128: 8 KB a stage, as in bf16.
-template <int D, int ROWS>
+template <int D_, int ROWS_>
 struct F32Core {
-    static constexpr int kGrp = 1024 / D;             // tokens of a group
-    static constexpr int kDpl = ROWS == 16 ? 4 : 8;   // dimensions of a lane's scores
-    static constexpr int kLpt = D / kDpl;             // lanes of a token
-    static constexpr int kMat = kGrp * D;             // floats of K (V) of a stage
-    static constexpr int kScores = kWarps * kGrp * ROWS;
-    static constexpr size_t kSmem = sizeof(float) * (kScores + kWarps * kStages * 2 * kMat);
-};
+    using T = float;
+    static constexpr int D = D_, ROWS = ROWS_, W = 4, kThreads = 32 * W;
+    static constexpr int kGrp = 1024 / D;           // tokens of a group
+    static constexpr int DPL = ROWS == 16 ? 4 : 8;  // dimensions of a lane's scores
+    static constexpr int LPT = D / DPL;             // lanes of a token
+    static constexpr int kMat = kGrp * D;           // floats of K (V) of a stage
+    static constexpr int kScores = W * kGrp * ROWS;
+    static constexpr int kSmem = sizeof(float) * (kScores + W * kStages * 2 * kMat);
 
-template <int D, int ROWS>
-__global__ void __launch_bounds__(kThreads)
-paged_decode_f32_kernel(const __grid_constant__ PagedDecodeArgs a) {
-    using C = F32Core<D, ROWS>;
-    constexpr int kGrp = C::kGrp, DPL = C::kDpl, LPT = C::kLpt, kMat = C::kMat;
-    constexpr int TPP = 32 / LPT;    // tokens whose scores a pass computes
-    constexpr int TS = 32 / ROWS;    // tokens of a softmax step
-    constexpr int CH = D / 4;        // 16-byte chunks of a row
-    constexpr int RPI = 32 / CH;     // rows of a warp-wide copy, tokens of a value step
-
-    extern __shared__ __align__(128) unsigned char smem[];
-
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int units = a.num_kv_heads * a.head_groups;
-    write_empty<float>(a);
-    Place at;
-    if (!find_place<kThreads>(a, units, blockIdx.x, at)) return;
-    long long w0 = at.w;
-    const long long w1 = min(at.all, w0 + at.chunk);
-    int b = at.b;
-
-    float *base = reinterpret_cast<float *>(smem);
-    float *pw = base + warp * kGrp * ROWS;  // [kGrp][ROWS] of this warp
-    float *ring = base + C::kScores + warp * kStages * 2 * kMat;
-    const uint32_t ring_u = ptx::smem_u32(ring);
-    const int sub = lane % LPT, sh = lane % ROWS;
-    // the head whose score the reduction leaves in this lane
-    int my_head = 0;
-    {
-        int n = ROWS;
+    static __device__ __forceinline__ void stream(const PagedDecodeArgs &a, unsigned char *smem, int b,
+                                                  int kvh, int head0, int heads, int t0, int t1) {
+        constexpr int TPP = 32 / LPT;    // tokens whose scores a pass computes
+        constexpr int TS = 32 / ROWS;    // tokens of a softmax step
+        constexpr int CH = D / 4;        // 16-byte chunks of a row
+        constexpr int RPI = 32 / CH;     // rows of a warp-wide copy, tokens of a value step
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        float *base = reinterpret_cast<float *>(smem);
+        float *pw = base + warp * kGrp * ROWS;  // [kGrp][ROWS] of this warp
+        float *ring = base + kScores + warp * kStages * 2 * kMat;
+        const uint32_t ring_u = ptx::smem_u32(ring);
+        const int sub = lane % LPT, sh = lane % ROWS;
+        // the head whose score the reduction leaves in this lane
+        int my_head = 0;
+        {
+            int n = ROWS;
 #pragma unroll
-        for (int o = LPT / 2; o > 0; o >>= 1)
-            if (n > 1) {
-                n >>= 1;
-                if (lane & o) my_head += n;
-            }
-    }
-
-    bool first = true;
-    long long unit0 = at.unit0;
-    for (; w0 < w1; ) {
-        if (b >= a.batch) return;
-        const int len = request_len(a, b);
-        const int tiles = (len + kTile - 1) / kTile, cost = unit_cost(len);
-        if (w0 >= unit0 + (long long)cost * units) {  // next request (empty ones pass)
-            unit0 += (long long)cost * units;
-            ++b;
-            continue;
+            for (int o = LPT / 2; o > 0; o >>= 1)
+                if (n > 1) {
+                    n >>= 1;
+                    if (lane & o) my_head += n;
+                }
         }
-        const int unit = tiles_div(w0 - unit0, cost);
-        const int at0 = (int)(w0 - unit0 - (long long)unit * cost);
-        const int at1 = (int)min((long long)cost, at0 + (w1 - w0));
-        const int tile0 = max(at0 - kOverhead, 0), tile1 = at1 - kOverhead;
-        w0 += at1 - at0;
-        if (tile1 <= 0) continue;  // only overhead: the next CTA starts the unit
-        const int kvh = unit / a.head_groups, hg = unit % a.head_groups;
-        const int head0 = kvh * a.group + hg * ROWS;
-        const int heads = min(ROWS, a.group - hg * ROWS);
-        const int t0 = tile0 * kTile, t1 = min(len, tile1 * kTile);
 
         const int32_t *pages = a.block_table + (size_t)b * a.table_stride;
         const int groups = (t1 - t0 + kGrp - 1) / kGrp;
@@ -666,12 +615,12 @@ paged_decode_f32_kernel(const __grid_constant__ PagedDecodeArgs a) {
 #pragma unroll
         for (int s = 0; s < kStages - 1; ++s) {
             int page, row;
-            locate(warp + s * kWarps, page, row);
+            locate(warp + s * W, page, row);
             have[s] = issue(s, page, row);
             cp_commit();
         }
         int npage, nrow;  // of the group that is issued next
-        locate(warp + (kStages - 1) * kWarps, npage, nrow);
+        locate(warp + (kStages - 1) * W, npage, nrow);
 
         // chunk sub + i LPT of every query row
         float2 q[ROWS][DPL / 2];
@@ -689,18 +638,18 @@ paged_decode_f32_kernel(const __grid_constant__ PagedDecodeArgs a) {
                 q[h][2 * i + 1] = make_float2(x.z, x.w);
             }
         float2 o[ROWS][2];
-        float mx = -CUDART_INF_F, l = 0.f;  // of head sh (l: this lane's tokens)
+        float mx = -kInf, l = 0.f;  // of head sh (l: this lane's tokens)
 #pragma unroll
         for (int h = 0; h < ROWS; ++h) o[h][0] = o[h][1] = make_float2(0.f, 0.f);
 
         int stage = 0;
-        for (int grp = warp; grp < groups; grp += kWarps) {
+        for (int grp = warp; grp < groups; grp += W) {
             {
                 const int ns = stage == 0 ? kStages - 1 : stage - 1;
                 __syncwarp();
                 have[kStages - 1] = issue(ns, npage, nrow);  // copies nothing past the end
                 cp_commit();
-                locate(grp + kStages * kWarps, npage, nrow);
+                locate(grp + kStages * W, npage, nrow);
             }
             cp_wait<kStages - 1>();
             __syncwarp();
@@ -744,18 +693,18 @@ paged_decode_f32_kernel(const __grid_constant__ PagedDecodeArgs a) {
             }
             __syncwarp();
             float p[kGrp / TS];
-            float top = -CUDART_INF_F;
+            float top = -kInf;
 #pragma unroll
             for (int i = 0; i < kGrp / TS; ++i) {
                 const int t = i * TS + lane / ROWS;
-                p[i] = (have[0] >> t) & 1 ? pw[t * ROWS + sh] * a.scale_log2 : -CUDART_INF_F;
+                p[i] = (have[0] >> t) & 1 ? pw[t * ROWS + sh] * a.scale_log2 : -kInf;
                 top = fmaxf(top, p[i]);
             }
 #pragma unroll
             for (int d = ROWS; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             if (__any_sync(0xffffffffu, top > mx)) {
                 const float nm = fmaxf(mx, top);
-                const float f = nm == -CUDART_INF_F ? 1.f : ex2(mx - nm);
+                const float f = nm == -kInf ? 1.f : ex2(mx - nm);
                 mx = nm;
                 l *= f;
 #pragma unroll
@@ -765,7 +714,7 @@ paged_decode_f32_kernel(const __grid_constant__ PagedDecodeArgs a) {
                     o[h][1] = ptx::f2_mul(o[h][1], make_float2(fh, fh));
                 }
             }
-            const float mb = mx == -CUDART_INF_F ? 0.f : mx;
+            const float mb = mx == -kInf ? 0.f : mx;
 #pragma unroll
             for (int i = 0; i < kGrp / TS; ++i) {
                 p[i] = ex2(p[i] - mb);
@@ -797,13 +746,12 @@ paged_decode_f32_kernel(const __grid_constant__ PagedDecodeArgs a) {
 #pragma unroll
         for (int d = ROWS; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
 
-        float *ow = base + C::kScores;  // [warp][head][D], over the rings
-        float *ml = base;               // [warp][head][2], over the scores
-        __syncthreads();
-        if (lane < ROWS) {
-            ml[(warp * ROWS + lane) * 2] = mx;
-            ml[(warp * ROWS + lane) * 2 + 1] = l;
-        }
+
+        // the warps' results
+        float *ow = base;
+        float2 *ml = reinterpret_cast<float2 *>(ow + W * ROWS * D);
+        __syncthreads();  // every warp has read its stages and scores
+        if (lane < ROWS) ml[warp * ROWS + lane] = make_float2(mx, l);
 #pragma unroll
         for (int h = 0; h < ROWS; ++h) {
             float4 x = make_float4(o[h][0].x, o[h][0].y, o[h][1].x, o[h][1].y);
@@ -813,48 +761,149 @@ paged_decode_f32_kernel(const __grid_constant__ PagedDecodeArgs a) {
                 x.z += __shfl_xor_sync(0xffffffffu, x.z, 16);
                 x.w += __shfl_xor_sync(0xffffffffu, x.w, 16);
             }
-            if (lane < CH)
-                *reinterpret_cast<float4 *>(ow + (warp * ROWS + h) * D + lane * 4) = x;
+            if (lane < CH) *reinterpret_cast<float4 *>(ow + (warp * ROWS + h) * D + lane * 4) = x;
         }
+    }
+};
+
+// ------------------------------------------------------------ split kernel
+template <typename Core>
+__global__ void __launch_bounds__(Core::kThreads, 2)
+paged_split_kernel(const __grid_constant__ PagedDecodeArgs a) {
+    constexpr int D = Core::D, ROWS = Core::ROWS;
+    extern __shared__ __align__(128) unsigned char smem[];
+
+    // launched as a dependent launch: the lengths, the table and the cache
+    // may have been written by the kernel before
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const int units = a.num_kv_heads * a.head_groups;
+    write_empty<typename Core::T>(a);
+    Place at;
+    if (!find_place<Core::kThreads>(a, units, blockIdx.x, at)) return;
+    long long w0 = at.w, unit0 = at.unit0;
+    const long long w1 = min(at.all, w0 + at.chunk);
+    int b = at.b;
+    bool first = true;
+    while (w0 < w1 && b < a.batch) {
+        const int len = request_len(a, b);
+        const int tiles = (len + kTile - 1) / kTile, cost = unit_cost(len);
+        if (w0 >= unit0 + (long long)cost * units) {  // next request (empty ones pass)
+            unit0 += (long long)cost * units;
+            ++b;
+            continue;
+        }
+        const int unit = tiles_div(w0 - unit0, cost);
+        const int at0 = (int)(w0 - unit0 - (long long)unit * cost);
+        const int at1 = (int)min((long long)cost, at0 + (w1 - w0));
+        const int tile0 = max(at0 - kOverhead, 0), tile1 = at1 - kOverhead;
+        w0 += at1 - at0;
+        if (tile1 <= 0) continue;  // only overhead: the next CTA starts the unit
+        const int kvh = unit / a.head_groups, hg = unit % a.head_groups;
+        const int head0 = kvh * a.group + hg * ROWS;
+        const int heads = min(ROWS, a.group - hg * ROWS);
+
+        Core::stream(a, smem, b, kvh, head0, heads, tile0 * kTile, min(len, tile1 * kTile));
         __syncthreads();
         const bool whole = tile0 == 0 && tile1 == tiles;
-        float *ws = whole ? nullptr : piece_at<D>(a, blockIdx.x, first, ROWS);
-        for (int i = threadIdx.x; i < heads * CH; i += kThreads) {
-            const int h = i / CH, d = (i % CH) * 4;
-            float m = -CUDART_INF_F;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[(w * ROWS + h) * 2]);
-            const float mb = m == -CUDART_INF_F ? 0.f : m;
-            float sum = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = ex2(ml[(w * ROWS + h) * 2] - mb);
-                const float4 x = *reinterpret_cast<const float4 *>(ow + (w * ROWS + h) * D + d);
-                sum += f * ml[(w * ROWS + h) * 2 + 1];
-                acc.x += f * x.x;
-                acc.y += f * x.y;
-                acc.z += f * x.z;
-                acc.w += f * x.w;
-            }
+        float *ws = piece_at<D>(a, blockIdx.x, first, ROWS);
+        for (int i = threadIdx.x; i < heads * (D / 4); i += Core::kThreads) {
+            const int h = i / (D / 4), d = (i % (D / 4)) * 4;
+            const Partial p = warps_sum<Core>(smem, h, d);
             if (whole) {
-                const size_t row = (size_t)b * a.num_heads + head0 + h;
-                const float r = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays NaN
-                *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * D + d) =
-                    make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r);
-                if (a.lse && d == 0)
-                    a.lse[row] = sum != 0.f ? (m + log2f(sum)) * (1.f / kLog2e) : -CUDART_INF_F;
+                p.write<typename Core::T>(a, (size_t)b * a.num_heads + head0 + h, d);
             } else {
-                *reinterpret_cast<float4 *>(ws + h * D + d) = acc;
-                if (d == 0) {
-                    ws[ROWS * D + 2 * h] = m;
-                    ws[ROWS * D + 2 * h + 1] = sum;
-                }
+                *reinterpret_cast<float4 *>(ws + h * D + d) = p.acc;
+                if (d == 0) *reinterpret_cast<float2 *>(ws + ROWS * D + 2 * h) = make_float2(p.m, p.sum);
             }
         }
-        __syncthreads();
+        __syncthreads();  // shared memory is the ring again
         first = false;
     }
+}
+
+// ---------------------------------------------------------- cluster kernel
+// Short tables: one cluster a unit, each CTA a run of its tiles, joined through
+// the cluster's shared memory: one launch, no workspace.
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float4 peer_load4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 peer_load2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                 : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+template <typename Core, int S>
+__global__ void __launch_bounds__(Core::kThreads, 2)
+paged_cluster_kernel(const __grid_constant__ PagedDecodeArgs a) {
+    constexpr int D = Core::D, ROWS = Core::ROWS;
+    extern __shared__ __align__(128) unsigned char smem[];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // a one-dimensional grid of one-dimensional clusters: the rank in the
+    // cluster is the block's index modulo its size
+    const int rank = blockIdx.x % S, units = a.num_kv_heads * a.head_groups;
+    const int b = blockIdx.x / S / units, unit = blockIdx.x / S % units;
+    const int kvh = unit / a.head_groups, hg = unit % a.head_groups;
+    const int head0 = kvh * a.group + hg * ROWS;
+    const int heads = min(ROWS, a.group - hg * ROWS);
+    const int len = request_len(a, b);
+    const int share = ((len + kTile - 1) / kTile + S - 1) / S * kTile;  // tokens of a CTA
+    const int t0 = rank * share, t1 = min(len, t0 + share);
+    const bool any = t0 < t1;
+    if (any) Core::stream(a, smem, b, kvh, head0, heads, t0, t1);
+    __syncthreads();
+    const size_t row0 = (size_t)b * a.num_heads + head0;
+    if (S == 1) {
+        for (int i = threadIdx.x; i < heads * (D / 4); i += Core::kThreads) {
+            const int h = i / (D / 4), d = (i % (D / 4)) * 4;
+            const Partial p = any ? warps_sum<Core>(smem, h, d) : Partial();
+            p.write<typename Core::T>(a, row0 + h, d);
+        }
+        return;
+    }
+    // this CTA's sums, behind the warps'
+    float *acc = reinterpret_cast<float *>(smem) + Core::W * ROWS * (D + 2);
+    static_assert(sizeof(float) * (Core::W + 1) * ROWS * (D + 2) <= Core::kSmem, "shared memory");
+    float2 *ms = reinterpret_cast<float2 *>(acc + ROWS * D);
+    for (int i = threadIdx.x; i < heads * (D / 4); i += Core::kThreads) {
+        const int h = i / (D / 4), d = (i % (D / 4)) * 4;
+        const Partial p = any ? warps_sum<Core>(smem, h, d) : Partial();
+        *reinterpret_cast<float4 *>(acc + h * D + d) = p.acc;
+        if (d == 0) ms[h] = make_float2(p.m, p.sum);
+    }
+    cluster_barrier();
+    const uint32_t acc_u = ptx::smem_u32(acc), ms_u = ptx::smem_u32(ms);
+    for (int i = rank * Core::kThreads + threadIdx.x; i < heads * (D / 4); i += S * Core::kThreads) {
+        const int h = i / (D / 4), d = (i % (D / 4)) * 4;
+        float2 m[S];
+        float4 x[S];
+#pragma unroll
+        for (int r = 0; r < S; ++r) {
+            m[r] = peer_load2(peer_smem(ms_u + h * 8, r));
+            x[r] = peer_load4(peer_smem(acc_u + (h * D + d) * 4, r));
+        }
+        Partial p;
+        p.add<S>(m, x);
+        p.write<typename Core::T>(a, row0 + h, d);
+    }
+    cluster_barrier();  // no CTA leaves while its shared memory is read
 }
 
 // -------------------------------------------------------------------- join
@@ -904,8 +953,7 @@ paged_join_kernel(const __grid_constant__ PagedDecodeArgs a) {
     const int slices = kJoin / cols;
     const int slice = threadIdx.x / cols, col = threadIdx.x - slice * cols;
     const int h = mine + (col / (D / 4)) * cuts, d = (col % (D / 4)) * 4;
-    float m = -CUDART_INF_F, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    Partial p;
     if (slice < slices) {
         // the first piece ends CTA c0's range (and is all of it if it began
         // there), the others begin theirs
@@ -918,93 +966,81 @@ paged_join_kernel(const __grid_constant__ PagedDecodeArgs a) {
             for (int f = 0; f < kFlight; ++f) {
                 const int i = i0 + f * slices;
                 x[f] = make_float4(0.f, 0.f, 0.f, 0.f);
-                ms[f] = make_float2(-CUDART_INF_F, 0.f);
+                ms[f] = make_float2(-kInf, 0.f);
                 if (i < pieces) {
-                    const float *p = piece_at<D>(a, c0 + i, i > 0 || whole, ROWS);
-                    x[f] = __ldcg(reinterpret_cast<const float4 *>(p + h * D + d));
-                    ms[f] = __ldcg(reinterpret_cast<const float2 *>(p + ROWS * D + 2 * h));
+                    const float *at_i = piece_at<D>(a, c0 + i, i > 0 || whole, ROWS);
+                    x[f] = __ldcg(reinterpret_cast<const float4 *>(at_i + h * D + d));
+                    ms[f] = __ldcg(reinterpret_cast<const float2 *>(at_i + ROWS * D + 2 * h));
                 }
             }
-            float top = m;
-#pragma unroll
-            for (int f = 0; f < kFlight; ++f) top = fmaxf(top, ms[f].x);
-            const float base = top == -CUDART_INF_F ? 0.f : top;
-            const float k = ex2(m - base);
-            m = top;
-            sum *= k;
-            acc.x *= k, acc.y *= k, acc.z *= k, acc.w *= k;
-#pragma unroll
-            for (int f = 0; f < kFlight; ++f) {
-                const float e = ex2(ms[f].x - base);
-                sum = fmaf(ms[f].y, e, sum);
-                acc.x = fmaf(x[f].x, e, acc.x);
-                acc.y = fmaf(x[f].y, e, acc.y);
-                acc.z = fmaf(x[f].z, e, acc.z);
-                acc.w = fmaf(x[f].w, e, acc.w);
-            }
+            p.add<kFlight>(ms, x);
         }
     }
-    part[threadIdx.x] = acc;
-    stat[threadIdx.x] = make_float2(m, sum);
+    part[threadIdx.x] = p.acc;
+    stat[threadIdx.x] = make_float2(p.m, p.sum);
     __syncthreads();
     if (slice > 0) return;
-    float top = m;
-    for (int i = 1; i < slices; ++i) top = fmaxf(top, stat[threadIdx.x + i * cols].x);
-    const float base = top == -CUDART_INF_F ? 0.f : top;
-    const float k = ex2(m - base);
-    sum *= k;
-    acc.x *= k, acc.y *= k, acc.z *= k, acc.w *= k;
     for (int i = 1; i < slices; ++i) {
-        const float4 x = part[threadIdx.x + i * cols];
-        const float2 ms = stat[threadIdx.x + i * cols];
-        const float e = ex2(ms.x - base);
-        sum = fmaf(ms.y, e, sum);
-        acc.x = fmaf(x.x, e, acc.x);
-        acc.y = fmaf(x.y, e, acc.y);
-        acc.z = fmaf(x.z, e, acc.z);
-        acc.w = fmaf(x.w, e, acc.w);
+        const float2 ms[1] = {stat[threadIdx.x + i * cols]};
+        const float4 x[1] = {part[threadIdx.x + i * cols]};
+        p.add<1>(ms, x);
     }
-    const float r = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays NaN
-    const size_t row = (size_t)at.b * a.num_heads + head0 + h;
-    T *o = static_cast<T *>(a.out) + row * D + d;
-    if constexpr (sizeof(T) == 2)
-        *reinterpret_cast<uint2 *>(o) = make_uint2(pack2(acc.x * r, acc.y * r), pack2(acc.z * r, acc.w * r));
-    else
-        *reinterpret_cast<float4 *>(o) = make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r);
-    if (a.lse && d == 0)
-        a.lse[row] = sum != 0.f ? (top + log2f(sum)) * (1.f / kLog2e) : -CUDART_INF_F;
+    p.write<T>(a, (size_t)at.b * a.num_heads + head0 + h, d);
 }
 
-// Opts `kern` into `smem` bytes of dynamic shared memory on every device it
-// is launched on (the call is cheap and idempotent).
-template <typename K> cudaError_t allow_smem(K kern, size_t smem) {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+// Opts a kernel into its dynamic shared memory, once per device (concurrent first
+// calls may both do it, which is harmless).
+template <auto Kern> cudaError_t allow_smem(int smem) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
+    return e;
 }
 
-template <typename T, int D, int ROWS>
-cudaError_t join(const PagedDecodeArgs &a) {
-    return launch_dependent(paged_join_kernel<T, D, ROWS>, kPagedCtas - 1, kJoin, 0, a.stream, a);
-}
-
-template <int D, int NT, bool QF32>
-cudaError_t launch_bf16(PagedDecodeArgs a) {
-    a.head_groups = (a.group + 8 * NT - 1) / (8 * NT);
-    auto kern = paged_decode_kernel<D, NT, QF32>;
-    constexpr size_t kSmem = Bf16Core<D, NT>::kSmem;
-    cudaError_t e = allow_smem(kern, kSmem);
-    if (e == cudaSuccess) e = launch_dependent(kern, kPagedCtas, kThreads, kSmem, a.stream, a);
-    if (e == cudaSuccess) e = join<__nv_bfloat16, D, 8 * NT>(a);
+template <typename Core, int S> cudaError_t launch_cluster(const PagedDecodeArgs &a) {
+    constexpr auto kern = paged_cluster_kernel<Core, S>;
+    cudaError_t e = allow_smem<kern>(Core::kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.batch * a.num_kv_heads * a.head_groups * S);
+    cfg.blockDim = dim3(Core::kThreads);
+    cfg.dynamicSmemBytes = Core::kSmem;
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = S;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, kern, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int D, int ROWS>
-cudaError_t launch_f32(PagedDecodeArgs a) {
-    a.head_groups = (a.group + ROWS - 1) / ROWS;
-    auto kern = paged_decode_f32_kernel<D, ROWS>;
-    constexpr size_t kSmem = F32Core<D, ROWS>::kSmem;
-    cudaError_t e = allow_smem(kern, kSmem);
-    if (e == cudaSuccess) e = launch_dependent(kern, kPagedCtas, kThreads, kSmem, a.stream, a);
-    if (e == cudaSuccess) e = join<float, D, ROWS>(a);
+template <typename Core> cudaError_t launch(PagedDecodeArgs a) {
+    a.head_groups = (a.group + Core::ROWS - 1) / Core::ROWS;
+    // What the table can hold bounds the lengths, which only the GPU knows.
+    // Up to kClusterTokens tokens a CTA, all units at once on the SMs: clusters.
+    const long units = (long)a.batch * a.num_kv_heads * a.head_groups;
+    constexpr int kClusterTokens = 2 * kTile;
+    const int need = (a.max_tokens + kClusterTokens - 1) / kClusterTokens;
+    if (need <= 1 && units <= kPagedCtas) return launch_cluster<Core, 1>(a);
+    if (need <= 2 && units * 2 <= kPagedCtas) return launch_cluster<Core, 2>(a);
+    if (need <= 4 && units * 4 <= kPagedCtas) return launch_cluster<Core, 4>(a);
+    if (need <= 8 && units * 8 <= kPagedCtas) return launch_cluster<Core, 8>(a);
+
+    constexpr auto kern = paged_split_kernel<Core>;
+    cudaError_t e = allow_smem<kern>(Core::kSmem);
+    if (e == cudaSuccess)
+        e = launch_dependent(kern, kPagedCtas, Core::kThreads, Core::kSmem, a.stream, a);
+    if (e == cudaSuccess)
+        e = launch_dependent(paged_join_kernel<typename Core::T, Core::D, Core::ROWS>, kPagedCtas - 1,
+                             kJoin, 0, a.stream, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -1013,10 +1049,10 @@ cudaError_t launch_f32(PagedDecodeArgs a) {
 template <int D>
 cudaError_t dispatch(const PagedDecodeArgs &a, bool bf16, bool q_f32) {
     if (!bf16)
-        return a.group <= 4 ? launch_f32<D, 4>(a) : a.group <= 8 ? launch_f32<D, 8>(a)
-                                                                 : launch_f32<D, 16>(a);
-    if (q_f32) return a.group <= 8 ? launch_bf16<D, 1, true>(a) : launch_bf16<D, 2, true>(a);
-    return a.group <= 8 ? launch_bf16<D, 1, false>(a) : launch_bf16<D, 2, false>(a);
+        return a.group <= 4 ? launch<F32Core<D, 4>>(a) : a.group <= 8 ? launch<F32Core<D, 8>>(a)
+                                                                      : launch<F32Core<D, 16>>(a);
+    if (q_f32) return a.group <= 8 ? launch<Bf16Core<D, 1, true>>(a) : launch<Bf16Core<D, 2, true>>(a);
+    return a.group <= 8 ? launch<Bf16Core<D, 1, false>>(a) : launch<Bf16Core<D, 2, false>>(a);
 }
 
 }  // namespace
