@@ -75,7 +75,7 @@ def _binding_commands(obj: str, out: str) -> list[list[str]]:
              *[f"-I{i}" for i in inc], "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj],
             [cxx, "-shared", "-o", out, obj, f"-L{BUILD_DIR}", "-l:" + LIB_NAME,
              "-Wl,-rpath,$ORIGIN", f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10",
-             "-lc10_cuda", f"-Wl,-rpath,{lib}"]]
+             "-lc10_cuda", "-ltorch_cuda", f"-Wl,-rpath,{lib}"]]
 
 
 def _run(cmd: list[str], what: str) -> str:

@@ -11,7 +11,8 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -79,6 +80,16 @@ struct Rows {
     int64_t stride = 0;
 };
 
+// `n` elements of a one-dimensional tensor from `at` on, sharing its storage.
+Tensor part_of(const Tensor &t, int64_t at, int64_t n) {
+    Tensor p = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW,
+                                                        c10::Storage(t.storage()), t.key_set(),
+                                                        t.dtype());
+    p.unsafeGetTensorImpl()->set_storage_offset(at);
+    p.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+    return p;
+}
+
 // Device, stream and allocations of one call: every tensor is on the first
 // one's device, which is current while the call runs; what the call allocates
 // belongs to the stream that it is launched on.
@@ -122,7 +133,7 @@ class Call {
         return t;
     }
     Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
-        return at::empty(shape, at::TensorOptions().device(device_).dtype(type));
+        return at::detail::empty_cuda(shape, type, device_, std::nullopt);
     }
     // [tokens, heads, d], each token's heads contiguous, any stride between tokens
     Rows rows(const Tensor &t, const char *name, int64_t tokens, int64_t heads, int64_t d,
@@ -165,13 +176,13 @@ class Call {
     }
     // Scratch memory of at least `need` bytes: the caller's or this call's own.
     std::pair<void *, int64_t> workspace(PyObject *o, int64_t need) {
-        if (none(o))
-            scratch_ = empty({need}, at::kByte);
-        else {
-            scratch_ = here(o, "workspace");
-            if (!scratch_.is_contiguous()) refuse(PyExc_ValueError, "workspace must be contiguous");
+        if (none(o)) {  // freed to the stream's pool when the call returns
+            scratch_ = c10::cuda::CUDACachingAllocator::get()->allocate(need);
+            return {scratch_.get(), need};
         }
-        return {scratch_.data_ptr(), (int64_t)scratch_.nbytes()};
+        const Tensor &t = here(o, "workspace");
+        if (!t.is_contiguous()) refuse(PyExc_ValueError, "workspace must be contiguous");
+        return {t.data_ptr(), (int64_t)t.nbytes()};
     }
 
   private:
@@ -179,7 +190,7 @@ class Call {
     cudaStream_t stream_ = nullptr;
     std::optional<c10::cuda::CUDAGuard> guard_;
     std::optional<c10::cuda::CUDAStreamGuard> on_;
-    Tensor scratch_;
+    c10::DataPtr scratch_;
 };
 
 // Raises the package's error for a status that is not LA_OK.
@@ -326,16 +337,6 @@ int64_t need_of(int64_t n) {
     return n;
 }
 
-// `n` elements of a one-dimensional tensor from `at` on, sharing its storage.
-Tensor part_of(const Tensor &t, int64_t at, int64_t n) {
-    Tensor p = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW,
-                                                        c10::Storage(t.storage()), t.key_set(),
-                                                        t.dtype());
-    p.unsafeGetTensorImpl()->set_storage_offset(at);
-    p.unsafeGetTensorImpl()->set_sizes_contiguous({n});
-    return p;
-}
-
 PyObject *wrap(const Tensor &t) {
     if (!t.defined()) Py_RETURN_NONE;
     return THPVariable_Wrap(t);
@@ -386,8 +387,9 @@ PyObject *qk_norm_rope_backward(PyObject *const *a) {
     if (has_k) dk = call.output(a[11], "dk", s.tokens, s.kv_heads, s.d, s.type, dk_);
     std::pair<void *, int64_t> ws{nullptr, 0};
     if (r.qw) {
-        dqw = call.empty({s.d}, at::kFloat);
-        if (has_k) dkw = call.empty({s.d}, at::kFloat);
+        const Tensor both = call.empty({2 * s.d}, at::kFloat);
+        dqw = part_of(both, 0, s.d);
+        if (has_k) dkw = part_of(both, s.d, s.d);
         ws = call.workspace(a[12], need_of(lightning_attn_qk_norm_rope_workspace_bytes(s.d)));
     }
     launch("lightning_attn_qk_norm_rope_backward", [&] {

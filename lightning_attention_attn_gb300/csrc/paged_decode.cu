@@ -35,7 +35,13 @@ namespace la {
 namespace {
 
 constexpr int kTile = 64;     // tokens of one tile of the work split
-constexpr int kOverhead = 3;  // tiles that starting a unit costs
+// Starting a unit (its page table, queries and first loads one after the other, then
+// the warps' join) takes a CTA about as long as streaming kOverheadBytes.  100 requests
+// of 1 to 3000 tokens, 8 key-value heads of 128, bf16: 64, 96, 128, 160, 192 KB give
+// 108, 104, 101, 98, 98 us; 128 of 1 to 1500, 64 wide: 45, 42, 41, 42, 43.
+constexpr int kOverheadBytes = 160 << 10;
+template <typename T, int D>
+constexpr int kOverhead = kOverheadBytes / (2 * kTile * D * (int)sizeof(T));  // in tiles
 constexpr int kStages = 3;    // of a warp's ring: two in flight, one read
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_huge_valf();
@@ -84,16 +90,16 @@ __device__ __forceinline__ float lo_of(uint32_t p) { return __uint_as_float(p <<
 __device__ __forceinline__ float hi_of(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
 
 // ------------------------------------------------------------ work split
+// What the kernel before may have written (it can still be running when this one is
+// scheduled) is read with plain loads behind the wait, never as constant data.
 // Length of request b as the kernels use it: inside [0, table capacity].
 __device__ __forceinline__ int request_len(const PagedDecodeArgs &a, int b) {
-    return min(max(__ldg(a.seq_lens + b), 0), a.max_tokens);
+    return min(max(a.seq_lens[b], 0), a.max_tokens);
 }
-// Cost of a unit of `len` tokens, in tiles: starting a unit (its page table, queries
-// and first loads one after the other, then the warps' join) takes a CTA about
-// as long as streaming kOverhead tiles.  A unit's cost range is the overhead, then
-// its tiles; a cut inside the overhead is a cut before the first tile.
-__device__ __forceinline__ int unit_cost(int len) {
-    return len > 0 ? kOverhead + (len + kTile - 1) / kTile : 0;
+// Cost of a unit of `len` tokens, in tiles: the overhead of starting it, then its
+// tiles.  A cut inside the overhead is a cut before the first tile.
+template <int OVERHEAD> __device__ __forceinline__ int unit_cost(int len) {
+    return len > 0 ? OVERHEAD + (len + kTile - 1) / kTile : 0;
 }
 
 // Where CTA `cta`'s range begins.  The costs of all units, request by request,
@@ -106,7 +112,7 @@ struct Place {
 
 // Whole block (kThr threads): false where the CTA has no range.  The lengths are
 // read once for up to kThr requests.
-template <int kThr>
+template <int kThr, int OVERHEAD>
 __device__ __forceinline__ bool find_place(const PagedDecodeArgs &a, int units, int cta, Place &p) {
     constexpr int kW = kThr / 32;
     __shared__ long long sums[kW];
@@ -116,7 +122,7 @@ __device__ __forceinline__ bool find_place(const PagedDecodeArgs &a, int units, 
     // inclusive prefix sum of the costs of requests b0 .. b0 + kThr - 1
     auto scan = [&](int b0, int &t) {
         const int i = b0 + threadIdx.x;
-        t = i < a.batch ? unit_cost(request_len(a, i)) : 0;
+        t = i < a.batch ? unit_cost<OVERHEAD>(request_len(a, i)) : 0;
         long long s = t;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -307,7 +313,7 @@ struct Bf16Core {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         float2 x = make_float2(0.f, 0.f);
-                        if (has) x = *reinterpret_cast<const float2 *>(qp + ks * 16 + i * 8);
+                        if (has) x = __ldcg(reinterpret_cast<const float2 *>(qp + ks * 16 + i * 8));
                         const uint32_t p = pack2(x.x, x.y);
                         qb[nt][ks][i] = p;
                         ql[nt][ks][i] = pack2(x.x - lo_of(p), x.y - hi_of(p));
@@ -320,7 +326,7 @@ struct Bf16Core {
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                         qb[nt][ks][i] =
-                            has ? *reinterpret_cast<const uint32_t *>(qp + ks * 16 + i * 8) : 0u;
+                            has ? __ldcg(reinterpret_cast<const uint32_t *>(qp + ks * 16 + i * 8)) : 0u;
             }
         }
         float o[NT][KS][4];
@@ -345,12 +351,12 @@ struct Bf16Core {
             if (t < t1) {
                 const int blk = t / a.page_size;
                 row = t - blk * a.page_size;
-                page = __ldg(pages + blk);
-                if (page >= a.num_pages) page = -1;
+                page = pages[blk];
             }
         };
         // Issues the copies of one group; returns the mask of its present rows.
         auto issue = [&](int stage, int page, int row) -> uint32_t {
+            if (page >= a.num_pages) page = -1;  // first use of the table's entry, a group after its load
             const uint32_t have = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
             const uint32_t dk = ring + stage * kStageBytes, dv = dk + kMat;
 #pragma unroll
@@ -589,11 +595,11 @@ struct F32Core {
             if (t < t1) {
                 const int blk = t / a.page_size;
                 row = t - blk * a.page_size;
-                page = __ldg(pages + blk);
-                if (page >= a.num_pages) page = -1;
+                page = pages[blk];
             }
         };
         auto issue = [&](int stage, int page, int row) -> uint32_t {
+            if (page >= a.num_pages) page = -1;  // first use of the table's entry, a group after its load
             const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
             const uint32_t dk = ring_u + stage * 2 * kMat * 4, dv = dk + kMat * 4;
             const int ch = lane % CH;
@@ -630,10 +636,10 @@ struct F32Core {
             for (int i = 0; i < DPL / 4; ++i) {
                 float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (h < heads)
-                    x = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) +
+                    x = __ldcg(reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) +
                                                           (size_t)b * a.q_stride +
                                                           (size_t)(head0 + h) * D +
-                                                          (sub + i * LPT) * 4);
+                                                          (sub + i * LPT) * 4));
                 q[h][2 * i] = make_float2(x.x, x.y);
                 q[h][2 * i + 1] = make_float2(x.z, x.w);
             }
@@ -771,6 +777,7 @@ template <typename Core>
 __global__ void __launch_bounds__(Core::kThreads, 2)
 paged_split_kernel(const __grid_constant__ PagedDecodeArgs a) {
     constexpr int D = Core::D, ROWS = Core::ROWS;
+    constexpr int kOver = kOverhead<typename Core::T, D>;
     extern __shared__ __align__(128) unsigned char smem[];
 
     // launched as a dependent launch: the lengths, the table and the cache
@@ -781,14 +788,14 @@ paged_split_kernel(const __grid_constant__ PagedDecodeArgs a) {
     const int units = a.num_kv_heads * a.head_groups;
     write_empty<typename Core::T>(a);
     Place at;
-    if (!find_place<Core::kThreads>(a, units, blockIdx.x, at)) return;
+    if (!find_place<Core::kThreads, kOver>(a, units, blockIdx.x, at)) return;
     long long w0 = at.w, unit0 = at.unit0;
     const long long w1 = min(at.all, w0 + at.chunk);
     int b = at.b;
     bool first = true;
     while (w0 < w1 && b < a.batch) {
         const int len = request_len(a, b);
-        const int tiles = (len + kTile - 1) / kTile, cost = unit_cost(len);
+        const int tiles = (len + kTile - 1) / kTile, cost = unit_cost<kOver>(len);
         if (w0 >= unit0 + (long long)cost * units) {  // next request (empty ones pass)
             unit0 += (long long)cost * units;
             ++b;
@@ -797,7 +804,7 @@ paged_split_kernel(const __grid_constant__ PagedDecodeArgs a) {
         const int unit = tiles_div(w0 - unit0, cost);
         const int at0 = (int)(w0 - unit0 - (long long)unit * cost);
         const int at1 = (int)min((long long)cost, at0 + (w1 - w0));
-        const int tile0 = max(at0 - kOverhead, 0), tile1 = at1 - kOverhead;
+        const int tile0 = max(at0 - kOver, 0), tile1 = at1 - kOver;
         w0 += at1 - at0;
         if (tile1 <= 0) continue;  // only overhead: the next CTA starts the unit
         const int kvh = unit / a.head_groups, hg = unit % a.head_groups;
@@ -926,15 +933,16 @@ paged_join_kernel(const __grid_constant__ PagedDecodeArgs a) {
     // scheduled; the pieces are read after the wait.
     Place at;
     const int c = blockIdx.x + 1;
-    const bool any = find_place<kJoin>(a, units, c, at);
+    constexpr int kOver = kOverhead<T, D>;
+    const bool any = find_place<kJoin, kOver>(a, units, c, at);
     int unit = 0, c0 = 0, c1 = 0;
     long long u0 = 0;
     if (any) {
-        const int cost = unit_cost(request_len(a, at.b));
+        const int cost = unit_cost<kOver>(request_len(a, at.b));
         unit = tiles_div(at.w - at.unit0, cost);
         u0 = at.unit0 + (long long)unit * cost;
         // the CTAs of the unit's first tile (behind its overhead) and of its last
-        c0 = (int)((u0 + kOverhead) / at.chunk);
+        c0 = (int)((u0 + kOver) / at.chunk);
         c1 = (int)((u0 + cost - 1) / at.chunk);
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1022,17 +1030,30 @@ template <typename Core, int S> cudaError_t launch_cluster(const PagedDecodeArgs
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// When the cluster kernel serves a call: up to kClusterTiles tiles a CTA with at most
+// eight CTAs a unit, all of them on the SMs at once (CTAs of one unit may queue up to
+// kClusterWaves deep).  64 query and 8 key-value heads of 128, cluster / split kernel:
+// 1 x 300 tokens 4.8 / 6.4 us, 16 x 512 8.0 / 12.4, 16 x 1000 11.6 / 15.4, 8 x 2000 11.7 /
+// 15.4, 128 x 128 15.7 / 19.8, 64 x 256 12.8 / 17.1; beyond it, with 16 tiles, 1 x 8000
+// 14.8 / 12.0.
+constexpr int kClusterTiles = 8;
+constexpr int kClusterWaves = 4;
+
 template <typename Core> cudaError_t launch(PagedDecodeArgs a) {
     a.head_groups = (a.group + Core::ROWS - 1) / Core::ROWS;
     // What the table can hold bounds the lengths, which only the GPU knows.
-    // Up to kClusterTokens tokens a CTA, all units at once on the SMs: clusters.
     const long units = (long)a.batch * a.num_kv_heads * a.head_groups;
-    constexpr int kClusterTokens = 2 * kTile;
-    const int need = (a.max_tokens + kClusterTokens - 1) / kClusterTokens;
-    if (need <= 1 && units <= kPagedCtas) return launch_cluster<Core, 1>(a);
-    if (need <= 2 && units * 2 <= kPagedCtas) return launch_cluster<Core, 2>(a);
-    if (need <= 4 && units * 4 <= kPagedCtas) return launch_cluster<Core, 4>(a);
-    if (need <= 8 && units * 8 <= kPagedCtas) return launch_cluster<Core, 8>(a);
+    const int tiles = (a.max_tokens + kTile - 1) / kTile;
+    int size = 8;
+    while (size > 1 && (size > tiles || units * size > kPagedCtas)) size >>= 1;
+    if (tiles <= kClusterTiles * size && units * size <= kClusterWaves * kPagedCtas) {
+        switch (size) {
+            case 1: return launch_cluster<Core, 1>(a);
+            case 2: return launch_cluster<Core, 2>(a);
+            case 4: return launch_cluster<Core, 4>(a);
+            default: return launch_cluster<Core, 8>(a);
+        }
+    }
 
     constexpr auto kern = paged_split_kernel<Core>;
     cudaError_t e = allow_smem<kern>(Core::kSmem);

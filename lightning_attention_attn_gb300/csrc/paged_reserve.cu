@@ -119,7 +119,8 @@ __device__ __forceinline__ void fill(const PagedReserveArgs &a, const Step &s, i
             a.positions[t] = position[f];
         }
     }
-    for (int j = i; j < pages; j += n) {
+    // from the last thread down: the first ones have tokens
+    for (int j = n - 1 - i; j < pages; j += n) {
         const int b = last_at(s.taken, a.batch, j);
         const int blk = blocks_of(s.old[b], a.page_size) + (j - s.taken[b]);
         a.block_table[(size_t)b * a.table_stride + blk] = __ldcg(a.free_pages + (top - j));
@@ -223,7 +224,9 @@ paged_reserve_kernel(const __grid_constant__ PagedReserveArgs a) {
     __syncthreads();
     if ((threadIdx.x & 31) == 0) sums[0][threadIdx.x >> 5] = left;
     __syncthreads();
-    for (int w = 0; w < threads >> 5; ++w) left = min(left, sums[0][w]);
+    left = (threadIdx.x & 31) < threads >> 5 ? sums[0][threadIdx.x & 31] : count;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) left = min(left, __shfl_xor_sync(0xffffffffu, left, o));
     if (threadIdx.x == 0) a.free_count_out[0] = (int)left;
     if (FILL) fill(a, s, (int)count - 1, (int)(count - left), threadIdx.x, threads);
 }

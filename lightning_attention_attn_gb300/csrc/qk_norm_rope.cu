@@ -86,7 +86,7 @@ __device__ __forceinline__ void load_rotation(const NormRopeArgs &a, int token, 
     if (ea >= a.rotary_dim) return;
     // positions are checked nowhere on the host: clamped, so every read stays
     // inside the table
-    const int pos = min(max(__ldg(a.positions + token), 0), a.rotary_rows - 1);
+    const int pos = min(max(__ldcg(a.positions + token), 0), a.rotary_rows - 1);
     const float *row = a.rotary + (size_t)pos * a.rotary_dim;
     const int half = a.rotary_dim >> 1;
     if (INTER) {
@@ -148,7 +148,7 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
     const int nk = (a.set[1].heads + kRows - 1) / kRows;
     const int nv = (a.set[2].heads + kRows - 1) / kRows;
     const int per = nq + nk + nv;
-    const int items = a.num_tokens * per;  // fits: the caller bounds the number of rows
+    const unsigned items = (unsigned)a.num_tokens * per;  // the caller bounds the rows by 2^31
 
     float2 dw[2][4];  // this lane's columns of the weights' gradients
     if (BACK) {
@@ -156,8 +156,8 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
         for (int i = 0; i < 4; ++i) dw[0][i] = dw[1][i] = twice(0.f);
     }
 
-    for (int item = blockIdx.x * kWarps + warp; item < items; item += gridDim.x * kWarps) {
-        const int token = item / per, c = item - token * per;
+    for (unsigned item = blockIdx.x * kWarps + warp; item < items; item += gridDim.x * kWarps) {
+        const int token = (int)(item / per), c = (int)item - token * per;
         const int kind = c < nq ? 0 : c < nq + nk ? 1 : 2;
         const NormRopeRows &s = a.set[kind];
         const int first = (kind == 0 ? c : kind == 1 ? c - nq : c - nq - nk) * kRows;
@@ -191,7 +191,7 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
         T *out = static_cast<T *>(s.out);
         size_t head = D;
         if (s.cache) {
-            const int slot = __ldg(a.slots + token);
+            const int slot = __ldcg(a.slots + token);
             if (slot < 0 || slot >= a.num_slots) {
                 cp_wait<0>();  // the stage is filled anew
                 continue;
@@ -333,7 +333,7 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
 // 32-byte sector of a partial result) a block, 128 slices of the blocks' axis.
 constexpr int kSumCols = 8, kSumSlices = 128;
 __global__ void __launch_bounds__(kSumCols *kSumSlices)
-norm_weight_sum_kernel(const float *__restrict__ partial, int blocks, int D, float *dwq, float *dwk) {
+norm_weight_sum_kernel(const float *partial, int blocks, int D, float *dwq, float *dwk) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ float red[kSumSlices][kSumCols + 1];
@@ -341,7 +341,7 @@ norm_weight_sum_kernel(const float *__restrict__ partial, int blocks, int D, flo
     const int c = blockIdx.x * kSumCols + x;
     float t = 0.f;
 #pragma unroll 8
-    for (int b = y; b < blocks; b += kSumSlices) t += partial[(size_t)b * 2 * D + c];
+    for (int b = y; b < blocks; b += kSumSlices) t += __ldcg(partial + (size_t)b * 2 * D + c);
     red[y][x] = t;
     __syncthreads();
     const int lane = threadIdx.x & 31, col = threadIdx.x >> 5;

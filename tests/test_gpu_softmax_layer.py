@@ -163,6 +163,21 @@ def test_norm_rope_in_place_and_strided_outputs():
     assert torch.equal(q, want[0]) and torch.equal(k, want[1])
 
 
+@pytest.mark.parametrize("dtype, inter", [(BF16, False), (BF16, True), (FP32, False)])
+def test_norm_rope_in_place_many_rows(dtype, inter):
+    """In place where a warp has many passes in flight, heads that end inside one."""
+    case = (dtype, 900, 37, 5, 64, 32, inter, True)
+    g, q, k, qw, kw, pos, table = norm_inputs(case, 6)
+    args = dict(q_weight=qw, k_weight=kw, eps=EPS, interleaved=inter)
+    dqo, dko = randn(q.shape, dtype, g), randn(k.shape, dtype, g)
+    want = la.qk_norm_rope(q, k, pos, table, **args)
+    grads = la.qk_norm_rope_backward(q, k, pos, table, dqo, dko, **args)
+    la.qk_norm_rope_backward(q, k, pos, table, dqo, dko, dq=dqo, dk=dko, **args)
+    assert torch.equal(dqo, grads[0]) and torch.equal(dko, grads[1])
+    la.qk_norm_rope(q, k, pos, table, q_out=q, k_out=k, **args)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+
+
 def test_norm_rope_edges():
     g = gen(5)
     table = la.rotary_table(100, 64, device="cuda")
@@ -284,6 +299,23 @@ def test_paged_decode_split(dtype, lens):
     g = gen(len(lens))
     kc, vc, bt, sl = pool(lens, 64, 2, 64, dtype, g)
     check_attention(randn((len(lens), 8, 64), dtype, g), kc, vc, bt, sl)
+
+
+@pytest.mark.parametrize("dtype, h, hk, d", [(BF16, 16, 2, 128), (BF16, 12, 1, 64), (FP32, 8, 4, 64),
+                                             (FP32, 16, 1, 128)])
+@pytest.mark.parametrize("longest", [50, 128, 500, 1900, 4096])
+def test_paged_decode_wide_and_narrow_tables(dtype, h, hk, d, longest):
+    """The same requests with a table that just holds them (one cluster a unit, of 1
+    to 8 CTAs) and one for contexts of 64K tokens (the split over all CTAs)."""
+    g = gen(longest + d)
+    lens_list = [longest, 0, longest // 3 + 1, 1]
+    kc, vc, bt, lens = pool(lens_list, 32, hk, d, dtype, g)
+    q = randn((4, h, d), dtype, g)
+    bt = bt[:, :-1] if bt.shape[1] > 1 else bt
+    check_attention(q, kc, vc, bt, lens)
+    wide = torch.full((4, 2048), -1, dtype=torch.int32, device="cuda")
+    wide[:, :bt.shape[1]] = bt
+    check_attention(q, kc, vc, wide, lens)
 
 
 def test_paged_decode_large_scores():
