@@ -299,47 +299,6 @@ struct Bf16Core {
         const int krow = lane & 15, kchunk = lane >> 4;
         const int vrow = (lane & 7) + ((lane >> 4) << 3), vchunk = (lane >> 3) & 1;
 
-        // queries as B operands, scaled after the product
-        uint32_t qb[NT][KS][2], ql[QF32 ? NT : 1][QF32 ? KS : 1][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int h = nt * 8 + g;
-            const bool has = h < heads;
-            if (QF32) {
-                const float *qp = static_cast<const float *>(a.q) +
-                                  (size_t)b * a.q_stride + (size_t)(head0 + h) * D + c2;
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float2 x = make_float2(0.f, 0.f);
-                        if (has) x = __ldcg(reinterpret_cast<const float2 *>(qp + ks * 16 + i * 8));
-                        const uint32_t p = pack2(x.x, x.y);
-                        qb[nt][ks][i] = p;
-                        ql[nt][ks][i] = pack2(x.x - lo_of(p), x.y - hi_of(p));
-                    }
-            } else {
-                const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q) +
-                                          (size_t)b * a.q_stride + (size_t)(head0 + h) * D + c2;
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        qb[nt][ks][i] =
-                            has ? __ldcg(reinterpret_cast<const uint32_t *>(qp + ks * 16 + i * 8)) : 0u;
-            }
-        }
-        float o[NT][KS][4];
-        float mx[NT][2], l[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            mx[nt][0] = mx[nt][1] = -kInf;
-            l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-                o[nt][ks][0] = o[nt][ks][1] = o[nt][ks][2] = o[nt][ks][3] = 0.f;
-        }
-
         const int32_t *pages = a.block_table + (size_t)b * a.table_stride;
         const int groups = (t1 - t0 + kGroup - 1) / kGroup;  // of the whole piece
         // This warp's groups: warp, warp + W, ...; lane r < 16 finds row
@@ -374,20 +333,63 @@ struct Bf16Core {
             return have;
         };
 
+        // The first groups' table entries together, then bf16 queries, then the copies
+        // (fp32 queries, which are converted, behind them): one latency of each.
+        int page0[kStages - 1], row0[kStages - 1], npage, nrow;
+#pragma unroll
+        for (int s = 0; s < kStages - 1; ++s) locate(warp + s * W, page0[s], row0[s]);
+        locate(warp + (kStages - 1) * W, npage, nrow);  // of the group that is issued next
+
+        // queries as B operands, scaled after the product
+        uint32_t qb[NT][KS][2], ql[QF32 ? NT : 1][QF32 ? KS : 1][2];
+        if (!QF32) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q) +
+                                          (size_t)b * a.q_stride + (size_t)(head0 + nt * 8 + g) * D + c2;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        qb[nt][ks][i] = nt * 8 + g < heads ? __ldcg(reinterpret_cast<const uint32_t *>(
+                                                                 qp + ks * 16 + i * 8))
+                                                           : 0u;
+            }
+        }
         uint32_t have[kStages];
 #pragma unroll
         for (int s = 0; s < kStages - 1; ++s) {
-            const int grp = warp + s * W;
-            have[s] = 0;
-            if (grp < groups) {
-                int page, row;
-                locate(grp, page, row);
-                have[s] = issue(s, page, row);
-            }
+            have[s] = issue(s, page0[s], row0[s]);  // copies nothing past the end
             cp_commit();
         }
-        int npage, nrow;  // of the group that is issued next
-        locate(warp + (kStages - 1) * W, npage, nrow);
+        if (QF32) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float *qp = static_cast<const float *>(a.q) + (size_t)b * a.q_stride +
+                                  (size_t)(head0 + nt * 8 + g) * D + c2;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float2 x = make_float2(0.f, 0.f);
+                        if (nt * 8 + g < heads)
+                            x = __ldcg(reinterpret_cast<const float2 *>(qp + ks * 16 + i * 8));
+                        const uint32_t p = pack2(x.x, x.y);
+                        qb[nt][ks][i] = p;
+                        ql[nt][ks][i] = pack2(x.x - lo_of(p), x.y - hi_of(p));
+                    }
+            }
+        }
+        float o[NT][KS][4];
+        float mx[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            mx[nt][0] = mx[nt][1] = -kInf;
+            l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+                o[nt][ks][0] = o[nt][ks][1] = o[nt][ks][2] = o[nt][ks][3] = 0.f;
+        }
 
         int stage = 0;
         for (int grp = warp; grp < groups; grp += W) {
@@ -617,16 +619,16 @@ struct F32Core {
             }
             return have;
         };
+        int page0[kStages - 1], row0[kStages - 1], npage, nrow;
+#pragma unroll
+        for (int s = 0; s < kStages - 1; ++s) locate(warp + s * W, page0[s], row0[s]);
+        locate(warp + (kStages - 1) * W, npage, nrow);  // of the group that is issued next
         uint32_t have[kStages];
 #pragma unroll
         for (int s = 0; s < kStages - 1; ++s) {
-            int page, row;
-            locate(warp + s * W, page, row);
-            have[s] = issue(s, page, row);
+            have[s] = issue(s, page0[s], row0[s]);
             cp_commit();
         }
-        int npage, nrow;  // of the group that is issued next
-        locate(warp + (kStages - 1) * W, npage, nrow);
 
         // chunk sub + i LPT of every query row
         float2 q[ROWS][DPL / 2];
@@ -786,12 +788,11 @@ paged_split_kernel(const __grid_constant__ PagedDecodeArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const int units = a.num_kv_heads * a.head_groups;
-    write_empty<typename Core::T>(a);
     Place at;
-    if (!find_place<Core::kThreads, kOver>(a, units, blockIdx.x, at)) return;
-    long long w0 = at.w, unit0 = at.unit0;
-    const long long w1 = min(at.all, w0 + at.chunk);
-    int b = at.b;
+    const bool any = find_place<Core::kThreads, kOver>(a, units, blockIdx.x, at);
+    long long w0 = any ? at.w : 0, unit0 = any ? at.unit0 : 0;
+    const long long w1 = any ? min(at.all, w0 + at.chunk) : 0;
+    int b = any ? at.b : 0;
     bool first = true;
     while (w0 < w1 && b < a.batch) {
         const int len = request_len(a, b);
@@ -828,6 +829,7 @@ paged_split_kernel(const __grid_constant__ PagedDecodeArgs a) {
         __syncthreads();  // shared memory is the ring again
         first = false;
     }
+    write_empty<typename Core::T>(a);
 }
 
 // ---------------------------------------------------------- cluster kernel

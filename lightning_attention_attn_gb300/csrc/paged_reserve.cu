@@ -284,11 +284,11 @@ cudaError_t paged_reserve(const PagedReserveArgs &a) {
                                      (int)most);
         if (e != cudaSuccess) return e;
     }
-    // a thread per request (and, where it writes them, per token); all for the
+    // a thread per request (and, where it writes them, per token); at least 512 for the
     // pages of finished requests, hundreds each
     int threads = small && a.num_tokens > a.batch ? a.num_tokens : a.batch;
-    threads = threads > kMaxThreads || a.finished ? kMaxThreads
-              : threads < 128 ? 128 : (threads + 31) / 32 * 32;
+    const int least = a.finished ? 512 : 128;
+    threads = threads > kMaxThreads ? kMaxThreads : threads < least ? least : (threads + 31) / 32 * 32;
     e = launch_dependent(kern, 1, threads, smem, a.stream, a);
     if (e == cudaSuccess && !small) {
         const int blocks = (a.num_tokens + kFillThreads - 1) / kFillThreads;
