@@ -923,11 +923,12 @@ paged_cluster_kernel(const __grid_constant__ PagedDecodeArgs a) {
 // kPagedCtas - 1 units are cut, whatever the batch.  A thread takes four columns of
 // every slices-th piece with a running maximum, its loads in flight together; the
 // slices are added in order.
-constexpr int kJoin = 512;
+template <int D, int ROWS> constexpr int kJoinThreads = ROWS * D / 4 > 256 ? ROWS * D / 4 : 256;
 
 template <typename T, int D, int ROWS>
-__global__ void __launch_bounds__(kJoin)
+__global__ void __launch_bounds__(kJoinThreads<D, ROWS>)
 paged_join_kernel(const __grid_constant__ PagedDecodeArgs a) {
+    constexpr int kJoin = kJoinThreads<D, ROWS>;
     __shared__ float4 part[kJoin];
     __shared__ float2 stat[kJoin];
     const int units = a.num_kv_heads * a.head_groups;
@@ -1063,7 +1064,7 @@ template <typename Core> cudaError_t launch(PagedDecodeArgs a) {
         e = launch_dependent(kern, kPagedCtas, Core::kThreads, Core::kSmem, a.stream, a);
     if (e == cudaSuccess)
         e = launch_dependent(paged_join_kernel<typename Core::T, Core::D, Core::ROWS>, kPagedCtas - 1,
-                             kJoin, 0, a.stream, a);
+                             kJoinThreads<Core::D, Core::ROWS>, 0, a.stream, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
