@@ -240,6 +240,28 @@ def test_paged_append(dtype, t, h, hk, d, page, rot):
     assert torch.equal(both, before)
 
 
+def test_paged_append_no_tokens_and_refusals():
+    g = gen(7)
+    q, k, v = qkv(3, 4, 2, 64, BF16, g)
+    kc = randn((4, 2, 16, 64), BF16, g)
+    slots = torch.tensor([5, 6, 7], dtype=torch.int32, device="cuda")
+    before = kc.clone()
+    out = la.paged_append(q[:0], k[:0], v[:0], None, None, kc, kc.clone(), slots[:0])
+    assert out.shape == (0, 4, 64) and torch.equal(kc, before)
+    for bad in (dict(slots=slots.long()), dict(slots=slots[:2]), dict(v=v[:, :1]), dict(kc=kc[:, :1]),
+                dict(kc=kc.float()), dict(kc=kc.transpose(1, 2)), dict(q=q.cpu())):
+        a = {**dict(q=q, k=k, v=v, kc=kc, slots=slots), **bad}
+        with pytest.raises((ValueError, la.LightningAttnError)):
+            la.paged_append(a["q"], a["k"], a["v"], None, None, a["kc"], kc.clone(), a["slots"])
+    with pytest.raises(ValueError):
+        la.paged_append(q, k, v, slots, None, kc, kc.clone(), slots)  # positions without a table
+    # queries rotated in place
+    table, pos = la.rotary_table(64, 64, device="cuda"), positions_of(3, 64, g)
+    want = la.paged_append(q, k, v, pos, table, kc, kc.clone(), slots)
+    assert la.paged_append(q, k, v, pos, table, kc, kc.clone(), slots, q_out=q).data_ptr() == q.data_ptr()
+    assert torch.equal(q, want)
+
+
 # --------------------------------------------------------------- attention
 def pool(lens, page, hk, d, dtype, g, spare=2, garbage=float("nan")):
     """Pages of the requests in random places; everything else is garbage."""
@@ -377,6 +399,30 @@ def test_paged_decode_offsets_past_32_bits():
     assert torch.equal(kc[-1, :, -1], k[1]) and torch.equal(vc[-1, :, 5], v[0])
     want, _, bound, _ = ref.attention(c(q), c(kc[-12:]), c(vc[-12:]), c(small), c(lens), d ** -0.5)
     ref.within(out, want, bound, ref.u_of(BF16), "out")
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_paged_decode_random(seed):
+    """Seeded random shapes, lengths, pages, strides and garbage."""
+    import random
+    rng = random.Random(seed)
+    dtype, d = rng.choice([BF16, BF16, FP32]), rng.choice([64, 128])
+    hk = rng.choice([1, 2, 3, 8])
+    h = hk * rng.choice([1, 2, 5, 8, 11, 16])
+    page = rng.choice([1, 3, 16, 24, 64, 300])
+    b = rng.choice([1, 2, 9, 40])
+    most = rng.choice([1, 20, 200, 3000 if b < 20 else 400])
+    lens_list = [rng.choice([0, 1, most, rng.randint(0, most)]) for _ in range(b)]
+    g = gen(seed)
+    kc, vc, bt, lens = pool(lens_list, page, hk, d, dtype, g, garbage=rng.choice([float("nan"),
+                                                                             float("-inf"), 3e38]))
+    if rng.random() < 0.5:  # a table for longer contexts
+        wide = torch.full((b, 20000 // page + bt.shape[1]), -1, dtype=torch.int32, device="cuda")
+        wide[:, :bt.shape[1]] = bt
+        bt = wide
+    x = randn((b, h + rng.choice([0, 2]), d), dtype, g) * rng.choice([0.1, 1, 4])
+    x = x.to(dtype)
+    check_attention(x[:, :h], kc, vc, bt, lens, scale=rng.choice([None, 0.02, 1.0]))
 
 
 def test_paged_decode_refusals():
@@ -613,12 +659,13 @@ def test_training_pass_through_the_lightning_layer():
         assert abs(slope - float((got * way).sum())) <= room
 
 
-def test_two_graphs_and_side_streams():
+@pytest.mark.parametrize("lengths", [(3000, 1700), (30000, 17000)])  # clusters; split and join
+def test_two_graphs_and_side_streams(lengths):
     """Two captured steps, each with its own workspace, replayed at once on two
     streams; and calls on a stream that is not the current one."""
     g = gen(22)
     sets = []
-    for n in (3000, 1700):
+    for n in lengths:
         kc, vc, bt, lens = pool([n, 50], 32, 2, 128, BF16, g)
         q = randn((2, 16, 128), BF16, g)
         sets.append((q, kc, vc, bt, lens, la.paged_decode(q, kc, vc, bt, lens)))
