@@ -23,6 +23,8 @@
 // barriers, while the token's cosines and sines and the weights arrive.  Those are
 // folded into two coefficients an element, y = r (x A + partner(x) B) with
 // A = w cos, B = +-w' sin, applied with packed fp32 pairs.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -124,7 +126,7 @@ template <int L> __device__ __forceinline__ float row_sum(float s) {
 }
 
 template <typename T, int D, int U, int G, bool BACK, bool INTER>
-__global__ void __launch_bounds__(32 * kWarps, BACK && U * G > 1 ? 5 : 8)
+__global__ void __launch_bounds__(32 * kWarps, BACK ? 5 : 8)
 qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
     constexpr int L = D / 8;            // lanes per row
     constexpr int R = 32 / L;           // rows per pass
@@ -163,7 +165,9 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
         const int first = (kind == 0 ? c : kind == 1 ? c - nq : c - nq - nk) * kRows;
         const int left = s.heads - first;  // rows of this item (and of later ones)
 
-        // A pass is R * D contiguous elements: lane's copies of 16 bytes each
+        // A pass is R * D contiguous elements, 16 bytes of it each copy of a lane.
+        // Items that have all their rows (most do) need no checks.
+        const bool full = left >= kRows;
         const char *xp = static_cast<const char *>(s.x) + (size_t)token * s.x_stride +
                          (size_t)first * D * sizeof(T) + lane * 16;
         const char *gp = BACK ? static_cast<const char *>(s.dy) + (size_t)token * s.dy_stride +
@@ -172,18 +176,31 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
         const uint32_t to = ptx::smem_u32(&stage[warp][0][0][0]) + lane * 16;
         constexpr uint32_t kPass = R * D * sizeof(T);
         __syncwarp();  // the previous item's rows have been read by all lanes
+        if (full) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (i * R < left) {  // the same in the whole warp
+            for (int i = 0; i < N; ++i) {
 #pragma unroll
                 for (int j = 0; j < kCopies; ++j) {
-                    const bool in = i * R + (lane * 16 + j * 512) / (D * (int)sizeof(T)) < left;
                     const uint32_t off = i * kPass + j * 512;
-                    cp_async16(to + off, in ? xp + off : xp - lane * 16, in);
-                    if (BACK) cp_async16(to + N * kPass + off, in ? gp + off : gp - lane * 16, in);
+                    cp_async16(to + off, xp + off, true);
+                    if (BACK) cp_async16(to + N * kPass + off, gp + off, true);
                 }
+                if (i % U == U - 1) cp_commit();
             }
-            if (i % U == U - 1) cp_commit();
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (i * R < left) {  // the same in the whole warp
+#pragma unroll
+                    for (int j = 0; j < kCopies; ++j) {
+                        const bool in = i * R + (lane * 16 + j * 512) / (D * (int)sizeof(T)) < left;
+                        const uint32_t off = i * kPass + j * 512;
+                        cp_async16(to + off, in ? xp + off : xp - lane * 16, in);
+                        if (BACK) cp_async16(to + N * kPass + off, in ? gp + off : gp - lane * 16, in);
+                    }
+                }
+                if (i % U == U - 1) cp_commit();
+            }
         }
 
         // destination of the token's rows: its row of the output, or its slot
@@ -225,78 +242,83 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) item_dw[i] = twice(0.f);
         }
+        T *oa = out + ea, *ob = out + eb;
+        const size_t step = R * head;
+        float *f32 = s.out_f32 ? static_cast<float *>(s.out) +
+                                     ((size_t)token * s.heads + first + sub) * D
+                               : nullptr;  // unrounded rows (the queries of a fused step)
+        auto rows = [&](auto all) {  // all: the item has all its rows
+            constexpr bool FULL = decltype(all)::value;
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            if (g * U * R >= left) break;
-            cp_wait_group<G>(g);
-            __syncwarp();
+            for (int g = 0; g < G; ++g) {
+                if (!FULL && g * U * R >= left) break;
+                cp_wait_group<G>(g);
+                __syncwarp();
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int pass = g * U + u;
-                if (U > 1 && pass * R >= left) break;
-                const bool in = pass * R + sub < left;
-                const T *row = &stage[warp][0][pass][sub * D];
-                T *o = out + pass * R * head;
-                float2 x[4];
-                load_chunk(row + ea, x);
-                load_chunk(row + eb, x + 2);
-                if (!BACK && kind == 2) {  // values: copied (exact: the chunks are not rounded anew)
-                    if (in) store_chunk(o + ea, x), store_chunk(o + eb, x + 2);
-                    continue;
-                }
-                float r = 1.f;
-                if (norm) {
-                    float2 ss = ptx::f2_mul(x[0], x[0]);
-#pragma unroll
-                    for (int i = 1; i < 4; ++i) ss = ptx::f2_fma(x[i], x[i], ss);
-                    // a row past the last head stays zero also where eps is 0
-                    r = row_sum<L>(ss.x + ss.y) * (1.f / D) + a.eps;
-                    r = in ? rsqrtf(r) : 0.f;
-                }
-                const float2 rr = twice(r);
-                if (BACK) {
-                    const T *grow = &stage[warp][kArrays - 1][pass][sub * D];
-                    float2 dy[4], g4[4];
-                    load_chunk(grow + ea, dy);
-                    load_chunk(grow + eb, dy + 2);
-                    float2 dot = twice(0.f);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        g4[i] = ptx::f2_fma(dy[i], ca[i], ptx::f2_mul(partner<INTER>(dy, i), cb[i]));
-                        if (norm) {
-                            x[i] = ptx::f2_mul(x[i], rr);
-                            const float2 p = ptx::f2_mul(g4[i], x[i]);
-                            item_dw[i] = ptx::f2_add(item_dw[i], p);
-                            dot = ptx::f2_fma(w[i], p, dot);
-                            g4[i] = ptx::f2_mul(g4[i], w[i]);
-                        }
+                for (int u = 0; u < U; ++u, oa += step, ob += step) {
+                    const int pass = g * U + u;
+                    if (!FULL && U > 1 && pass * R >= left) break;
+                    const bool in = FULL || pass * R + sub < left;
+                    const T *row = &stage[warp][0][pass][sub * D];
+                    float2 x[4];
+                    load_chunk(row + ea, x);
+                    load_chunk(row + eb, x + 2);
+                    if (!BACK && kind == 2) {  // values: copied (exact: the chunks are not rounded anew)
+                        if (in) store_chunk(oa, x), store_chunk(ob, x + 2);
+                        continue;
                     }
+                    float r = 1.f;
                     if (norm) {
-                        const float2 m = twice(row_sum<L>(dot.x + dot.y) * (-1.f / D));
+                        float2 ss = ptx::f2_mul(x[0], x[0]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            g4[i] = ptx::f2_mul(rr, ptx::f2_fma(x[i], m, g4[i]));
+                        for (int i = 1; i < 4; ++i) ss = ptx::f2_fma(x[i], x[i], ss);
+                        r = rsqrtf(row_sum<L>(ss.x + ss.y) * (1.f / D) + a.eps);
+                        if (!in) r = 0.f;  // a row past the last head stays zero also where eps is 0
                     }
-                    if (in) store_chunk(o + ea, g4), store_chunk(o + eb, g4 + 2);
-                } else {
-                    float2 y[4];
+                    const float2 rr = twice(r);
+                    if (BACK) {
+                        const T *grow = &stage[warp][kArrays - 1][pass][sub * D];
+                        float2 dy[4], g4[4];
+                        load_chunk(grow + ea, dy);
+                        load_chunk(grow + eb, dy + 2);
+                        float2 dot = twice(0.f);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        y[i] = ptx::f2_fma(x[i], ca[i], ptx::f2_mul(partner<INTER>(x, i), cb[i]));
-                        if (norm) y[i] = ptx::f2_mul(y[i], rr);
-                    }
-                    if (in && s.out_f32) {  // unrounded rows (the queries of a fused step)
-                        float *f = static_cast<float *>(s.out) +
-                                   ((size_t)token * s.heads + first + pass * R + sub) * D;
-                        store_chunk(f + ea, y);
-                        store_chunk(f + eb, y + 2);
-                    } else if (in) {
-                        store_chunk(o + ea, y);
-                        store_chunk(o + eb, y + 2);
+                        for (int i = 0; i < 4; ++i) {
+                            g4[i] = ptx::f2_fma(dy[i], ca[i], ptx::f2_mul(partner<INTER>(dy, i), cb[i]));
+                            if (norm) {
+                                x[i] = ptx::f2_mul(x[i], rr);
+                                const float2 p = ptx::f2_mul(g4[i], x[i]);
+                                item_dw[i] = ptx::f2_add(item_dw[i], p);
+                                dot = ptx::f2_fma(w[i], p, dot);
+                                g4[i] = ptx::f2_mul(g4[i], w[i]);
+                            }
+                        }
+                        if (norm) {
+                            const float2 m = twice(row_sum<L>(dot.x + dot.y) * (-1.f / D));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                g4[i] = ptx::f2_mul(rr, ptx::f2_fma(x[i], m, g4[i]));
+                        }
+                        if (in) store_chunk(oa, g4), store_chunk(ob, g4 + 2);
+                    } else {
+                        float2 y[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            y[i] = ptx::f2_fma(x[i], ca[i], ptx::f2_mul(partner<INTER>(x, i), cb[i]));
+                            if (norm) y[i] = ptx::f2_mul(y[i], rr);
+                        }
+                        if (in && f32) {
+                            store_chunk(f32 + pass * R * D + ea, y);
+                            store_chunk(f32 + pass * R * D + eb, y + 2);
+                        } else if (in) {
+                            store_chunk(oa, y);
+                            store_chunk(ob, y + 2);
+                        }
                     }
                 }
             }
-        }
+        };
+        if (full) rows(std::true_type()); else rows(std::false_type());
         cp_wait<0>();  // also the groups of rows past the last head: none in flight
         if (BACK) {
 #pragma unroll
@@ -380,11 +402,12 @@ cudaError_t launch_u(const NormRopeArgs &a) {
 
 template <typename T, int D, bool BACK>
 cudaError_t launch(const NormRopeArgs &a) {
-    // Few rows: one pass a warp spreads them over many SMs.  Many: the token's
-    // cosines, sines and weights are loaded once for up to U * G passes.  8192
-    // tokens of 64 + 64 bf16 heads, forward: G = 1, 2, 4 take 103, 90, 97 us (8
-    // blocks an SM fit at G = 2; 7 or 10 take 93, 94); gradients, where the sums over a
-    // block's rows come on top: 183, 144, 134 us.
+    // Few rows: one pass a warp spreads them over many SMs (1021 tokens of 16 fp32
+    // heads, above the limit: 6.0 us in long items, 6.9 in single passes).  Many: the
+    // token's cosines, sines and weights are loaded once for up to U * G passes.  8192
+    // tokens of 64 + 64 bf16 heads, forward: G = 1, 2, 3, 4 take 96, 81, 83, 83 us
+    // (a plain copy of the bytes 85; of 64 + 8 heads into the cache 60, 54, 60, 64);
+    // gradients, where the sums over a block's rows come on top: 185, 144, 134, 131.
     constexpr int R = 32 / (D / 8);
     constexpr int U = 8 / (int)sizeof(T) / (BACK ? 2 : 1);
     const long rows = (long)a.num_tokens * (a.set[0].heads + a.set[1].heads + a.set[2].heads);
