@@ -10,14 +10,15 @@
 // the kernel is a stream over HBM and its layout serves the loads.
 //
 // Split.  The work is cut into tiles of kTile tokens of one unit (a request's
-// key-value head, or 16 query heads of one).  The tiles of all units, one after the other,
-// are divided evenly among a fixed number of CTAs, whatever the lengths are: no
-// host copy of the lengths, no plan, the same launch for one long request and
-// for many ragged ones.  A unit that lies inside one CTA's range is finished
+// key-value head, or 16 query heads of one).  The tiles of all units, one after the
+// other, are divided evenly (but for the cost of starting a unit) among a fixed
+// number of CTAs, whatever the lengths are: no host copy of the lengths, no plan, the
+// same launch for one long request and for many ragged ones.  A unit that lies inside one CTA's range is finished
 // there; a piece of a unit leaves its unnormalised sums, maxima and
 // exponential sums in the workspace (a CTA has at most two such pieces: the
 // end of one unit and the start of another), and a second kernel joins the
-// pieces of each unit in the order of their tokens.
+// pieces of each unit in the order of their tokens.  Where the table bounds the
+// lengths to short ones, a cluster of CTAs a unit takes the place of both.
 //
 // Inside a CTA each warp streams its own token groups through its own ring
 // of shared-memory stages (cp.async, 16 bytes a lane) with its own running
@@ -91,10 +92,12 @@ __device__ __forceinline__ float hi_of(uint32_t p) { return __uint_as_float(p & 
 
 // ------------------------------------------------------------ work split
 // What the kernel before may have written (it can still be running when this one is
-// scheduled) is read with plain loads behind the wait, never as constant data.
+// scheduled) is never read as constant data: the lengths, which the join reads before
+// its wait, through L2, the rest with plain loads behind the wait (a table entry serves
+// several groups: reading it through L2 each time cost 4 to 15 %).
 // Length of request b as the kernels use it: inside [0, table capacity].
 __device__ __forceinline__ int request_len(const PagedDecodeArgs &a, int b) {
-    return min(max(a.seq_lens[b], 0), a.max_tokens);
+    return min(max(__ldcg(a.seq_lens + b), 0), a.max_tokens);
 }
 // Cost of a unit of `len` tokens, in tiles: the overhead of starting it, then its
 // tiles.  A cut inside the overhead is a cut before the first tile.
@@ -268,13 +271,17 @@ __device__ __forceinline__ Partial warps_sum(const unsigned char *smem, int h, i
 // ldmatrix), so up to 8 (16) query heads share one read of the cache and no
 // row of an MMA is padding when G is 8 (16).  P^T is S^T's accumulator
 // rounded to bf16 with the remainder as a second bf16 operand (P = hi + lo,
-// 2^-17 relative): the tensor pipe is idle most of the time and the second
-// product keeps the result at fp32 accuracy.  fp32 queries are split alike.
-// mma.sync rather than tcgen05: with 8 or 16 columns the products take a few percent
-// of the tensor pipe, and accumulators in registers feed the softmax without a
-// trip through tensor memory.
+// 2^-16 relative): the tensor pipe is idle most of the time and the second
+// product keeps the error far below the output's rounding.  fp32 queries are
+// split alike.
+// mma.sync rather than tcgen05: with 8 columns the products keep the tensor pipe 12 to
+// 15 % busy while HBM is at its limit, and accumulators in registers feed the softmax
+// without a trip through tensor memory.
 // Four warps of a 16-token, 8 KB stage (D = 128) or eight of 4 KB (D = 64): two CTAs
-// an SM either way, 128 KB in flight.
+// an SM either way, 128 KB in flight.  Measured, 8 key-value heads of 128: 128 requests of
+// 1K to 32K tokens 1260 us (7.0 TB/s), one of 128K 88 us, 20 of 4096 58 us; of 64, 20 x
+// 8192 59 us (with four warps 70).  One CTA of eight warps an SM instead: 62 us for the
+// 20 x 4096, 40 instead of 31 for 100 requests up to 600 tokens.
 template <int D_, int NT, bool QF32>
 struct Bf16Core {
     using T = __nv_bfloat16;
@@ -513,7 +520,6 @@ struct Bf16Core {
         }
         cp_wait<0>();
 
-
         // the warps' results
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -553,6 +559,9 @@ struct Bf16Core {
 //   values   a lane owns four columns of all heads (of every other token where 16
 //            lanes cover a row)
 // A group is 16 tokens of 64 dimensions or 8 of 128: 8 KB a stage, as in bf16.
+// 16 requests of 16K / (kv heads) tokens, 128 wide: 49 us with one to four query heads a
+// kv head (5.5 TB/s), 55 with eight, 95 with 16, where the CUDA cores bound it (64 packed
+// FMAs a token and warp).
 template <int D_, int ROWS_>
 struct F32Core {
     using T = float;
@@ -1033,9 +1042,9 @@ template <typename Core, int S> cudaError_t launch_cluster(const PagedDecodeArgs
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// When the cluster kernel serves a call: up to kClusterTiles tiles a CTA with at most
-// eight CTAs a unit, all of them on the SMs at once (CTAs of one unit may queue up to
-// kClusterWaves deep).  64 query and 8 key-value heads of 128, cluster / split kernel:
+// When the cluster kernel serves a call: up to kClusterTiles tiles a CTA, with as many CTAs
+// a unit, at most eight, as fit the SMs at once; units of one CTA may be up to
+// kClusterWaves times what fits.  64 query and 8 key-value heads of 128, cluster / split kernel:
 // 1 x 300 tokens 4.8 / 6.4 us, 16 x 512 8.0 / 12.4, 16 x 1000 11.6 / 15.4, 8 x 2000 11.7 /
 // 15.4, 128 x 128 15.7 / 19.8, 64 x 256 12.8 / 17.1; beyond it, with 16 tiles, 1 x 8000
 // 14.8 / 12.0.

@@ -143,8 +143,9 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
     const int sub = lane / L, u0 = lane % L;
     // the lane's chunks: a rotated pair of chunks, or two behind the rotated part
     const int pairs = a.rotary_dim / 8;  // lanes of the rotated part
-    const int ea = 4 * (u0 < pairs ? u0 : pairs + u0);
-    const int eb = ea + (u0 < pairs ? a.rotary_dim / 2 : (D - a.rotary_dim) / 2);
+    const bool rotated = u0 < pairs;     // elsewhere no partner's infinity or NaN reaches an element
+    const int ea = 4 * (rotated ? u0 : pairs + u0);
+    const int eb = ea + (rotated ? a.rotary_dim / 2 : (D - a.rotary_dim) / 2);
 
     const int nq = (a.set[0].heads + kRows - 1) / kRows;
     const int nk = (a.set[1].heads + kRows - 1) / kRows;
@@ -260,13 +261,17 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
                     if (!FULL && U > 1 && pass * R >= left) break;
                     const bool in = FULL || pass * R + sub < left;
                     const T *row = &stage[warp][0][pass][sub * D];
+                    if (!BACK && kind == 2) {  // values: copied, bit for bit
+                        using Chunk = std::conditional_t<sizeof(T) == 2, uint2, uint4>;
+                        if (in) {
+                            *reinterpret_cast<Chunk *>(oa) = *reinterpret_cast<const Chunk *>(row + ea);
+                            *reinterpret_cast<Chunk *>(ob) = *reinterpret_cast<const Chunk *>(row + eb);
+                        }
+                        continue;
+                    }
                     float2 x[4];
                     load_chunk(row + ea, x);
                     load_chunk(row + eb, x + 2);
-                    if (!BACK && kind == 2) {  // values: copied (exact: the chunks are not rounded anew)
-                        if (in) store_chunk(oa, x), store_chunk(ob, x + 2);
-                        continue;
-                    }
                     float r = 1.f;
                     if (norm) {
                         float2 ss = ptx::f2_mul(x[0], x[0]);
@@ -284,7 +289,8 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
                         float2 dot = twice(0.f);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            g4[i] = ptx::f2_fma(dy[i], ca[i], ptx::f2_mul(partner<INTER>(dy, i), cb[i]));
+                            g4[i] = ptx::f2_mul(dy[i], ca[i]);
+                            if (rotated) g4[i] = ptx::f2_fma(partner<INTER>(dy, i), cb[i], g4[i]);
                             if (norm) {
                                 x[i] = ptx::f2_mul(x[i], rr);
                                 const float2 p = ptx::f2_mul(g4[i], x[i]);
@@ -304,7 +310,8 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
                         float2 y[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            y[i] = ptx::f2_fma(x[i], ca[i], ptx::f2_mul(partner<INTER>(x, i), cb[i]));
+                            y[i] = ptx::f2_mul(x[i], ca[i]);
+                            if (rotated) y[i] = ptx::f2_fma(partner<INTER>(x, i), cb[i], y[i]);
                             if (norm) y[i] = ptx::f2_mul(y[i], rr);
                         }
                         if (in && f32) {

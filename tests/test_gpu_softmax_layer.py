@@ -189,6 +189,19 @@ def test_norm_rope_edges():
     a = la.qk_norm_rope(q, k, far, table, q_weight=w[0], k_weight=w[1])
     b = la.qk_norm_rope(q, k, near, table, q_weight=w[0], k_weight=w[1])
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    # without a norm: an infinity or NaN stays with its rotated pair
+    x = q.clone()
+    x[0, 0, 50], x[1, 1, 3] = float("inf"), float("nan")
+    half = la.rotary_table(100, 32, device="cuda")
+    out, _ = la.qk_norm_rope(x, None, near, half)
+    want, bound = ref.norm_rope(c(q), None, 0, c(half), c(near), False)
+    bad = torch.zeros(4, 2, 64, dtype=torch.bool)
+    bad[0, 0, 50] = bad[1, 1, 3] = bad[1, 1, 19] = True  # 50 is not rotated, 3 with 19
+    assert torch.equal(~torch.isfinite(out).cpu(), bad)
+    ref.within(out.cpu()[~bad], want[~bad], bound[~bad], ref.u_of(BF16), "finite")
+    out, _ = la.qk_norm_rope(x, None)  # neither norm nor rotation: a copy
+    assert torch.equal(torch.isnan(out), torch.isnan(x))  # (a NaN's payload is not kept)
+    assert torch.equal(out[~torch.isnan(x)], x[~torch.isnan(x)])
     # rows of zeros: zero, and a zero gradient direction of r only
     z = torch.zeros_like(q)
     out, _ = la.qk_norm_rope(z, None, near, table, q_weight=w[0], eps=1e-6)
@@ -224,6 +237,7 @@ def test_paged_append(dtype, t, h, hk, d, page, rot):
     both = randn((pages, 2, hk, page, d), dtype, g)  # one array of pages, keys and values
     kc, vc = both[:, 0], both[:, 1]
     before = both.clone()
+    v.view(torch.int16 if dtype == BF16 else torch.int32)[0, 0, :3] = -5  # NaNs with a payload
     slots = torch.randperm(pages * page, generator=g, device="cuda")[:t].int()
     if t > 4:  # padding and a slot outside the pool: no row written
         slots[1], slots[3] = -1, pages * page
@@ -237,7 +251,8 @@ def test_paged_append(dtype, t, h, hk, d, page, rot):
         if 0 <= s < pages * page:
             before[s // page, 0, :, s % page] = wk[i]
             before[s // page, 1, :, s % page] = v[i]
-    assert torch.equal(both, before)
+    bits = torch.int16 if dtype == BF16 else torch.int32  # values are copied bit for bit
+    assert torch.equal(both.view(bits), before.view(bits))
 
 
 def test_paged_append_no_tokens_and_refusals():
