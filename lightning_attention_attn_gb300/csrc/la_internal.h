@@ -13,7 +13,9 @@ namespace la {
 // while the kernel before it in the stream is finishing, and waits
 // (grid_dependency_wait) before its first global-memory access, so stream
 // order is kept for every memory effect.  Only kernels that begin with that
-// wait are launched this way.
+// wait are launched this way (the join of the paged attention reads the lengths
+// before it: the kernel in front of it lets it be scheduled only once it has
+// itself waited for whatever wrote them).
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_dependent(void (*kern)(KArgs...), unsigned grid, unsigned block,
                                     size_t smem, cudaStream_t stream, Args &&...args) {
