@@ -704,6 +704,43 @@ def test_two_graphs_and_side_streams(lengths):
         assert all(torch.equal(o, want) for o in outs)
 
 
+def test_two_host_threads():
+    """Calls from two threads, each on its own stream: results as alone."""
+    import threading
+    g = gen(24)
+    kc, vc, bt, lens = pool([2000, 3, 700], 16, 2, 64, BF16, g)
+    wide = torch.full((3, 3000), -1, dtype=torch.int32, device="cuda")
+    wide[:, :bt.shape[1]] = bt
+    q = randn((3, 8, 64), BF16, g)
+    case = (FP32, 60, 4, 4, 64, 64, False, True)
+    _, x, y, qw, kw, pos, table = norm_inputs(case, 25)
+    dy = randn(x.shape, FP32, g)
+
+    def work():
+        return (la.paged_decode(q, kc, vc, bt, lens), la.paged_decode(q, kc, vc, wide, lens),
+                *la.qk_norm_rope_backward(x, y, pos, table, dy, dy, q_weight=qw, k_weight=kw))
+
+    want = work()
+    torch.cuda.synchronize()
+    bad = []
+
+    def run():
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(30):
+                got = work()
+                stream.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                    bad.append(1)
+
+    threads = [threading.Thread(target=run) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
 def test_backward_in_a_graph_beside_eager_calls():
     case = (BF16, 130, 8, 2, 128, 64, False, True)
     g, q, k, qw, kw, pos, table = norm_inputs(case, 23)
