@@ -507,11 +507,13 @@ int64_t lightning_attn_paged_step_workspace_bytes(int32_t batch, int32_t num_hea
  *              of every new token; slot -1, position 0 for tokens of requests
  *              not served and for entries past the last new token.  num_tokens is
  *              the arrays' size: tokens past it are not written.
- * cu_seqlens   [batch + 1] int32: first new token of every request, and the total.
+ * cu_seqlens   [batch + 1] int32: first new token of every request, and the total;
+ *              2^31 - 1 where that or more come before (past num_tokens: the
+ *              other outputs do not depend on it).
  * served       [batch] bytes, 1 or 0.
  * seq_lens_out [batch], free_count_out [1] int32: lengths after the step (a request
  *              not served keeps its length, 0 if it finished) and the stack's
- *              height.  They may be seq_lens and free_count.
+ *              height.  They may be seq_lens and free_count (not new_lens).
  * batch <= 8192 (LA_ERR_UNSUPPORTED above).  Other overlaps are not allowed.
  */
 la_status lightning_attn_paged_reserve(

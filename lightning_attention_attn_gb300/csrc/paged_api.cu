@@ -423,6 +423,9 @@ la_status lightning_attn_paged_reserve(
                           free_pages, slots, positions};
     for (const void *p : ints)
         if (!aligned(p, 4)) return LA_INVALID("int32 arrays must be 4-byte aligned");
+    // a long step reads new_lens again after the other arrays have been written
+    if (new_lens == seq_lens_out || new_lens == free_count_out)
+        return LA_INVALID("new_lens is an output too");
     la::PagedReserveArgs a;
     a.block_table = block_table;
     a.table_stride = table_stride;

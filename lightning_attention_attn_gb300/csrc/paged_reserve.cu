@@ -251,7 +251,8 @@ paged_fill_kernel(const __grid_constant__ PagedReserveArgs a) {
             from = __ldcg(a.cu_seqlens + b);
             const int len = __ldcg(a.seq_lens_out + b);
             ok = __ldcg(a.served + b) != 0;
-            was = ok ? len - (__ldcg(a.cu_seqlens + b + 1) - from) : len;
+            // (not from the offsets, which stop at 2^31 - 1)
+            was = ok ? len - max(__ldcg(a.new_lens + b), 0) : len;
             if (ok) need = blocks_of(len, a.page_size) - blocks_of(was, a.page_size);
         }
         Pair all;

@@ -193,8 +193,9 @@ def paged_reserve(block_table, seq_lens, new_lens, free_pages, free_count, page_
     to the stack first.  Requests are served in order as long as there are
     pages (a request that needs none always is); the tokens of the others get
     slot -1.  slots, positions: int32 [num_tokens] (past the last new token: -1
-    and 0); cu_seqlens: int32 [B + 1]; served: bool [B].  The new lengths and the
-    stack's height go to seq_lens_out and free_count_out: by default in place.
+    and 0); cu_seqlens: int32 [B + 1] (2^31 - 1 from there on); served: bool [B].  The
+    new lengths and the stack's height go to seq_lens_out and free_count_out: by
+    default in place (new_lens is never an output).
     """
     return (_binding or _calls()).paged_reserve(
         block_table, seq_lens, new_lens, free_pages, free_count, page_size, num_tokens, finished,

@@ -67,3 +67,33 @@ def test_long_sums_do_not_drift(d, h):
     mean = out.mean((0, 1, 2)).abs().item()
     print(f"mean {mean:.3e}, bound {bound:.3e}")
     assert mean <= bound
+
+
+# ------------------------------------------------------------- page reservation
+@pytest.mark.parametrize("num_tokens", [16, 4096, 4097, 5016])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_paged_reserve_total_past_32_bits(num_tokens, in_place):
+    """A refused request of nearly 2^31 tokens before a served one: the pages, slots and lengths
+    are those of the requests themselves, and the offsets stop at 2^31 - 1."""
+    page, width, pages = 16, 400, 1000
+    table = torch.full((4, width), -7, dtype=torch.int32, device="cuda")
+    lens, new = ints([0, 3, 20, 0]), ints([5000, 2 ** 31 - 1, 16, 2 ** 31 - 1])
+    table[1, 0], table[2, :2] = 998, ints([996, 997])
+    stack, count = torch.arange(pages, device="cuda").int(), ints([990])
+    out = {} if in_place else dict(seq_lens_out=torch.empty_like(lens), free_count_out=torch.empty_like(count))
+    slots, pos, cu, served = la.paged_reserve(table, lens, new, stack, count, page, num_tokens, **out)
+    assert served.tolist() == [True, False, True, False]
+    assert out.get("seq_lens_out", lens).tolist() == [5000, 3, 36, 0]
+    assert out.get("free_count_out", count).tolist() == [990 - 313 - 1]
+    assert stack.tolist() == list(range(pages))
+    want = torch.full((4, width), -7)
+    want[0, :313] = 989 - torch.arange(313)  # from the top of the stack
+    want[1, 0] = 998
+    want[2, :3] = torch.tensor([996, 997, 989 - 313])
+    assert torch.equal(table.cpu(), want.int())
+    assert cu.tolist() == [0, 5000, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1]
+    t = torch.arange(num_tokens)
+    mine = t < 5000
+    assert torch.equal(pos.cpu(), torch.where(mine, t, 0).int())
+    rows = want[0, (t // page).clamp(max=312)] * page + t % page
+    assert torch.equal(slots.cpu(), torch.where(mine, rows, -1).int())
