@@ -448,7 +448,11 @@ la_status lightning_attn_paged_append(
  *              16-byte aligned; scratch, not shared by calls that may overlap
  *              (two captured graphs that may run at once need one each).
  * num_heads is a multiple of num_kv_heads.  What lies in the cache past a
- * request's last token is not used, whatever it holds.
+ * request's last token is not used, whatever it holds.  Infinities that are
+ * attended to count as the formula has it: a score of -infinity has weight 0, one
+ * of +infinity (or NaN) makes the head's row NaN, an infinite value makes its
+ * column that infinity, or NaN where both signs meet or where its weight is 0 or
+ * less than 2^-100 of the largest.
  */
 la_status lightning_attn_paged_decode(
     const void *q, int64_t q_stride, const void *k_cache, int64_t k_page_stride,

@@ -86,9 +86,21 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&p);
 }
-// The value of each half of a packed pair, exactly.
-__device__ __forceinline__ float lo_of(uint32_t p) { return __uint_as_float(p << 16); }
-__device__ __forceinline__ float hi_of(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
+// x as two bf16 numbers, hi + lo, off by at most 2^-16 |x|: x cut off after hi's bits, and
+// what that leaves (and 2^-23 x more, for where it leaves nothing).  So both have x's
+// sign and neither is 0 unless x is (or, for lo, below 2^-110), and an infinity times x is
+// what it is times either.  Rounding x to the nearest hi instead halves the error (2e-6 of an
+// output before its own rounding, instead of 4e-6, and the same time) but lets lo be 0
+// or of the other sign, which makes NaN of an infinite key or value.
+struct Parts {
+    uint32_t hi, lo;  // of a pair
+};
+__device__ __forceinline__ Parts parts_of(float x, float y) {
+    constexpr float kUp = 1.f + 0x1p-23f;
+    const uint32_t u = __float_as_uint(x), v = __float_as_uint(y);
+    return {__byte_perm(u, v, 0x7632), pack2(fmaf(x, kUp, -__uint_as_float(u & 0xffff0000u)),
+                                             fmaf(y, kUp, -__uint_as_float(v & 0xffff0000u)))};
+}
 
 // ------------------------------------------------------------ work split
 // What the kernel before may have written (it can still be running when this one is
@@ -269,15 +281,14 @@ __device__ __forceinline__ Partial warps_sum(const unsigned char *smem, int h, i
 //     S^T [16 tokens x 8] = K [16 x D] Q^T,   O^T [D x 8] += V^T [D x 16] P^T
 // K and V are the A operands straight from shared memory (V transposed by
 // ldmatrix), so up to 8 (16) query heads share one read of the cache and no
-// row of an MMA is padding when G is 8 (16).  P^T is S^T's accumulator
-// rounded to bf16 with the remainder as a second bf16 operand (P = hi + lo,
-// 2^-16 relative): the tensor pipe is idle most of the time and the second
-// product keeps the error far below the output's rounding.  fp32 queries are
-// split alike.  O^T of a group is added to the running sums on the CUDA cores: the tensor
-// core drops the bits that do not fit where the CUDA cores round to nearest, and over the 500
-// groups a warp adds up at 64 requests of 9K to 32K tokens that made the sums (before the
-// output's rounding) 7e-6 too small, their error 9.5e-6 instead of 2.3e-6.  It costs 2 % at
-// 64 wide with 16 heads a kv head (37.2 -> 38.1 us), less than 0.5 % elsewhere.
+// row of an MMA is padding when G is 8 (16).  P^T is S^T's accumulator as two
+// bf16 operands (P = hi + lo, 2^-16 relative; parts_of): the tensor pipe is idle most of
+// the time and the second product keeps the error far below the output's rounding.
+// fp32 queries are split alike.  O^T of a group is added to the running sums on the CUDA
+// cores: the tensor core drops the bits that do not fit where the CUDA cores round to
+// nearest, which over the 500 groups a warp adds up at 64 requests of 9K to 32K tokens made
+// the sums 7e-6 too small (now 1e-7).  It costs 2 % at 64 wide with 16 heads a kv head
+// (37.2 -> 38.1 us), less than 0.5 % elsewhere.
 // mma.sync rather than tcgen05: with 8 columns the products keep the tensor pipe 12 to
 // 15 % busy while HBM is at its limit, and accumulators in registers feed the softmax
 // without a trip through tensor memory.
@@ -385,9 +396,9 @@ struct Bf16Core {
                         float2 x = make_float2(0.f, 0.f);
                         if (nt * 8 + g < heads)
                             x = __ldcg(reinterpret_cast<const float2 *>(qp + ks * 16 + i * 8));
-                        const uint32_t p = pack2(x.x, x.y);
-                        qb[nt][ks][i] = p;
-                        ql[nt][ks][i] = pack2(x.x - lo_of(p), x.y - hi_of(p));
+                        const Parts p = parts_of(x.x, x.y);
+                        qb[nt][ks][i] = p.hi;
+                        ql[nt][ks][i] = p.lo;
                     }
             }
         }
@@ -495,11 +506,11 @@ struct Bf16Core {
                 const float p2 = ex2(s[nt][2] - b0), p3 = ex2(s[nt][3] - b1);
                 l[nt][0] += p0 + p2;
                 l[nt][1] += p1 + p3;
-                const uint32_t h0 = pack2(p0, p1), h1 = pack2(p2, p3);
-                ph[nt][0] = transpose8x8(h0);
-                ph[nt][1] = transpose8x8(h1);
-                pl[nt][0] = transpose8x8(pack2(p0 - lo_of(h0), p1 - hi_of(h0)));
-                pl[nt][1] = transpose8x8(pack2(p2 - lo_of(h1), p3 - hi_of(h1)));
+                const Parts a0 = parts_of(p0, p1), a1 = parts_of(p2, p3);
+                ph[nt][0] = transpose8x8(a0.hi);
+                ph[nt][1] = transpose8x8(a1.hi);
+                pl[nt][0] = transpose8x8(a0.lo);
+                pl[nt][1] = transpose8x8(a1.lo);
             }
 #pragma unroll
             for (int k0 = 0; k0 < KS; k0 += kAhead) {

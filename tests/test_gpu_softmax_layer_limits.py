@@ -97,3 +97,117 @@ def test_paged_reserve_total_past_32_bits(num_tokens, in_place):
     assert torch.equal(pos.cpu(), torch.where(mine, t, 0).int())
     rows = want[0, (t // page).clamp(max=312)] * page + t % page
     assert torch.equal(slots.cpu(), torch.where(mine, rows, -1).int())
+
+
+# ------------------------------------------------ infinities that are attended to
+def attend(q, kc, vc, bt, lens, out, lse, without=()):
+    """Checks out and lse: NaN and infinities where the formula has them, the rest within
+    the bounds.  without: (request, block) that the reference leaves out, for keys whose
+    score is -infinity (weight 0), which would make the bound itself infinite."""
+    left = bt.clone()
+    for b, blk in without:
+        left[b, blk] = -1
+    want, wlse, bound, lbound = ref.attention(q.cpu(), kc.cpu(), vc.cpu(), left.cpu(), lens.cpu(),
+                                              q.shape[-1] ** -0.5)
+    out, lse = out.cpu().double(), lse.cpu().double()
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    some = ~torch.isnan(want)
+    bound = torch.where(torch.isfinite(want), bound, torch.zeros_like(bound))
+    ref.within(out[some], want[some], bound[some], ref.u_of(vc.dtype), "out")
+    some = ~torch.isnan(wlse)
+    ref.within(lse[some], wlse[some], lbound[some], ref.u_of(FP32), "lse")
+    return want
+
+
+def caches(lens, page, hk, d, dtype, g):
+    blocks = [-(-n // page) for n in lens]
+    kc, vc = (randn((sum(blocks) + 1, hk, page, d), dtype, g) for _ in range(2))
+    bt = torch.full((len(lens), max(blocks)), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for b, n in enumerate(blocks):
+        bt[b, :n] = torch.arange(at, at + n)
+        at += n
+    return kc, vc, bt, ints(lens)
+
+
+def widened(bt, width):
+    wide = torch.full((bt.shape[0], width), -1, dtype=torch.int32, device="cuda")
+    wide[:, :bt.shape[1]] = bt
+    return wide
+
+
+SHAPES = [(BF16, 128, 8, 1), (BF16, 64, 12, 1), (BF16, 64, 4, 2), (BF16, 128, 32, 2), (FP32, 64, 6, 2),
+          (FP32, 128, 16, 1)]
+
+
+@pytest.mark.parametrize("wide", [False, True])  # one cluster a unit; the split over all CTAs
+@pytest.mark.parametrize("dtype, d, h, hk", SHAPES)
+def test_infinite_values(dtype, d, h, hk, wide):
+    """Infinite values among those attended to: their column is that infinity for every head,
+    or NaN where both signs or a NaN meet; the other columns are what they are without it.
+    Scores are small, so that every weight is a normal number."""
+    g = gen(d + h)
+    lens = [700, 33, 1, 2000]
+    kc, vc, bt, sl = caches(lens, 16, hk, d, dtype, g)
+    v = vc[:, 0]
+    v[bt[0, 3], 5, 7] = INF
+    v[bt[0, 40], 1, 9] = -INF
+    v[bt[0, 1], 2, 11], v[bt[0, 30], 2, 11] = INF, -INF
+    v[bt[1, 2], 0, 0] = -INF
+    v[bt[2, 0], 0, d - 1] = INF
+    v[bt[3, 100], 8, 20] = NAN
+    q = randn((4, h, d), dtype, g)
+    table = widened(bt, 20000) if wide else bt
+    lse = torch.empty((4, h), device="cuda")
+    out = la.paged_decode(q, kc, vc, table, sl, lse=lse)
+    want = attend(q, kc, vc, bt, sl, out, lse)
+    assert torch.isinf(want[0, 0, 7]) and torch.isnan(want[0, 0, 11]) and torch.isfinite(want[0, 0, 8])
+    # the fused step of the same caches
+    k1, v1 = kc[bt[:, 0].long(), :, 0].contiguous(), vc[bt[:, 0].long(), :, 0].contiguous()
+    out = la.paged_step(q, k1, v1, None, None, kc, vc, bt[:, 0] * 16, table, sl, lse=lse)
+    attend(q, kc, vc, bt, sl, out, lse)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("dtype, d, h, hk", SHAPES)
+def test_infinite_keys(dtype, d, h, hk, wide):
+    """A key with an infinity has the score -infinity (weight 0) for queries of one sign there and
+    +infinity (NaN) for the other: the same in paged_decode and in paged_step, whose queries
+    are fp32."""
+    g = gen(d + h + 1)
+    lens = [600, 17, 40]
+    kc, vc, bt, sl = caches(lens, 1, hk, d, dtype, g)  # a page a token: the reference can leave it out
+    kc[bt[0, 100], :, 0, 3] = -INF
+    kc[bt[0, 500], :, 0, 3] = -INF
+    kc[bt[1, 16], :, 0, 3] = -INF
+    q = randn((3, h, d), dtype, g)
+    q[:, :, 3] = q[:, :, 3].abs() + 0.5
+    gone = [(0, 100), (0, 500), (1, 16)]
+    table = widened(bt, 300000) if wide else bt
+    lse = torch.empty((3, h), device="cuda")
+    weight = 1 + 0.25 * torch.rand(d, generator=g, device="cuda")  # queries that are no bf16 numbers
+    k1, v1 = kc[bt[:, 0].long(), :, 0].contiguous(), vc[bt[:, 0].long(), :, 0].contiguous()
+    args = dict(q_weight=weight, k_weight=torch.ones(d, device="cuda"), eps=EPS)
+    for sign in (1, -1):
+        q[0, 0, 3] = sign * q[0, 0, 3].abs()  # one head that sees +infinity at the second turn
+        out = la.paged_decode(q, kc, vc, table, sl, lse=lse)
+        want = attend(q, kc, vc, bt, sl, out, lse, gone) if sign > 0 else None
+        step = la.paged_step(q, k1, v1, None, None, kc, vc, bt[:, 0].contiguous(), table, sl, lse=lse, **args)
+        rotated, _ = ref.norm_rope(q.cpu(), weight.cpu(), EPS, None, None, False)
+        want, wlse, bound, _ = ref.attention(rotated, kc.cpu(), vc.cpu(), _left(bt, gone).cpu(), sl.cpu(),
+                                             d ** -0.5)
+        # 2^-16 of an element for split queries, their own 64 e beside it: see test_paged_step
+        more = 1 + (2.0 ** -16 + 128 * ref.E) / (2 * ref.E * (d + 8))
+        some = torch.ones(3, h, dtype=torch.bool)
+        if sign < 0:
+            some[0, 0] = False
+            assert torch.isnan(out[0, 0]).all() and torch.isnan(step[0, 0]).all()
+        ref.within(step.cpu()[some], want[some], bound[some] * more, ref.u_of(dtype), "step")
+        assert torch.isfinite(out.cpu()[some]).all()
+
+
+def _left(bt, gone):
+    left = bt.clone()
+    for b, blk in gone:
+        left[b, blk] = -1
+    return left
