@@ -440,7 +440,8 @@ la_status lightning_attn_paged_append(
  *              [0, num_pages) leaves its tokens out of the softmax.
  * seq_lens     [batch] int32; negative counts as 0, more than table_width *
  *              page_size as that.  A request with no token (or none left) gets
- *              zeros, and -infinity as its lse.
+ *              zeros, and -infinity as its lse; one whose scores are all -infinity
+ *              NaN, with the same lse.
  * scale        softmax scale (e.g. head_dim^-1/2).
  * out          [batch, num_heads, head_dim], contiguous.
  * lse          nullable; [batch, num_heads] fp32: log sum_t e^(scale q . k_t).

@@ -46,6 +46,9 @@ constexpr int kOverhead = kOverheadBytes / (2 * kTile * D * (int)sizeof(T));  //
 constexpr int kStages = 3;    // of a warp's ring: two in flight, one read
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_huge_valf();
+// The running maximum is -kInf until a token is present and at least kLowest from there on,
+// so that scores that are all -infinity (0 / 0: NaN) are told from no tokens (zeros).
+constexpr float kLowest = -3.402823466e38f;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
     // an invalid row is filled with zeros, nothing is read
@@ -244,7 +247,7 @@ struct Partial {
     // Writes columns d .. d + 3 of the output's row (and its lse).
     template <typename T>
     __device__ __forceinline__ void write(const PagedDecodeArgs &a, size_t row, int d) const {
-        const float r = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays NaN
+        const float r = m == -kInf ? 0.f : 1.f / sum;  // no token; a sum of 0 gives NaN
         T *o = static_cast<T *>(a.out) + row * a.head_dim + d;
         if constexpr (sizeof(T) == 2)
             *reinterpret_cast<uint2 *>(o) = make_uint2(pack2(acc.x * r, acc.y * r), pack2(acc.z * r, acc.w * r));
@@ -469,6 +472,7 @@ struct Bf16Core {
                     if (QF32) s[nt][i] += s3[nt][i] + s4[nt][i];
                 }
             const bool v0 = (have[0] >> g) & 1, v1 = (have[0] >> (g + 8)) & 1;
+            const float least = have[0] ? kLowest : -kInf;
             uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -477,7 +481,8 @@ struct Bf16Core {
                     s[nt][j] = v0 ? s[nt][j] * a.scale_log2 : -kInf;
                     s[nt][2 + j] = v1 ? s[nt][2 + j] * a.scale_log2 : -kInf;
                 }
-                float t0m = fmaxf(s[nt][0], s[nt][2]), t1m = fmaxf(s[nt][1], s[nt][3]);
+                float t0m = fmaxf(fmaxf(s[nt][0], s[nt][2]), least);
+                float t1m = fmaxf(fmaxf(s[nt][1], s[nt][3]), least);
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) {
                     t0m = fmaxf(t0m, __shfl_xor_sync(0xffffffffu, t0m, d));
@@ -735,7 +740,7 @@ struct F32Core {
             }
             __syncwarp();
             float p[kGrp / TS];
-            float top = -kInf;
+            float top = have[0] ? kLowest : -kInf;
 #pragma unroll
             for (int i = 0; i < kGrp / TS; ++i) {
                 const int t = i * TS + lane / ROWS;

@@ -211,3 +211,27 @@ def _left(bt, gone):
     for b, blk in gone:
         left[b, blk] = -1
     return left
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("dtype, d, h, hk", SHAPES)
+def test_scores_that_are_all_minus_infinity(dtype, d, h, hk, wide):
+    """0 / 0: NaN, with -infinity as the logarithm of the sum; zeros only where there is no
+    token.  A finite score anywhere makes the others weight 0."""
+    g = gen(d + h + 2)
+    lens = [300, 1, 0, 513, 40]
+    kc, vc, bt, sl = caches(lens, 16, hk, d, dtype, g)
+    q = randn((5, h, d), dtype, g)
+    q[:, :, 3] = 1.0
+    for b, n in ((0, 300), (1, 1), (3, 513)):
+        kc[bt[b, :-(-n // 16)].long(), :, :, 3] = -INF
+    kc[bt[3, 32], :, 0, 3] = 0.25          # request 3: its last token alone counts
+    bt[4] = -1                              # request 4: no page is left
+    table = widened(bt, 20000) if wide else bt
+    lse = torch.empty((5, h), device="cuda")
+    out = la.paged_decode(q, kc, vc, table, sl, lse=lse)
+    assert torch.isnan(out[:2]).all() and (lse[:2] == -INF).all()
+    assert (out[2] == 0).all() and (lse[2] == -INF).all()
+    assert (out[4] == 0).all() and (lse[4] == -INF).all()
+    only = vc[bt[3, 32].long(), :, 0].repeat_interleave(h // hk, 0)
+    assert torch.equal(out[3], only)
