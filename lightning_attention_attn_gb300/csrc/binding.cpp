@@ -92,7 +92,9 @@ Tensor part_of(const Tensor &t, int64_t at, int64_t n) {
 
 // Device, stream and allocations of one call: every tensor is on the first
 // one's device, which is current while the call runs; what the call allocates
-// belongs to the stream that it is launched on.
+// belongs to the stream that it is launched on.  Where that is not the caller's current
+// one, the allocator is told that the call's stream uses the inputs and the caller's the
+// new outputs: neither is handed out again before both streams are done with it.
 class Call {
   public:
     Call(PyObject *first, const char *name, PyObject *stream) {
@@ -101,8 +103,9 @@ class Call {
             refuse(PyExc_ValueError, "%s must be a CUDA tensor (got %s)", name, t.device().str().c_str());
         device_ = t.device();
         guard_.emplace(device_.index());
+        const auto current = c10::cuda::getCurrentCUDAStream(device_.index());
         if (none(stream)) {
-            stream_ = c10::cuda::getCurrentCUDAStream(device_.index()).stream();
+            stream_ = current.stream();
         } else {
             PyObject *h = PyObject_GetAttrString(stream, "cuda_stream");
             if (!h) throw PythonError();
@@ -118,10 +121,15 @@ class Call {
                 refuse(PyExc_ValueError, "stream is on device %ld, the tensors on %s", index,
                                           device_.str().c_str());
             stream_ = static_cast<cudaStream_t>(raw);
-            // the null stream has no external handle; it is the default stream
-            on_.emplace(raw ? c10::cuda::getStreamFromExternal(stream_, device_.index())
-                            : c10::cuda::getDefaultCUDAStream(device_.index()));
+            if (stream_ != current.stream()) {
+                // the null stream has no external handle; it is the default stream
+                own_ = raw ? c10::cuda::getStreamFromExternal(stream_, device_.index())
+                           : c10::cuda::getDefaultCUDAStream(device_.index());
+                on_.emplace(*own_);
+                current_ = current;
+            }
         }
+        used(t);
     }
     void *stream() const { return stream_; }
 
@@ -130,17 +138,17 @@ class Call {
         if (t.device() != device_)
             refuse(PyExc_ValueError, "%s must be on %s (got %s)", name, device_.str().c_str(),
                                       t.device().str().c_str());
+        used(t);
         return t;
     }
     Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
-        return at::detail::empty_cuda(shape, type, device_, std::nullopt);
+        const Tensor t = at::detail::empty_cuda(shape, type, device_, std::nullopt);
+        if (current_) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), *current_);
+        return t;
     }
     // [tokens, heads, d], each token's heads contiguous, any stride between tokens
     Rows rows(const Tensor &t, const char *name, int64_t tokens, int64_t heads, int64_t d,
               at::ScalarType type) const {
-        if (t.device() != device_)
-            refuse(PyExc_ValueError, "%s must be on %s (got %s)", name, device_.str().c_str(),
-                                      t.device().str().c_str());
         if (t.scalar_type() != type || t.dim() != 3 || t.size(0) != tokens || t.size(1) != heads ||
             t.size(2) != d)
             refuse(PyExc_ValueError, "%s must be %s of shape (%lld, %lld, %lld)", name,
@@ -152,12 +160,12 @@ class Call {
     }
     Rows rows(PyObject *o, const char *name, int64_t tokens, int64_t heads, int64_t d,
               at::ScalarType type) const {
-        return rows(tensor(o, name), name, tokens, heads, d, type);
+        return rows(here(o, name), name, tokens, heads, d, type);
     }
     // An output of that shape: the caller's, or a new one in `made`.
     Rows output(PyObject *o, const char *name, int64_t tokens, int64_t heads, int64_t d,
                 at::ScalarType type, Tensor &made) const {
-        made = none(o) ? empty({tokens, heads, d}, type) : tensor(o, name);
+        made = none(o) ? empty({tokens, heads, d}, type) : here(o, name);
         return rows(made, name, tokens, heads, d, type);
     }
     int32_t *ints(PyObject *o, const char *name, int64_t n) const {
@@ -186,8 +194,15 @@ class Call {
     }
 
   private:
+    // A tensor of the caller's, which the call's stream reads or writes.
+    void used(const Tensor &t) const {
+        if (own_) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), *own_);
+    }
+
     at::Device device_{at::kCUDA, 0};
     cudaStream_t stream_ = nullptr;
+    // the call's stream and the caller's, where they differ
+    std::optional<c10::cuda::CUDAStream> own_, current_;
     std::optional<c10::cuda::CUDAGuard> guard_;
     std::optional<c10::cuda::CUDAStreamGuard> on_;
     c10::DataPtr scratch_;

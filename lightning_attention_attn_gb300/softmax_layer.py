@@ -15,8 +15,11 @@ As in the rest of the package, nothing is computed here and there is no
 fallback: a native binding (``csrc/binding.cpp``) checks the arguments and
 launches the library's kernels on ``stream`` (default: the current stream
 of the tensors' device, whichever device is current).  Scratch memory and
-outputs that a call allocates come from that stream's pool, so they are safe
-on any stream and inside a CUDA graph.
+outputs that a call allocates come from that stream's pool.  Where ``stream`` is
+not the current one, its use of the inputs and the current stream's use of the
+outputs are recorded with the allocator, so either may be dropped after the call;
+a third stream's use is the caller's to record, and so is the order of the streams
+(``wait_stream``).
 """
 from __future__ import annotations
 

@@ -235,3 +235,47 @@ def test_scores_that_are_all_minus_infinity(dtype, d, h, hk, wide):
     assert (out[4] == 0).all() and (lse[4] == -INF).all()
     only = vc[bt[3, 32].long(), :, 0].repeat_interleave(h // hk, 0)
     assert torch.equal(out[3], only)
+
+
+# ------------------------------------------------------------------- streams
+def busy(stream):
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(200_000_000)  # about 0.1 s
+
+
+def test_outputs_and_inputs_of_a_call_on_another_stream():
+    """Memory of a call on a stream that is not the current one is not handed out again
+    while either stream still has to use it."""
+    g = gen(30)
+    side, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    n, h, d = 1031, 16, 128  # a size that nothing else has
+    x = randn((n, h, d), BF16, g)
+    la.qk_norm_rope(x, None, stream=side)
+    torch.cuda.synchronize()
+
+    # the output: dropped while the current stream has yet to read it
+    out, _ = la.qk_norm_rope(x, None, stream=side)
+    here.wait_stream(side)
+    busy(here)
+    copy = out.clone()
+    at, want = out.data_ptr(), x.clone()
+    del out
+    with torch.cuda.stream(side):
+        again = torch.empty((n, h, d), dtype=BF16, device="cuda")
+    assert again.data_ptr() != at
+    again, _ = la.qk_norm_rope(torch.zeros_like(x), None, stream=side)
+    assert again.data_ptr() != at
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want)
+    del again, copy
+
+    # an input: dropped while the call has yet to run
+    y = x.clone()
+    side.wait_stream(here)
+    busy(side)
+    out, _ = la.qk_norm_rope(y, None, stream=side)
+    at = y.data_ptr()
+    del y
+    assert torch.empty((n, h, d), dtype=BF16, device="cuda").data_ptr() != at
+    torch.cuda.synchronize()
+    assert torch.equal(out, x)
