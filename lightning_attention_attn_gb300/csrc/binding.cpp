@@ -208,6 +208,15 @@ class Call {
     c10::DataPtr scratch_;
 };
 
+// A tensor of the caller's has been written: autograd checks the version of what it saved.
+// (Tensors made in inference mode have none.)
+void written(const Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(PyObject *o) {
+    if (!none(o)) written(THPVariable_Unpack(o));
+}
+
 // Raises the package's error for a status that is not LA_OK.
 void check(la_status status, const char *name) {
     if (status == LA_OK) return;
@@ -380,6 +389,8 @@ PyObject *qk_norm_rope(PyObject *const *a) {
                                            s.kv_heads, s.d, s.code, qo.p, qo.stride, ko.p, ko.stride,
                                            call.stream());
     });
+    written(a[8]);
+    if (has_k) written(a[9]);
     return tuple(q_out, k_out);
 }
 
@@ -416,6 +427,8 @@ PyObject *qk_norm_rope_backward(PyObject *const *a) {
             dkw.defined() ? static_cast<float *>(dkw.data_ptr()) : nullptr, ws.first, ws.second,
             call.stream());
     });
+    written(a[10]);
+    if (has_k) written(a[11]);
     return tuple(dq_, dk_, dqw, dkw);
 }
 
@@ -439,6 +452,7 @@ PyObject *paged_append(PyObject *const *a) {
             r.interleaved, r.qw, r.kw, r.eps, s.tokens, s.heads, s.kv_heads, s.d, s.code, qo.p,
             qo.stride, c.k, c.ks, c.v, c.vs, slots, c.pages, c.page, call.stream());
     });
+    for (int i : {5, 6, 12}) written(a[i]);
     return wrap(q_out);
 }
 
@@ -460,6 +474,7 @@ PyObject *paged_decode(PyObject *const *a) {
                                            s.code, scale, out.data_ptr(), lse, ws.first, ws.second,
                                            call.stream());
     });
+    for (int i : {6, 7}) written(a[i]);
     return wrap(out);
 }
 
@@ -489,6 +504,7 @@ PyObject *paged_step(PyObject *const *a) {
             lens, c.pages, c.page, s.tokens, s.heads, s.kv_heads, s.d, s.code, scale,
             out.data_ptr(), lse, ws.first, ws.second, call.stream());
     });
+    for (int i : {5, 6, 15, 16}) written(a[i]);
     return wrap(out);
 }
 
@@ -530,6 +546,7 @@ PyObject *paged_reserve(PyObject *const *a) {
             base, base + n, base + 2 * n, static_cast<uint8_t *>(served.data_ptr()), lens_out,
             count_out, call.stream());
     });
+    for (PyObject *o : {a[0], a[3], none(a[8]) ? a[1] : a[8], none(a[9]) ? a[4] : a[9]}) written(o);
     return tuple(part_of(all, 0, tokens), part_of(all, n, tokens), part_of(all, 2 * n, b + 1), served);
 }
 

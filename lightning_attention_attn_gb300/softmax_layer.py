@@ -20,6 +20,11 @@ not the current one, its use of the inputs and the current stream's use of the
 outputs are recorded with the allocator, so either may be dropped after the call;
 a third stream's use is the caller's to record, and so is the order of the streams
 (``wait_stream``).
+
+Nothing here is recorded for autograd: outputs of inputs that require a gradient do
+not (gradients come from :func:`qk_norm_rope_backward`, e.g. in an
+``autograd.Function``).  What a call writes of the caller's has its version raised, so
+autograd refuses a backward pass whose saved inputs were overwritten.
 """
 from __future__ import annotations
 

@@ -279,3 +279,50 @@ def test_outputs_and_inputs_of_a_call_on_another_stream():
     assert torch.empty((n, h, d), dtype=BF16, device="cuda").data_ptr() != at
     torch.cuda.synchronize()
     assert torch.equal(out, x)
+
+
+# ------------------------------------------------------- what autograd is told
+def test_writes_are_seen_by_autograd():
+    g = gen(31)
+    h, hk, d, page = 4, 2, 64, 16
+    q, k, v = (randn((2, n, d), BF16, g) for n in (h, hk, hk))
+    kc, vc = (randn((6, hk, page, d), BF16, g) for _ in range(2))
+    bt, lens, new = ints([[0, 1], [2, 3]]), ints([20, 17]), ints([1, 1])
+    stack, count = ints([4, 5, 0, 0, 0, 0]), ints([2])
+    out, lse = torch.empty_like(q), torch.empty((2, h), device="cuda")
+    qo, ko, dq, dk = (torch.empty_like(z) for z in (q, k, q, k))
+    lo, co = torch.empty_like(lens), torch.empty_like(count)
+
+    def raised(f, written, kept):
+        before = [t._version for t in (*written, *kept)]
+        f()
+        after = [t._version for t in (*written, *kept)]
+        assert all(a > b for a, b in zip(after[:len(written)], before))
+        assert after[len(written):] == before[len(written):]
+
+    w = torch.ones(d, device="cuda")
+    slots = ints([19, 48])
+    raised(lambda: la.qk_norm_rope(q, k, q_out=qo, k_out=ko), (qo, ko), (q, k))
+    raised(lambda: la.qk_norm_rope(q, k, q_out=q, k_out=k), (q, k), ())
+    raised(lambda: la.qk_norm_rope_backward(q, k, None, None, qo, ko, q_weight=w, k_weight=w, dq=dq, dk=dk),
+           (dq, dk), (q, k, qo, ko, w))
+    raised(lambda: la.paged_append(q, k, v, None, None, kc, vc, slots, q_out=qo), (kc, vc, qo), (q, k, v, slots))
+    raised(lambda: la.paged_decode(q, kc, vc, bt, lens, out=out, lse=lse), (out, lse), (q, kc, vc, bt, lens))
+    raised(lambda: la.paged_step(q, k, v, None, None, kc, vc, slots, bt, lens, out=out, lse=lse),
+           (kc, vc, out, lse), (q, k, v, bt, lens))
+    raised(lambda: la.paged_reserve(bt, lens, new, stack, count, page, 2, seq_lens_out=lo, free_count_out=co),
+           (bt, stack, lo, co), (lens, new, count))
+    raised(lambda: la.paged_reserve(bt, lens, new, stack, count, page, 2), (bt, stack, lens, count), (new,))
+
+    # a saved input that is overwritten: an error instead of a wrong gradient
+    a = torch.ones((2, h, d), device="cuda", requires_grad=True)
+    b = a * 2
+    c = b * b
+    la.qk_norm_rope(b.detach(), None, q_weight=w, q_out=b.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        c.sum().backward()
+    # tensors without a version are written all the same
+    with torch.inference_mode():
+        t = q.clone()
+        la.qk_norm_rope(t, None, q_weight=w, q_out=t)
+    la.qk_norm_rope(t, None, q_weight=w, q_out=t)
