@@ -193,6 +193,32 @@ __device__ __forceinline__ int tiles_div(long long n, int d) {
     return (n >> 32) == 0 ? (int)((uint32_t)n / (uint32_t)d) : (int)(n / d);
 }
 
+// The first request from b on that has tokens, and how many (whole warps); a.batch: none.
+// Idle rows of a large batch are passed 128 at a time: 5000 of them between two requests of
+// 30000 tokens take 95 us (none of them 35), one by one, each load behind the last, 1105.
+__device__ __forceinline__ int next_request(const PagedDecodeArgs &a, int b, int &len) {
+    constexpr int kLook = 4;
+    const int lane = threadIdx.x & 31;
+    for (; b < a.batch; b += 32 * kLook) {
+        int lens[kLook];
+#pragma unroll
+        for (int i = 0; i < kLook; ++i) {
+            const int at = b + i * 32 + lane;
+            lens[i] = at < a.batch ? request_len(a, at) : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < kLook; ++i) {
+            const uint32_t has = __ballot_sync(0xffffffffu, lens[i] > 0);
+            if (has) {
+                const int first = __ffs(has) - 1;
+                len = __shfl_sync(0xffffffffu, lens[i], first);
+                return b + i * 32 + first;
+            }
+        }
+    }
+    return a.batch;
+}
+
 // Zeros for the requests without tokens, which are nobody's tiles.
 template <typename T>
 __device__ __forceinline__ void write_empty(const PagedDecodeArgs &a) {
@@ -832,13 +858,13 @@ paged_split_kernel(const __grid_constant__ PagedDecodeArgs a) {
     long long w0 = any ? at.w : 0, unit0 = any ? at.unit0 : 0;
     const long long w1 = any ? min(at.all, w0 + at.chunk) : 0;
     int b = any ? at.b : 0;
+    int len = any ? request_len(a, b) : 0;
     bool first = true;
     while (w0 < w1 && b < a.batch) {
-        const int len = request_len(a, b);
         const int tiles = (len + kTile - 1) / kTile, cost = unit_cost<kOver>(len);
-        if (w0 >= unit0 + (long long)cost * units) {  // next request (empty ones pass)
+        if (w0 >= unit0 + (long long)cost * units) {
             unit0 += (long long)cost * units;
-            ++b;
+            b = next_request(a, b + 1, len);
             continue;
         }
         const int unit = tiles_div(w0 - unit0, cost);

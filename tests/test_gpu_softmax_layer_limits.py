@@ -326,3 +326,25 @@ def test_writes_are_seen_by_autograd():
         t = q.clone()
         la.qk_norm_rope(t, None, q_weight=w, q_out=t)
     la.qk_norm_rope(t, None, q_weight=w, q_out=t)
+
+
+@pytest.mark.parametrize("dtype, hk, empty", [(BF16, 1, 0), (FP32, 2, 0), (BF16, 2, 3000), (FP32, 1, 700)])
+def test_more_requests_than_a_block_has_threads(dtype, hk, empty):
+    """Hundreds of requests, long ones among them at the ends and in the middle, so that the pieces of
+    cut units are joined from several rounds of the prefix sums; optionally with thousands
+    without tokens in between."""
+    g = gen(hk + empty)
+    h, d, page = 8 * hk, 64, 64
+    long = {0: 9000, 149: 3000, 299: 5000, 599: 7001}
+    lens_list = [long.get(i, 1 + i % 40) for i in range(300)] + [0] * empty + \
+        [long.get(i, 1 + i % 40) for i in range(300, 600)]
+    b = len(lens_list)
+    pages = 160
+    kc, vc = (randn((pages, hk, page, d), dtype, g) for _ in range(2))
+    bt = torch.randint(0, pages, (b, 9000 // page + 2000), generator=g, device="cuda", dtype=torch.int32)
+    q = randn((b, h, d), dtype, g)
+    lens, lse = ints(lens_list), torch.empty((b, h), device="cuda")
+    out = la.paged_decode(q, kc, vc, bt, lens, lse=lse)
+    want, wlse, bound, lbound = ref.attention(q.cpu(), kc.cpu(), vc.cpu(), bt.cpu(), lens.cpu(), d ** -0.5)
+    ref.within(out, want, bound, ref.u_of(dtype), "out")
+    ref.within(lse, wlse, lbound, ref.u_of(FP32), "lse")
