@@ -5,15 +5,18 @@ Every ``csrc/*.cu`` is compiled in parallel to an object file, then linked
 into one shared library (CUDA runtime linked statically, so loading the
 library needs no GPU driver; the driver is only touched by the first CUDA
 call).  ``csrc/binding.cpp`` is compiled against the installed torch into
-_lightning_binding.so, which is linked to the library beside it.  A content
-hash of the sources, flags and versions skips rebuilds that would produce the
-same files.
+_lightning_binding.so, which is linked to the library beside it.  The library
+needs neither torch nor Python's headers: without torch it is built alone, and
+where the binding cannot be built it is in place before the error is raised.  A
+content hash of each one's sources, flags and versions skips rebuilds that would
+produce the same file.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
 import hashlib
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -45,19 +48,31 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _fingerprint(extra):
+def _fingerprint(files, *words) -> str:
     h = hashlib.sha256()
-    files = _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
-        sorted(glob.glob(os.path.join(CSRC, "*.cpp"))) + \
-        sorted(glob.glob(os.path.join(CSRC, "*.h"))) + \
-        sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
     for f in files:
         h.update(f.encode())
         with open(f, "rb") as fh:
             h.update(fh.read())
-    import torch
-    h.update(" ".join(ARCH + NVCC_FLAGS + list(extra) + [torch.__version__, sys.version]).encode())
+    h.update(" ".join(words).encode())
     return h.hexdigest()
+
+
+def _library_fingerprint(extra) -> str:
+    files = _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
+        sorted(glob.glob(os.path.join(CSRC, "*.h"))) + \
+        sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
+    return _fingerprint(files, *ARCH, *NVCC_FLAGS, *extra)
+
+
+def _binding_fingerprint() -> str:
+    import torch
+    files = [os.path.join(CSRC, "binding.cpp")] + sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
+    return _fingerprint(files, torch.__version__, sys.version)
+
+
+def _current(path: str, stamp: str, fingerprint: str) -> bool:
+    return os.path.exists(path) and os.path.exists(stamp) and open(stamp).read().strip() == fingerprint
 
 
 def _binding_commands(obj: str, out: str) -> list[list[str]]:
@@ -87,41 +102,48 @@ def _run(cmd: list[str], what: str) -> str:
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(),
           jobs: int | None = None) -> str:
-    """Compile and link the library; returns its path."""
+    """Compile and link the library (and, where torch is installed, the binding);
+    returns the library's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
-    stamp = os.path.join(BUILD_DIR, "fingerprint.txt")
-    fp = _fingerprint(extra_flags)
-    if (not force and os.path.exists(LIB_PATH) and os.path.exists(BINDING_PATH)
-            and os.path.exists(stamp) and open(stamp).read().strip() == fp):
-        return LIB_PATH
-    cc = nvcc()
-
-    def compile_one(src):
-        obj = os.path.join(BUILD_DIR, os.path.basename(src)[:-3] + ".o")
-        cmd = [cc, *ARCH, *NVCC_FLAGS, *extra_flags, "-c", src, "-o", obj]
-        if verbose:
-            cmd.insert(1, "-Xptxas=-v")
-        return obj, _run(cmd, f"nvcc for {src}")
-
-    binding_obj = os.path.join(BUILD_DIR, "binding.o")
-    binding_cc, binding_ld = _binding_commands(binding_obj, BINDING_PATH + ".tmp")
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=jobs or min(8, len(srcs) + 1)) as ex:
-        binding = ex.submit(_run, binding_cc, "binding")
-        results = list(ex.map(compile_one, srcs))
-        binding.result()
-    if verbose:
-        for _, log in results:
-            if log.strip():
-                print(log)
-    tmp = LIB_PATH + ".tmp"
-    cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp] + [o for o, _ in results]
-    _run(cmd, "link")
-    os.replace(tmp, LIB_PATH)
-    _run(binding_ld, "binding link")
-    os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
-    with open(stamp, "w") as f:
-        f.write(fp)
+        binding = None
+        if importlib.util.find_spec("torch") is not None:
+            binding_stamp, binding_fp = BINDING_PATH + ".fingerprint.txt", _binding_fingerprint()
+            if force or not _current(BINDING_PATH, binding_stamp, binding_fp):
+                compile_, link = _binding_commands(os.path.join(BUILD_DIR, "binding.o"), BINDING_PATH + ".tmp")
+                binding = ex.submit(_run, compile_, "binding")
+        elif verbose:
+            print("torch is not installed: the library without its Python binding")
+
+        stamp, fp = os.path.join(BUILD_DIR, "fingerprint.txt"), _library_fingerprint(extra_flags)
+        if force or not _current(LIB_PATH, stamp, fp):
+            cc = nvcc()
+
+            def compile_one(src):
+                obj = os.path.join(BUILD_DIR, os.path.basename(src)[:-3] + ".o")
+                cmd = [cc, *ARCH, *NVCC_FLAGS, *extra_flags, "-c", src, "-o", obj]
+                if verbose:
+                    cmd.insert(1, "-Xptxas=-v")
+                return obj, _run(cmd, f"nvcc for {src}")
+
+            results = list(ex.map(compile_one, srcs))
+            if verbose:
+                for _, log in results:
+                    if log.strip():
+                        print(log)
+            tmp = LIB_PATH + ".tmp"
+            _run([cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp] + [o for o, _ in results], "link")
+            os.replace(tmp, LIB_PATH)
+            with open(stamp, "w") as f:
+                f.write(fp)
+
+        if binding is not None:
+            binding.result()
+            _run(link, "binding link")
+            os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
+            with open(binding_stamp, "w") as f:
+                f.write(binding_fp)
     return LIB_PATH
 
 
