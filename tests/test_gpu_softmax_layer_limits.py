@@ -328,6 +328,69 @@ def test_writes_are_seen_by_autograd():
     la.qk_norm_rope(t, None, q_weight=w, q_out=t)
 
 
+# ------------------------------------------------- paths of large calls alone
+@pytest.mark.parametrize("dtype, t, h, hk, d, rot, inter", [
+    (BF16, 700, 64, 64, 64, 64, False), (BF16, 500, 64, 64, 64, 32, True), (BF16, 600, 64, 16, 128, 64, False),
+    (BF16, 600, 64, 16, 128, 128, True), (BF16, 300, 96, 32, 128, 48, True), (FP32, 500, 64, 64, 128, 128, False),
+    (FP32, 500, 64, 64, 128, 64, True), (FP32, 700, 64, 64, 64, 64, True), (FP32, 700, 64, 64, 64, 48, False),
+    (BF16, 700, 33, 17, 64, 32, False), (FP32, 700, 33, 17, 128, 16, True)])
+def test_norm_rope_of_many_rows(dtype, t, h, hk, d, rot, inter):
+    """Forward and gradients where a warp takes several passes, for every type, width and rotation;
+    heads that fill its passes (no checks inside) and heads that do not."""
+    assert t * (h + hk) > 152 * 16 * (32 // (d // 8))  # above the limit of single passes
+    g = gen(t + d + rot)
+    x = randn((t, h + hk, d), dtype, g)
+    q, k = x[:, :h], x[:, h:]
+    w = [1 + 0.3 * torch.randn(d, generator=g, device="cuda") for _ in range(2)]
+    table = la.rotary_table(5000, rot, device="cuda")
+    pos = torch.randint(0, 5000, (t,), generator=g, device="cuda", dtype=torch.int32)
+    args = dict(q_weight=w[0], k_weight=w[1], eps=EPS, interleaved=inter)
+    outs = la.qk_norm_rope(q, k, pos, table, **args)
+    dy = [randn(z.shape, dtype, g) for z in (q, k)]
+    grads = la.qk_norm_rope_backward(q, k, pos, table, *dy, **args)
+    for i, z in enumerate((q, k)):
+        a = (z.cpu(), w[i].cpu(), EPS, table.cpu(), pos.cpu(), inter)
+        want, bound = ref.norm_rope(*a)
+        ref.within(outs[i], want, bound, ref.u_of(dtype), "y")
+        want, wantw, bound, boundw = ref.norm_rope_backward(*a, dy[i].cpu())
+        ref.within(grads[i], want, bound, ref.u_of(dtype), "dx")
+        ref.within(grads[2 + i], wantw, boundw, ref.u_of(FP32), "dw")
+
+
+@pytest.mark.parametrize("dtype, b, h, hk, d, rot, inter", [
+    (BF16, 128, 64, 8, 128, 64, False), (BF16, 200, 64, 8, 64, 64, True), (BF16, 300, 24, 1, 128, 32, True),
+    (FP32, 128, 64, 8, 128, 128, False), (FP32, 140, 48, 12, 64, 16, False)])
+def test_paged_step_of_a_full_batch(dtype, b, h, hk, d, rot, inter):
+    """Steps whose queries pass from one half to the other out of warps that take several passes."""
+    assert b * (h + 2 * hk) > 152 * 16 * (32 // (d // 8))
+    g = gen(b + d)
+    page, most = 16, 150
+    lens = torch.randint(1, most, (b,), generator=g, device="cuda", dtype=torch.int32)
+    blocks = -(-most // page)
+    kc, vc = (randn((b * blocks, hk, page, d), dtype, g) for _ in range(2))
+    bt = torch.randperm(b * blocks, generator=g, device="cuda").int().reshape(b, blocks)
+    x = randn((b, h + 2 * hk, d), dtype, g)
+    q, k, v = x[:, :h], x[:, h:h + hk], x[:, h + hk:]
+    w = [1 + 0.3 * torch.randn(d, generator=g, device="cuda") for _ in range(2)]
+    table = la.rotary_table(most, rot, device="cuda")
+    pos = lens - 1
+    slots = bt.gather(1, (pos // page)[:, None].long())[:, 0] * page + pos % page
+    args = dict(q_weight=w[0], k_weight=w[1], eps=EPS, interleaved=inter)
+    lse = torch.empty((b, h), device="cuda")
+    out = la.paged_step(q, k, v, pos, table, kc, vc, slots, bt, lens, lse=lse, **args)
+    at = (slots // page).long(), slice(None), (slots % page).long()
+    assert torch.equal(vc[at], v)
+    want, bound = ref.norm_rope(k.cpu(), w[1].cpu(), EPS, table.cpu(), pos.cpu(), inter)
+    ref.within(kc[at], want, bound, ref.u_of(dtype), "key")
+    rotated, qbound = ref.norm_rope(q.cpu(), w[0].cpu(), EPS, table.cpu(), pos.cpu(), inter)
+    want, wlse, bound, lbound = ref.attention(rotated, kc.cpu(), vc.cpu(), bt.cpu(), lens.cpu(), d ** -0.5)
+    # the queries' own fp32 error and their split into two bf16 parts, as in test_paged_step
+    extra = (qbound / rotated.abs().amax(-1, keepdim=True).clamp(min=1e-3)).amax() + 2.0 ** -16
+    more = 1 + float(extra) / (2 * ref.E * (d + 8))
+    ref.within(out, want, bound * more, ref.u_of(dtype), "out")
+    ref.within(lse, wlse, lbound * more, ref.u_of(FP32), "lse")
+
+
 @pytest.mark.parametrize("dtype, hk, empty", [(BF16, 1, 0), (FP32, 2, 0), (BF16, 2, 3000), (FP32, 1, 700)])
 def test_more_requests_than_a_block_has_threads(dtype, hk, empty):
     """Hundreds of requests, long ones among them at the ends and in the middle, so that the pieces of
