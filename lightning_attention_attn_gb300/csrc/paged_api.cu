@@ -226,6 +226,8 @@ la_status lightning_attn_qk_norm_rope(
     if ((q_out == q && q_out_stride != q_stride) ||
         (num_kv_heads > 0 && k_out == k && k_out_stride != k_stride))
         return LA_INVALID("an output in place of its input needs the input's stride");
+    if (num_kv_heads > 0 && (q_out == k || k_out == q || k_out == q_out))
+        return LA_INVALID("an output is the other input or the other output");
     la::NormRopeArgs a = norm_args(positions, rotary, rotary_rows, rotary_dim, interleaved, eps,
                                    num_tokens, head_dim, stream);
     a.set[0] = rows(q, q_stride, q_out, q_out_stride, q_weight, num_heads, dtype);
@@ -254,6 +256,8 @@ la_status lightning_attn_qk_norm_rope_backward(
         if (!d_q_weight || !aligned(d_q_weight, 4) ||
             (num_kv_heads > 0 && (!d_k_weight || !aligned(d_k_weight, 4))))
             return LA_INVALID("null or misaligned gradient of a weight");
+        if (num_kv_heads > 0 && d_q_weight == d_k_weight)
+            return LA_INVALID("the two weights' gradients are one array");
     }
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (num_tokens == 0) {  // sums over no rows
@@ -272,7 +276,8 @@ la_status lightning_attn_qk_norm_rope_backward(
         LA_TRY(check_rows("d_k_out", d_k_out, d_k_out_stride, num_kv_heads, head_dim, dtype));
         LA_TRY(check_rows("d_k", d_k, d_k_stride, num_kv_heads, head_dim, dtype));
     }
-    if (d_q == q || (num_kv_heads > 0 && (d_k == k || d_k == d_q)))
+    if (d_q == q || (num_kv_heads > 0 && (d_k == k || d_k == d_q || d_q == k || d_k == q ||
+                                          d_q == d_k_out || d_k == d_q_out)))
         return LA_INVALID("a gradient aliases an input or another gradient");
     if ((d_q == d_q_out && d_q_stride != d_q_out_stride) ||
         (num_kv_heads > 0 && d_k == d_k_out && d_k_stride != d_k_out_stride))
@@ -314,6 +319,8 @@ la_status lightning_attn_paged_append(
     LA_TRY(check_rows("q_out", q_out, q_out_stride, num_heads, head_dim, dtype));
     if (q_out == q && q_out_stride != q_stride)
         return LA_INVALID("an output in place of its input needs the input's stride");
+    if (q_out == k || q_out == v) return LA_INVALID("q_out is k or v");
+    if (num_pages > 0 && k_cache == v_cache) return LA_INVALID("k_cache and v_cache are one array");
     if (num_pages > 0) {
         LA_TRY(check_cache("k_cache", k_cache, k_page_stride, num_kv_heads, page_size, head_dim, dtype));
         LA_TRY(check_cache("v_cache", v_cache, v_page_stride, num_kv_heads, page_size, head_dim, dtype));
@@ -382,6 +389,7 @@ la_status lightning_attn_paged_step(
     LA_TRY(check_rows("k", k, k_stride, num_kv_heads, head_dim, dtype));
     LA_TRY(check_rows("v", v, v_stride, num_kv_heads, head_dim, dtype));
     if (!slots || !aligned(slots, 4)) return LA_INVALID("slots must be a 4-byte aligned device array");
+    if (num_pages > 0 && k_cache == v_cache) return LA_INVALID("k_cache and v_cache are one array");
     LA_TRY(check_workspace(workspace, workspace_bytes,
                            lightning_attn_paged_step_workspace_bytes(batch, num_heads, head_dim)));
     float *rotated = reinterpret_cast<float *>(static_cast<char *>(workspace) + decode_workspace(head_dim));

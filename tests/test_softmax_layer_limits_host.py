@@ -25,6 +25,41 @@ def test_paged_reserve_refuses_new_lens_as_an_output(lib, lens_out, count_out):
     assert "new_lens" in lib.lightning_attn_last_error().decode()
 
 
+# ----------------------------------------- outputs that a call still reads
+# bf16, 4 tokens, 8 query and 2 key-value heads of 64; every array in a place of its own
+AT = {n: A * (i + 1) for i, n in enumerate("q k v qo ko dqo dko dq dk dqw dkw w table pos kc vc slots bt "
+                                           "lens out ws".split())}
+
+
+def _call(lib, name, at):
+    p = {**AT, **{n: AT[o] for n, o in at.items()}}
+    rot, shape = [p["pos"], p["table"], 64, 64, 0, p["w"], p["w"], 1e-6], [4, 8, 2, 64, la.LA_DTYPE_BF16]
+    q, k, v = [p["q"], 512], [p["k"], 128], [p["v"], 128]
+    cache = [p["kc"], 2048, p["vc"], 2048]
+    args = {
+        "qk_norm_rope": q + k + rot + shape + [p["qo"], 512, p["ko"], 128, None],
+        "qk_norm_rope_backward": q + k + rot + shape + [p["dqo"], 512, p["dko"], 128, p["dq"], 512, p["dk"],
+                                                        128, p["dqw"], p["dkw"], p["ws"], 1 << 30, None],
+        "paged_append": q + k + v + rot + shape + [p["qo"], 512] + cache + [p["slots"], 10, 16, None],
+        "paged_step": q + k + v + rot + cache + [p["slots"], p["bt"], 5, 5, p["lens"], 10, 16] + shape +
+        [0.1, p["out"], None, p["ws"], 1 << 30, None],
+    }[name]
+    return getattr(lib, "lightning_attn_" + name)(*args)
+
+
+@pytest.mark.parametrize("name, at", [
+    ("qk_norm_rope", dict(qo="k")), ("qk_norm_rope", dict(ko="q")), ("qk_norm_rope", dict(ko="qo")),
+    ("qk_norm_rope_backward", dict(dq="k")), ("qk_norm_rope_backward", dict(dk="q")),
+    ("qk_norm_rope_backward", dict(dq="dko")), ("qk_norm_rope_backward", dict(dk="dqo")),
+    ("qk_norm_rope_backward", dict(dkw="dqw")),
+    ("paged_append", dict(qo="k")), ("paged_append", dict(qo="v")), ("paged_append", dict(vc="kc")),
+    ("paged_step", dict(vc="kc"))])
+def test_outputs_over_other_arguments_are_refused(lib, name, at):
+    assert _call(lib, name, at) == la.LA_ERR_INVALID_ARG
+    assert " one array" in lib.lightning_attn_last_error().decode() or \
+        any(w in lib.lightning_attn_last_error().decode() for w in ("other", "aliases", "q_out is"))
+
+
 def test_library_builds_without_torch():
     """The C library needs neither torch nor the package (which imports it)."""
     path = labuild.build()
