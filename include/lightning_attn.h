@@ -367,9 +367,11 @@ la_status lightning_attn_mixed_step(const void *q, const void *k, const void *v,
  *             of page s / page_size; num_pages * page_size < 2^31.  page_size
  *             is any number >= 1.
  *   - dtype of q, k, v, the cache and the outputs is LA_DTYPE_BF16 or
- *             LA_DTYPE_FP32; head_dim 64 or 128.  Arithmetic is fp32
- *             throughout (bf16 products exact, fp32 sums), rounded once into
- *             an output.
+ *             LA_DTYPE_FP32; head_dim 64 or 128.  Arithmetic and sums are fp32
+ *             (squares too: a norm's elements up to about 10^19), rounded once
+ *             into an output.  One exception: over a bf16 cache the softmax
+ *             weights, and the queries of lightning_attn_paged_step, enter the
+ *             products as two bf16 numbers, off by at most 2^-16 of each.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -469,8 +471,9 @@ int64_t lightning_attn_paged_decode_workspace_bytes(int32_t head_dim);
 /*
  * One serving step of a softmax layer: lightning_attn_paged_append of each
  * request's new token (row b of q, k, v), then lightning_attn_paged_decode over
- * the cache that now holds it.  The normed and rotated queries stay fp32
- * between the two (in the workspace), so out is rounded once.  seq_lens counts the
+ * the cache that now holds it.  The normed and rotated queries pass between the
+ * two in fp32 (in the workspace; see above for their products), so out is rounded
+ * once.  seq_lens counts the
  * new tokens.  workspace: lightning_attn_paged_step_workspace_bytes(...) bytes,
  * 16-byte aligned.
  */

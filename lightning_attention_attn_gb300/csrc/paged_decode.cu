@@ -6,7 +6,7 @@
 //     s_t = scale q_h . k_t,   out_h = sum_t e^(s_t - m) v_t / sum_t e^(s_t - m)
 // in one pass with the running maximum m and sum l of a softmax, in fp32.
 //
-// Bound: every key and value is read once, 2 G flops a byte of bf16 cache, so
+// Bound: every key and value is read once, G flops a byte of bf16 cache, so
 // the kernel is a stream over HBM and its layout serves the loads.
 //
 // Split.  The work is cut into tiles of kTile tokens of one unit (a request's
@@ -325,7 +325,8 @@ __device__ __forceinline__ Partial warps_sum(const unsigned char *smem, int h, i
 // an SM either way, 128 KB in flight.  Measured, 8 key-value heads of 128: 128 requests of
 // 1K to 32K tokens 1260 us (7.0 TB/s), one of 128K 88 us, 20 of 4096 58 us; of 64, 20 x
 // 8192 59 us (with four warps 70).  One CTA of eight warps an SM instead: 62 us for the
-// 20 x 4096, 40 instead of 31 for 100 requests up to 600 tokens.
+// 20 x 4096, 40 instead of 31 for 100 requests up to 600 tokens.  (Of the variants one, 64 wide
+// with fp32 queries of 9 to 16 heads, spills: 48 bytes at its 128 registers.)
 template <int D_, int NT, bool QF32>
 struct Bf16Core {
     using T = __nv_bfloat16;
@@ -615,9 +616,12 @@ struct Bf16Core {
 //   values   a lane owns four columns of all heads (of every other token where 16
 //            lanes cover a row)
 // A group is 16 tokens of 64 dimensions or 8 of 128: 8 KB a stage, as in bf16.
-// 16 requests of 16K / (kv heads) tokens, 128 wide: 49 us with one to four query heads a
-// kv head (5.5 TB/s), 55 with eight, 95 with 16, where the CUDA cores bound it (64 packed
-// FMAs a token and warp).
+// 16 requests of 64K / (kv heads) tokens, 128 wide: 165 us with one query head a kv head (6.5
+// TB/s), 170 with four, 178 with eight (6.0), 335 with 16 (3.2).  There it is bound by the
+// latencies of its own instructions, not by a pipe: twice the instructions of eight heads
+// (a lane keeps four dimensions, so every score goes through more of the reduction, and
+// the weights of 16 heads are read back), issued in 47 % of the slots by two warps a
+// scheduler, the fp32 pipe 44 % and the shared memory 36 % busy, HBM at 39 %.
 template <int D_, int ROWS_>
 struct F32Core {
     using T = float;
@@ -1101,8 +1105,8 @@ template <typename Core, int S> cudaError_t launch_cluster(const PagedDecodeArgs
 // When the cluster kernel serves a call: up to kClusterTiles tiles a CTA, with as many CTAs
 // a unit, at most eight, as fit the SMs at once; units of one CTA may be up to
 // kClusterWaves times what fits.  64 query and 8 key-value heads of 128, cluster / split kernel:
-// 1 x 300 tokens 4.8 / 6.4 us, 16 x 512 8.0 / 12.4, 16 x 1000 11.6 / 15.4, 8 x 2000 11.7 /
-// 15.4, 128 x 128 15.7 / 19.8, 64 x 256 12.8 / 17.1; beyond it, with 16 tiles, 1 x 8000
+// 1 x 300 tokens 4.9 / 6.6 us, 16 x 512 8.1 / 11.9, 16 x 1000 11.5 / 15.0, 8 x 2000 11.9 /
+// 14.4, 128 x 128 15.7 / 19.8, 64 x 256 13.0 / 16.2; beyond it, with 16 tiles, 1 x 8000
 // 14.8 / 12.0.
 constexpr int kClusterTiles = 8;
 constexpr int kClusterWaves = 4;
@@ -1133,8 +1137,10 @@ template <typename Core> cudaError_t launch(PagedDecodeArgs a) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Query heads of a unit: as many as share a key-value head, up to 16 (a
-// further unit for every 16).
+// Query heads of a unit: as many as share a key-value head, up to 16.  Further heads are a
+// further unit, which streams the cache once more: a unit's sums fill the registers at 16
+// heads.  64 query heads over bf16 keys and values of 0.54 GB each: 4 to 16 heads a kv head
+// 165 to 175 us, 32 heads 325.
 template <int D>
 cudaError_t dispatch(const PagedDecodeArgs &a, bool bf16, bool q_f32) {
     if (!bf16)

@@ -18,7 +18,8 @@
 // SMs, reads the lengths after the step and the offsets that the first has
 // written and fills slots, positions and table, so lengths and count may be
 // updated in place.  Measured: a step of 128 requests, 12 of them ending with 3000 pages,
-// 6.6 us; 16 prompts of 270K tokens 6.9 us (38 us when one cluster of eight CTAs did it all).
+// 6.8 us; 16 prompts of 270K tokens 8.0 us (7.4 in a graph; 38 when one cluster of eight
+// CTAs did it all).
 #include <cuda_runtime.h>
 
 #include "la_internal.h"

@@ -153,7 +153,10 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
     const int per = nq + nk + nv;
     const unsigned items = (unsigned)a.num_tokens * per;  // the caller bounds the rows by 2^31
 
-    float2 dw[2][4];  // this lane's columns of the weights' gradients
+    // This lane's columns of the weights' gradients: fp32 sums, a warp's rows one after the
+    // other, then the rows of a pass, the warps and the blocks (1.4e-7 off in 1021 fp32 tokens,
+    // where a 64-bit sum rounded at the end is 0.8e-7 off).
+    float2 dw[2][4];
     if (BACK) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) dw[0][i] = dw[1][i] = twice(0.f);
@@ -409,9 +412,13 @@ cudaError_t launch_u(const NormRopeArgs &a) {
 
 template <typename T, int D, bool BACK>
 cudaError_t launch(const NormRopeArgs &a) {
-    // Few rows: one pass a warp spreads them over many SMs (1021 tokens of 16 fp32
-    // heads, above the limit: 6.0 us in long items, 6.9 in single passes).  Many: the
-    // token's cosines, sines and weights are loaded once for up to U * G passes.  8192
+    // Few rows: one pass a warp spreads them over many SMs.  Many: the token's cosines,
+    // sines and weights are loaded once for up to U * G passes.  Measured with 64 + 8 heads of 128,
+    // single passes / long items, us, at half the limit, at it, twice and four times it:
+    // forward bf16 2.1 / 3.0, 2.5 / 3.0, 2.8 / 3.3, 4.5 / 3.6; fp32 2.2 / 2.4, 2.5 / 2.5, 3.0 / 2.8,
+    // 4.6 / 3.6; gradients bf16 4.8 / 5.2, 6.0 / 5.3, 7.3 / 6.3, 9.0 / 7.4; fp32 4.8 / 4.3, 6.1 / 5.2,
+    // 7.4 / 6.2, 9.3 / 8.2.  64 wide and with 12 + 4 heads they cross between the same points: the
+    // limit is within half a microsecond of each type's own, the gradients' within one.  8192
     // tokens of 64 + 64 bf16 heads, forward: G = 1, 2, 3, 4 take 96, 81, 83, 83 us
     // (a plain copy of the bytes 85; of 64 + 8 heads into the cache 60, 54, 60, 64);
     // gradients, where the sums over a block's rows come on top: 185, 144, 134, 131.

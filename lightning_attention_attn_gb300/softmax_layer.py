@@ -182,7 +182,7 @@ def paged_step(q, k, v, positions, table, k_cache, v_cache, slots, block_table, 
                scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
     """One serving step of a softmax layer: :func:`paged_append` of each request's
     new token, then :func:`paged_decode` over the cache that now holds it (the
-    queries stay fp32 in between, so out is rounded once).  q: [B, H, d], k, v:
+    queries are fp32 in between, not rounded to q's dtype).  q: [B, H, d], k, v:
     [B, Hkv, d]; ``seq_lens`` counts the new tokens.  Returns out [B, H, d]."""
     return (_binding or _calls()).paged_step(
         q, k, v, positions, table, k_cache, v_cache, slots, block_table, seq_lens, q_weight,
