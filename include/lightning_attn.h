@@ -453,7 +453,7 @@ la_status lightning_attn_paged_append(
  * num_heads is a multiple of num_kv_heads.  What lies in the cache past a
  * request's last token is not used, whatever it holds.  Infinities that are
  * attended to count as the formula has it: a score of -infinity has weight 0, one
- * of +infinity (or NaN) makes the head's row NaN, an infinite value makes its
+ * of +infinity (or NaN) makes the head's row and lse NaN, an infinite value makes its
  * column that infinity, or NaN where both signs meet or where its weight is 0 or
  * less than 2^-100 of the largest.
  */
@@ -497,6 +497,7 @@ int64_t lightning_attn_paged_step_workspace_bytes(int32_t batch, int32_t num_hea
  *   1. A finished request (finished[b] != 0; finished may be NULL) pushes the
  *      pages of its ceil(seq_lens[b] / page_size) first blocks onto the free
  *      stack, requests and blocks in ascending order, and has length 0 from there on.
+ *      The table's entries go as they are, so they have to be pages here.
  *   2. Request b asks for the pages that new_lens[b] more tokens need beyond
  *      those it has.  Requests are served in ascending order: b is served if its
  *      tokens fit its table row, and if it needs no page or the pages needed by

@@ -281,6 +281,45 @@ def test_outputs_and_inputs_of_a_call_on_another_stream():
     assert torch.equal(out, x)
 
 
+def test_streams_inside_a_graph_and_the_default_stream():
+    """A captured call on a stream that was forked from the capturing one, its output used and
+    dropped inside the capture; and the default stream named while another one is current."""
+    g = gen(32)
+    kc, vc, bt, sl = caches([5000, 40, 0, 900], 16, 2, 64, BF16, g)
+    vc[bt[0, 100], 0, 3, 5] = INF
+    table = widened(bt, 4096)
+    q = randn((4, 8, 64), BF16, g)
+    want = la.paged_decode(q, kc, vc, table, sl)
+    side, own = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        outs = []
+        for _ in range(3):
+            side.wait_stream(here)
+            out = la.paged_decode(q, kc, vc, table, sl, stream=side)
+            here.wait_stream(side)
+            outs.append(out.clone())
+            del out
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+    for o in outs:
+        assert torch.equal(o, want)
+    default = torch.cuda.default_stream()
+    with torch.cuda.stream(own):
+        x = q + 0
+        default.wait_stream(own)
+        out = la.paged_decode(x, kc, vc, table, sl, stream=default)
+        own.wait_stream(default)
+        del x
+        got = out.clone()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.isinf(want[0, 0, 5])
+
+
 # ------------------------------------------------------- what autograd is told
 def test_writes_are_seen_by_autograd():
     g = gen(31)
