@@ -492,6 +492,70 @@ int64_t lightning_attn_paged_step_workspace_bytes(int32_t batch, int32_t num_hea
                                                   int32_t head_dim);
 
 /*
+ * Long contexts: attention over a few pages of the cache that are chosen by a cheap score.
+ *
+ * lightning_attn_paged_bounds keeps, for every page and key-value head, the smallest and the
+ * largest value of each channel of the page's keys, as they enter the cache.
+ * bounds is [num_pages, num_kv_heads, 2, head_dim], minima then maxima, in the cache's dtype (and so
+ * exact; bounds_page_stride elements from one page to the next).  Tokens
+ * first[b] .. seq_lens[b] - 1 of request b are new: bounds of a block that begins among them are
+ * written, those of the block that begins before them (first[b] inside it) are extended, all others stay.
+ * After tokens of a block have been replaced, its bounds are taken anew with first[b]
+ * at its beginning.  Values outside [0, table_width * page_size] are clamped to it; nothing is
+ * done for a request without new tokens, nor for a block whose page is outside [0, num_pages).  The
+ * blocks with new tokens lie in distinct pages.  A NaN key makes both bounds of its channel NaN.
+ */
+la_status lightning_attn_paged_bounds(
+    const void *k_cache, int64_t k_page_stride, void *bounds, int64_t bounds_page_stride,
+    const int32_t *block_table, int32_t table_stride, int32_t table_width, const int32_t *first,
+    const int32_t *seq_lens, int32_t num_pages, int32_t page_size, int32_t batch,
+    int32_t num_kv_heads, int32_t head_dim, la_dtype dtype, void *stream);
+
+/*
+ * Chooses `count` blocks of every request and key-value head.  The score of a block is
+ *     max over the heads h that share the key-value head of  sum_d max(q_hd lo_d, q_hd hi_d),
+ * which no q_h . k of the block exceeds; as by arithmetic in 64 bits on these inputs, however
+ * near two scores are.  Equal scores go to the lower block, NaN counts as infinity.
+ *
+ * q            [batch, num_heads, head_dim] (row stride q_stride), as for the attention.
+ * bounds       as lightning_attn_paged_bounds keeps them, for all blocks of the requests.
+ * keep_first, keep_last  the first and the last blocks of a request that are chosen whatever their
+ *              scores; together at most count.
+ * selected     [batch, num_kv_heads, count] int32: the chosen blocks (indices into the request's
+ *              row of block_table) in ascending order, then -1 where the request has fewer.
+ *              Blocks whose page is outside [0, num_pages) are not chosen.
+ * workspace    lightning_attn_paged_select_workspace_bytes(...) bytes, 16-byte aligned; scratch, not
+ *              shared by calls that may overlap.
+ */
+la_status lightning_attn_paged_select(
+    const void *q, int64_t q_stride, const void *bounds, int64_t bounds_page_stride,
+    const int32_t *block_table, int32_t table_stride, int32_t table_width, const int32_t *seq_lens,
+    int32_t num_pages, int32_t page_size, int32_t batch, int32_t num_heads, int32_t num_kv_heads,
+    int32_t head_dim, la_dtype dtype, int32_t count, int32_t keep_first, int32_t keep_last,
+    int32_t *selected, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of lightning_attn_paged_select; -1 for invalid sizes. */
+int64_t lightning_attn_paged_select_workspace_bytes(int32_t batch, int32_t num_kv_heads,
+                                                    int32_t table_width);
+
+/*
+ * lightning_attn_paged_decode over the tokens of chosen blocks alone.
+ *
+ * selected     [batch, num_kv_heads, count] int32, blocks of the request (in any order); of a row the
+ *              first min(count, ceil(seq_lens[b] / page_size)) entries count.  An entry outside
+ *              the request's blocks stands for no tokens, one that is there twice for its tokens twice.
+ * The rest is as for lightning_attn_paged_decode (the workspace too); a head whose choice holds no token
+ * gets zeros and an lse of -infinity.  count * page_size is at most 2^31 - 2^16 (LA_ERR_UNSUPPORTED).
+ */
+la_status lightning_attn_paged_sparse_decode(
+    const void *q, int64_t q_stride, const void *k_cache, int64_t k_page_stride,
+    const void *v_cache, int64_t v_page_stride, const int32_t *block_table, int32_t table_stride,
+    int32_t table_width, const int32_t *seq_lens, const int32_t *selected, int32_t count,
+    int32_t num_pages, int32_t page_size, int32_t batch, int32_t num_heads, int32_t num_kv_heads,
+    int32_t head_dim, la_dtype dtype, float scale, void *out, float *lse, void *workspace,
+    int64_t workspace_bytes, void *stream);
+
+/*
  * Page bookkeeping of one serving step, from the requests' lengths, on the GPU.
  * In this order:
  *   1. A finished request (finished[b] != 0; finished may be NULL) pushes the

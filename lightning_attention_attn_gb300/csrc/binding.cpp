@@ -508,6 +508,104 @@ PyObject *paged_step(PyObject *const *a) {
     return wrap(out);
 }
 
+// [pages, Hkv, 2, d] of a cache's pages
+int64_t bounds_of(const Call &call, PyObject *o, int64_t pages, int64_t kv_heads, int64_t d,
+                  at::ScalarType type, void *&p) {
+    const Tensor &t = call.here(o, "bounds");
+    const int64_t stride = page_stride(t, "bounds", d, type);
+    if (t.size(2) != 2 || (pages >= 0 && (t.size(0) != pages || t.size(1) != kv_heads)))
+        refuse(PyExc_ValueError, "bounds must be [pages, Hkv, 2, d]");
+    p = t.data_ptr();
+    return stride;
+}
+
+// k_cache, bounds, block_table, first, seq_lens, stream
+PyObject *paged_bounds(PyObject *const *a) {
+    Call call(a[0], "k_cache", a[5]);
+    const Tensor &k = tensor(a[0], "k_cache");
+    if (k.dim() != 4) refuse(PyExc_ValueError, "k_cache must be [pages, Hkv, page_size, d]");
+    const la_dtype code = dtype_of(k);
+    const int64_t d = k.size(3), ks = page_stride(k, "k_cache", d, k.scalar_type());
+    const int32_t pages = size32(k.size(0), "k_cache"), heads = size32(k.size(1), "k_cache");
+    const int32_t page = size32(k.size(2), "k_cache");
+    void *bounds;
+    const int64_t bs = bounds_of(call, a[1], pages, heads, d, k.scalar_type(), bounds);
+    const Tensor &bt = tensor(a[2], "block_table");
+    if (bt.dim() != 2) refuse(PyExc_ValueError, "block_table must be int32 [B, blocks]");
+    const int32_t b = size32(bt.size(0), "block_table");
+    const Table t = table_of(call, a[2], b);
+    const int32_t *first = call.ints(a[3], "first", b), *lens = call.ints(a[4], "seq_lens", b);
+    launch("lightning_attn_paged_bounds", [&] {
+        return lightning_attn_paged_bounds(k.data_ptr(), ks, bounds, bs, t.p, t.stride, t.width, first, lens,
+                                           pages, page, b, heads, size32(d, "k_cache"), code, call.stream());
+    });
+    written(a[1]);
+    return wrap(THPVariable_Unpack(a[1]));
+}
+
+// q, bounds, block_table, seq_lens, page_size, count, keep_first, keep_last, out, workspace, stream
+PyObject *paged_select(PyObject *const *a) {
+    Call call(a[0], "q", a[10]);
+    const Shape s = shape_of(a[0], Py_None, false);
+    const Rows q = call.rows(a[0], "q", s.tokens, s.heads, s.d, s.type);
+    void *bounds;
+    const int64_t bs = bounds_of(call, a[1], -1, 0, s.d, s.type, bounds);
+    const Tensor &bt = tensor(a[1], "bounds");
+    const int32_t pages = size32(bt.size(0), "bounds"), kv = size32(bt.size(1), "bounds");
+    const Table t = table_of(call, a[2], s.tokens);
+    const int32_t *lens = call.ints(a[3], "seq_lens", s.tokens);
+    const int32_t page = integer(a[4], "page_size"), count = integer(a[5], "count");
+    const int32_t first = integer(a[6], "keep_first"), last = integer(a[7], "keep_last");
+    if (count < 1) refuse(PyExc_ValueError, "count must be at least 1");
+    Tensor out;
+    if (none(a[8])) {
+        out = call.empty({s.tokens, kv, count}, at::kInt);
+    } else {
+        out = call.here(a[8], "out");
+        if (out.scalar_type() != at::kInt || out.dim() != 3 || out.size(0) != s.tokens ||
+            out.size(1) != kv || out.size(2) != count || !out.is_contiguous())
+            refuse(PyExc_ValueError, "out must be a contiguous int32 [%d, %d, %d]", s.tokens, kv, count);
+    }
+    const int64_t need = lightning_attn_paged_select_workspace_bytes(s.tokens, std::max(kv, 1), t.width);
+    if (need < 0) refuse(PyExc_ValueError, "too many blocks");
+    const auto ws = call.workspace(a[9], std::max<int64_t>(need, 16));
+    launch("lightning_attn_paged_select", [&] {
+        return lightning_attn_paged_select(q.p, q.stride, bounds, bs, t.p, t.stride, t.width, lens, pages,
+                                           page, s.tokens, s.heads, kv, s.d, s.code, count, first, last,
+                                           static_cast<int32_t *>(out.data_ptr()), ws.first, ws.second,
+                                           call.stream());
+    });
+    written(a[8]);
+    return wrap(out);
+}
+
+// q, k_cache, v_cache, block_table, seq_lens, selected, scale, out, lse, workspace, stream
+PyObject *paged_sparse_decode(PyObject *const *a) {
+    Call call(a[0], "q", a[10]);
+    const Shape s = shape_of(a[0], Py_None, false);
+    const Rows q = call.rows(a[0], "q", s.tokens, s.heads, s.d, s.type);
+    const Cache c = cache_of(call, a[1], a[2], s.d, s.type);
+    const Table t = table_of(call, a[3], s.tokens);
+    const int32_t *lens = call.ints(a[4], "seq_lens", s.tokens);
+    const Tensor &sel = call.here(a[5], "selected");
+    if (sel.scalar_type() != at::kInt || sel.dim() != 3 || sel.size(0) != s.tokens ||
+        sel.size(1) != c.kv_heads || !sel.is_contiguous())
+        refuse(PyExc_ValueError, "selected must be a contiguous int32 [%d, %d, count]", s.tokens, c.kv_heads);
+    const int32_t count = size32(sel.size(2), "selected");
+    const float scale = scale_of(a[6], s);
+    const Tensor out = attention_out(call, a[7], s);
+    float *lse = lse_of(call, a[8], s);
+    const auto ws = call.workspace(a[9], need_of(lightning_attn_paged_decode_workspace_bytes(s.d)));
+    launch("lightning_attn_paged_sparse_decode", [&] {
+        return lightning_attn_paged_sparse_decode(
+            q.p, q.stride, c.k, c.ks, c.v, c.vs, t.p, t.stride, t.width, lens,
+            static_cast<const int32_t *>(sel.data_ptr()), count, c.pages, c.page, s.tokens, s.heads,
+            c.kv_heads, s.d, s.code, scale, out.data_ptr(), lse, ws.first, ws.second, call.stream());
+    });
+    for (int i : {7, 8}) written(a[i]);
+    return wrap(out);
+}
+
 // block_table, seq_lens, new_lens, free_pages, free_count, page_size, num_tokens, finished,
 // seq_lens_out, free_count_out, stream
 PyObject *paged_reserve(PyObject *const *a) {
@@ -567,6 +665,8 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
 PyMethodDef kMethods[] = {METHOD(qk_norm_rope, 11), METHOD(qk_norm_rope_backward, 14),
                           METHOD(paged_append, 14), METHOD(paged_decode, 10),
                           METHOD(paged_step, 19),   METHOD(paged_reserve, 11),
+                          METHOD(paged_bounds, 6),  METHOD(paged_select, 11),
+                          METHOD(paged_sparse_decode, 11),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_lightning_binding", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

@@ -165,6 +165,23 @@ constexpr int kNormBackwardBlocks = 152 * 5;
 cudaError_t qk_norm_rope(const NormRopeArgs &a, bool bf16);
 cudaError_t qk_norm_rope_backward(const NormRopeArgs &a, bool bf16);
 
+// Most tokens of a request: room for some tiles past the end in 32-bit token indices.
+constexpr int kMaxTokens = 0x7fff0000;
+
+// What the attention over a shared prefix leaves for the requests behind it: the tiles of all units
+// (unit_rows query rows of one key-value head; row r is head r % group of the head's group, of request
+// r / group), one unit after the other, are cut into `ctas` equal ranges.  CTA c's part of unit u is
+// in slots (c + u) * parts .. + parts - 1: along the ranges either c or u grows from one
+// part to the next, so c + u is theirs alone.  A slot holds the unnormalised sums [stride][D]
+// and (maximum, exponential sum) [stride].
+struct PrefixPieces {
+    const int32_t *len = nullptr;  // [1] tokens, on the device
+    int max_tokens = 0;            // capacity of the prefix's table
+    int tile = 1, ctas = 1, units = 1, units_per_head = 1, unit_rows = 1;
+    int parts = 1, stride = 0;
+    float *pieces = nullptr;
+};
+
 struct PagedDecodeArgs {
     const void *q;                 // [B, H, D] (fp32 where q_f32), q_stride elements a request
     int64_t q_stride;
@@ -181,6 +198,9 @@ struct PagedDecodeArgs {
     float *workspace;              // [kPagedCtas][2][rows][D + 2]
     cudaStream_t stream;
     int head_groups = 1;           // units a key-value head is cut into (set by the launcher)
+    const int32_t *chosen = nullptr;  // [B, Hkv, chosen_count] blocks of the request
+    int chosen_count = 0;
+    PrefixPieces prefix;
 };
 
 // CTAs the work of the paged attention is divided among (two per SM), and
@@ -189,6 +209,43 @@ constexpr int kPagedCtas = 152 * 2;
 constexpr int kPagedMaxRows = 16;
 
 cudaError_t paged_decode(const PagedDecodeArgs &a, bool bf16, bool q_f32);
+
+cudaError_t paged_sparse_decode(const PagedDecodeArgs &a, bool bf16);
+
+// Bounds of the pages' keys: [pages, Hkv, 2, D], the minimum of every channel, then the maximum.
+struct PagedBoundsArgs {
+    const void *k;                 // [pages, Hkv, page_size, D]
+    void *bounds;
+    int64_t k_page_stride, bounds_page_stride;  // elements
+    const int32_t *block_table;    // [B, table_stride]
+    const int32_t *first, *seq_lens;  // [B]: the new tokens are first .. seq_lens - 1
+    int table_stride, table_width, max_tokens;
+    int num_pages, page_size;
+    int batch, num_kv_heads, head_dim;
+    cudaStream_t stream;
+};
+
+cudaError_t paged_bounds(const PagedBoundsArgs &a, bool bf16);
+
+struct PagedSelectArgs {
+    const void *q;                 // [B, H, D], q_stride elements a request
+    int64_t q_stride;
+    const void *bounds;
+    int64_t bounds_page_stride;
+    const int32_t *block_table;    // [B, table_stride]
+    const int32_t *seq_lens;       // [B]
+    int table_stride, table_width, max_tokens;
+    int num_pages, page_size;
+    int batch, num_kv_heads, group, head_dim;
+    int count, keep_first, keep_last;
+    int32_t *selected;             // [B, Hkv, count]
+    void *workspace;
+    cudaStream_t stream;
+};
+
+// Bytes of its workspace, or -1 where they pass 2^62.
+int64_t paged_select_workspace(int64_t batch, int64_t num_kv_heads, int64_t table_width);
+cudaError_t paged_select(const PagedSelectArgs &a, bool bf16);
 
 struct PagedReserveArgs {
     int32_t *block_table;          // [B, table_stride]

@@ -159,6 +159,12 @@ la_status check_decode(const int32_t *block_table, int32_t table_stride, int32_t
     return LA_OK;
 }
 
+// Tokens that a row of a table can hold.
+int capacity(int32_t table_width, int32_t page_size) {
+    const long long most = (long long)table_width * page_size;
+    return (int)(most < la::kMaxTokens ? most : la::kMaxTokens);
+}
+
 la::PagedDecodeArgs decode_args(const void *q, int64_t q_stride, const void *k_cache,
                                 int64_t k_page_stride, const void *v_cache, int64_t v_page_stride,
                                 const int32_t *block_table, int32_t table_stride,
@@ -176,9 +182,7 @@ la::PagedDecodeArgs decode_args(const void *q, int64_t q_stride, const void *k_c
     a.block_table = block_table;
     a.seq_lens = seq_lens;
     a.table_stride = table_stride;
-    const long long most = (long long)table_width * page_size;
-    // room for a tile past the end in 32-bit token indices
-    a.max_tokens = (int)(most < 0x7fff0000LL ? most : 0x7fff0000LL);
+    a.max_tokens = capacity(table_width, page_size);
     a.num_pages = num_pages;
     a.page_size = page_size;
     a.batch = batch;
@@ -409,6 +413,125 @@ la_status lightning_attn_paged_step(
         block_table, table_stride, table_width, seq_lens, num_pages, page_size, batch, num_heads,
         num_kv_heads, head_dim, scale, out, lse, workspace, stream);
     return from_cuda(la::paged_decode(a, dtype == LA_DTYPE_BF16, true), "paged_step (attention)");
+}
+
+la_status lightning_attn_paged_bounds(
+    const void *k_cache, int64_t k_page_stride, void *bounds, int64_t bounds_page_stride,
+    const int32_t *block_table, int32_t table_stride, int32_t table_width, const int32_t *first,
+    const int32_t *seq_lens, int32_t num_pages, int32_t page_size, int32_t batch,
+    int32_t num_kv_heads, int32_t head_dim, la_dtype dtype, void *stream) {
+    if (num_kv_heads < 1) return LA_INVALID("num_kv_heads < 1 (%d)", num_kv_heads);
+    LA_TRY(check_shape(batch, num_kv_heads, 0, head_dim, dtype));
+    LA_TRY(check_pool(num_pages, page_size));
+    if (batch == 0) return LA_OK;
+    LA_TRY(check_table(block_table, table_stride, table_width, seq_lens));
+    if (!first || !aligned(first, 4)) return LA_INVALID("first must be a 4-byte aligned device array");
+    if (num_pages == 0) return LA_OK;
+    LA_TRY(check_cache("k_cache", k_cache, k_page_stride, num_kv_heads, page_size, head_dim, dtype));
+    LA_TRY(check_cache("bounds", bounds, bounds_page_stride, num_kv_heads, 2, head_dim, dtype));
+    if (bounds == k_cache) return LA_INVALID("bounds and k_cache are one array");
+    la::PagedBoundsArgs a;
+    a.k = k_cache;
+    a.bounds = bounds;
+    a.k_page_stride = k_page_stride;
+    a.bounds_page_stride = bounds_page_stride;
+    a.block_table = block_table;
+    a.first = first;
+    a.seq_lens = seq_lens;
+    a.table_stride = table_stride;
+    a.table_width = table_width;
+    a.max_tokens = capacity(table_width, page_size);
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.batch = batch;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return from_cuda(la::paged_bounds(a, dtype == LA_DTYPE_BF16), "paged_bounds");
+}
+
+int64_t lightning_attn_paged_select_workspace_bytes(int32_t batch, int32_t num_kv_heads,
+                                                    int32_t table_width) {
+    if (batch < 0 || num_kv_heads < 1 || table_width < 0) return -1;
+    return la::paged_select_workspace(batch, num_kv_heads, table_width);
+}
+
+la_status lightning_attn_paged_select(
+    const void *q, int64_t q_stride, const void *bounds, int64_t bounds_page_stride,
+    const int32_t *block_table, int32_t table_stride, int32_t table_width, const int32_t *seq_lens,
+    int32_t num_pages, int32_t page_size, int32_t batch, int32_t num_heads, int32_t num_kv_heads,
+    int32_t head_dim, la_dtype dtype, int32_t count, int32_t keep_first, int32_t keep_last,
+    int32_t *selected, void *workspace, int64_t workspace_bytes, void *stream) {
+    LA_TRY(check_shape(batch, num_heads, num_kv_heads, head_dim, dtype));
+    if (num_kv_heads < 1 || num_heads % num_kv_heads != 0)
+        return LA_INVALID("num_heads (%d) must be a multiple of num_kv_heads (%d)", num_heads,
+                          num_kv_heads);
+    LA_TRY(check_pool(num_pages, page_size));
+    if (count < 1) return LA_INVALID("count < 1 (%d)", count);
+    if (keep_first < 0 || keep_last < 0 || (long long)keep_first + keep_last > count)
+        return LA_INVALID("keep_first (%d) and keep_last (%d) must be at least 0 and together at most "
+                          "count (%d)", keep_first, keep_last, count);
+    if (batch == 0) return LA_OK;
+    LA_TRY(check_table(block_table, table_stride, table_width, seq_lens));
+    LA_TRY(check_rows("q", q, q_stride, num_heads, head_dim, dtype));
+    if (num_pages > 0)
+        LA_TRY(check_cache("bounds", bounds, bounds_page_stride, num_kv_heads, 2, head_dim, dtype));
+    if (!selected || !aligned(selected, 4))
+        return LA_INVALID("selected must be a 4-byte aligned device array");
+    const int64_t need = la::paged_select_workspace(batch, num_kv_heads, table_width);
+    if (need < 0) return LA_INVALID("too many blocks");
+    LA_TRY(check_workspace(workspace, workspace_bytes, need));
+    la::PagedSelectArgs a;
+    a.q = q;
+    a.q_stride = q_stride;
+    a.bounds = bounds;
+    a.bounds_page_stride = bounds_page_stride;
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.table_stride = table_stride;
+    a.table_width = table_width;
+    a.max_tokens = capacity(table_width, page_size);
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.batch = batch;
+    a.num_kv_heads = num_kv_heads;
+    a.group = num_heads / num_kv_heads;
+    a.head_dim = head_dim;
+    a.count = count;
+    a.keep_first = keep_first;
+    a.keep_last = keep_last;
+    a.selected = selected;
+    a.workspace = workspace;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return from_cuda(la::paged_select(a, dtype == LA_DTYPE_BF16), "paged_select");
+}
+
+la_status lightning_attn_paged_sparse_decode(
+    const void *q, int64_t q_stride, const void *k_cache, int64_t k_page_stride,
+    const void *v_cache, int64_t v_page_stride, const int32_t *block_table, int32_t table_stride,
+    int32_t table_width, const int32_t *seq_lens, const int32_t *selected, int32_t count,
+    int32_t num_pages, int32_t page_size, int32_t batch, int32_t num_heads, int32_t num_kv_heads,
+    int32_t head_dim, la_dtype dtype, float scale, void *out, float *lse, void *workspace,
+    int64_t workspace_bytes, void *stream) {
+    LA_TRY(check_shape(batch, num_heads, num_kv_heads, head_dim, dtype));
+    LA_TRY(check_decode(block_table, table_stride, table_width, seq_lens, k_cache, k_page_stride,
+                        v_cache, v_page_stride, num_pages, page_size, batch, num_heads,
+                        num_kv_heads, head_dim, dtype, scale, out, lse));
+    if (count < 1) return LA_INVALID("count < 1 (%d)", count);
+    if (batch == 0) return LA_OK;
+    if (!selected || !aligned(selected, 4))
+        return LA_INVALID("selected must be a 4-byte aligned device array");
+    if ((long long)count * page_size > la::kMaxTokens)
+        return LA_FAIL(LA_ERR_UNSUPPORTED, "count * page_size must be at most %d", la::kMaxTokens);
+    LA_TRY(check_rows("q", q, q_stride, num_heads, head_dim, dtype));
+    LA_TRY(check_workspace(workspace, workspace_bytes, decode_workspace(head_dim)));
+    la::PagedDecodeArgs a = decode_args(
+        q, q_stride, k_cache, k_page_stride, v_cache, v_page_stride, block_table, table_stride,
+        table_width, seq_lens, num_pages, page_size, batch, num_heads, num_kv_heads, head_dim,
+        scale, out, lse, workspace, stream);
+    a.chosen = selected;
+    a.chosen_count = count;
+    return from_cuda(la::paged_sparse_decode(a, dtype == LA_DTYPE_BF16), "paged_sparse_decode");
 }
 
 la_status lightning_attn_paged_reserve(

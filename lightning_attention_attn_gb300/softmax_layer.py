@@ -8,7 +8,14 @@ step of such a layer is
     out = paged_step(q, k, v, positions, table, k_cache, v_cache, slots, block_table, seq_lens)
 
 beside :func:`decode` of the lightning layers; a prompt enters the cache through
-:func:`paged_append`.  :func:`qk_norm_rope` and its gradients also precede
+:func:`paged_append`.  Where contexts are long, a step may read a few pages of each:
+
+    q = paged_append(q, k, v, positions, table, k_cache, v_cache, slots)
+    paged_bounds(k_cache, bounds, block_table, old_lens, seq_lens)
+    selected = paged_select(q, bounds, block_table, seq_lens, page_size, count)
+    out = paged_sparse_decode(q, k_cache, v_cache, block_table, seq_lens, selected)
+
+:func:`qk_norm_rope` and its gradients also precede
 :func:`prefill` and follow :func:`backward` in training.
 
 As in the rest of the package, nothing is computed here and there is no
@@ -49,12 +56,16 @@ def declare(lib) -> None:
         "paged_decode": [p, l] + cache + [p, i, i, p, i, i] + shape + [f, p, p, p, l, p],
         "paged_step": [p, l] * 3 + rotary + cache + [p, p, i, i, p, i, i] + shape +
                       [f, p, p, p, l, p],
+        "paged_bounds": [p, l, p, l, p, i, i, p, p] + [i] * 5 + [c, p],
+        "paged_select": [p, l, p, l, p, i, i, p, i, i] + shape + [i, i, i, p, p, l, p],
+        "paged_sparse_decode": [p, l] + cache + [p, i, i, p, p, i, i, i] + shape + [f, p, p, p, l, p],
         "paged_reserve": [p, i, i, p, p, p, i, p, p, i, i, i, p, p, p, p, p, p, p],
     }.items():
         fn = getattr(lib, "lightning_attn_" + name)
         fn.argtypes, fn.restype = args, ctypes.c_int
     for name, args in {"qk_norm_rope_workspace_bytes": [i], "paged_decode_workspace_bytes": [i],
-                       "paged_step_workspace_bytes": [i, i, i]}.items():
+                       "paged_step_workspace_bytes": [i, i, i],
+                       "paged_select_workspace_bytes": [i, i, i]}.items():
         fn = getattr(lib, "lightning_attn_" + name)
         fn.argtypes, fn.restype = args, ctypes.c_int64
 
@@ -187,6 +198,49 @@ def paged_step(q, k, v, positions, table, k_cache, v_cache, slots, block_table, 
     return (_binding or _calls()).paged_step(
         q, k, v, positions, table, k_cache, v_cache, slots, block_table, seq_lens, q_weight,
         k_weight, eps, interleaved, scale, out, lse, workspace, stream)
+
+
+def paged_bounds(k_cache, bounds, block_table, first, seq_lens, *, stream=None):
+    """Smallest and largest value of every channel of a page's keys, kept as the keys enter the
+    cache.  Returns ``bounds``.
+
+    bounds: [pages, Hkv, 2, d] in the cache's dtype (minima, then maxima); first, seq_lens: int32
+    [B]: tokens first[b] .. seq_lens[b] - 1 are new.  A block that begins among them gets new
+    bounds, the one that first[b] is inside of has its bounds extended (``first`` at the block's
+    beginning takes them anew).  The blocks with new tokens lie in distinct pages.
+    """
+    return (_binding or _calls()).paged_bounds(k_cache, bounds, block_table, first, seq_lens, stream)
+
+
+def paged_select_workspace_bytes(batch: int, num_kv_heads: int, blocks: int) -> int:
+    """Bytes of workspace :func:`paged_select` needs (blocks: the width of block_table)."""
+    return _bytes("lightning_attn_paged_select_workspace_bytes", batch, num_kv_heads, blocks)
+
+
+def paged_select(q, bounds, block_table, seq_lens, page_size: int, count: int, *, keep_first: int = 1,
+                 keep_last: int = 1, out=None, workspace=None, stream=None):
+    """The ``count`` blocks of every request and key-value head whose bounds allow the largest q . k.
+    Returns int32 [B, Hkv, count]: blocks in ascending order, then -1.
+
+    q: [B, H, d]; bounds: of :func:`paged_bounds`, for all blocks of the requests.  A block's score
+    is the largest, over the heads that share the key-value head, of sum_d max(q_d lo_d, q_d hi_d);
+    the choice is that of scores in 64 bits, ties to the lower block.  The first ``keep_first`` and
+    the last ``keep_last`` blocks of a request are always chosen.
+    """
+    return (_binding or _calls()).paged_select(q, bounds, block_table, seq_lens, page_size, count,
+                                               keep_first, keep_last, out, workspace, stream)
+
+
+def paged_sparse_decode(q, k_cache, v_cache, block_table, seq_lens, selected, *,
+                        scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
+    """:func:`paged_decode` over the tokens of chosen blocks alone.  Returns out [B, H, d].
+
+    selected: int32 [B, Hkv, count], of :func:`paged_select` or of the caller's own (in any order): the
+    first min(count, blocks of the request) entries of a row count; one that is no block of the
+    request stands for no tokens.  Other arguments as for :func:`paged_decode`.
+    """
+    return (_binding or _calls()).paged_sparse_decode(q, k_cache, v_cache, block_table, seq_lens,
+                                                      selected, scale, out, lse, workspace, stream)
 
 
 def paged_reserve(block_table, seq_lens, new_lens, free_pages, free_count, page_size: int,
