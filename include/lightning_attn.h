@@ -556,6 +556,32 @@ la_status lightning_attn_paged_sparse_decode(
     int64_t workspace_bytes, void *stream);
 
 /*
+ * lightning_attn_paged_decode where the requests share a prefix (a system prompt, a document):
+ * request b attends to the first prefix_len[0] tokens of the prefix's pages and to the first
+ * seq_lens[b] tokens of its own, and the prefix's keys and values are read for the batch as a whole.
+ *
+ * prefix_table [prefix_width] int32, prefix_len [1] int32: as a row of block_table and its length.
+ * block_table, seq_lens  the requests' own tokens behind the prefix, which begin with a
+ *              page of their own; 0 tokens are allowed.  (Both kinds of pages are of one pool;
+ *              pages outside [0, num_pages) leave their tokens out.)
+ * workspace    lightning_attn_paged_prefix_decode_workspace_bytes(...) bytes, 16-byte aligned;
+ *              scratch, not shared by calls that may overlap.
+ * The rest, infinities included, is as for lightning_attn_paged_decode; lse is that of all tokens.
+ */
+la_status lightning_attn_paged_prefix_decode(
+    const void *q, int64_t q_stride, const void *k_cache, int64_t k_page_stride,
+    const void *v_cache, int64_t v_page_stride, const int32_t *prefix_table, int32_t prefix_width,
+    const int32_t *prefix_len, const int32_t *block_table, int32_t table_stride,
+    int32_t table_width, const int32_t *seq_lens, int32_t num_pages, int32_t page_size,
+    int32_t batch, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, la_dtype dtype,
+    float scale, void *out, float *lse, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of lightning_attn_paged_prefix_decode; -1 for invalid sizes. */
+int64_t lightning_attn_paged_prefix_decode_workspace_bytes(int32_t batch, int32_t num_heads,
+                                                           int32_t num_kv_heads, int32_t head_dim,
+                                                           la_dtype dtype);
+
+/*
  * Page bookkeeping of one serving step, from the requests' lengths, on the GPU.
  * In this order:
  *   1. A finished request (finished[b] != 0; finished may be NULL) pushes the

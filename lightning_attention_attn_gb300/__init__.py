@@ -25,7 +25,8 @@ import torch
 from . import softmax_layer
 from . import workloads  # noqa: F401  (seeded input recipes)
 from .softmax_layer import (paged_append, paged_bounds, paged_decode,  # noqa: F401
-                            paged_decode_workspace_bytes, paged_reserve, paged_select,
+                            paged_decode_workspace_bytes, paged_prefix_decode,
+                            paged_prefix_decode_workspace_bytes, paged_reserve, paged_select,
                             paged_select_workspace_bytes, paged_sparse_decode, paged_step,
                             paged_step_workspace_bytes, qk_norm_rope, qk_norm_rope_backward,
                             rotary_table)

@@ -606,6 +606,38 @@ PyObject *paged_sparse_decode(PyObject *const *a) {
     return wrap(out);
 }
 
+// q, k_cache, v_cache, prefix_table, prefix_len, block_table, seq_lens, scale, out, lse, workspace,
+// stream
+PyObject *paged_prefix_decode(PyObject *const *a) {
+    Call call(a[0], "q", a[11]);
+    const Shape s = shape_of(a[0], Py_None, false);
+    const Rows q = call.rows(a[0], "q", s.tokens, s.heads, s.d, s.type);
+    const Cache c = cache_of(call, a[1], a[2], s.d, s.type);
+    const Tensor &front = tensor(a[3], "prefix_table");
+    if (front.dim() != 1) refuse(PyExc_ValueError, "prefix_table must be an int32 [blocks] tensor");
+    const int32_t width = size32(front.size(0), "prefix_table");
+    const int32_t *pages = call.ints(a[3], "prefix_table", width), *len = call.ints(a[4], "prefix_len", 1);
+    const Table t = table_of(call, a[5], s.tokens);
+    const int32_t *lens = call.ints(a[6], "seq_lens", s.tokens);
+    const float scale = scale_of(a[7], s);
+    const Tensor out = attention_out(call, a[8], s);
+    float *lse = lse_of(call, a[9], s);
+    const int64_t need = lightning_attn_paged_prefix_decode_workspace_bytes(s.tokens, s.heads, c.kv_heads,
+                                                                            s.d, s.code);
+    if (need < 0)
+        refuse(PyExc_ValueError, "%d heads over %d key-value heads of %d, batch %d", s.heads, c.kv_heads, s.d,
+               s.tokens);
+    const auto ws = call.workspace(a[10], need);
+    launch("lightning_attn_paged_prefix_decode", [&] {
+        return lightning_attn_paged_prefix_decode(
+            q.p, q.stride, c.k, c.ks, c.v, c.vs, pages, width, len, t.p, t.stride, t.width, lens, c.pages,
+            c.page, s.tokens, s.heads, c.kv_heads, s.d, s.code, scale, out.data_ptr(), lse, ws.first,
+            ws.second, call.stream());
+    });
+    for (int i : {8, 9}) written(a[i]);
+    return wrap(out);
+}
+
 // block_table, seq_lens, new_lens, free_pages, free_count, page_size, num_tokens, finished,
 // seq_lens_out, free_count_out, stream
 PyObject *paged_reserve(PyObject *const *a) {
@@ -666,7 +698,7 @@ PyMethodDef kMethods[] = {METHOD(qk_norm_rope, 11), METHOD(qk_norm_rope_backward
                           METHOD(paged_append, 14), METHOD(paged_decode, 10),
                           METHOD(paged_step, 19),   METHOD(paged_reserve, 11),
                           METHOD(paged_bounds, 6),  METHOD(paged_select, 11),
-                          METHOD(paged_sparse_decode, 11),
+                          METHOD(paged_sparse_decode, 11), METHOD(paged_prefix_decode, 12),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_lightning_binding", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

@@ -212,6 +212,11 @@ cudaError_t paged_decode(const PagedDecodeArgs &a, bool bf16, bool q_f32);
 
 cudaError_t paged_sparse_decode(const PagedDecodeArgs &a, bool bf16);
 
+// The split of a shared prefix (all but len, max_tokens and pieces), and the attention behind it:
+// a.prefix is complete.
+PrefixPieces paged_prefix_pieces(int64_t batch, int64_t num_heads, int64_t num_kv_heads, bool bf16);
+cudaError_t paged_prefix_decode(const PagedDecodeArgs &a, const int32_t *prefix_table, bool bf16);
+
 // Bounds of the pages' keys: [pages, Hkv, 2, D], the minimum of every channel, then the maximum.
 struct PagedBoundsArgs {
     const void *k;                 // [pages, Hkv, page_size, D]

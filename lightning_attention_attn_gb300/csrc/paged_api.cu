@@ -207,6 +207,11 @@ la_status check_workspace(const void *workspace, int64_t bytes, int64_t need) {
     return LA_OK;
 }
 
+int64_t prefix_workspace(const la::PrefixPieces &f, int32_t head_dim) {
+    return decode_workspace(head_dim) + ((int64_t)f.ctas + f.units) * f.parts * f.stride *
+                                            (head_dim + 2) * (int64_t)sizeof(float);
+}
+
 }  // namespace
 
 extern "C" {
@@ -532,6 +537,48 @@ la_status lightning_attn_paged_sparse_decode(
     a.chosen = selected;
     a.chosen_count = count;
     return from_cuda(la::paged_sparse_decode(a, dtype == LA_DTYPE_BF16), "paged_sparse_decode");
+}
+
+int64_t lightning_attn_paged_prefix_decode_workspace_bytes(int32_t batch, int32_t num_heads,
+                                                           int32_t num_kv_heads, int32_t head_dim,
+                                                           la_dtype dtype) {
+    if (batch < 0 || num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads != 0 ||
+        (head_dim != 64 && head_dim != 128) || (dtype != LA_DTYPE_BF16 && dtype != LA_DTYPE_FP32) ||
+        (long long)batch * num_heads > 0x7fffffffLL)
+        return -1;
+    return prefix_workspace(la::paged_prefix_pieces(batch, num_heads, num_kv_heads, dtype == LA_DTYPE_BF16),
+                            head_dim);
+}
+
+la_status lightning_attn_paged_prefix_decode(
+    const void *q, int64_t q_stride, const void *k_cache, int64_t k_page_stride,
+    const void *v_cache, int64_t v_page_stride, const int32_t *prefix_table, int32_t prefix_width,
+    const int32_t *prefix_len, const int32_t *block_table, int32_t table_stride,
+    int32_t table_width, const int32_t *seq_lens, int32_t num_pages, int32_t page_size,
+    int32_t batch, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, la_dtype dtype,
+    float scale, void *out, float *lse, void *workspace, int64_t workspace_bytes, void *stream) {
+    LA_TRY(check_shape(batch, num_heads, num_kv_heads, head_dim, dtype));
+    LA_TRY(check_decode(block_table, table_stride, table_width, seq_lens, k_cache, k_page_stride,
+                        v_cache, v_page_stride, num_pages, page_size, batch, num_heads,
+                        num_kv_heads, head_dim, dtype, scale, out, lse));
+    if (prefix_width < 0) return LA_INVALID("prefix_width < 0 (%d)", prefix_width);
+    if (batch == 0) return LA_OK;
+    if ((prefix_width > 0 && !prefix_table) || !prefix_len)
+        return LA_INVALID("null prefix_table or prefix_len");
+    if (!aligned(prefix_table, 4) || !aligned(prefix_len, 4))
+        return LA_INVALID("prefix_table and prefix_len must be 4-byte aligned");
+    LA_TRY(check_rows("q", q, q_stride, num_heads, head_dim, dtype));
+    la::PrefixPieces f = la::paged_prefix_pieces(batch, num_heads, num_kv_heads, dtype == LA_DTYPE_BF16);
+    LA_TRY(check_workspace(workspace, workspace_bytes, prefix_workspace(f, head_dim)));
+    f.len = prefix_len;
+    f.max_tokens = capacity(prefix_width, page_size);
+    f.pieces = reinterpret_cast<float *>(static_cast<char *>(workspace) + decode_workspace(head_dim));
+    la::PagedDecodeArgs a = decode_args(
+        q, q_stride, k_cache, k_page_stride, v_cache, v_page_stride, block_table, table_stride,
+        table_width, seq_lens, num_pages, page_size, batch, num_heads, num_kv_heads, head_dim,
+        scale, out, lse, workspace, stream);
+    a.prefix = f;
+    return from_cuda(la::paged_prefix_decode(a, prefix_table, dtype == LA_DTYPE_BF16), "paged_prefix_decode");
 }
 
 la_status lightning_attn_paged_reserve(

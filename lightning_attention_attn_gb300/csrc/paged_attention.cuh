@@ -347,13 +347,13 @@ __device__ __forceinline__ void write_empty(const PagedDecodeArgs &a) {
         if constexpr (KV == Kv::kBehind) {
             for (int i = threadIdx.x * 4; i < row; i += blockDim.x * 4)
                 Partial().write<T, KV>(a, (size_t)b * a.num_heads + i / a.head_dim, i % a.head_dim);
-            continue;
+        } else {
+            for (int i = threadIdx.x; i < row; i += blockDim.x)
+                static_cast<T *>(a.out)[(size_t)b * row + i] = T(0.f);
+            if (a.lse)
+                for (int i = threadIdx.x; i < a.num_heads; i += blockDim.x)
+                    a.lse[(size_t)b * a.num_heads + i] = -kInf;
         }
-        for (int i = threadIdx.x; i < row; i += blockDim.x)
-            static_cast<T *>(a.out)[(size_t)b * row + i] = T(0.f);
-        if (a.lse)
-            for (int i = threadIdx.x; i < a.num_heads; i += blockDim.x)
-                a.lse[(size_t)b * a.num_heads + i] = -kInf;
     }
 }
 
@@ -1272,12 +1272,13 @@ template <typename Core> cudaError_t launch(PagedDecodeArgs a) {
 // heads.  64 query heads over bf16 keys and values of 0.54 GB each: 4 to 16 heads a kv head
 // 165 to 175 us, 32 heads 325.
 template <Kv KV, int D>
-cudaError_t dispatch(const PagedDecodeArgs &a, bool bf16, bool q_f32) {
+cudaError_t dispatch(const PagedDecodeArgs &a, bool bf16, bool q_f32 = false) {
     if (!bf16)
         return a.group <= 4   ? launch<F32Core<KV, D, 4>>(a)
                : a.group <= 8 ? launch<F32Core<KV, D, 8>>(a)
                               : launch<F32Core<KV, D, 16>>(a);
-    if (q_f32) return a.group <= 8 ? launch<Bf16Core<KV, D, 1, true>>(a) : launch<Bf16Core<KV, D, 2, true>>(a);
+    if constexpr (KV == Kv::kOwn)  // the queries of a whole step
+        if (q_f32) return a.group <= 8 ? launch<Bf16Core<KV, D, 1, true>>(a) : launch<Bf16Core<KV, D, 2, true>>(a);
     return a.group <= 8 ? launch<Bf16Core<KV, D, 1, false>>(a) : launch<Bf16Core<KV, D, 2, false>>(a);
 }
 

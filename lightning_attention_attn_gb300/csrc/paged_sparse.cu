@@ -8,8 +8,8 @@
 namespace la {
 
 cudaError_t paged_sparse_decode(const PagedDecodeArgs &a, bool bf16) {
-    if (a.head_dim == 128) return dispatch<Kv::kChosen, 128>(a, bf16, !bf16);
-    if (a.head_dim == 64) return dispatch<Kv::kChosen, 64>(a, bf16, !bf16);
+    if (a.head_dim == 128) return dispatch<Kv::kChosen, 128>(a, bf16);
+    if (a.head_dim == 64) return dispatch<Kv::kChosen, 64>(a, bf16);
     return cudaErrorNotSupported;
 }
 

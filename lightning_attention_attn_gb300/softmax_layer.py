@@ -15,7 +15,7 @@ beside :func:`decode` of the lightning layers; a prompt enters the cache through
     selected = paged_select(q, bounds, block_table, seq_lens, page_size, count)
     out = paged_sparse_decode(q, k_cache, v_cache, block_table, seq_lens, selected)
 
-:func:`qk_norm_rope` and its gradients also precede
+and where the batch shares a prefix, ``paged_prefix_decode`` reads that once for all.  :func:`qk_norm_rope` and its gradients also precede
 :func:`prefill` and follow :func:`backward` in training.
 
 As in the rest of the package, nothing is computed here and there is no
@@ -59,13 +59,15 @@ def declare(lib) -> None:
         "paged_bounds": [p, l, p, l, p, i, i, p, p] + [i] * 5 + [c, p],
         "paged_select": [p, l, p, l, p, i, i, p, i, i] + shape + [i, i, i, p, p, l, p],
         "paged_sparse_decode": [p, l] + cache + [p, i, i, p, p, i, i, i] + shape + [f, p, p, p, l, p],
+        "paged_prefix_decode": [p, l] + cache + [p, i, p, p, i, i, p, i, i] + shape + [f, p, p, p, l, p],
         "paged_reserve": [p, i, i, p, p, p, i, p, p, i, i, i, p, p, p, p, p, p, p],
     }.items():
         fn = getattr(lib, "lightning_attn_" + name)
         fn.argtypes, fn.restype = args, ctypes.c_int
     for name, args in {"qk_norm_rope_workspace_bytes": [i], "paged_decode_workspace_bytes": [i],
                        "paged_step_workspace_bytes": [i, i, i],
-                       "paged_select_workspace_bytes": [i, i, i]}.items():
+                       "paged_select_workspace_bytes": [i, i, i],
+                       "paged_prefix_decode_workspace_bytes": [i, i, i, i, c]}.items():
         fn = getattr(lib, "lightning_attn_" + name)
         fn.argtypes, fn.restype = args, ctypes.c_int64
 
@@ -241,6 +243,27 @@ def paged_sparse_decode(q, k_cache, v_cache, block_table, seq_lens, selected, *,
     """
     return (_binding or _calls()).paged_sparse_decode(q, k_cache, v_cache, block_table, seq_lens,
                                                       selected, scale, out, lse, workspace, stream)
+
+
+def paged_prefix_decode_workspace_bytes(batch: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                        dtype=torch.bfloat16) -> int:
+    """Bytes of workspace :func:`paged_prefix_decode` needs, whatever the lengths."""
+    return _bytes("lightning_attn_paged_prefix_decode_workspace_bytes", batch, num_heads, num_kv_heads,
+                  head_dim, 0 if dtype == torch.bfloat16 else 1)
+
+
+def paged_prefix_decode(q, k_cache, v_cache, prefix_table, prefix_len, block_table, seq_lens, *,
+                        scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
+    """:func:`paged_decode` of a batch whose requests share a prefix (a system prompt, a document),
+    whose keys and values are read for the batch as a whole.  Returns out [B, H, d].
+
+    prefix_table: int32 [blocks], prefix_len: int32 [1], the prefix's pages and its tokens; block_table,
+    seq_lens: the requests' own tokens behind it, on pages of their own (0 tokens are allowed).
+    lse is that of all tokens; other arguments as for :func:`paged_decode`.
+    """
+    return (_binding or _calls()).paged_prefix_decode(q, k_cache, v_cache, prefix_table, prefix_len,
+                                                      block_table, seq_lens, scale, out, lse, workspace,
+                                                      stream)
 
 
 def paged_reserve(block_table, seq_lens, new_lens, free_pages, free_count, page_size: int,

@@ -359,6 +359,230 @@ def test_sparse_refusals():
     assert la.paged_sparse_decode(q[:0], kc, vc, bt[:0], lens[:0], sel[:0]).shape == (0, 4, 64)
 
 
+# ------------------------------------------------------ behind a shared prefix
+def behind(prefix, lens, page, hk, d, dtype, g, garbage=NAN):
+    """A pool with the prefix and the requests' own tokens anywhere in it, garbage elsewhere."""
+    bt, pages = tables(blocks_of([prefix] + lens, page), g)
+    kc = torch.full((pages, hk, page, d), garbage, dtype=dtype, device="cuda")
+    vc = kc.clone()
+    for row, n in zip(bt, [prefix] + lens):
+        t = torch.arange(n, device="cuda")
+        for cache in (kc, vc):
+            cache[row[t // page].long(), :, t % page] = randn((n, hk, d), dtype, g)
+    return kc, vc, bt[0].clone(), ints([prefix]), bt[1:].clone(), ints(lens)
+
+
+def check_prefix(q, kc, vc, pt, pl, bt, lens, scale=None, **kw):
+    b, h, d = q.shape
+    lse = torch.empty((b, h), device="cuda")
+    out = la.paged_prefix_decode(q, kc, vc, pt, pl, bt, lens, scale=scale, lse=lse, **kw)
+    scale = d ** -0.5 if scale is None else scale
+    parts = lref.Behind((c(kc), c(vc)), c(pt), c(pl), c(bt), c(lens))
+    want, wlse, bound, lbound = lref.over(c(q), parts, scale, tile=128)
+    ref.within(out, want, bound, ref.u_of(q.dtype), "out")
+    ref.within(lse, wlse, lbound, ref.u_of(FP32), "lse")
+    return out
+
+
+@pytest.mark.parametrize("dtype, h, hk, d", [(BF16, 16, 2, 128), (BF16, 12, 1, 64), (FP32, 6, 2, 64),
+                                             (FP32, 16, 1, 128), (BF16, 40, 2, 128), (BF16, 3, 3, 64)])
+@pytest.mark.parametrize("prefix, page", [(0, 16), (1, 16), (127, 1), (128, 64), (129, 48), (1000, 5), (4001, 64)])
+def test_prefix(dtype, h, hk, d, prefix, page):
+    g = gen(prefix + h)
+    lens = [0, 1, 64, 65, 300]
+    args = behind(prefix, lens, page, hk, d, dtype, g)
+    out = check_prefix(randn((5, h, d), dtype, g), *args)
+    if prefix == 0:
+        assert (out[0] == 0).all()
+
+
+@pytest.mark.parametrize("dtype, h, hk, d, batch", [
+    (BF16, 8, 8, 128, 1), (BF16, 8, 8, 64, 3), (BF16, 64, 8, 128, 15), (BF16, 64, 8, 128, 16),
+    (BF16, 64, 8, 128, 17), (BF16, 16, 1, 64, 16), (BF16, 7, 1, 128, 37), (BF16, 32, 2, 128, 41),
+    (FP32, 4, 4, 64, 1), (FP32, 4, 1, 128, 2), (FP32, 16, 2, 64, 33), (BF16, 48, 1, 64, 11)])
+def test_prefix_batches(dtype, h, hk, d, batch):
+    """Rows of a key-value head from one to several hundred, in every relation to the tiles."""
+    g = gen(batch + h)
+    lens = [(37 * i) % 90 for i in range(batch)]
+    args = behind(700, lens, 32, hk, d, dtype, g)
+    check_prefix(randn((batch, h, d), dtype, g), *args)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_prefix_long_and_wide(dtype):
+    """A prefix of many tiles a CTA, own tokens for the split over all CTAs, a table much wider
+    than the prefix, and the other way round."""
+    g = gen(41)
+    lens = [5000, 0, 9000, 3]
+    kc, vc, pt, pl, bt, sl = behind(20000, lens, 64, 2, 64, dtype, g)
+    q = randn((4, 16, 64), dtype, g)
+    out = check_prefix(q, kc, vc, pt, pl, bt, sl)
+    wide = torch.full((pt.numel() + 5000,), -1, dtype=torch.int32, device="cuda")
+    wide[:pt.numel()] = pt
+    assert torch.equal(la.paged_prefix_decode(q, kc, vc, wide, pl, bt, sl), out)
+    own = torch.full((4, 4000), -1, dtype=torch.int32, device="cuda")
+    own[:, :bt.shape[1]] = bt
+    check_prefix(q, kc, vc, pt, pl, own, ints([1, 2, 0, 3]))
+    check_prefix(q, kc, vc, pt, ints([64]), own[:, :3], ints([1, 2, 0, 3]))
+
+
+def test_prefix_is_the_dense_one():
+    g = gen(42)
+    page, n, lens = 16, 320, [5, 0, 70]
+    kc, vc, pt, pl, bt, sl = behind(n, lens, page, 2, 128, BF16, g)
+    q = randn((3, 16, 128), BF16, g)
+    out = check_prefix(q, kc, vc, pt, pl, bt, sl).float()
+    rows = torch.cat([pt[None, :n // page].expand(3, -1), bt], 1).contiguous()
+    dense = la.paged_decode(q, kc, vc, rows, sl + n).float()
+    assert ((out - dense).abs() <= 2 ** -7 * dense.abs() + 1e-3).all()  # as for chosen pages
+
+
+def test_prefix_absent_pages_and_lengths():
+    g = gen(43)
+    page, lens = 16, [40, 3, 0, 17]
+    kc, vc, pt, pl, bt, sl = behind(600, lens, page, 2, 128, BF16, g)
+    q = randn((4, 8, 128), BF16, g)
+    pt[3], pt[20] = -1, 10 ** 9
+    bt[0, 0] = -5
+    check_prefix(q, kc, vc, pt, pl, bt, sl)
+    pt[16:24] = -1  # a whole tile of 128
+    check_prefix(q, kc, vc, pt, pl, bt, sl)
+    pt[:] = -1     # nothing is left of the prefix
+    out = check_prefix(q, kc, vc, pt, pl, bt, sl)
+    assert (out[2] == 0).all()
+    check_prefix(q, kc, vc, pt, ints([-3]), bt, sl)
+    check_prefix(q, kc, vc, pt[:0], ints([100]), bt, sl)
+    good = behind(600, lens, page, 2, 128, BF16, g)
+    pt = good[2][:37]  # the table holds 592 tokens of 2^31 - 1
+    check_prefix(q, good[0], good[1], pt, ints([2 ** 31 - 1]), good[4], good[5])
+
+
+@pytest.mark.parametrize("dtype, batch", [(BF16, 3), (BF16, 40), (FP32, 3)])
+def test_prefix_large_scores(dtype, batch):
+    """Scores in the hundreds that rise or fall along the prefix: the running maximum moves often."""
+    g = gen(44)
+    lens = [(i * 13) % 50 for i in range(batch)]
+    kc, vc, pt, pl, bt, sl = behind(2000, lens, 16, 1, 128, dtype, g, garbage=0.0)
+    ramp = torch.linspace(0.1, 9, 2000, device="cuda")
+    t = torch.arange(2000, device="cuda")
+    at = (pt[t // 16].long(), 0, t % 16)
+    kc[at] = (kc[at].float() * ramp[:, None]).to(dtype)
+    q = randn((batch, 8, 128), dtype, g)
+    check_prefix(q * 3, kc, vc, pt, pl, bt, sl, scale=0.7)
+    kc[at] = kc[at].flip(0)
+    check_prefix(q, kc, vc, pt, pl, bt, sl, scale=-0.5)
+
+
+def test_prefix_infinities_that_are_attended_to():
+    g = gen(45)
+    kc, vc, pt, pl, bt, sl = behind(300, [20] * 3, 16, 1, 128, BF16, g)
+    q = randn((3, 4, 128), BF16, g)
+    q[..., 0] = q[..., 0].abs() + 1
+    # keys of -infinity where every q is positive: weight 0, also for a whole tile and all own tokens
+    for t in list(range(128, 256)) + [290]:
+        kc[pt[t // 16].long(), 0, t % 16, 0] = -INF
+    kc[bt[1, :2].long(), 0, :, 0] = -INF
+    good = la.paged_prefix_decode(q, kc, vc, pt, pl, bt, sl)
+    left = [t for t in range(300) if not (128 <= t < 256 or t == 290)]
+    for r in range(3):
+        own = [] if r == 1 else range(20)
+        k, v = (torch.cat([torch.stack([x[pt[t // 16].long(), 0, t % 16] for t in left]).cpu()] +
+                          [x[bt[r, t // 16].long(), 0, t % 16][None].cpu() for t in own]) for x in (kc, vc))
+        want, _, bound, _ = lref.attend(c(q[r]), k, v, 128 ** -0.5, 128)
+        ref.within(good[r], want, bound, ref.u_of(BF16), "out")
+    # an infinite value makes its column that infinity for all requests, one of another request not
+    vc[pt[2].long(), 0, 5, 9] = -INF
+    vc[bt[0, 0].long(), 0, 3, 11] = INF
+    out = la.paged_prefix_decode(q, kc, vc, pt, pl, bt, sl)
+    assert (out[:, :, 9] == -INF).all() and (out[0, :, 11] == INF).all()
+    keep = torch.ones(3, 4, 128, dtype=torch.bool, device="cuda")
+    keep[:, :, 9] = False
+    keep[0, :, 11] = False
+    assert torch.equal(out[keep], good[keep])
+    # scores that are all -infinity, or one of +infinity or NaN: NaN
+    lse = torch.empty((3, 4), device="cuda")
+    dead = kc.clone()
+    dead[..., 0] = -INF
+    out = la.paged_prefix_decode(q, dead, vc, pt, pl, bt, sl, lse=lse)
+    assert torch.isnan(out).all() and (lse == -INF).all()
+    kc[pt[0].long(), 0, 0, 0] = INF
+    assert torch.isnan(la.paged_prefix_decode(q, kc, vc, pt, pl, bt, sl)).all()
+
+
+def test_prefix_strides_guards_and_refusals():
+    g = gen(46)
+    kc, vc, pt, pl, bt, sl = behind(130, [65, 200, 9], 16, 2, 64, BF16, g)
+    both = torch.stack([kc, vc], dim=1)
+    wide = torch.full((3, bt.shape[1] + 5), -1, dtype=torch.int32, device="cuda")
+    wide[:, :bt.shape[1]] = bt
+    x = randn((3, 12, 64), BF16, g)
+    buf = torch.full((5, 8, 64), 3.0, dtype=BF16, device="cuda")
+    size = la.paged_prefix_decode_workspace_bytes(3, 8, 2, 64)
+    ws = torch.full((size + 256,), 77, dtype=torch.uint8, device="cuda")
+    out = check_prefix(x[:, :8], both[:, 0], both[:, 1], pt, pl, wide[:, :bt.shape[1]], sl, out=buf[1:4],
+                       workspace=ws[:size])
+    assert (buf[0] == 3).all() and (buf[4] == 3).all() and (ws[size:] == 77).all()
+    assert torch.equal(out, la.paged_prefix_decode(x[:, :8].contiguous(), kc, vc, pt, pl, bt, sl))
+    q = x[:, :8]
+    for bad in (dict(pt=pt.long()), dict(pt=pt[None]), dict(pl=ints([1, 2])), dict(pl=130), dict(q=x[:, :7]),
+                dict(ws=ws[:size - 16]), dict(pt=pt.cpu()), dict(sl=sl[:2]), dict(vc=vc[:, :1])):
+        a = {**dict(q=q, kc=kc, vc=vc, pt=pt, pl=pl, sl=sl, ws=None), **bad}
+        with pytest.raises((ValueError, TypeError, la.LightningAttnError)):
+            la.paged_prefix_decode(a["q"], a["kc"], a["vc"], a["pt"], a["pl"], bt, a["sl"], workspace=a["ws"])
+    assert la.paged_prefix_decode(q[:0], kc, vc, pt, pl, bt[:0], sl[:0]).shape == (0, 8, 64)
+
+
+@pytest.mark.parametrize("batch", [2, 40])
+def test_prefix_same_bits_from_a_graph_and_beside_other_calls(batch):
+    """Equal calls give equal bits: eager, replayed for other lengths, and two at once on two streams."""
+    g = gen(47)
+    lens = [(i * 31) % 200 for i in range(batch)]
+    kc, vc, pt, pl, bt, sl = behind(9000, lens, 64, 2, 128, BF16, g)
+    q = randn((batch, 16, 128), BF16, g)
+    want = la.paged_prefix_decode(q, kc, vc, pt, pl, bt, sl)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = la.paged_prefix_decode(q, kc, vc, pt, pl, bt, sl)
+    for n in (9000, 1, 4444, 0):
+        pl.fill_(n)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, check_prefix(q, kc, vc, pt, pl, bt, sl))
+    pl.fill_(9000)
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for i in range(6):
+        outs.append(la.paged_prefix_decode(q, kc, vc, pt, pl, bt, sl, stream=streams[i % 2]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
+def test_prefix_long_sums_do_not_drift():
+    """As for the paged attention: a prefix whose second half has the first one's keys and the negative
+    values, the largest scores first.  The formula's output is 0; what remains are additions to a running sum
+    below 1.5 sum p, each of which errs by at most 2^-24 of it with either sign where it is rounded to
+    nearest.  Additions that drop the excess bits would err to one side, steps 2^-25 in the mean."""
+    g = gen(48)
+    n, page, d, b = 32768, 64, 128, 64
+    k = randn((n // 2, d), FP32, g)
+    q = torch.zeros((b, 16, d), device="cuda")
+    q[:, :, 0] = 1.0
+    k[:, 0] = -k[:, 0].abs()
+    k[:256] = 0.0
+    v = (0.5 + torch.rand((n // 2, d), generator=g, device="cuda")).to(BF16)
+    kc = torch.cat([k, k]).to(BF16).reshape(n // page, 1, page, d)
+    vc = torch.cat([v, -v]).reshape(n // page, 1, page, d)
+    pt = torch.arange(n // page, dtype=torch.int32, device="cuda")
+    bt, lens = torch.zeros((b, 1), dtype=torch.int32, device="cuda"), ints([0] * b)
+    out = la.paged_prefix_decode(q.to(BF16), kc, vc, pt, ints([n]), bt, lens, scale=1.0).double()
+    steps, samples = n // 16, d
+    bound = 10 * math.sqrt(steps) * ref.E * 1.5 / math.sqrt(samples)
+    mean = out.mean((0, 1, 2)).abs().item()
+    print(f"mean {mean:.3e}, bound {bound:.3e}")
+    assert mean <= bound
+
+
 # ---------------------------------------------------------------- together
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_serving_loop(dtype):

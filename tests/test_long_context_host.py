@@ -140,6 +140,33 @@ def test_paged_sparse_decode_refusals(lib, kw, status):
         assert lib.lightning_attn_last_error().decode() != ""
 
 
+def _prefix(lib, **kw):
+    a = dict(q=A, qs=512, pt=A, pw=7, pl=A, scale=0.1, out=A, lse=None, ws=A, wsb=1 << 30, **SHAPE, **CACHE, **TABLE)
+    a.update(kw)
+    return lib.lightning_attn_paged_prefix_decode(
+        a["q"], a["qs"], a["kc"], a["kps"], a["vc"], a["vps"], a["pt"], a["pw"], a["pl"], a["bt"], a["bts"],
+        a["btw"], a["lens"], a["pages"], a["page"], a["T"], a["H"], a["HK"], a["d"], a["dtype"], a["scale"],
+        a["out"], a["lse"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw, status", SHAPES + TABLES + QUERIES + WORK + KEYS + VALUES + OUTPUTS + [
+    (dict(pt=None), BAD), (dict(pt=A + 2), BAD), (dict(pl=None), BAD), (dict(pl=A + 1), BAD), (dict(pw=-1), BAD)])
+def test_paged_prefix_decode_refusals(lib, kw, status):
+    assert _prefix(lib, **kw) == status
+    if status:
+        assert lib.lightning_attn_last_error().decode() != ""
+
+
+def test_prefix_workspace_sizes(lib):
+    size = lib.lightning_attn_paged_prefix_decode_workspace_bytes
+    for dtype in (0, 1):
+        assert size(1, 8, 8, 128, dtype) > la.paged_decode_workspace_bytes(128)
+        assert size(128, 64, 8, 128, dtype) > size(1, 64, 8, 128, dtype) and size(0, 1, 1, 64, dtype) > 0
+    for bad in ((-1, 8, 8, 64, 0), (1, 0, 1, 64, 0), (1, 8, 0, 64, 0), (1, 8, 3, 64, 0), (1, 8, 8, 32, 0),
+                (1, 8, 8, 64, 2), (2 ** 30, 8, 8, 64, 0)):
+        assert size(*bad) == -1
+
+
 def test_select_workspace_sizes(lib):
     size = lib.lightning_attn_paged_select_workspace_bytes
     assert size(1, 1, 100) >= 1200 and size(0, 1, 0) >= 0
@@ -153,6 +180,7 @@ def test_binding_refuses_cpu_tensors():
     i, bt = torch.zeros(2, dtype=torch.int32), torch.zeros(2, 3, dtype=torch.int32)
     sel = torch.zeros(2, 2, 1, dtype=torch.int32)
     for call in (lambda: la.paged_bounds(k, k[:, :, :2], bt, i, i), lambda: la.paged_select(q, k[:, :, :2], bt, i, 16, 1),
-                 lambda: la.paged_sparse_decode(q, k, k, bt, i, sel)):
+                 lambda: la.paged_sparse_decode(q, k, k, bt, i, sel),
+                 lambda: la.paged_prefix_decode(q, k, k, i, i[:1], bt, i)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
