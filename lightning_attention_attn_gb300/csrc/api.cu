@@ -501,13 +501,15 @@ la_status lightning_attn_mixed_step(const void *q, const void *k, const void *v,
 }
 
 la_status lightning_attn_device_status(void *stream) {
-    unsigned int err = 0, err_cw = 0;
+    unsigned int err = 0, err_cw = 0, err_prefix = 0;
     la_status st =
         from_cuda(la::take_device_error(static_cast<cudaStream_t>(stream), &err), "device_status");
     if (st != LA_OK) return st;
     st = from_cuda(la::take_cw_device_error(&err_cw), "device_status");
     if (st != LA_OK) return st;
-    err |= err_cw;
+    st = from_cuda(la::take_prefix_device_error(&err_prefix), "device_status");
+    if (st != LA_OK) return st;
+    err |= err_cw | err_prefix;
     if (err) return fail(LA_ERR_TIMEOUT, "a bounded device-side wait gave up");
     return LA_OK;
 }

@@ -212,6 +212,15 @@ cudaError_t paged_decode(const PagedDecodeArgs &a, bool bf16, bool q_f32);
 
 cudaError_t paged_sparse_decode(const PagedDecodeArgs &a, bool bf16);
 
+// Tokens of a tile of a shared prefix on the tensor cores, whose CTAs take an SM each.
+constexpr int kPrefixTile = 128;
+constexpr int kPrefixCtas = 152;
+// The tensor-core kernel over the prefix (bf16): a.block_table is the prefix's, a.prefix as
+// paged_prefix_pieces has it.
+cudaError_t paged_prefix_tc(const PagedDecodeArgs &a);
+// Reads and clears its device error word (the caller has synchronised the stream).
+cudaError_t take_prefix_device_error(unsigned int *err);
+
 // The split of a shared prefix (all but len, max_tokens and pieces), and the attention behind it:
 // a.prefix is complete.
 PrefixPieces paged_prefix_pieces(int64_t batch, int64_t num_heads, int64_t num_kv_heads, bool bf16);

@@ -16,7 +16,7 @@
 namespace la {
 namespace {
 
-// The streaming core of paged_attention.cuh on up to 16 rows.
+// fp32: the streaming core of paged_attention.cuh on up to 16 rows.  (bf16: paged_prefix_tc.cu.)
 template <typename Core>
 __global__ void __launch_bounds__(Core::kThreads, 2)
 paged_prefix_kernel(const __grid_constant__ PagedDecodeArgs a) {
@@ -58,17 +58,13 @@ template <typename Core> cudaError_t launch_prefix(const PagedDecodeArgs &a) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Rows of a unit: as many as there are, up to 16.
-int rows_of(int64_t all) { return all <= 4 ? 4 : all <= 8 ? 8 : 16; }
-
 template <int D> cudaError_t run(PagedDecodeArgs a, const int32_t *prefix_table, bool bf16) {
     if (a.prefix.max_tokens > 0) {
         PagedDecodeArgs p = a;
         p.block_table = prefix_table;
         cudaError_t e;
         if (bf16)
-            e = a.prefix.unit_rows <= 8 ? launch_prefix<Bf16Core<Kv::kPrefix, D, 1, false>>(p)
-                                        : launch_prefix<Bf16Core<Kv::kPrefix, D, 2, false>>(p);
+            e = paged_prefix_tc(p);
         else
             e = a.prefix.unit_rows == 4   ? launch_prefix<F32Core<Kv::kPrefix, D, 4>>(p)
                 : a.prefix.unit_rows == 8 ? launch_prefix<F32Core<Kv::kPrefix, D, 8>>(p)
@@ -83,13 +79,22 @@ template <int D> cudaError_t run(PagedDecodeArgs a, const int32_t *prefix_table,
 PrefixPieces paged_prefix_pieces(int64_t batch, int64_t num_heads, int64_t num_kv_heads, bool bf16) {
     PrefixPieces f;
     const int64_t rows = batch * (num_heads / num_kv_heads);
-    f.unit_rows = bf16 && rows <= 8 ? 8 : rows_of(rows);
-    f.tile = kTile;
-    f.ctas = kPagedCtas;
+    if (bf16) {
+        // up to 128 rows: two parts of every other tile each
+        const bool shared = rows > 128;
+        f.unit_rows = shared ? 256 : 128;
+        f.parts = shared ? 1 : 2;
+        f.tile = kPrefixTile;
+        f.ctas = kPrefixCtas;
+        f.stride = shared ? 256 : (int)(rows + 7) / 8 * 8;
+    } else {
+        f.unit_rows = rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
+        f.tile = kTile;
+        f.ctas = kPagedCtas;
+        f.stride = f.unit_rows;
+    }
     f.units_per_head = (int)((rows + f.unit_rows - 1) / f.unit_rows);
     f.units = (int)(f.units_per_head * num_kv_heads);
-    f.parts = 1;
-    f.stride = f.unit_rows;
     return f;
 }
 

@@ -408,6 +408,24 @@ def test_prefix_batches(dtype, h, hk, d, batch):
     check_prefix(randn((batch, h, d), dtype, g), *args)
 
 
+@pytest.mark.parametrize("h, hk, batch, prefix", [(8, 8, 1, 5120), (16, 2, 4, 20000), (24, 12, 70, 2900),
+                                                  (160, 160, 2, 100), (200, 200, 130, 300)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefix_parts_of_several_units(h, hk, batch, prefix, d):
+    """CTAs whose range ends one unit and begins another, or holds several units, with odd and even
+    numbers of tiles of each."""
+    g = gen(h + d)
+    args = behind(prefix, [i % 3 for i in range(batch)], 64, hk, d, BF16, g, garbage=0.0)
+    q = randn((batch, h, d), BF16, g)
+    some = list(range(0, batch, 40))  # the reference for a few requests
+    kc, vc, pt, pl, bt, sl = args
+    out = la.paged_prefix_decode(q, *args)
+    parts = lref.Behind((c(kc), c(vc)), c(pt), c(pl), c(bt[some]), c(sl[some]))
+    want, _, bound, _ = lref.over(c(q[some]), parts, d ** -0.5, tile=128)
+    ref.within(out[some], want, bound, ref.u_of(BF16), "out")
+    la.device_status()
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_prefix_long_and_wide(dtype):
     """A prefix of many tiles a CTA, own tokens for the split over all CTAs, a table much wider
