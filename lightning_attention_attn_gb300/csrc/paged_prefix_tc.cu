@@ -25,13 +25,16 @@
 // Warp roles (640 threads):
 //   warps 0-7    rows of A: two threads a row, each with 64 of a tile's tokens and half of
 //                the columns of o; warps 8-15 those of B
-//   warps 16, 17 MMA issuers of A and B: S of the next tile follows P V of this one at once (one
-//                thread's MMAs run in the order of their issue, so S does not overtake the P V that
-//                reads P in its place)
+//   warp 16      MMA issuer: P V of a tile of one group, then that group's next S, then the other
+//                group's (one thread's MMAs run in the order of their issue, so S does not overtake
+//                the P V that reads P in its place).  One issuer keeps the groups half a period apart; with
+//                one each they ran in step, and the tensor core idled while both took exponentials
 //   warps 18, 19 copies of K and V (cp.async: a page's rows are contiguous, but pages are of any
 //                size and lie anywhere), each half of a tile's tokens, into a ring of four tiles
 // Every wait is bounded; one that gives up sets the CTA's abort flag, all roles leave, copies and MMAs
 // are drained, TMEM is freed and the device error word is raised.
+#include <type_traits>
+
 #include "paged_attention.cuh"
 
 namespace la {
@@ -45,7 +48,7 @@ using namespace ptx;
 constexpr int kTokens = kPrefixTile;  // of a tile
 constexpr int kRows = 128;            // of a group
 constexpr int kGroupWarps = 8;
-constexpr int kIssue0 = 16, kCopy0 = 18, kCopyWarps = 2;
+constexpr int kIssue = 16, kCopy0 = 18, kCopyWarps = 2;
 constexpr int kTcThreads = 640;
 constexpr int kRing = 4;              // tiles of shared memory: K and V of two tiles of tokens
 constexpr uint32_t kAtoms = kTokens * 128;  // 128 rows of 64 bf16
@@ -55,12 +58,12 @@ static_assert(kTokens == 128 && kRows == 128, "operand shapes");
 
 struct TcShared {
     uint64_t full[kRing], empty[kRing];
-    uint64_t q_ready[2], s_full[2], p_ready[2], done[2];
+    uint64_t q_ready[2], s_full[2], p_ready[2], x_full[2], done;
     uint32_t have[2][4];        // present tokens of a tile of K, by ring slot
-    uint32_t mask[2][2][4];     // the same for the rows: group, tile & 1
+    alignas(16) uint32_t mask[2][2][4];     // the same for the rows: group, tile & 1
     uint32_t tmem_base;
     int abort;
-    float part[2][2][2][kRows];  // group, tile & 1, half: a row's maximum over the half's tokens
+    alignas(1024) float part[2][2][2][kRows];  // group, tile & 1, half: a row's maximum over the half's tokens
 };
 
 template <int D> struct TcSizes {
@@ -78,6 +81,17 @@ __device__ __forceinline__ uint32_t place(int r, int c) {
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, kTimeoutNs));
 }
+// The same for the warps that hold rows, without a call: their registers would have to be stored for it.
+__device__ __forceinline__ bool row_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+        while (!(ok = mbar_try_wait_sleep(bar, parity, 200000u)) && !*abort)
+            if (globaltimer_ns() - t0 > kTimeoutNs) *abort = 1;
+    }
+    return __all_sync(0xffffffffu, ok);
+}
 // Barrier of the 64 threads of a row quarter; true where all of them say so.
 __device__ __forceinline__ bool pair_and(int id, bool ok) {
     uint32_t r;
@@ -86,6 +100,51 @@ __device__ __forceinline__ bool pair_and(int id, bool ok) {
                  : "=r"(r) : "r"(id), "r"((uint32_t)ok) : "memory");
     return r != 0;
 }
+__device__ __forceinline__ void st_part(uint32_t at, float x) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
+}
+__device__ __forceinline__ float ld_part(uint32_t at) {
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+    return x;
+}
+// Gives registers of the warps that copy and issue to those that hold rows: 512 threads of 104 and 128
+// of 64 are the 640 of 96 that the kernel is launched with.
+template <int N> __device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+static_assert(512 * 104 + 128 * 64 <= kTcThreads * 96, "registers");
+
+// The weights of 16 scores of a row in their place: the sum to l, the high parts (as parts_of has
+// them) of tokens i and i + 8 to element i, the low ones to element i + 8.
+__device__ __forceinline__ void weights_of(float (&v)[16], float scale, float base, float2 &l) {
+    const float2 up = make_float2(1.f + 0x1p-23f, 1.f + 0x1p-23f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 t = f2_fma(make_float2(v[i], v[i + 8]), make_float2(scale, scale), make_float2(base, base));
+        const float2 p = make_float2(ex2(t.x), ex2(t.y));
+        l = f2_add(l, p);
+        const uint32_t x = __float_as_uint(p.x), y = __float_as_uint(p.y);
+        const float2 rest = f2_fma(p, up, make_float2(__uint_as_float((x & 0xffff0000u) ^ 0x80000000u),
+                                                      __uint_as_float((y & 0xffff0000u) ^ 0x80000000u)));
+        v[i] = __uint_as_float(__byte_perm(x, y, 0x7632));
+        v[i + 8] = __uint_as_float(pack2(rest.x, rest.y));
+    }
+}
+// Bits 0, 2, 4, ... of x.
+__device__ __forceinline__ uint16_t every_other(uint32_t x) {
+    x &= 0x55555555u;
+    x = (x | x >> 1) & 0x33333333u;
+    x = (x | x >> 2) & 0x0f0f0f0fu;
+    x = (x | x >> 4) & 0x00ff00ffu;
+    return (uint16_t)(x | x >> 8);
+}
+// The row of V's tile that token r has: in the order of the weights.
+__device__ __forceinline__ int weight_row(int r) { return (r & ~15) | ((r & 7) << 1) | ((r >> 3) & 1); }
+
 // A CTA's parts of units, in order.
 struct Walk {
     long long w, end;
@@ -141,14 +200,15 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < kRing; ++i) {
             mbar_init(bar(cs.full[i]), kCopyWarps);
-            mbar_init(bar(cs.empty[i]), kShared ? 2 : 1);  // the issuers that read the tile
+            mbar_init(bar(cs.empty[i]), 1);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(bar(cs.q_ready[x]), kGroupWarps);
             mbar_init(bar(cs.s_full[x]), 2);  // the MMAs, and the issuer's mask
             mbar_init(bar(cs.p_ready[x]), kGroupWarps);
-            mbar_init(bar(cs.done[x]), 1);
+            mbar_init(bar(cs.x_full[x]), 1);
         }
+        mbar_init(bar(cs.done), 1);
         cs.abort = 0;
         fence_mbar_init();
     }
@@ -169,14 +229,21 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a) {
         // leave TMEM alone; the error word is raised below
     } else if (warp < 2 * kGroupWarps) {
         // ================= rows =================
+        more_registers<104>();
         const int x = warp / kGroupWarps, quarter = warp & 3, half = (warp >> 2) & 1;
         const int r = quarter * 32 + lane;  // row of the group, TMEM lane
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t ts = tmem + lanes + x * 128 + half * 64;
         const uint32_t tx = tmem + lanes + kColX + x * 128 + half * (D / 2);
         const int pair = 1 + x * 4 + quarter;
-        const uint32_t s_bar = bar(cs.s_full[x]);
-        uint32_t steps = 0;  // completions of s_full
+        // A negative scale goes into the signs of Q, so that the largest score is the largest S, and a
+        // scale of 0 into Q as a whole, so that an S of -infinity has weight 0 whatever the scale.
+        const float scale = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
+        const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u, keep = a.scale_log2 == 0.f ? 0u : ~0u;
+        // where the two threads of a row exchange a number: halves and tiles apart by powers of two
+        constexpr uint32_t kOther = kRows * 4, kNext = 2 * kOther;
+        const uint32_t mine = smem_u32(&cs.part[x][0][half][r]);
+        uint32_t tiles = 0;  // of this group so far
         bool ok = true;
         while (ok && walk.next()) {
             const int kvh = walk.unit / f.units_per_head;
@@ -195,7 +262,8 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a) {
                     uint4 v = make_uint4(0, 0, 0, 0);
                     if (row < all_rows) v = __ldcg(qp + ch);
                     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(q_at + place(r, ch)),
-                                 "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+                                 "r"((v.x ^ flip) & keep), "r"((v.y ^ flip) & keep), "r"((v.z ^ flip) & keep),
+                                 "r"((v.w ^ flip) & keep) : "memory");
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -206,86 +274,71 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a) {
             for (int i = 0; i < D / 4; ++i) o[i] = make_float2(0.f, 0.f);
             float m = -kInf;
             float2 l2 = make_float2(0.f, 0.f);
-            // o <- (o + X) f
-            auto add_x = [&](float k) {
-                const bool scale = __any_sync(0xffffffffu, k != 1.f);
-                const float2 k2 = make_float2(k, k);
+            // o <- o + X of the tile before, while the tensor core takes the next S
+            auto add_x = [&]() -> bool {
+                if (!row_wait(bar(cs.x_full[x]), (tiles - 1) & 1, abort_flag)) return false;
+                tc_fence_after();
+                float v[16];
+                tmem_ld16(tx, v);
 #pragma unroll
                 for (int c = 0; c < D / 2; c += 16) {
-                    float v[16];
-                    tmem_ld16(tx + c, v);
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         o[c / 2 + i] = f2_add(o[c / 2 + i], make_float2(v[2 * i], v[2 * i + 1]));
-                    if (scale) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) o[c / 2 + i] = f2_mul(o[c / 2 + i], k2);
-                    }
+                    if (c + 16 < D / 2) tmem_ld16(tx + c + 16, v);
                 }
+                return true;
             };
-            const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
-            for (int j = 0; j < n; ++j) {
-                ok = warp_wait(s_bar, steps & 1, abort_flag);
-                ++steps;
+            for (int j = 0; j < n; ++j, ++tiles) {
+                if (j > 0) ok = add_x();
+                if (ok) ok = row_wait(bar(cs.s_full[x]), tiles & 1, abort_flag);
                 tc_fence_after();
-                const uint32_t *mask = cs.mask[x][j & 1];
-                const uint32_t h0 = mask[2 * half], h1 = mask[2 * half + 1];
-                const bool whole = (mask[0] & mask[1] & mask[2] & mask[3]) == 0xffffffffu;
-                const bool some = (mask[0] | mask[1] | mask[2] | mask[3]) != 0;
-                float top = some ? kLowest : -kInf;
-                if (ok) {
-#pragma unroll
-                    for (int c = 0; c < 64; c += 32) {
-                        float v[32];
-                        tmem_ld32(ts + c, v);
+                const uint4 mask = *reinterpret_cast<const uint4 *>(cs.mask[x][tiles & 1]);
+                if (ok && (mask.x & mask.y & mask.z & mask.w) != 0xffffffffu) {
+                    // tokens that are not there: S is -infinity
+#pragma unroll 1
+                    for (int c = 0; c < 64; c += 16) {
+                        const uint32_t here = (half ? c & 32 ? mask.w : mask.z : c & 32 ? mask.y : mask.x) >> (c & 16);
+                        float v[16];
+                        tmem_ld16(ts + c, v);
                         tmem_wait_ld();
-                        if (!whole) {
-                            const uint32_t h = c ? h1 : h0;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if ((h >> i) & 1) top = fmaxf(top, v[i] * a.scale_log2);
-                        } else {
+                        for (int i = 0; i < 16; ++i) v[i] = (here >> i) & 1 ? v[i] : -kInf;
+                        tmem_st16(ts + c, reinterpret_cast<const uint32_t (&)[16]>(v));
+                    }
+                    tmem_wait_st();
+                }
+                float top = -kInf, v[16];
+                if (ok) {
+                    tmem_ld16(ts, v);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float2 t = f2_mul(make_float2(v[2 * i], v[2 * i + 1]), sc2);
-                                top = fmaxf(top, fmaxf(t.x, t.y));
-                            }
-                        }
+                    for (int c = 0; c < 64; c += 16) {
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) top = fmaxf(fmaxf(top, v[i]), v[i + 1]);
+                        tmem_ld16(ts + (c + 16 < 64 ? c + 16 : 0), v);  // in the end the first again
                     }
                 }
-                cs.part[x][j & 1][half][r] = top;
+                st_part(mine + (j & 1) * kNext, top);
                 ok = pair_and(pair, ok);
                 if (!ok) break;
-                top = fmaxf(top, *const_cast<volatile float *>(&cs.part[x][j & 1][half ^ 1][r]));
-                const float now = fmaxf(m, top);
+                top = fmaxf(top, ld_part((mine ^ kOther) + (j & 1) * kNext)) * scale;
+                const float now = fmaxf(fmaxf(m, top), (mask.x | mask.y | mask.z | mask.w) != 0 ? kLowest : -kInf);
                 const float k = now == m ? 1.f : ex2(m - now);
                 m = now;
-                if (j > 0) add_x(k);  // X of the tile before: S came after it
-                l2 = f2_mul(l2, make_float2(k, k));
+                if (__any_sync(0xffffffffu, k != 1.f)) {
+                    l2 = f2_mul(l2, make_float2(k, k));
+#pragma unroll
+                    for (int i = 0; i < D / 4; ++i) o[i] = f2_mul(o[i], make_float2(k, k));
+                }
                 const float b = m == -kInf ? 0.f : -m;
-                const float2 b2 = make_float2(b, b);
 #pragma unroll
                 for (int c = 0; c < 64; c += 16) {
-                    float v[16];
-                    tmem_ld16(ts + c, v);
                     tmem_wait_ld();
-                    uint32_t w[16];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 t = f2_fma(make_float2(v[2 * i], v[2 * i + 1]), sc2, b2);
-                        float2 p = make_float2(ex2(t.x), ex2(t.y));
-                        if (!whole) {
-                            const uint32_t h = (c & 32 ? h1 : h0) >> ((c & 16) + 2 * i);
-                            p.x = h & 1 ? p.x : 0.f;
-                            p.y = h & 2 ? p.y : 0.f;
-                        }
-                        l2 = f2_add(l2, p);
-                        const Parts q = parts_of(p.x, p.y);
-                        w[i] = q.hi;
-                        w[8 + i] = q.lo;
-                    }
-                    tmem_st16(ts + c, w);
+                    weights_of(v, scale, b, l2);
+                    tmem_st16(ts + c, reinterpret_cast<const uint32_t (&)[16]>(v));
+                    if (c + 16 < 64) tmem_ld16(ts + c + 16, v);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -295,16 +348,13 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a) {
             if (!ok) break;
             float l = l2.x + l2.y;
             if (n > 0) {
-                ok = warp_wait(s_bar, steps & 1, abort_flag);
-                ++steps;
-                tc_fence_after();
-                if (ok) add_x(1.f);
+                ok = add_x();
                 tc_fence_before();
                 // (the buffer of tile n - 2: its last readers have passed tile n - 1's barrier)
-                cs.part[x][n & 1][half][r] = l;
+                st_part(mine + (n & 1) * kNext, l);
                 ok = pair_and(pair, ok);
                 if (!ok) break;
-                l += *const_cast<volatile float *>(&cs.part[x][n & 1][half ^ 1][r]);
+                l += ld_part((mine ^ kOther) + (n & 1) * kNext);
             }
             if (row < all_rows) {
                 float *slot = f.pieces + ((size_t)(blockIdx.x + walk.unit) * f.parts + (kShared ? 0 : x)) *
@@ -318,70 +368,87 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a) {
             }
         }
     } else if (warp < kCopy0) {
-        // ================= MMA issuers =================
-        const int x = warp - kIssue0;
-        const uint64_t dq = sdesc_sw128(sb + x * (kRows * D * 2), 16, 1024);
-        const uint32_t t_s = x * 128, t_x = kColX + x * 128;
-        uint32_t parts = 0, tiles = 0;
-        bool ok = true;
-        while (ok && walk.next()) {
-            const int first = kShared ? 0 : (x - walk.at) & 1, step = kShared ? 1 : 2;
-            if (first < walk.n) {
-                ok = warp_wait(bar(cs.q_ready[x]), parts & 1, abort_flag);
-                ++parts;
-            }
-            int j = 0;
-            for (int i = first; ok && i < walk.n; i += step, ++j, ++tiles) {
-                const int t = walk.at + i, ks = (2 * t) & (kRing - 1), vs = ks + 1;
-                const uint32_t ph = (t >> 1) & 1;
-                ok = warp_wait(bar(cs.full[ks]), ph, abort_flag);
-                if (!ok) break;
+        // ================= MMA issuer =================
+        fewer_registers<64>();
+        if (warp == kIssue) {
+            // Item k is group k & 1's tile number k / 2: tile k / 2 of the CTA where the groups share
+            // them, tile k where they do not.
+            const int items = (int)(walk.end - walk.w) * (kShared ? 2 : 1);
+            int part_end = 0;                          // tiles of the parts entered so far
+            bool fresh[2] = {false, false};            // a group's Q has not been waited for
+            uint32_t parts[2] = {0, 0};
+            auto issue_s = [&](int k) -> bool {
+                const int x = k & 1, t = kShared ? k >> 1 : k, ks = (2 * t) & (kRing - 1);
+                while (t >= part_end) {
+                    walk.next();
+                    part_end = walk.done;
+                    fresh[0] = fresh[1] = true;
+                }
+                if (x ? fresh[1] : fresh[0]) {
+                    if (!warp_wait(bar(cs.q_ready[x]), (x ? parts[1] : parts[0]) & 1, abort_flag)) return false;
+                    if (x) {
+                        fresh[1] = false;
+                        ++parts[1];
+                    } else {
+                        fresh[0] = false;
+                        ++parts[0];
+                    }
+                }
+                if (!warp_wait(bar(cs.full[ks]), (t >> 1) & 1, abort_flag)) return false;
                 tc_fence_after();
-                if (lane < 4) cs.mask[x][j & 1][lane] = cs.have[t & 1][lane];
+                if (lane < 4) cs.mask[x][(k >> 1) & 1][lane] = cs.have[t & 1][lane];
+                const uint64_t dq = sdesc_sw128(sb + x * (kRows * D * 2), 16, 1024);
                 const uint64_t dk = sdesc_sw128(ring(ks), 16, 1024);
+                const uint32_t t_s = x * 128;
                 __syncwarp();
                 if (elect_one()) {
 #pragma unroll
-                    for (uint32_t k = 0; k < KS; ++k)
-                        mma_bf16(t_s, dq + (uint64_t)((k & 3u) * 2 + (k >> 2) * (kAtoms >> 4)),
-                                 dk + (uint64_t)((k & 3u) * 2 + (k >> 2) * (kAtoms >> 4)), kIdescS, k ? 1u : 0u);
+                    for (uint32_t i = 0; i < KS; ++i)
+                        mma_bf16(t_s, dq + (uint64_t)((i & 3u) * 2 + (i >> 2) * (kAtoms >> 4)),
+                                 dk + (uint64_t)((i & 3u) * 2 + (i >> 2) * (kAtoms >> 4)), kIdescS, i ? 1u : 0u);
                     mma_commit(bar(cs.s_full[x]));
-                    mma_commit(bar(cs.empty[ks]));
+                    if (!kShared || x) mma_commit(bar(cs.empty[ks]));
                     mbar_arrive(bar(cs.s_full[x]));
                 }
                 __syncwarp();
-                ok = warp_wait(bar(cs.p_ready[x]), tiles & 1, abort_flag) &&
-                     warp_wait(bar(cs.full[vs]), ph, abort_flag);
-                if (!ok) break;
+                return true;
+            };
+            auto issue_x = [&](int k) -> bool {
+                const int x = k & 1, t = kShared ? k >> 1 : k, vs = ((2 * t) & (kRing - 1)) + 1;
+                if (!warp_wait(bar(cs.full[vs]), (t >> 1) & 1, abort_flag) ||
+                    !warp_wait(bar(cs.p_ready[x]), (k >> 1) & 1, abort_flag))
+                    return false;
                 tc_fence_after();
                 const uint64_t dv = sdesc_sw128(ring(vs), kAtoms, 1024);
+                const uint32_t t_s = x * 128, t_x = kColX + x * 128;
                 if (elect_one()) {
 #pragma unroll
-                    for (uint32_t k = 0; k < 8; ++k) {
-                        mma_bf16_tmem_a(t_x, t_s + 16 * k + 8, dv + (uint64_t)(128u * k), kIdescX, k ? 1u : 0u);
-                        mma_bf16_tmem_a(t_x, t_s + 16 * k, dv + (uint64_t)(128u * k), kIdescX, 1u);
+                    for (uint32_t i = 0; i < 8; ++i) {
+                        mma_bf16_tmem_a(t_x, t_s + 16 * i + 8, dv + (uint64_t)(128u * i), kIdescX, i ? 1u : 0u);
+                        mma_bf16_tmem_a(t_x, t_s + 16 * i, dv + (uint64_t)(128u * i), kIdescX, 1u);
                     }
-                    mma_commit(bar(cs.empty[vs]));
+                    mma_commit(bar(cs.x_full[x]));
+                    if (!kShared || x) mma_commit(bar(cs.empty[vs]));
                 }
                 __syncwarp();
-            }
-            if (ok && j > 0 && elect_one()) {
-                mma_commit(bar(cs.s_full[x]));
-                mbar_arrive(bar(cs.s_full[x]));
-            }
+                return true;
+            };
+            bool ok = issue_s(0) && (items < 2 || issue_s(1));
+            for (int k = 0; ok && k < items; ++k) ok = issue_x(k) && (k + 2 >= items || issue_s(k + 2));
+            // all MMAs have to be finished before TMEM is released
+            if (elect_one()) mma_commit(bar(cs.done));
             __syncwarp();
+            int no_abort = 0;
+            warp_wait(bar(cs.done), 0, &no_abort);
         }
-        // all MMAs have to be finished before TMEM is released
-        if (elect_one()) mma_commit(bar(cs.done[x]));
-        __syncwarp();
-        int no_abort = 0;
-        warp_wait(bar(cs.done[x]), 0, &no_abort);
     } else {
         // ================= copies =================
-        // Rows c * 64 .. + 63 of every tile; lane l finds rows l and l + 32 of them.
+        fewer_registers<64>();
+        // Warp w copies rows 64 w .. + 63 of every tile, two lanes a row (32 bytes, a sector, at a time):
+        // lane l the rows l / 2 + 16 i of those, from one pointer each, without an exchange of addresses.
         const int w = warp - kCopy0;
-        const int first = w * 64;
-        int pending = 0;  // copies (groups) that have not been reported
+        constexpr int kMine = 4;  // rows of a lane
+        int pending = 0;          // copies (groups) that have not been reported
         int reported = 0, issued = 0;
         bool ok = true;
         auto report = [&]() {  // the oldest of them has landed
@@ -401,47 +468,44 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a) {
                 report();
             }
         };
-        auto locate = [&](int tile, int(&page)[2], int(&rw)[2]) {
+        // Pages and offsets inside a page of this lane's rows of a tile (page -1: not there).
+        auto locate = [&](int tile, int(&page)[kMine], uint32_t(&in)[kMine]) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int t = tile * kTokens + first + i * 32 + lane;
+            for (int i = 0; i < kMine; ++i) {
+                const int t = tile * kTokens + w * 64 + i * 16 + (lane >> 1);
                 page[i] = -1;
-                rw[i] = 0;
+                in[i] = 0;
                 if (t < len) {
                     const int blk = t / a.page_size;
-                    rw[i] = t - blk * a.page_size;
+                    in[i] = t - blk * a.page_size;
                     page[i] = a.block_table[blk];
-                    if (page[i] >= a.num_pages) page[i] = -1;
                 }
             }
         };
-        auto copy = [&](const __nv_bfloat16 *cache, int64_t page_stride, int kvh, const int(&page)[2],
-                        const int(&rw)[2]) -> bool {
+        auto copy = [&](auto values, const void *cache, int64_t page_stride, int kvh, const int(&page)[kMine],
+                        const uint32_t(&in)[kMine]) -> bool {
+            constexpr bool V = decltype(values)::value;
             const int slot = issued & (kRing - 1);
             const uint32_t parity = ((issued / kRing) & 1) ^ 1;
             if (!__all_sync(0xffffffffu, mbar_try_wait(bar(cs.empty[slot]), parity))) {
                 drain();  // nothing to do but report what has come
                 if (!warp_wait(bar(cs.empty[slot]), parity, abort_flag)) return false;
             }
-            if ((issued & 1) == 0) {  // K: which of its tokens there are
-                const uint32_t lo = __ballot_sync(0xffffffffu, page[0] >= 0);
-                const uint32_t hi = __ballot_sync(0xffffffffu, page[1] >= 0);
-                if (lane == 0) {
-                    cs.have[(issued >> 1) & 1][2 * w] = lo;
-                    cs.have[(issued >> 1) & 1][2 * w + 1] = hi;
-                }
-            }
-            constexpr int RPI = 32 / CH;  // rows of a warp-wide copy
-            const int ch = lane % CH;
-            const uint32_t dst = ring(slot);
 #pragma unroll
-            for (int i = 0; i < 64 / RPI; ++i) {
-                const int rr = i * RPI + lane / CH;  // of the warp's 64
-                const int pg = __shfl_sync(0xffffffffu, page[i * RPI / 32], rr & 31);
-                const int rowp = __shfl_sync(0xffffffffu, rw[i * RPI / 32], rr & 31);
-                const __nv_bfloat16 *src = cache + (size_t)max(pg, 0) * page_stride +
-                                           ((size_t)kvh * a.page_size + rowp) * D + ch * 8;
-                cp_async16(dst + place(first + rr, ch), src, pg >= 0);
+            for (int i = 0; i < kMine; ++i) {
+                const bool there = page[i] >= 0 && page[i] < a.num_pages;
+                if (!V) {  // which tokens there are: bits of rows 16 i .. + 15, from every other lane
+                    const uint32_t both = __ballot_sync(0xffffffffu, there);
+                    if (lane == 0) reinterpret_cast<uint16_t *>(cs.have[(issued >> 1) & 1])[w * kMine + i] = every_other(both);
+                }
+                const char *src = static_cast<const char *>(cache) + (lane & 1) * 16 +
+                                  ((there ? (size_t)page[i] * page_stride : 0) +
+                                   ((size_t)kvh * a.page_size + in[i]) * D) * 2;
+                const int r = w * 64 + i * 16 + (lane >> 1), to = V ? weight_row(r) : r;
+                const uint32_t dst = ring(slot) + to * 128, turn = (to & 7) << 4, odd = (lane & 1) << 4;
+#pragma unroll
+                for (int c = 0; c < CH; c += 2)  // chunk c + lane & 1
+                    cp_async16(dst + (c >> 3) * kAtoms + ((((c & 7) << 4) | odd) ^ turn), src + c * 16, there);
             }
             cp_commit();
             ++issued;
@@ -451,19 +515,21 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a) {
             }
             return true;
         };
-        int page[2], rw[2];
+        int page[kMine];
+        uint32_t in[kMine];
         while (ok && walk.next()) {
             const int kvh = walk.unit / f.units_per_head;
-            locate(walk.tile, page, rw);
+            locate(walk.tile, page, in);
             for (int i = 0; ok && i < walk.n; ++i) {
-                int page2[2], rw2[2];
-                locate(walk.tile + i + 1, page2, rw2);  // the table is read a tile ahead
-                ok = copy(static_cast<const __nv_bfloat16 *>(a.k), a.k_page_stride, kvh, page, rw) &&
-                     copy(static_cast<const __nv_bfloat16 *>(a.v), a.v_page_stride, kvh, page, rw);
+                int page2[kMine];
+                uint32_t in2[kMine];
+                locate(walk.tile + i + 1, page2, in2);  // the table is read a tile ahead
+                ok = copy(std::false_type(), a.k, a.k_page_stride, kvh, page, in) &&
+                     copy(std::true_type(), a.v, a.v_page_stride, kvh, page, in);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < kMine; ++e) {
                     page[e] = page2[e];
-                    rw[e] = rw2[e];
+                    in[e] = in2[e];
                 }
             }
         }
