@@ -29,10 +29,14 @@
 //                group's (one thread's MMAs run in the order of their issue, so S does not overtake
 //                the P V that reads P in its place).  One issuer keeps the groups half a period apart; with
 //                one each they ran in step, and the tensor core idled while both took exponentials
-//   warps 18, 19 copies of K and V (cp.async: a page's rows are contiguous, but pages are of any
-//                size and lie anywhere), each half of a tile's tokens, into a ring of four tiles
+//   warps 18, 19 copies of K and V into a ring of four tiles: TMA boxes of as many rows as divide
+//                both a page and a tile, where those are at least eight; other page sizes and the rows behind
+//                the prefix's end (which may hold anything, and are read as zeros) row by row with cp.async
 // Every wait is bounded; one that gives up sets the CTA's abort flag, all roles leave, copies and MMAs
 // are drained, TMEM is freed and the device error word is raised.
+#include <cuda.h>
+
+#include <mutex>
 #include <type_traits>
 
 #include "paged_attention.cuh"
@@ -52,6 +56,9 @@ constexpr int kIssue = 16, kCopy0 = 18, kCopyWarps = 2;
 constexpr int kTcThreads = 640;
 constexpr int kRing = 4;              // tiles of shared memory: K and V of two tiles of tokens
 constexpr uint32_t kAtoms = kTokens * 128;  // 128 rows of 64 bf16
+// The maximum that weights are taken against moves when the true one is this far (in log2) above it:
+// weights of up to 2^8 lose nothing in floating point, and o is rescaled seldom.
+constexpr float kSlackLog2 = 8.f;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr uint32_t kColX = 256;
 static_assert(kTokens == 128 && kRows == 128, "operand shapes");
@@ -119,20 +126,23 @@ template <int N> __device__ __forceinline__ void fewer_registers() {
 static_assert(512 * 104 + 128 * 64 <= kTcThreads * 96, "registers");
 
 // The weights of 16 scores of a row in their place: the sum to l, the high parts (as parts_of has
-// them) of tokens i and i + 8 to element i, the low ones to element i + 8.
+// them) of tokens 2 i and 2 i + 1 to element i, the low ones to element i + 8.
 __device__ __forceinline__ void weights_of(float (&v)[16], float scale, float base, float2 &l) {
     const float2 up = make_float2(1.f + 0x1p-23f, 1.f + 0x1p-23f);
+    uint32_t lo[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float2 t = f2_fma(make_float2(v[i], v[i + 8]), make_float2(scale, scale), make_float2(base, base));
+        const float2 t = f2_fma(make_float2(v[2 * i], v[2 * i + 1]), make_float2(scale, scale), make_float2(base, base));
         const float2 p = make_float2(ex2(t.x), ex2(t.y));
         l = f2_add(l, p);
         const uint32_t x = __float_as_uint(p.x), y = __float_as_uint(p.y);
         const float2 rest = f2_fma(p, up, make_float2(__uint_as_float((x & 0xffff0000u) ^ 0x80000000u),
                                                       __uint_as_float((y & 0xffff0000u) ^ 0x80000000u)));
         v[i] = __uint_as_float(__byte_perm(x, y, 0x7632));
-        v[i + 8] = __uint_as_float(pack2(rest.x, rest.y));
+        lo[i] = pack2(rest.x, rest.y);
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[8 + i] = __uint_as_float(lo[i]);
 }
 // Bits 0, 2, 4, ... of x.
 __device__ __forceinline__ uint16_t every_other(uint32_t x) {
@@ -142,9 +152,6 @@ __device__ __forceinline__ uint16_t every_other(uint32_t x) {
     x = (x | x >> 4) & 0x00ff00ffu;
     return (uint16_t)(x | x >> 8);
 }
-// The row of V's tile that token r has: in the order of the weights.
-__device__ __forceinline__ int weight_row(int r) { return (r & ~15) | ((r & 7) << 1) | ((r >> 3) & 1); }
-
 // A CTA's parts of units, in order.
 struct Walk {
     long long w, end;
@@ -169,7 +176,8 @@ struct Walk {
 // barriers tell a use only from the one before it.
 template <int D, bool kShared>
 __global__ void __launch_bounds__(kTcThreads, 1)
-paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a) {
+paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_constant__ CUtensorMap map_k,
+                       const __grid_constant__ CUtensorMap map_v, int box) {
     using Z = TcSizes<D>;
     constexpr int KS = D / 16;          // K steps of S
     constexpr int CH = D / 8;           // 16-byte chunks of a row
@@ -324,7 +332,8 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a) {
                 ok = pair_and(pair, ok);
                 if (!ok) break;
                 top = fmaxf(top, ld_part((mine ^ kOther) + (j & 1) * kNext)) * scale;
-                const float now = fmaxf(fmaxf(m, top), (mask.x | mask.y | mask.z | mask.w) != 0 ? kLowest : -kInf);
+                top = fmaxf(top, (mask.x | mask.y | mask.z | mask.w) != 0 ? kLowest : -kInf);
+                const float now = top > m + kSlackLog2 ? top : m;
                 const float k = now == m ? 1.f : ex2(m - now);
                 m = now;
                 if (__any_sync(0xffffffffu, k != 1.f)) {
@@ -482,15 +491,18 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a) {
                 }
             }
         };
+        // Waits for the slot of the next matrix.
+        auto slot_free = [&]() -> bool {
+            const uint32_t empty = bar(cs.empty[issued & (kRing - 1)]), parity = ((issued / kRing) & 1) ^ 1;
+            if (__all_sync(0xffffffffu, mbar_try_wait(empty, parity))) return true;
+            drain();  // nothing to do but report what has come
+            return warp_wait(empty, parity, abort_flag);
+        };
         auto copy = [&](auto values, const void *cache, int64_t page_stride, int kvh, const int(&page)[kMine],
                         const uint32_t(&in)[kMine]) -> bool {
             constexpr bool V = decltype(values)::value;
-            const int slot = issued & (kRing - 1);
-            const uint32_t parity = ((issued / kRing) & 1) ^ 1;
-            if (!__all_sync(0xffffffffu, mbar_try_wait(bar(cs.empty[slot]), parity))) {
-                drain();  // nothing to do but report what has come
-                if (!warp_wait(bar(cs.empty[slot]), parity, abort_flag)) return false;
-            }
+            if (!slot_free()) return false;
+            const uint32_t at = ring(issued & (kRing - 1));
 #pragma unroll
             for (int i = 0; i < kMine; ++i) {
                 const bool there = page[i] >= 0 && page[i] < a.num_pages;
@@ -501,8 +513,8 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a) {
                 const char *src = static_cast<const char *>(cache) + (lane & 1) * 16 +
                                   ((there ? (size_t)page[i] * page_stride : 0) +
                                    ((size_t)kvh * a.page_size + in[i]) * D) * 2;
-                const int r = w * 64 + i * 16 + (lane >> 1), to = V ? weight_row(r) : r;
-                const uint32_t dst = ring(slot) + to * 128, turn = (to & 7) << 4, odd = (lane & 1) << 4;
+                const int r = w * 64 + i * 16 + (lane >> 1);
+                const uint32_t dst = at + r * 128, turn = (r & 7) << 4, odd = (lane & 1) << 4;
 #pragma unroll
                 for (int c = 0; c < CH; c += 2)  // chunk c + lane & 1
                     cp_async16(dst + (c >> 3) * kAtoms + ((((c & 7) << 4) | odd) ^ turn), src + c * 16, there);
@@ -515,26 +527,74 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a) {
             }
             return true;
         };
-        int page[kMine];
+        // Whole tiles of pages that `box` rows divide: lane l of the first warp has the TMA copy of rows
+        // l / halves * box .. of 64-column half l % halves.  A page that is none is out of the map's
+        // range and read as zeros.
+        constexpr int kHalves = D / 64;
+        auto find_box = [&](int tile, int &page, int &in) {
+            const int t = tile * kTokens + lane / kHalves * box;
+            page = -1;
+            in = 0;
+            if (lane < kTokens / box * kHalves && t < len) {
+                const int blk = t / a.page_size;
+                in = t - blk * a.page_size;
+                page = a.block_table[blk];
+            }
+        };
+        auto tma = [&](auto values, const CUtensorMap &map, int kvh, int page, int in) -> bool {
+            constexpr bool V = decltype(values)::value;
+            drain();
+            if (!slot_free()) return false;
+            const int slot = issued & (kRing - 1);
+            const uint32_t full = bar(cs.full[slot]);
+            if (w == 0) {
+                const bool there = page >= 0 && page < a.num_pages;
+                if (!V) {  // lane l < 16: tokens 8 l .. + 7
+                    const int from = (lane & 15) * 8 / box * kHalves;
+                    const bool eight = __shfl_sync(0xffffffffu, (int)there, from);
+                    if (lane < 16)
+                        reinterpret_cast<uint8_t *>(cs.have[(issued >> 1) & 1])[lane] = eight ? 0xff : 0;
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive_expect_tx(full, Z::kTile);
+                __syncwarp();
+                if (lane < kTokens / box * kHalves)
+                    tma_load_3d(ring(slot) + lane % kHalves * kAtoms + lane / kHalves * box * 128, &map, full,
+                                lane % kHalves * 64, kvh * a.page_size + in, there ? page : -1);
+                __syncwarp();
+            } else if (lane == 0) {
+                mbar_arrive(full);
+            }
+            ++issued;
+            reported = issued;
+            return true;
+        };
+        int page[kMine], page_at = -1, in_at = 0;
         uint32_t in[kMine];
         while (ok && walk.next()) {
             const int kvh = walk.unit / f.units_per_head;
-            locate(walk.tile, page, in);
+            if (box) find_box(walk.tile, page_at, in_at);
             for (int i = 0; ok && i < walk.n; ++i) {
-                int page2[kMine];
-                uint32_t in2[kMine];
-                locate(walk.tile + i + 1, page2, in2);  // the table is read a tile ahead
+                const int tile = walk.tile + i;
+                if (box && (tile + 1) * kTokens <= len) {
+                    const int page_now = page_at, in_now = in_at;
+                    find_box(tile + 1, page_at, in_at);  // the table is read a tile ahead
+                    ok = tma(std::false_type(), map_k, kvh, page_now, in_now) &&
+                         tma(std::true_type(), map_v, kvh, page_now, in_now);
+                    continue;
+                }
+                locate(tile, page, in);
                 ok = copy(std::false_type(), a.k, a.k_page_stride, kvh, page, in) &&
                      copy(std::true_type(), a.v, a.v_page_stride, kvh, page, in);
-#pragma unroll
-                for (int e = 0; e < kMine; ++e) {
-                    page[e] = page2[e];
-                    in[e] = in2[e];
-                }
             }
         }
         if (ok) drain();
         cp_wait<0>();
+        // No TMA copy may be landing when the CTA exits.  (Of a CTA that ran to its end all have been used.)
+        int no_abort = 0;
+        if (!ok && w == 0)
+            for (int i = max(0, issued - kRing); i < issued; ++i)
+                warp_wait(bar(cs.full[i & (kRing - 1)]), (i / kRing) & 1, &no_abort);
     }
 
     tc_fence_before();
@@ -546,12 +606,53 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a) {
     if (threadIdx.x == 0 && (cs.abort || !tmem_ok)) atomicOr(&g_prefix_error, 1u);
 }
 
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encoder() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
+
+// A cache as [pages][Hkv * page_size][D] bf16, box = `box` rows of 64 columns, 128-byte swizzle.
+bool make_map(CUtensorMap *m, const void *cache, int64_t page_stride, const PagedDecodeArgs &a, int box) {
+    const EncodeTiledFn enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.num_kv_heads * a.page_size,
+                                (cuuint64_t)a.num_pages};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.head_dim * 2, (cuuint64_t)page_stride * 2};
+    const cuuint32_t boxes[3] = {64, (cuuint32_t)box, 1}, ones[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(cache), dims, strides, boxes, ones,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, bool kShared> cudaError_t launch_tc(const PagedDecodeArgs &a) {
     constexpr auto kern = paged_prefix_tc_kernel<D, kShared>;
     constexpr int smem = (int)TcSizes<D>::kSmem;
     static_assert(TcSizes<D>::kSmem <= 232448, "shared memory budget");
+    // rows of a box: the largest power of two that divides a page, up to a tile; caches that no map
+    // can describe (a stride or a size past its range) go without
+    int box = a.page_size & -a.page_size;
+    box = box > kTokens ? kTokens : box;
+    CUtensorMap map_k = {}, map_v = {};
+    if (box < 8 || a.num_pages == 0 || (int64_t)a.num_kv_heads * a.page_size > 0x7fffffffLL || !make_map(&map_k, a.k, a.k_page_stride, a, box) ||
+        !make_map(&map_v, a.v, a.v_page_stride, a, box))
+        box = 0;
     cudaError_t e = allow_smem<kern>(smem);
-    if (e == cudaSuccess) e = launch_dependent(kern, a.prefix.ctas, kTcThreads, smem, a.stream, a);
+    if (e == cudaSuccess)
+        e = launch_dependent(kern, a.prefix.ctas, kTcThreads, smem, a.stream, a, map_k, map_v, box);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
