@@ -19,8 +19,11 @@
 // exponentials.  Where a key-value head has no more than 128 rows, both groups have the same
 // rows and every other tile each, and leave a part each.
 //
-// TMEM (512 columns): S of A and B 128 columns each, X of A and B 128 each.  P takes the place of S:
-// 16 tokens' scores are 16 columns, their weights 8 columns of high and 8 of low parts.
+// TMEM (512 columns): S of A and B 128 columns each, X 128, Q of A and B 64 each.  P takes the place of S:
+// 16 tokens' scores are 16 columns, their weights 8 columns of high and 8 of low parts.  Q is there because a
+// 128 x 128 product of two operands in shared memory runs at half the rate (1024 cycles for S instead
+// of 512); the room for it comes from X, which the two groups share: a group takes its X to registers
+// while its own next S runs, before the other group's P V needs the place.
 //
 // Warp roles (640 threads):
 //   warps 0-7    rows of A: two threads a row, each with 64 of a tile's tokens and half of
@@ -54,19 +57,20 @@ constexpr int kRows = 128;            // of a group
 constexpr int kGroupWarps = 8;
 constexpr int kIssue = 16, kCopy0 = 18, kCopyWarps = 2;
 constexpr int kTcThreads = 640;
-constexpr int kRing = 4;              // tiles of shared memory: K and V of two tiles of tokens
+constexpr int kTiles = 3;             // tiles of tokens in shared memory
+constexpr int kRing = 2 * kTiles;     // their K and V
 constexpr uint32_t kAtoms = kTokens * 128;  // 128 rows of 64 bf16
 // The maximum that weights are taken against moves when the true one is this far (in log2) above it:
 // weights of up to 2^8 lose nothing in floating point, and o is rescaled seldom.
 constexpr float kSlackLog2 = 8.f;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr uint32_t kColX = 256;
+constexpr uint32_t kColX = 256, kColQ = 384;
 static_assert(kTokens == 128 && kRows == 128, "operand shapes");
 
 struct TcShared {
     uint64_t full[kRing], empty[kRing];
-    uint64_t q_ready[2], s_full[2], p_ready[2], x_full[2], done;
-    uint32_t have[2][4];        // present tokens of a tile of K, by ring slot
+    uint64_t q_ready[2], s_full[2], p_ready[2], x_full[2], x_taken, done;
+    alignas(16) uint32_t have[kTiles][4];  // present tokens of a tile, by its place in the ring
     alignas(16) uint32_t mask[2][2][4];     // the same for the rows: group, tile & 1
     uint32_t tmem_base;
     int abort;
@@ -75,8 +79,7 @@ struct TcShared {
 
 template <int D> struct TcSizes {
     static constexpr uint32_t kTile = kTokens * D * 2;
-    static constexpr uint32_t kRingAt = 2 * kRows * D * 2;  // behind Q of A and B
-    static constexpr uint32_t kCtrl = kRingAt + kRing * kTile;
+    static constexpr uint32_t kCtrl = kRing * kTile;
     static constexpr uint32_t kSmem = kCtrl + sizeof(TcShared) + 1024;  // + alignment slack
 };
 
@@ -172,8 +175,7 @@ struct Walk {
 };
 
 // kShared: the two groups have rows of their own and share the tiles; otherwise they have the same
-// rows, A the CTA's tiles 0, 2, ... and B 1, 3, ...: each sees every use of its slots of the ring, whose
-// barriers tell a use only from the one before it.
+// rows, A the CTA's tiles 0, 2, ... and B 1, 3, ...
 template <int D, bool kShared>
 __global__ void __launch_bounds__(kTcThreads, 1)
 paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_constant__ CUtensorMap map_k,
@@ -216,6 +218,7 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
             mbar_init(bar(cs.p_ready[x]), kGroupWarps);
             mbar_init(bar(cs.x_full[x]), 1);
         }
+        mbar_init(bar(cs.x_taken), kGroupWarps);
         mbar_init(bar(cs.done), 1);
         cs.abort = 0;
         fence_mbar_init();
@@ -231,7 +234,7 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
     const uint32_t tmem = __shfl_sync(0xffffffffu, cs.tmem_base, 0);
     volatile int *abort_flag = &cs.abort;
     const bool tmem_ok = tmem == 0;  // never expected to fail
-    auto ring = [&](int slot) { return sb + Z::kRingAt + slot * Z::kTile; };
+    auto ring = [&](int slot) { return sb + slot * Z::kTile; };
 
     if (!tmem_ok) {
         // leave TMEM alone; the error word is raised below
@@ -242,7 +245,7 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
         const int r = quarter * 32 + lane;  // row of the group, TMEM lane
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t ts = tmem + lanes + x * 128 + half * 64;
-        const uint32_t tx = tmem + lanes + kColX + x * 128 + half * (D / 2);
+        const uint32_t tx = tmem + lanes + kColX + half * (D / 2);
         const int pair = 1 + x * 4 + quarter;
         // A negative scale goes into the signs of Q, so that the largest score is the largest S, and a
         // scale of 0 into Q as a whole, so that an S of -infinity has weight 0 whatever the scale.
@@ -262,18 +265,24 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
                 const int request = row / a.group;
                 const uint4 *qp = reinterpret_cast<const uint4 *>(
                     static_cast<const __nv_bfloat16 *>(a.q) + (size_t)request * a.q_stride +
-                    (size_t)(kvh * a.group + row - request * a.group) * D);
-                const uint32_t q_at = sb + x * (kRows * D * 2);
+                    (size_t)(kvh * a.group + row - request * a.group) * D) + half * (CH / 2);
+                const uint32_t q_at = tmem + lanes + kColQ + x * 64 + half * (D / 4);
 #pragma unroll
-                for (int c = 0; c < CH / 2; ++c) {
-                    const int ch = half * (CH / 2) + c;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (row < all_rows) v = __ldcg(qp + ch);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(q_at + place(r, ch)),
-                                 "r"((v.x ^ flip) & keep), "r"((v.y ^ flip) & keep), "r"((v.z ^ flip) & keep),
-                                 "r"((v.w ^ flip) & keep) : "memory");
+                for (int c = 0; c < CH / 2; c += 4) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (row < all_rows) v = __ldcg(qp + c + i);
+                        w[4 * i] = (v.x ^ flip) & keep;
+                        w[4 * i + 1] = (v.y ^ flip) & keep;
+                        w[4 * i + 2] = (v.z ^ flip) & keep;
+                        w[4 * i + 3] = (v.w ^ flip) & keep;
+                    }
+                    tmem_st16(q_at + 4 * c, w);
                 }
-                fence_proxy_async_smem();
+                tmem_wait_st();
+                tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(cs.q_ready[x]));
             }
@@ -296,6 +305,9 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
                         o[c / 2 + i] = f2_add(o[c / 2 + i], make_float2(v[2 * i], v[2 * i + 1]));
                     if (c + 16 < D / 2) tmem_ld16(tx + c + 16, v);
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(cs.x_taken));
                 return true;
             };
             for (int j = 0; j < n; ++j, ++tiles) {
@@ -386,64 +398,88 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
             int part_end = 0;                          // tiles of the parts entered so far
             bool fresh[2] = {false, false};            // a group's Q has not been waited for
             uint32_t parts[2] = {0, 0};
-            auto issue_s = [&](int k) -> bool {
-                const int x = k & 1, t = kShared ? k >> 1 : k, ks = (2 * t) & (kRing - 1);
-                while (t >= part_end) {
+            auto tile_of = [&](int k) { return kShared ? k >> 1 : k; };
+            // Whether item k is the first of its group in a part, whose Q is then to be waited for.
+            auto is_fresh = [&](int k) {
+                while (tile_of(k) >= part_end) {
                     walk.next();
                     part_end = walk.done;
                     fresh[0] = fresh[1] = true;
                 }
-                if (x ? fresh[1] : fresh[0]) {
-                    if (!warp_wait(bar(cs.q_ready[x]), (x ? parts[1] : parts[0]) & 1, abort_flag)) return false;
-                    if (x) {
-                        fresh[1] = false;
-                        ++parts[1];
-                    } else {
-                        fresh[0] = false;
-                        ++parts[0];
-                    }
+                return k & 1 ? fresh[1] : fresh[0];
+            };
+            auto wait_q = [&](int k) -> bool {
+                const int x = k & 1;
+                if (!warp_wait(bar(cs.q_ready[x]), (x ? parts[1] : parts[0]) & 1, abort_flag)) return false;
+                if (x) {
+                    fresh[1] = false;
+                    ++parts[1];
+                } else {
+                    fresh[0] = false;
+                    ++parts[0];
                 }
-                if (!warp_wait(bar(cs.full[ks]), (t >> 1) & 1, abort_flag)) return false;
-                tc_fence_after();
-                if (lane < 4) cs.mask[x][(k >> 1) & 1][lane] = cs.have[t & 1][lane];
-                const uint64_t dq = sdesc_sw128(sb + x * (kRows * D * 2), 16, 1024);
-                const uint64_t dk = sdesc_sw128(ring(ks), 16, 1024);
-                const uint32_t t_s = x * 128;
-                __syncwarp();
-                if (elect_one()) {
-#pragma unroll
-                    for (uint32_t i = 0; i < KS; ++i)
-                        mma_bf16(t_s, dq + (uint64_t)((i & 3u) * 2 + (i >> 2) * (kAtoms >> 4)),
-                                 dk + (uint64_t)((i & 3u) * 2 + (i >> 2) * (kAtoms >> 4)), kIdescS, i ? 1u : 0u);
-                    mma_commit(bar(cs.s_full[x]));
-                    if (!kShared || x) mma_commit(bar(cs.empty[ks]));
-                    mbar_arrive(bar(cs.s_full[x]));
-                }
+                return true;
+            };
+            // K of item k is there: its mask to the rows.
+            auto wait_k = [&](int k) -> bool {
+                const int x = k & 1, t = tile_of(k), place = t % kTiles;
+                if (!warp_wait(bar(cs.full[2 * place]), (t / kTiles) & 1, abort_flag)) return false;
+                if (lane < 4) cs.mask[x][(k >> 1) & 1][lane] = cs.have[place][lane];
                 __syncwarp();
                 return true;
             };
-            auto issue_x = [&](int k) -> bool {
-                const int x = k & 1, t = kShared ? k >> 1 : k, vs = ((2 * t) & (kRing - 1)) + 1;
-                if (!warp_wait(bar(cs.full[vs]), (t >> 1) & 1, abort_flag) ||
-                    !warp_wait(bar(cs.p_ready[x]), (k >> 1) & 1, abort_flag))
-                    return false;
-                tc_fence_after();
-                const uint64_t dv = sdesc_sw128(ring(vs), kAtoms, 1024);
-                const uint32_t t_s = x * 128, t_x = kColX + x * 128;
-                if (elect_one()) {
+            // (by one lane, with operands that the whole warp has computed: else each MMA becomes a loop)
+            auto issue_s = [&](uint32_t s, uint32_t q, uint64_t dk, uint32_t full, uint32_t empty, bool last) {
 #pragma unroll
-                    for (uint32_t i = 0; i < 8; ++i) {
-                        mma_bf16_tmem_a(t_x, t_s + 16 * i + 8, dv + (uint64_t)(128u * i), kIdescX, i ? 1u : 0u);
-                        mma_bf16_tmem_a(t_x, t_s + 16 * i, dv + (uint64_t)(128u * i), kIdescX, 1u);
-                    }
-                    mma_commit(bar(cs.x_full[x]));
-                    if (!kShared || x) mma_commit(bar(cs.empty[vs]));
+                for (uint32_t i = 0; i < KS; ++i)
+                    mma_bf16_tmem_a(s, q + 8 * i,
+                                    dk + (uint64_t)((i & 3u) * 2 + (i >> 2) * (kAtoms >> 4)), kIdescS, i ? 1u : 0u);
+                mma_commit(full);
+                if (last) mma_commit(empty);
+                mbar_arrive(full);
+            };
+            auto issue_x = [&](uint32_t s, uint64_t dv, uint32_t full, uint32_t empty, bool last) {
+#pragma unroll
+                for (uint32_t i = 0; i < 8; ++i) {
+                    mma_bf16_tmem_a(kColX, s + 16 * i + 8, dv + (uint64_t)(128u * i), kIdescX, i ? 1u : 0u);
+                    mma_bf16_tmem_a(kColX, s + 16 * i, dv + (uint64_t)(128u * i), kIdescX, 1u);
                 }
+                mma_commit(full);
+                if (last) mma_commit(empty);
+            };
+            auto start = [&](int k) -> bool {  // S of an item, waiting for its Q where that is new
+                if ((is_fresh(k) && !wait_q(k)) || !wait_k(k)) return false;
+                tc_fence_after();
+                const int x = k & 1, slot = tile_of(k) % kTiles * 2;
+                const uint32_t s_at = x * 128, q_at = kColQ + x * 64, full = bar(cs.s_full[x]);
+                const uint64_t dk = sdesc_sw128(ring(slot), 16, 1024);
+                const uint32_t empty = bar(cs.empty[slot]);
+                if (elect_one()) issue_s(s_at, q_at, dk, full, empty, !kShared || x);
                 __syncwarp();
                 return true;
             };
-            bool ok = issue_s(0) && (items < 2 || issue_s(1));
-            for (int k = 0; ok && k < items; ++k) ok = issue_x(k) && (k + 2 >= items || issue_s(k + 2));
+            bool ok = start(0) && (items < 2 || start(1));
+            for (int k = 0; ok && k < items; ++k) {
+                // what is there anyway first, so that P V and the group's next S go out together
+                const bool follows = k + 2 < items && !is_fresh(k + 2);
+                const int x = k & 1, t = tile_of(k), vs = t % kTiles * 2 + 1, ks = tile_of(k + 2) % kTiles * 2;
+                const uint32_t s_at = x * 128, q_at = kColQ + x * 64;
+                const uint64_t dv = sdesc_sw128(ring(vs), kAtoms, 1024), dk = sdesc_sw128(ring(ks), 16, 1024);
+                const uint32_t s_full = bar(cs.s_full[x]), x_full = bar(cs.x_full[x]);
+                const uint32_t v_empty = bar(cs.empty[vs]), k_empty = bar(cs.empty[ks]);
+                ok = (!follows || wait_k(k + 2)) &&
+                     warp_wait(bar(cs.full[vs]), (t / kTiles) & 1, abort_flag) &&
+                     (k == 0 || warp_wait(bar(cs.x_taken), (k - 1) & 1, abort_flag)) &&
+                     warp_wait(bar(cs.p_ready[x]), (k >> 1) & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    issue_x(s_at, dv, x_full, v_empty, !kShared || x);
+                    if (follows) issue_s(s_at, q_at, dk, s_full, k_empty, !kShared || x);
+                }
+                __syncwarp();
+                if (!follows && k + 2 < items) ok = start(k + 2);
+            }
             // all MMAs have to be finished before TMEM is released
             if (elect_one()) mma_commit(bar(cs.done));
             __syncwarp();
@@ -463,7 +499,7 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
         auto report = [&]() {  // the oldest of them has landed
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(cs.full[reported & (kRing - 1)]));
+            if (lane == 0) mbar_arrive(bar(cs.full[reported % kRing]));
             ++reported;
             --pending;
         };
@@ -493,7 +529,7 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
         };
         // Waits for the slot of the next matrix.
         auto slot_free = [&]() -> bool {
-            const uint32_t empty = bar(cs.empty[issued & (kRing - 1)]), parity = ((issued / kRing) & 1) ^ 1;
+            const uint32_t empty = bar(cs.empty[issued % kRing]), parity = ((issued / kRing) & 1) ^ 1;
             if (__all_sync(0xffffffffu, mbar_try_wait(empty, parity))) return true;
             drain();  // nothing to do but report what has come
             return warp_wait(empty, parity, abort_flag);
@@ -502,13 +538,13 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
                         const uint32_t(&in)[kMine]) -> bool {
             constexpr bool V = decltype(values)::value;
             if (!slot_free()) return false;
-            const uint32_t at = ring(issued & (kRing - 1));
+            const uint32_t at = ring(issued % kRing);
 #pragma unroll
             for (int i = 0; i < kMine; ++i) {
                 const bool there = page[i] >= 0 && page[i] < a.num_pages;
                 if (!V) {  // which tokens there are: bits of rows 16 i .. + 15, from every other lane
                     const uint32_t both = __ballot_sync(0xffffffffu, there);
-                    if (lane == 0) reinterpret_cast<uint16_t *>(cs.have[(issued >> 1) & 1])[w * kMine + i] = every_other(both);
+                    if (lane == 0) reinterpret_cast<uint16_t *>(cs.have[issued / 2 % kTiles])[w * kMine + i] = every_other(both);
                 }
                 const char *src = static_cast<const char *>(cache) + (lane & 1) * 16 +
                                   ((there ? (size_t)page[i] * page_stride : 0) +
@@ -545,7 +581,7 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
             constexpr bool V = decltype(values)::value;
             drain();
             if (!slot_free()) return false;
-            const int slot = issued & (kRing - 1);
+            const int slot = issued % kRing;
             const uint32_t full = bar(cs.full[slot]);
             if (w == 0) {
                 const bool there = page >= 0 && page < a.num_pages;
@@ -553,7 +589,7 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
                     const int from = (lane & 15) * 8 / box * kHalves;
                     const bool eight = __shfl_sync(0xffffffffu, (int)there, from);
                     if (lane < 16)
-                        reinterpret_cast<uint8_t *>(cs.have[(issued >> 1) & 1])[lane] = eight ? 0xff : 0;
+                        reinterpret_cast<uint8_t *>(cs.have[issued / 2 % kTiles])[lane] = eight ? 0xff : 0;
                     __syncwarp();
                 }
                 if (lane == 0) mbar_arrive_expect_tx(full, Z::kTile);
@@ -594,7 +630,7 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
         int no_abort = 0;
         if (!ok && w == 0)
             for (int i = max(0, issued - kRing); i < issued; ++i)
-                warp_wait(bar(cs.full[i & (kRing - 1)]), (i / kRing) & 1, &no_abort);
+                warp_wait(bar(cs.full[i % kRing]), (i / kRing) & 1, &no_abort);
     }
 
     tc_fence_before();
