@@ -20,7 +20,8 @@
 // rows and every other tile each, and leave a part each.
 //
 // TMEM (512 columns): S of A and B 128 columns each, X 128, Q of A and B 64 each.  P takes the place of S:
-// 16 tokens' scores are 16 columns, their weights 8 columns of high and 8 of low parts.  Q is there because a
+// 8 tokens' scores are 8 columns, their weights 4 columns of high and 4 of low parts, which together are one
+// K step of 16; its operand V is the 8 tokens' rows twice (a stride of 0 between groups of 8 rows).  Q is there because a
 // 128 x 128 product of two operands in shared memory runs at half the rate (1024 cycles for S instead
 // of 512); the room for it comes from X, which the two groups share: a group takes its X to registers
 // while its own next S runs, before the other group's P V needs the place.
@@ -32,7 +33,7 @@
 //                group's (one thread's MMAs run in the order of their issue, so S does not overtake
 //                the P V that reads P in its place).  One issuer keeps the groups half a period apart; with
 //                one each they ran in step, and the tensor core idled while both took exponentials
-//   warps 18, 19 copies of K and V into a ring of four tiles: TMA boxes of as many rows as divide
+//   warp 17      copies of K (18 and 19 only give up registers) and V into a ring of four tiles: TMA boxes of as many rows as divide
 //                both a page and a tile, where those are at least eight; other page sizes and the rows behind
 //                the prefix's end (which may hold anything, and are read as zeros) row by row with cp.async
 // Every wait is bounded; one that gives up sets the CTA's abort flag, all roles leave, copies and MMAs
@@ -55,26 +56,28 @@ using namespace ptx;
 constexpr int kTokens = kPrefixTile;  // of a tile
 constexpr int kRows = 128;            // of a group
 constexpr int kGroupWarps = 8;
-constexpr int kIssue = 16, kCopy0 = 18, kCopyWarps = 2;
+constexpr int kIssue = 16, kCopy = 17;
 constexpr int kTcThreads = 640;
 constexpr int kTiles = 3;             // tiles of tokens in shared memory
 constexpr int kRing = 2 * kTiles;     // their K and V
 constexpr uint32_t kAtoms = kTokens * 128;  // 128 rows of 64 bf16
-// The maximum that weights are taken against moves when the true one is this far (in log2) above it:
-// weights of up to 2^8 lose nothing in floating point, and o is rescaled seldom.
-constexpr float kSlackLog2 = 8.f;
+// Weights are taken against a base that may lie below the row's maximum: the maximum of the tiles
+// before, so that a tile's weights need not wait for its own.  Weights of up to 2^kRedo lose nothing in
+// floating point; a tile whose maximum is further above is taken again (S once more, then its maximum first).
+// A base that is kMove below is moved after the tile.  (log2)
+constexpr float kRedo = 8.f, kMove = 4.f;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr uint32_t kColX = 256, kColQ = 384;
 static_assert(kTokens == 128 && kRows == 128, "operand shapes");
 
 struct TcShared {
-    uint64_t full[kRing], empty[kRing];
-    uint64_t q_ready[2], s_full[2], p_ready[2], x_full[2], x_taken, done;
+    uint64_t full[kTiles], empty[kTiles];
+    uint64_t q_ready[2], s_full[2], p_ready[2], x_full[2], done;
     alignas(16) uint32_t have[kTiles][4];  // present tokens of a tile, by its place in the ring
-    alignas(16) uint32_t mask[2][2][4];     // the same for the rows: group, tile & 1
     uint32_t tmem_base;
+    int redo[2];                // the group wants S of its tile once more
     int abort;
-    alignas(1024) float part[2][2][2][kRows];  // group, tile & 1, half: a row's maximum over the half's tokens
+    alignas(1024) float part[2][3][2][kRows];  // group, tile & 1, half: a row's maximum over the half's tokens
 };
 
 template <int D> struct TcSizes {
@@ -83,11 +86,6 @@ template <int D> struct TcSizes {
     static constexpr uint32_t kSmem = kCtrl + sizeof(TcShared) + 1024;  // + alignment slack
 };
 
-// Byte offset of 16-byte chunk c of row r in an operand of 128 rows: 64-column halves of
-// 128-byte swizzled rows.
-__device__ __forceinline__ uint32_t place(int r, int c) {
-    return (uint32_t)(c >> 3) * kAtoms + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-}
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, kTimeoutNs));
 }
@@ -102,12 +100,12 @@ __device__ __forceinline__ bool row_wait(uint32_t bar, uint32_t parity, volatile
     }
     return __all_sync(0xffffffffu, ok);
 }
-// Barrier of the 64 threads of a row quarter; true where all of them say so.
-__device__ __forceinline__ bool pair_and(int id, bool ok) {
+// Barrier of a group's 256 threads; true where any of them says so.
+__device__ __forceinline__ bool group_any(int id, bool some) {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
-                 "barrier.cta.red.and.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(r) : "r"(id), "r"((uint32_t)ok) : "memory");
+                 "barrier.cta.red.or.pred q, %1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"(id), "r"((uint32_t)some) : "memory");
     return r != 0;
 }
 __device__ __forceinline__ void st_part(uint32_t at, float x) {
@@ -118,8 +116,8 @@ __device__ __forceinline__ float ld_part(uint32_t at) {
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
     return x;
 }
-// Gives registers of the warps that copy and issue to those that hold rows: 512 threads of 104 and 128
-// of 64 are the 640 of 96 that the kernel is launched with.
+// Gives registers of the other warps to those that hold rows: 512 threads of 104 and 128 of 64 are the 640
+// of 96 that the kernel is launched with.
 template <int N> __device__ __forceinline__ void more_registers() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
@@ -128,13 +126,13 @@ template <int N> __device__ __forceinline__ void fewer_registers() {
 }
 static_assert(512 * 104 + 128 * 64 <= kTcThreads * 96, "registers");
 
-// The weights of 16 scores of a row in their place: the sum to l, the high parts (as parts_of has
-// them) of tokens 2 i and 2 i + 1 to element i, the low ones to element i + 8.
-__device__ __forceinline__ void weights_of(float (&v)[16], float scale, float base, float2 &l) {
+// The weights of 8 scores of a row in their place: the sum to l, the high parts (as parts_of has
+// them) of tokens 2 i and 2 i + 1 to element i, the low ones to element i + 4.
+__device__ __forceinline__ void weights_of(float (&v)[8], float scale, float base, float2 &l) {
     const float2 up = make_float2(1.f + 0x1p-23f, 1.f + 0x1p-23f);
-    uint32_t lo[8];
+    uint32_t lo[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
         const float2 t = f2_fma(make_float2(v[2 * i], v[2 * i + 1]), make_float2(scale, scale), make_float2(base, base));
         const float2 p = make_float2(ex2(t.x), ex2(t.y));
         l = f2_add(l, p);
@@ -145,7 +143,7 @@ __device__ __forceinline__ void weights_of(float (&v)[16], float scale, float ba
         lo[i] = pack2(rest.x, rest.y);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[8 + i] = __uint_as_float(lo[i]);
+    for (int i = 0; i < 4; ++i) v[4 + i] = __uint_as_float(lo[i]);
 }
 // Bits 0, 2, 4, ... of x.
 __device__ __forceinline__ uint16_t every_other(uint32_t x) {
@@ -208,17 +206,16 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
 
     auto bar = [&](const uint64_t &b) { return smem_u32(&b); };
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kRing; ++i) {
-            mbar_init(bar(cs.full[i]), kCopyWarps);
+        for (int i = 0; i < kTiles; ++i) {
+            mbar_init(bar(cs.full[i]), 1);
             mbar_init(bar(cs.empty[i]), 1);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(bar(cs.q_ready[x]), kGroupWarps);
-            mbar_init(bar(cs.s_full[x]), 2);  // the MMAs, and the issuer's mask
-            mbar_init(bar(cs.p_ready[x]), kGroupWarps);
+            mbar_init(bar(cs.s_full[x]), 2);  // the MMAs, and the issuer for the copies' `have`
+            mbar_init(bar(cs.p_ready[x]), 1 + kGroupWarps);  // P, and the place of X from the other group
             mbar_init(bar(cs.x_full[x]), 1);
         }
-        mbar_init(bar(cs.x_taken), kGroupWarps);
         mbar_init(bar(cs.done), 1);
         cs.abort = 0;
         fence_mbar_init();
@@ -236,17 +233,20 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
     const bool tmem_ok = tmem == 0;  // never expected to fail
     auto ring = [&](int slot) { return sb + slot * Z::kTile; };
 
+    if (warp < 2 * kGroupWarps)
+        more_registers<104>();
+    else
+        fewer_registers<64>();
     if (!tmem_ok) {
         // leave TMEM alone; the error word is raised below
     } else if (warp < 2 * kGroupWarps) {
         // ================= rows =================
-        more_registers<104>();
         const int x = warp / kGroupWarps, quarter = warp & 3, half = (warp >> 2) & 1;
         const int r = quarter * 32 + lane;  // row of the group, TMEM lane
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t ts = tmem + lanes + x * 128 + half * 64;
         const uint32_t tx = tmem + lanes + kColX + half * (D / 2);
-        const int pair = 1 + x * 4 + quarter;
+        const int group = 1 + x;
         // A negative scale goes into the signs of Q, so that the largest score is the largest S, and a
         // scale of 0 into Q as a whole, so that an S of -infinity has weight 0 whatever the scale.
         const float scale = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
@@ -254,7 +254,8 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
         // where the two threads of a row exchange a number: halves and tiles apart by powers of two
         constexpr uint32_t kOther = kRows * 4, kNext = 2 * kOther;
         const uint32_t mine = smem_u32(&cs.part[x][0][half][r]);
-        uint32_t tiles = 0;  // of this group so far
+        const bool leads = (threadIdx.x & (32 * kGroupWarps - 1)) == 0;
+        uint32_t tiles = 0, steps = 0;  // of this group so far: tiles, and its S
         bool ok = true;
         while (ok && walk.next()) {
             const int kvh = walk.unit / f.units_per_head;
@@ -291,6 +292,14 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
             for (int i = 0; i < D / 4; ++i) o[i] = make_float2(0.f, 0.f);
             float m = -kInf;
             float2 l2 = make_float2(0.f, 0.f);
+            // Another base.
+            auto rescale = [&](float to) {
+                const float k = to == m ? 1.f : ex2(m - to);
+                m = to;
+                l2 = f2_mul(l2, make_float2(k, k));
+#pragma unroll
+                for (int i = 0; i < D / 4; ++i) o[i] = f2_mul(o[i], make_float2(k, k));
+            };
             // o <- o + X of the tile before, while the tensor core takes the next S
             auto add_x = [&]() -> bool {
                 if (!row_wait(bar(cs.x_full[x]), (tiles - 1) & 1, abort_flag)) return false;
@@ -307,75 +316,100 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(cs.x_taken));
+                if (lane == 0) mbar_arrive(bar(cs.p_ready[x ^ 1]));
                 return true;
             };
+            bool based = false;   // there is a base (the same for all rows)
+            float next = -kInf;   // the base of the next tile
             for (int j = 0; j < n; ++j, ++tiles) {
-                if (j > 0) ok = add_x();
-                if (ok) ok = row_wait(bar(cs.s_full[x]), tiles & 1, abort_flag);
-                tc_fence_after();
-                const uint4 mask = *reinterpret_cast<const uint4 *>(cs.mask[x][tiles & 1]);
-                if (ok && (mask.x & mask.y & mask.z & mask.w) != 0xffffffffu) {
-                    // tokens that are not there: S is -infinity
+                if (j > 0) {
+                    ok = add_x();
+                    if (__any_sync(0xffffffffu, next != m)) rescale(next);
+                }
+                while (true) {
+                    if (ok) ok = row_wait(bar(cs.s_full[x]), steps & 1, abort_flag);
+                    ++steps;
+                    tc_fence_after();
+                    const uint4 mask = *reinterpret_cast<const uint4 *>(cs.have[(kShared ? walk.at + j : 2 * (int)tiles + x) % kTiles]);
+                    if (ok && (mask.x & mask.y & mask.z & mask.w) != 0xffffffffu) {
+                        // tokens that are not there: S is -infinity
 #pragma unroll 1
-                    for (int c = 0; c < 64; c += 16) {
-                        const uint32_t here = (half ? c & 32 ? mask.w : mask.z : c & 32 ? mask.y : mask.x) >> (c & 16);
-                        float v[16];
-                        tmem_ld16(ts + c, v);
-                        tmem_wait_ld();
+                        for (int c = 0; c < 64; c += 16) {
+                            const uint32_t here = (half ? c & 32 ? mask.w : mask.z : c & 32 ? mask.y : mask.x) >> (c & 16);
+                            float v[16];
+                            tmem_ld16(ts + c, v);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = (here >> i) & 1 ? v[i] : -kInf;
-                        tmem_st16(ts + c, reinterpret_cast<const uint32_t (&)[16]>(v));
+                            for (int i = 0; i < 16; ++i) v[i] = (here >> i) & 1 ? v[i] : -kInf;
+                            tmem_st16(ts + c, reinterpret_cast<const uint32_t (&)[16]>(v));
+                        }
+                        tmem_wait_st();
                     }
-                    tmem_wait_st();
-                }
-                float top = -kInf, v[16];
-                if (ok) {
-                    tmem_ld16(ts, v);
+                    float top = -kInf;
+                    if (!based) {  // the row's maximum first
+                        if (ok) {
+#pragma unroll 1
+                            for (int c = 0; c < 64; c += 16) {
+                                float v[16];
+                                tmem_ld16(ts + c, v);
+                                tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 64; c += 16) {
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) top = fmaxf(fmaxf(top, v[i]), v[i + 1]);
-                        tmem_ld16(ts + (c + 16 < 64 ? c + 16 : 0), v);  // in the end the first again
+                                for (int i = 0; i < 16; i += 2) top = fmaxf(fmaxf(top, v[i]), v[i + 1]);
+                            }
+                        }
+                        st_part(mine + 2 * kNext, top);
+                        ok = !group_any(group, !ok);
+                        if (!ok) break;
+                        top = fmaxf(top, ld_part((mine ^ kOther) + 2 * kNext)) * scale;
+                        based = (mask.x | mask.y | mask.z | mask.w) != 0;
+                        rescale(fmaxf(m, fmaxf(top, based ? kLowest : -kInf)));
+                        top = -kInf;
                     }
+                    const float b = m == -kInf ? 0.f : -m;
+                    float2 sum = make_float2(0.f, 0.f);
+                    if (ok) {
+                        float v[2][8];
+                        tmem_ld8(ts, v[0]);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            float (&u)[8] = v[c & 1];
+                            tmem_wait_ld();
+                            if (c < 7) tmem_ld8(ts + 8 * c + 8, v[(c + 1) & 1]);
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2) top = fmaxf(fmaxf(top, u[i]), u[i + 1]);
+                            weights_of(u, scale, b, sum);
+                            tmem_st8(ts + 8 * c, reinterpret_cast<const uint32_t (&)[8]>(u));
+                        }
+                        tmem_wait_st();
+                    }
+                    tc_fence_before();
+                    // (two places in turn: a partner may be reading the one of the tile before)
+                    st_part(mine + (tiles & 1) * kNext, top);
+                    const bool again = group_any(group, !ok || top * scale > m + kRedo);
+                    if (again) ok = !group_any(group, !ok);  // one outcome for all warps
+                    if (!ok) break;
+                    if (leads) {
+                        cs.redo[x] = again;
+                        mbar_arrive(bar(cs.p_ready[x]));
+                    }
+                    if (!again) {
+                        l2 = f2_add(l2, sum);
+                        top = fmaxf(top, ld_part((mine ^ kOther) + (tiles & 1) * kNext)) * scale;
+                        next = top > m + kMove ? top : m;
+                        break;
+                    }
+                    based = false;
                 }
-                st_part(mine + (j & 1) * kNext, top);
-                ok = pair_and(pair, ok);
                 if (!ok) break;
-                top = fmaxf(top, ld_part((mine ^ kOther) + (j & 1) * kNext)) * scale;
-                top = fmaxf(top, (mask.x | mask.y | mask.z | mask.w) != 0 ? kLowest : -kInf);
-                const float now = top > m + kSlackLog2 ? top : m;
-                const float k = now == m ? 1.f : ex2(m - now);
-                m = now;
-                if (__any_sync(0xffffffffu, k != 1.f)) {
-                    l2 = f2_mul(l2, make_float2(k, k));
-#pragma unroll
-                    for (int i = 0; i < D / 4; ++i) o[i] = f2_mul(o[i], make_float2(k, k));
-                }
-                const float b = m == -kInf ? 0.f : -m;
-#pragma unroll
-                for (int c = 0; c < 64; c += 16) {
-                    tmem_wait_ld();
-                    weights_of(v, scale, b, l2);
-                    tmem_st16(ts + c, reinterpret_cast<const uint32_t (&)[16]>(v));
-                    if (c + 16 < 64) tmem_ld16(ts + c + 16, v);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(cs.p_ready[x]));
             }
             if (!ok) break;
             float l = l2.x + l2.y;
             if (n > 0) {
                 ok = add_x();
-                tc_fence_before();
-                // (the buffer of tile n - 2: its last readers have passed tile n - 1's barrier)
-                st_part(mine + (n & 1) * kNext, l);
-                ok = pair_and(pair, ok);
+                st_part(mine + 2 * kNext, l);
+                ok = !group_any(group, !ok);
                 if (!ok) break;
-                l += ld_part((mine ^ kOther) + (n & 1) * kNext);
+                l += ld_part((mine ^ kOther) + 2 * kNext);
             }
             if (row < all_rows) {
                 float *slot = f.pieces + ((size_t)(blockIdx.x + walk.unit) * f.parts + (kShared ? 0 : x)) *
@@ -388,182 +422,149 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
                     *reinterpret_cast<float2 *>(slot + (size_t)f.stride * D + 2 * in_unit) = make_float2(m, l);
             }
         }
-    } else if (warp < kCopy0) {
+    } else if (warp == kIssue) {
         // ================= MMA issuer =================
-        fewer_registers<64>();
-        if (warp == kIssue) {
-            // Item k is group k & 1's tile number k / 2: tile k / 2 of the CTA where the groups share
-            // them, tile k where they do not.
-            const int items = (int)(walk.end - walk.w) * (kShared ? 2 : 1);
-            int part_end = 0;                          // tiles of the parts entered so far
-            bool fresh[2] = {false, false};            // a group's Q has not been waited for
-            uint32_t parts[2] = {0, 0};
-            auto tile_of = [&](int k) { return kShared ? k >> 1 : k; };
-            // Whether item k is the first of its group in a part, whose Q is then to be waited for.
-            auto is_fresh = [&](int k) {
-                while (tile_of(k) >= part_end) {
-                    walk.next();
-                    part_end = walk.done;
-                    fresh[0] = fresh[1] = true;
-                }
-                return k & 1 ? fresh[1] : fresh[0];
-            };
-            auto wait_q = [&](int k) -> bool {
-                const int x = k & 1;
-                if (!warp_wait(bar(cs.q_ready[x]), (x ? parts[1] : parts[0]) & 1, abort_flag)) return false;
-                if (x) {
-                    fresh[1] = false;
-                    ++parts[1];
-                } else {
-                    fresh[0] = false;
-                    ++parts[0];
-                }
-                return true;
-            };
-            // K of item k is there: its mask to the rows.
-            auto wait_k = [&](int k) -> bool {
-                const int x = k & 1, t = tile_of(k), place = t % kTiles;
-                if (!warp_wait(bar(cs.full[2 * place]), (t / kTiles) & 1, abort_flag)) return false;
-                if (lane < 4) cs.mask[x][(k >> 1) & 1][lane] = cs.have[place][lane];
-                __syncwarp();
-                return true;
-            };
-            // (by one lane, with operands that the whole warp has computed: else each MMA becomes a loop)
-            auto issue_s = [&](uint32_t s, uint32_t q, uint64_t dk, uint32_t full, uint32_t empty, bool last) {
-#pragma unroll
-                for (uint32_t i = 0; i < KS; ++i)
-                    mma_bf16_tmem_a(s, q + 8 * i,
-                                    dk + (uint64_t)((i & 3u) * 2 + (i >> 2) * (kAtoms >> 4)), kIdescS, i ? 1u : 0u);
-                mma_commit(full);
-                if (last) mma_commit(empty);
-                mbar_arrive(full);
-            };
-            auto issue_x = [&](uint32_t s, uint64_t dv, uint32_t full, uint32_t empty, bool last) {
-#pragma unroll
-                for (uint32_t i = 0; i < 8; ++i) {
-                    mma_bf16_tmem_a(kColX, s + 16 * i + 8, dv + (uint64_t)(128u * i), kIdescX, i ? 1u : 0u);
-                    mma_bf16_tmem_a(kColX, s + 16 * i, dv + (uint64_t)(128u * i), kIdescX, 1u);
-                }
-                mma_commit(full);
-                if (last) mma_commit(empty);
-            };
-            auto start = [&](int k) -> bool {  // S of an item, waiting for its Q where that is new
-                if ((is_fresh(k) && !wait_q(k)) || !wait_k(k)) return false;
-                tc_fence_after();
-                const int x = k & 1, slot = tile_of(k) % kTiles * 2;
-                const uint32_t s_at = x * 128, q_at = kColQ + x * 64, full = bar(cs.s_full[x]);
-                const uint64_t dk = sdesc_sw128(ring(slot), 16, 1024);
-                const uint32_t empty = bar(cs.empty[slot]);
-                if (elect_one()) issue_s(s_at, q_at, dk, full, empty, !kShared || x);
-                __syncwarp();
-                return true;
-            };
-            bool ok = start(0) && (items < 2 || start(1));
-            for (int k = 0; ok && k < items; ++k) {
-                // what is there anyway first, so that P V and the group's next S go out together
-                const bool follows = k + 2 < items && !is_fresh(k + 2);
-                const int x = k & 1, t = tile_of(k), vs = t % kTiles * 2 + 1, ks = tile_of(k + 2) % kTiles * 2;
-                const uint32_t s_at = x * 128, q_at = kColQ + x * 64;
-                const uint64_t dv = sdesc_sw128(ring(vs), kAtoms, 1024), dk = sdesc_sw128(ring(ks), 16, 1024);
-                const uint32_t s_full = bar(cs.s_full[x]), x_full = bar(cs.x_full[x]);
-                const uint32_t v_empty = bar(cs.empty[vs]), k_empty = bar(cs.empty[ks]);
-                ok = (!follows || wait_k(k + 2)) &&
-                     warp_wait(bar(cs.full[vs]), (t / kTiles) & 1, abort_flag) &&
-                     (k == 0 || warp_wait(bar(cs.x_taken), (k - 1) & 1, abort_flag)) &&
-                     warp_wait(bar(cs.p_ready[x]), (k >> 1) & 1, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    issue_x(s_at, dv, x_full, v_empty, !kShared || x);
-                    if (follows) issue_s(s_at, q_at, dk, s_full, k_empty, !kShared || x);
-                }
-                __syncwarp();
-                if (!follows && k + 2 < items) ok = start(k + 2);
+        // Item k is group k & 1's tile number k / 2: tile k / 2 of the CTA where the groups share
+        // them, tile k where they do not.  What the warp does between two items counts twice a tile, so it
+        // waits for as few things as there can be: a tile (K and V together), and a group's weights
+        // together with the other group's word that X has been taken.
+        const int items = (int)(walk.end - walk.w) * (kShared ? 2 : 1);
+        int part_end = 0;                          // tiles of the parts entered so far
+        int loaded = 0;                            // tiles that have been waited for
+        bool fresh[2] = {false, false};            // a group's Q has not been waited for
+        uint32_t parts[2] = {0, 0}, weights[2] = {0, 0};  // phases of q_ready and p_ready
+        auto tile_of = [&](int k) { return kShared ? k >> 1 : k; };
+        // Whether item k is the first of its group in a part, whose Q is then to be waited for.
+        auto is_fresh = [&](int k) {
+            while (tile_of(k) >= part_end) {
+                walk.next();
+                part_end = walk.done;
+                fresh[0] = fresh[1] = true;
             }
-            // all MMAs have to be finished before TMEM is released
-            if (elect_one()) mma_commit(bar(cs.done));
+            return k & 1 ? fresh[1] : fresh[0];
+        };
+        auto wait_q = [&](int k) -> bool {
+            const int x = k & 1;
+            if (!warp_wait(bar(cs.q_ready[x]), (x ? parts[1] : parts[0]) & 1, abort_flag)) return false;
+            if (x) {
+                fresh[1] = false;
+                ++parts[1];
+            } else {
+                fresh[0] = false;
+                ++parts[0];
+            }
+            return true;
+        };
+        auto wait_tile = [&](int t) -> bool {
+            if (t < loaded) return true;
+            loaded = t + 1;
+            return warp_wait(bar(cs.full[t % kTiles]), (t / kTiles) & 1, abort_flag);
+        };
+        // (by one lane, with operands that the whole warp has computed: else each MMA becomes a loop)
+        auto issue_s = [&](uint32_t s, uint32_t q, uint64_t dk, uint32_t full) {
+#pragma unroll
+            for (uint32_t i = 0; i < KS; ++i)
+                mma_bf16_tmem_a(s, q + 8 * i, dk + (uint64_t)((i & 3u) * 2 + (i >> 2) * (kAtoms >> 4)), kIdescS,
+                                i ? 1u : 0u);
+            mma_commit(full);
+            mbar_arrive(full);
+        };
+        auto issue_x = [&](uint32_t s, uint64_t dv, uint32_t full, uint32_t empty, bool last) {
+#pragma unroll
+            for (uint32_t i = 0; i < 16; ++i)
+                mma_bf16_tmem_a(kColX, s + 8 * i, dv + (uint64_t)(64u * i), kIdescX, i ? 1u : 0u);
+            mma_commit(full);
+            if (last) mma_commit(empty);  // (K could be wanted once more until the weights were there)
+        };
+        auto start = [&](int k) -> bool {  // S of an item, waiting for its Q where that is new
+            if ((is_fresh(k) && !wait_q(k)) || !wait_tile(tile_of(k))) return false;
+            tc_fence_after();
+            const int x = k & 1;
+            const uint32_t s_at = x * 128, q_at = kColQ + x * 64, full = bar(cs.s_full[x]);
+            const uint64_t dk = sdesc_sw128(ring(tile_of(k) % kTiles * 2), 16, 1024);
+            if (elect_one()) issue_s(s_at, q_at, dk, full);
             __syncwarp();
-            int no_abort = 0;
-            warp_wait(bar(cs.done), 0, &no_abort);
+            return true;
+        };
+        if (lane < kGroupWarps) mbar_arrive(bar(cs.p_ready[0]));  // nobody's X is in the first item's way
+        __syncwarp();
+        bool ok = start(0) && (items < 2 || start(1));
+        for (int k = 0; ok && k < items; ++k) {
+            // P V of the item and the group's next S go out together where nothing is to be waited for
+            const bool follows = k + 2 < items && !is_fresh(k + 2);
+            const int x = k & 1, at = tile_of(k) % kTiles, next = tile_of(k + 2) % kTiles;
+            const uint32_t s_at = x * 128, q_at = kColQ + x * 64;
+            const uint64_t dv = sdesc_sw128(ring(2 * at + 1), kAtoms, 0), dk = sdesc_sw128(ring(2 * next), 16, 1024);
+            const uint32_t s_full = bar(cs.s_full[x]), x_full = bar(cs.x_full[x]), p_ready = bar(cs.p_ready[x]);
+            const uint32_t empty = bar(cs.empty[at]);
+            ok = !follows || wait_tile(tile_of(k + 2));
+            while (ok) {
+                ok = warp_wait(p_ready, (x ? weights[1]++ : weights[0]++) & 1, abort_flag);
+                if (!ok || !*const_cast<volatile int *>(&cs.redo[x])) break;
+                const uint64_t dk_now = sdesc_sw128(ring(2 * at), 16, 1024);
+                if (lane < kGroupWarps) mbar_arrive(p_ready);  // X has been taken already
+                tc_fence_after();
+                __syncwarp();
+                if (elect_one()) issue_s(s_at, q_at, dk_now, s_full);
+                __syncwarp();
+            }
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+                issue_x(s_at, dv, x_full, empty, !kShared || x);
+                if (follows) issue_s(s_at, q_at, dk, s_full);
+            }
+            __syncwarp();
+            if (!follows && k + 2 < items) ok = start(k + 2);
         }
-    } else {
+        // all MMAs have to be finished before TMEM is released
+        if (elect_one()) mma_commit(bar(cs.done));
+        __syncwarp();
+        int no_abort = 0;
+        warp_wait(bar(cs.done), 0, &no_abort);
+    } else if (warp == kCopy) {
         // ================= copies =================
-        fewer_registers<64>();
-        // Warp w copies rows 64 w .. + 63 of every tile, two lanes a row (32 bytes, a sector, at a time):
-        // lane l the rows l / 2 + 16 i of those, from one pointer each, without an exchange of addresses.
-        const int w = warp - kCopy0;
-        constexpr int kMine = 4;  // rows of a lane
-        int pending = 0;          // copies (groups) that have not been reported
-        int reported = 0, issued = 0;
-        bool ok = true;
-        auto report = [&]() {  // the oldest of them has landed
+        // Row by row: two lanes a row (32 bytes, a sector, at a time), lane l the rows l / 2 + 16 i, from one
+        // pointer each, without an exchange of addresses.
+        constexpr int kMine = 8;  // rows of a lane
+        int issued = 0;           // tiles
+        bool ok = true, unsaid = false;  // the last tile's copies (cp.async) have not been reported
+        auto report = [&](int tile) {  // whose copies have landed
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(cs.full[reported % kRing]));
-            ++reported;
-            --pending;
-        };
-        auto drain = [&]() {
-            if (pending == 2) {
-                cp_wait<1>();
-                report();
-            }
-            if (pending == 1) {
-                cp_wait<0>();
-                report();
-            }
+            if (lane == 0) mbar_arrive(bar(cs.full[tile % kTiles]));
         };
         // Pages and offsets inside a page of this lane's rows of a tile (page -1: not there).
         auto locate = [&](int tile, int(&page)[kMine], uint32_t(&in)[kMine]) {
 #pragma unroll
             for (int i = 0; i < kMine; ++i) {
-                const int t = tile * kTokens + w * 64 + i * 16 + (lane >> 1);
+                const int t = tile * kTokens + i * 16 + (lane >> 1);
                 page[i] = -1;
                 in[i] = 0;
                 if (t < len) {
                     const int blk = t / a.page_size;
                     in[i] = t - blk * a.page_size;
                     page[i] = a.block_table[blk];
+                    if (page[i] >= a.num_pages) page[i] = -1;
                 }
             }
         };
-        // Waits for the slot of the next matrix.
-        auto slot_free = [&]() -> bool {
-            const uint32_t empty = bar(cs.empty[issued % kRing]), parity = ((issued / kRing) & 1) ^ 1;
-            if (__all_sync(0xffffffffu, mbar_try_wait(empty, parity))) return true;
-            drain();  // nothing to do but report what has come
-            return warp_wait(empty, parity, abort_flag);
-        };
-        auto copy = [&](auto values, const void *cache, int64_t page_stride, int kvh, const int(&page)[kMine],
-                        const uint32_t(&in)[kMine]) -> bool {
-            constexpr bool V = decltype(values)::value;
-            if (!slot_free()) return false;
-            const uint32_t at = ring(issued % kRing);
+        auto copy = [&](uint32_t at, const void *cache, int64_t page_stride, int kvh, const int(&page)[kMine],
+                        const uint32_t(&in)[kMine]) {
 #pragma unroll
             for (int i = 0; i < kMine; ++i) {
-                const bool there = page[i] >= 0 && page[i] < a.num_pages;
-                if (!V) {  // which tokens there are: bits of rows 16 i .. + 15, from every other lane
-                    const uint32_t both = __ballot_sync(0xffffffffu, there);
-                    if (lane == 0) reinterpret_cast<uint16_t *>(cs.have[issued / 2 % kTiles])[w * kMine + i] = every_other(both);
-                }
+                const bool there = page[i] >= 0;
                 const char *src = static_cast<const char *>(cache) + (lane & 1) * 16 +
                                   ((there ? (size_t)page[i] * page_stride : 0) +
                                    ((size_t)kvh * a.page_size + in[i]) * D) * 2;
-                const int r = w * 64 + i * 16 + (lane >> 1);
+                const int r = i * 16 + (lane >> 1);
                 const uint32_t dst = at + r * 128, turn = (r & 7) << 4, odd = (lane & 1) << 4;
 #pragma unroll
                 for (int c = 0; c < CH; c += 2)  // chunk c + lane & 1
                     cp_async16(dst + (c >> 3) * kAtoms + ((((c & 7) << 4) | odd) ^ turn), src + c * 16, there);
             }
-            cp_commit();
-            ++issued;
-            if (++pending > 2) {
-                cp_wait<2>();
-                report();
-            }
-            return true;
         };
-        // Whole tiles of pages that `box` rows divide: lane l of the first warp has the TMA copy of rows
+        // Whole tiles of pages that `box` rows divide: lane l has the TMA copy of rows
         // l / halves * box .. of 64-column half l % halves.  A page that is none is out of the map's
         // range and read as zeros.
         constexpr int kHalves = D / 64;
@@ -577,33 +578,11 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
                 page = a.block_table[blk];
             }
         };
-        auto tma = [&](auto values, const CUtensorMap &map, int kvh, int page, int in) -> bool {
-            constexpr bool V = decltype(values)::value;
-            drain();
-            if (!slot_free()) return false;
-            const int slot = issued % kRing;
-            const uint32_t full = bar(cs.full[slot]);
-            if (w == 0) {
-                const bool there = page >= 0 && page < a.num_pages;
-                if (!V) {  // lane l < 16: tokens 8 l .. + 7
-                    const int from = (lane & 15) * 8 / box * kHalves;
-                    const bool eight = __shfl_sync(0xffffffffu, (int)there, from);
-                    if (lane < 16)
-                        reinterpret_cast<uint8_t *>(cs.have[issued / 2 % kTiles])[lane] = eight ? 0xff : 0;
-                    __syncwarp();
-                }
-                if (lane == 0) mbar_arrive_expect_tx(full, Z::kTile);
-                __syncwarp();
-                if (lane < kTokens / box * kHalves)
-                    tma_load_3d(ring(slot) + lane % kHalves * kAtoms + lane / kHalves * box * 128, &map, full,
-                                lane % kHalves * 64, kvh * a.page_size + in, there ? page : -1);
-                __syncwarp();
-            } else if (lane == 0) {
-                mbar_arrive(full);
-            }
-            ++issued;
-            reported = issued;
-            return true;
+        auto tma = [&](uint32_t at, uint32_t full, const CUtensorMap &map, int kvh, int page, int in) {
+            if (lane < kTokens / box * kHalves)
+                tma_load_3d(at + lane % kHalves * kAtoms + lane / kHalves * box * 128, &map, full,
+                            lane % kHalves * 64, kvh * a.page_size + in, page);
+            __syncwarp();
         };
         int page[kMine], page_at = -1, in_at = 0;
         uint32_t in[kMine];
@@ -612,25 +591,55 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
             if (box) find_box(walk.tile, page_at, in_at);
             for (int i = 0; ok && i < walk.n; ++i) {
                 const int tile = walk.tile + i;
-                if (box && (tile + 1) * kTokens <= len) {
-                    const int page_now = page_at, in_now = in_at;
-                    find_box(tile + 1, page_at, in_at);  // the table is read a tile ahead
-                    ok = tma(std::false_type(), map_k, kvh, page_now, in_now) &&
-                         tma(std::true_type(), map_v, kvh, page_now, in_now);
-                    continue;
+                const bool whole = box && (tile + 1) * kTokens <= len;
+                const int page_now = page_at >= 0 && page_at < a.num_pages ? page_at : -1, in_now = in_at;
+                if (whole) find_box(tile + 1, page_at, in_at);  // the table is read a tile ahead
+                else locate(tile, page, in);
+                const int slot = issued % kTiles;
+                const uint32_t empty = bar(cs.empty[slot]), parity = ((issued / kTiles) & 1) ^ 1;
+                if (unsaid && (whole || !__all_sync(0xffffffffu, mbar_try_wait(empty, parity)))) {
+                    cp_wait<0>();
+                    report(issued - 1);
+                    unsaid = false;
                 }
-                locate(tile, page, in);
-                ok = copy(std::false_type(), a.k, a.k_page_stride, kvh, page, in) &&
-                     copy(std::true_type(), a.v, a.v_page_stride, kvh, page, in);
+                ok = warp_wait(empty, parity, abort_flag);
+                if (!ok) break;
+                const uint32_t k_at = ring(2 * slot), v_at = ring(2 * slot + 1), full = bar(cs.full[slot]);
+                if (whole) {
+                    // lane l < 16: tokens 8 l .. + 7
+                    const int eight = __shfl_sync(0xffffffffu, page_now, (lane & 15) * 8 / box * kHalves);
+                    if (lane < 16) reinterpret_cast<uint8_t *>(cs.have[slot])[lane] = eight >= 0 ? 0xff : 0;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_expect_tx(full, 2 * Z::kTile);
+                    __syncwarp();
+                    tma(k_at, full, map_k, kvh, page_now, in_now);
+                    tma(v_at, full, map_v, kvh, page_now, in_now);
+                    ++issued;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < kMine; ++e) {  // rows 16 e .. + 15, from every other lane
+                        const uint32_t both = __ballot_sync(0xffffffffu, page[e] >= 0);
+                        if (lane == 0) reinterpret_cast<uint16_t *>(cs.have[slot])[e] = every_other(both);
+                    }
+                    copy(k_at, a.k, a.k_page_stride, kvh, page, in);
+                    copy(v_at, a.v, a.v_page_stride, kvh, page, in);
+                    cp_commit();
+                    if (unsaid) {
+                        cp_wait<1>();
+                        report(issued - 1);
+                    }
+                    unsaid = true;
+                    ++issued;
+                }
             }
         }
-        if (ok) drain();
         cp_wait<0>();
+        if (unsaid) report(issued - 1);
         // No TMA copy may be landing when the CTA exits.  (Of a CTA that ran to its end all have been used.)
         int no_abort = 0;
-        if (!ok && w == 0)
-            for (int i = max(0, issued - kRing); i < issued; ++i)
-                warp_wait(bar(cs.full[i % kRing]), (i / kRing) & 1, &no_abort);
+        if (!ok)
+            for (int i = max(0, issued - kTiles); i < issued; ++i)
+                warp_wait(bar(cs.full[i % kTiles]), (i / kTiles) & 1, &no_abort);
     }
 
     tc_fence_before();
