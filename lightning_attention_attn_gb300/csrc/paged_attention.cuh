@@ -280,12 +280,13 @@ struct Partial {
         const int unit = kvh * f.units_per_head + r / f.unit_rows, in = r % f.unit_rows;
         const long long chunk = prefix_chunk(f, tiles), w = (long long)unit * tiles;
         const int c0 = range_of(w, chunk), c1 = range_of(w + tiles - 1, chunk);
-        const int first = (c0 + unit) * f.parts, n = (c1 - c0 + 1) * f.parts;
-        const size_t size = (size_t)f.stride * (a.head_dim + 2);
-        const float *at = f.pieces + first * size;
+        // (the further parts of a CTA with a single tile are empty, and not written)
+        const int parts = chunk == 1 ? 1 : f.parts, n = (c1 - c0 + 1) * parts;
+        const size_t size = (size_t)f.stride * (a.head_dim + 2) * (chunk == 1 ? f.parts : 1);
+        const float *at = f.pieces + (size_t)(c0 + unit) * f.parts * f.stride * (a.head_dim + 2);
         const float *x_at = at + (size_t)in * a.head_dim + d;
         const float *m_at = at + (size_t)f.stride * a.head_dim + 2 * in;
-        constexpr int kFlight = 4;
+        constexpr int kFlight = 8;
         for (int i = 0; i < n; i += kFlight) {
             float4 x[kFlight];
             float2 ms[kFlight];

@@ -153,21 +153,19 @@ __device__ __forceinline__ uint16_t every_other(uint32_t x) {
     x = (x | x >> 4) & 0x00ff00ffu;
     return (uint16_t)(x | x >> 8);
 }
-// A CTA's parts of units, in order.
+// A CTA's parts of units, in order: `left` tiles from tile `tile` of unit `unit` on.
 struct Walk {
-    long long w, end;
-    int tiles;         // of the prefix
+    int tiles;    // of the prefix
+    int left, at; // the CTA's tiles behind this part, before it
     int unit, tile, n;  // this part: tiles tile .. tile + n - 1 of the unit
-    int at, done = 0;   // the CTA's tiles before it, with it
 
     __device__ __forceinline__ bool next() {
-        if (w >= end) return false;
-        at = done;
-        unit = range_of(w, tiles);
-        tile = (int)(w - (long long)unit * tiles);
-        n = (int)min((long long)(tiles - tile), end - w);
-        w += n;
-        done += n;
+        if (left == 0) return false;
+        at += n;
+        tile = n ? 0 : tile;  // (the first part may begin anywhere, the others begin their unit)
+        unit += n ? 1 : 0;
+        n = min(tiles - tile, left);
+        left -= n;
         return true;
     }
 };
@@ -196,12 +194,19 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
     const PrefixPieces &f = a.prefix;
     const int len = min(max(__ldcg(f.len), 0), f.max_tokens);
     Walk walk;
+    bool alone;  // a CTA has a single tile
     walk.tiles = prefix_tiles(f);
     if (walk.tiles == 0) return;
-    const long long chunk = prefix_chunk(f, walk.tiles);
-    walk.w = blockIdx.x * chunk;
-    walk.end = min(walk.w + chunk, (long long)f.units * walk.tiles);
-    if (walk.w >= walk.end) return;
+    {
+        const long long chunk = prefix_chunk(f, walk.tiles), w = blockIdx.x * chunk;
+        const long long end = min(w + chunk, (long long)f.units * walk.tiles);
+        if (w >= end) return;
+        walk.unit = range_of(w, walk.tiles);
+        walk.tile = (int)(w - (long long)walk.unit * walk.tiles);
+        walk.left = (int)(end - w);
+        walk.at = walk.n = 0;
+        alone = chunk == 1;
+    }
     const int all_rows = a.batch * a.group;
 
     auto bar = [&](const uint64_t &b) { return smem_u32(&b); };
@@ -304,19 +309,27 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
             auto add_x = [&]() -> bool {
                 if (!row_wait(bar(cs.x_full[x]), (tiles - 1) & 1, abort_flag)) return false;
                 tc_fence_after();
-                float v[16];
-                tmem_ld16(tx, v);
+                constexpr int kBlocks = D / 32;  // of 16 columns
+                float v[2][16];
+                tmem_ld16(tx, v[0]);
+                tmem_ld16(tx + 16, v[1]);
 #pragma unroll
-                for (int c = 0; c < D / 2; c += 16) {
+                for (int c = 0; c < kBlocks; c += 2) {
                     tmem_wait_ld();
+                    if (c + 2 == kBlocks) {  // X is in registers: its place is the other group's
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(cs.p_ready[x ^ 1]));
+                    }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        o[c / 2 + i] = f2_add(o[c / 2 + i], make_float2(v[2 * i], v[2 * i + 1]));
-                    if (c + 16 < D / 2) tmem_ld16(tx + c + 16, v);
+                    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            o[c * 8 + e * 8 + i] =
+                                f2_add(o[c * 8 + e * 8 + i], make_float2(v[e][2 * i], v[e][2 * i + 1]));
+                        if (c + 2 < kBlocks) tmem_ld16(tx + 16 * (c + 2 + e), v[e]);
+                    }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(cs.p_ready[x ^ 1]));
                 return true;
             };
             bool based = false;   // there is a base (the same for all rows)
@@ -411,7 +424,7 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
                 if (!ok) break;
                 l += ld_part((mine ^ kOther) + 2 * kNext);
             }
-            if (row < all_rows) {
+            if (row < all_rows && (n > 0 || !alone)) {
                 float *slot = f.pieces + ((size_t)(blockIdx.x + walk.unit) * f.parts + (kShared ? 0 : x)) *
                                              f.stride * (D + 2);
                 float *at = slot + (size_t)in_unit * D + half * (D / 2);
@@ -428,7 +441,7 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
         // them, tile k where they do not.  What the warp does between two items counts twice a tile, so it
         // waits for as few things as there can be: a tile (K and V together), and a group's weights
         // together with the other group's word that X has been taken.
-        const int items = (int)(walk.end - walk.w) * (kShared ? 2 : 1);
+        const int items = walk.left * (kShared ? 2 : 1);
         int part_end = 0;                          // tiles of the parts entered so far
         int loaded = 0;                            // tiles that have been waited for
         bool fresh[2] = {false, false};            // a group's Q has not been waited for
@@ -438,7 +451,7 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
         auto is_fresh = [&](int k) {
             while (tile_of(k) >= part_end) {
                 walk.next();
-                part_end = walk.done;
+                part_end = walk.at + walk.n;
                 fresh[0] = fresh[1] = true;
             }
             return k & 1 ? fresh[1] : fresh[0];
