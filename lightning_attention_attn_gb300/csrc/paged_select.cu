@@ -4,8 +4,8 @@
 // For a page with keys k_t, channel by channel
 //     lo_d = min_t k_td,   hi_d = max_t k_td,
 // and for a query q
-//     q . k_t <= s = sum_d max(q_d lo_d, q_d hi_d) = sum_d (q+_d hi_d + q-_d lo_d)
-// with q+ = max(q, 0), q- = min(q, 0).  A block's score is the largest s of the query
+//     q . k_t <= s = sum_d max(q_d lo_d, q_d hi_d) = sum_d (q+_d max(lo_d, hi_d) + q-_d min(lo_d, hi_d))
+// with q+ = max(q, 0), q- = min(q, 0) (the second form holds for any two numbers, in whatever order).  A block's score is the largest s of the query
 // heads that share the key-value head; the `count` blocks with the largest scores are chosen, ties to
 // the lower block.
 //
@@ -14,8 +14,10 @@
 // first taken in fp32 with a bound on their error, e = kSlack sum|q| max|bound| (the largest of the
 // heads and of the unit's pages), and with T the count-th largest of them
 //     s > T + 2 e  is chosen,   s < T - 2 e  is not,
-// whatever the true scores are; those in between (a few) are taken again in 64 bits and ranked.
-// Where e is not finite (an infinity or NaN among bounds or queries) all of them are.
+// whatever the true scores are; those in between (a few) are taken again in 64 bits and ranked, and of their
+// heads only those that fp32 cannot tell from the largest (the fp64 pipe does two lanes a cycle: all
+// heads of them took 120 of 180 us for 128 requests of 1K to 32K tokens, 64 query heads).
+// Where e is not finite (an infinity or NaN among bounds or queries) all blocks and heads are.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -180,15 +182,22 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // bf16: 16 blocks x 8 heads a product, blocks in its rows.  A sum does not depend on the order of
 // its terms, so a lane's 16-byte chunks of a row are operands as they are loaded, with the same
 // elements of the query beside them.  The products are exact; the tensor core's sum of 16 of them and the running
 // one keeps at least 23 bits of the largest, so 2 D / 16 such sums are off by at most
-// 2 D / 16 * 17 * 2^-23 < 2^-14.9 (D = 128) of the sum of |terms|, which sum|q| max|bound| exceeds.
-template <int D> struct Bf16Scores {
+// 2 D / 16 * 17 * 2^-23 of the sum of |terms|, which sum|q| max|bound| exceeds.
+// All chunks of a tile are loaded at once (8 KB a warp where D is 128), the table's entries a tile ahead.
+template <int D, int NT> struct Bf16Scores {
     using T = __nv_bfloat16;
-    static constexpr int HEADS = 16;  // of one pass
-    static constexpr float kSlack = 0x1p-14f;
+    static constexpr int HEADS = 8 * NT;  // of one pass
+    static constexpr float kSlack = 2 * D / 16 * 17 * 0x1p-23f;
 
     static __device__ __forceinline__ void run(const PagedSelectArgs &a, int b, int kvh, int blocks,
                                                int split, int splits, float *scores, float &most) {
@@ -199,9 +208,15 @@ template <int D> struct Bf16Scores {
         uint32_t top = 0;  // largest |bound| of either half
         for (int h0 = 0; h0 < a.group; h0 += HEADS) {
             const int heads = min(HEADS, a.group - h0);
-            uint32_t q[2][CPL][4];
+            int page[2];  // of rows g and g + 8 of the tile
+            auto find = [&](int i0) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
+                for (int r = 0; r < 2; ++r) page[r] = i0 + r * 8 + g < blocks ? pages[i0 + r * 8 + g] : -1;
+            };
+            find(split * kScoreTile);
+            uint32_t q[NT][CPL / 2][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
                 const uint4 *qp = reinterpret_cast<const uint4 *>(
                     static_cast<const T *>(a.q) + (size_t)b * a.q_stride +
                     (size_t)(kvh * a.group + h0 + n * 8 + g) * D);
@@ -209,33 +224,38 @@ template <int D> struct Bf16Scores {
                 for (int c = 0; c < CPL / 2; ++c) {
                     uint4 x = make_uint4(0, 0, 0, 0);
                     if (n * 8 + g < heads) x = __ldcg(qp + t + 4 * c);
-                    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const uint32_t neg = ((u[w] >> 15) & 0x00010001u) * 0xffffu;
-                        q[n][c][w] = u[w] & neg;
-                        q[n][CPL / 2 + c][w] = u[w] & ~neg;
-                    }
+                    q[n][c][0] = x.x, q[n][c][1] = x.y, q[n][c][2] = x.z, q[n][c][3] = x.w;
                 }
             }
             for (int i0 = split * kScoreTile; i0 < blocks; i0 += splits * kScoreTile) {
-                // rows g and g + 8 of the tile
-                int page[2];
                 uint4 x[2][CPL];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const int i = i0 + r * 8 + g;
-                    page[r] = i < blocks ? pages[i] : -1;
-                    if (page[r] >= a.num_pages) page[r] = -1;
-                }
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
+                    // (a page that is none: any row, its score is not used)
+                    const bool there = page[r] >= 0 && page[r] < a.num_pages;
                     const uint4 *p = reinterpret_cast<const uint4 *>(
-                        bounds + (size_t)max(page[r], 0) * a.bounds_page_stride);
+                        bounds + (there ? (size_t)page[r] : 0) * a.bounds_page_stride) + t;
 #pragma unroll
-                    for (int c = 0; c < CPL; ++c) x[r][c] = page[r] >= 0 ? p[t + 4 * c] : make_uint4(0, 0, 0, 0);
+                    for (int c = 0; c < CPL; ++c) {
+                        x[r][c] = make_uint4(0, 0, 0, 0);
+                        if (there) x[r][c] = p[4 * c];
+                    }
                 }
-                float s[2][4] = {};
+                find(i0 + splits * kScoreTile);
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int c = 0; c < CPL / 2; ++c) {
+                        uint32_t *u = reinterpret_cast<uint32_t *>(&x[r][c]);
+                        uint32_t *v = reinterpret_cast<uint32_t *>(&x[r][CPL / 2 + c]);
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const uint32_t low = Chunk<T>::low(u[w], v[w]);
+                            v[w] = Chunk<T>::high(u[w], v[w]);
+                            u[w] = low;
+                        }
+                    }
+                float s[NT][4] = {};
 #pragma unroll
                 for (int c = 0; c < CPL; ++c) {
                     const uint32_t *u = reinterpret_cast<const uint32_t *>(&x[0][c]);
@@ -246,17 +266,23 @@ template <int D> struct Bf16Scores {
                         top = __vmaxu2(top, v[w] & 0x7fff7fffu);
                     }
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
-                        if (n == 0 || heads > 8) {
-                            mma16816(s[n], u[0], v[0], u[1], v[1], q[n][c][0], q[n][c][1]);
-                            mma16816(s[n], u[2], v[2], u[3], v[3], q[n][c][2], q[n][c][3]);
+                    for (int n = 0; n < NT; ++n) {
+                        uint32_t e[4];  // the query's negative elements beside minima, the others beside maxima
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const uint32_t y = q[n][c % (CPL / 2)][w];
+                            const uint32_t neg = ((y >> 15) & 0x00010001u) * 0xffffu;
+                            e[w] = c < CPL / 2 ? y & neg : y & ~neg;
                         }
+                        mma16816(s[n], u[0], v[0], u[1], v[1], e[0], e[1]);
+                        mma16816(s[n], u[2], v[2], u[3], v[3], e[2], e[3]);
+                    }
                 }
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     float m = -kInf;
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
                             if (n * 8 + 2 * t + j < heads) m = fmaxf(m, s[n][2 * r + j]);
@@ -276,7 +302,7 @@ template <int D> struct Bf16Scores {
 };
 
 // fp32: D / 4 lanes a block, four channels of a lane; sums of 8 products and log2(D / 4) levels, each
-// rounded: off by at most 13 * 2^-24 of the sum of |terms|.
+// rounded: off by at most 13 * 2^-24 < 2^-20 of the sum of |terms|.
 template <int D> struct F32Scores {
     using T = float;
     static constexpr int HEADS = 8;
@@ -317,8 +343,9 @@ template <int D> struct F32Scores {
                             bounds + (size_t)max(page, 0) * a.bounds_page_stride);
                         lo[f] = hi[f] = make_float4(0.f, 0.f, 0.f, 0.f);
                         if (page >= 0) {
-                            lo[f] = p[sub];
-                            hi[f] = p[LPB + sub];
+                            const float4 u = p[sub], v = p[LPB + sub];
+                            lo[f] = make_float4(min_nan(u.x, v.x), min_nan(u.y, v.y), min_nan(u.z, v.z), min_nan(u.w, v.w));
+                            hi[f] = make_float4(max_nan(u.x, v.x), max_nan(u.y, v.y), max_nan(u.z, v.z), max_nan(u.w, v.w));
                         }
                     }
 #pragma unroll
@@ -474,25 +501,57 @@ __device__ __forceinline__ K radix_pick(PickSpace &s, int n, int rank, int &equa
     return prefix;
 }
 
-// The score of a block in 64 bits (whole warp): NaN counts as infinity, so that it is not overlooked.
+// The score of a block in 64 bits (whole warp).  err: the fp32 scores' error, which these sums of D
+// products have too (4 of a lane, 5 levels); where it is not finite the formula is taken
+// word by word, and NaN counts as infinity, so that it is not overlooked.
 template <typename T, int D>
-__device__ __forceinline__ double exact_score(const PagedSelectArgs &a, int b, int kvh, int page) {
+__device__ __noinline__ double exact_score(const PagedSelectArgs &a, int b, int kvh, int page, float err) {
+    constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
-    const T *lo = static_cast<const T *>(a.bounds) + (size_t)page * a.bounds_page_stride + (size_t)kvh * 2 * D;
-    const T *q = static_cast<const T *>(a.q) + (size_t)b * a.q_stride + (size_t)kvh * a.group * D;
+    const T *lo = static_cast<const T *>(a.bounds) + (size_t)page * a.bounds_page_stride + (size_t)kvh * 2 * D + lane * E;
+    const T *q = static_cast<const T *>(a.q) + (size_t)b * a.q_stride + (size_t)kvh * a.group * D + lane * E;
+    float l[E], h[E];
+#pragma unroll
+    for (int d = 0; d < E; ++d) {
+        l[d] = fminf((float)lo[d], (float)lo[D + d]);
+        h[d] = fmaxf((float)lo[d], (float)lo[D + d]);
+    }
     double most = -(double)kInf;
-    for (int h = 0; h < a.group; ++h) {
+    auto add = [&](int g, bool plain) {
         double sum = 0.0;
-        for (int d = lane; d < D; d += 32) {
-            const double x = (double)(float)q[h * D + d];
-            const double m = x * (double)(float)lo[d], n = x * (double)(float)lo[D + d];
-            sum += m != m || n != n ? m + n : fmax(m, n);
+#pragma unroll
+        for (int d = 0; d < E; ++d) {
+            const float x = (float)q[g * D + d];
+            if (plain) {  // finite numbers
+                sum = fma((double)x, (double)(x < 0.f ? l[d] : h[d]), sum);
+            } else {
+                const double m = (double)x * (double)(float)lo[d], n = (double)x * (double)(float)lo[D + d];
+                sum += m != m || n != n ? m + n : fmax(m, n);
+            }
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (sum != sum) sum = (double)kInf;
         most = fmax(most, sum);
+    };
+    if (!(err < 1e30f)) {
+        for (int g = 0; g < a.group; ++g) add(g, false);
+        return most;
     }
+    float first = -kInf;  // the largest fp32 sum
+    for (int pass = 0; pass < 2; ++pass)
+        for (int g = 0; g < a.group; ++g) {
+            float s = 0.f;
+#pragma unroll
+            for (int d = 0; d < E; ++d) {
+                const float x = (float)q[g * D + d];
+                s = fmaf(x, x < 0.f ? l[d] : h[d], s);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (pass == 0) first = fmaxf(first, s);
+            else if (s >= first - 2.02f * err) add(g, true);
+        }
     return most;
 }
 
@@ -573,9 +632,9 @@ paged_pick_kernel(const __grid_constant__ PagedSelectArgs a, const __grid_consta
                         return true;
                     });
                     const float t = value_of(k);
-                    // rounding the two sums is covered by doubling the error once more
-                    above = t + 4.f * err;
-                    below = t - 4.f * err;
+                    // (2 e, and room for the rounding of these two sums: e is at least 2^-20 of |t|)
+                    above = t + 2.25f * err;
+                    below = t - 2.25f * err;
                 }
                 int sure = 0, maybe = 0;
                 for (int i = tid; i < blocks; i += kPick)
@@ -601,7 +660,7 @@ paged_pick_kernel(const __grid_constant__ PagedSelectArgs a, const __grid_consta
                             if (in_band(i)) s.list[atomicAdd(&s.found, 1)] = i;
                         __syncthreads();
                         for (int c = warp; c < maybe; c += kPickWarps) {
-                            const double x = exact_score<T, D>(a, b, kvh, pages[s.list[c]]);
+                            const double x = exact_score<T, D>(a, b, kvh, pages[s.list[c]], err);
                             if (lane == 0) exact[s.list[c]] = x;
                         }
                         __syncthreads();
@@ -622,7 +681,7 @@ paged_pick_kernel(const __grid_constant__ PagedSelectArgs a, const __grid_consta
                     } else {
                         for (int i = warp; i < blocks; i += kPickWarps)
                             if (in_band(i)) {
-                                const double x = exact_score<T, D>(a, b, kvh, pages[i]);
+                                const double x = exact_score<T, D>(a, b, kvh, pages[i], err);
                                 if (lane == 0) exact[i] = x;
                             }
                         __syncthreads();
@@ -733,8 +792,14 @@ int64_t paged_select_workspace(int64_t batch, int64_t num_kv_heads, int64_t tabl
 }
 
 cudaError_t paged_select(const PagedSelectArgs &a, bool bf16) {
-    if (a.head_dim == 128) return bf16 ? launch_select<Bf16Scores<128>, 128>(a) : launch_select<F32Scores<128>, 128>(a);
-    if (a.head_dim == 64) return bf16 ? launch_select<Bf16Scores<64>, 64>(a) : launch_select<F32Scores<64>, 64>(a);
+    if (a.head_dim == 128)
+        return !bf16          ? launch_select<F32Scores<128>, 128>(a)
+               : a.group <= 8 ? launch_select<Bf16Scores<128, 1>, 128>(a)
+                              : launch_select<Bf16Scores<128, 2>, 128>(a);
+    if (a.head_dim == 64)
+        return !bf16          ? launch_select<F32Scores<64>, 64>(a)
+               : a.group <= 8 ? launch_select<Bf16Scores<64, 1>, 64>(a)
+                              : launch_select<Bf16Scores<64, 2>, 64>(a);
     return cudaErrorNotSupported;
 }
 
