@@ -418,9 +418,12 @@ paged_score_kernel(const __grid_constant__ PagedSelectArgs a, const __grid_const
 }
 
 // ------------------------------------------------------------------ choice
-// One CTA a unit.
+// One CTA a unit.  The blocks' keys (the scores' order as unsigned integers) stay in shared memory, up to
+// kKeys of them; further ones are made again from the scores where they are wanted.
 constexpr int kPick = 256, kPickWarps = kPick / 32;
-constexpr int kRanked = 64;  // candidates that are ranked by comparing all with all
+constexpr int kRanked = 64;   // candidates that are ranked by comparing all with all
+constexpr int kKeys = 8192;
+constexpr uint32_t kAbsent = 0u, kKept = ~0u;  // of no finite score
 
 // Order of the values as unsigned integers; -0 and 0 are one value.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -437,48 +440,52 @@ __device__ __forceinline__ uint64_t key_of(double x) {
 
 struct PickSpace {
     int hist[256];
-    int warps[kPickWarps];
+    int2 warps[2][kPickWarps];
     int pair[2];
-    float real;
-    float most;
+    float norm, most;
     int found;
     int last;          // last block of the ranking's least value that is chosen
     uint64_t least;    // that value
     int list[kRanked];
 };
 
-// Sum over the CTA of x, to every thread.
-__device__ __forceinline__ int block_sum(PickSpace &s, int x) {
+// Sums over the CTA of x and y, to every thread.  (Two places in turn: one barrier.)
+__device__ __forceinline__ int2 block_sum(PickSpace &s, int turn, int x, int y) {
     x = __reduce_add_sync(0xffffffffu, x);
+    y = __reduce_add_sync(0xffffffffu, y);
+    if ((threadIdx.x & 31) == 0) s.warps[turn][threadIdx.x >> 5] = make_int2(x, y);
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) s.warps[threadIdx.x >> 5] = x;
-    __syncthreads();
-    int t = 0;
+    int2 t = make_int2(0, 0);
 #pragma unroll
-    for (int w = 0; w < kPickWarps; ++w) t += s.warps[w];
+    for (int w = 0; w < kPickWarps; ++w) {
+        t.x += s.warps[turn][w].x;
+        t.y += s.warps[turn][w].y;
+    }
     return t;
 }
 
 // The rank-th largest (from 1) of the keys that key(i, k) gives for i < n, and how many of those
-// that equal it are among the rank largest.
+// that equal it are among the rank largest.  Eight bits a pass.
 template <typename K, typename F>
 __device__ __forceinline__ K radix_pick(PickSpace &s, int n, int rank, int &equal, F key) {
+    constexpr int kTop = sizeof(K) * 8 - 8;
     K prefix = 0;
-    for (int shift = sizeof(K) * 8 - 8; shift >= 0; shift -= 8) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < 256; i += kPick) s.hist[i] = 0;
-        __syncthreads();
+    __syncthreads();
+    s.hist[threadIdx.x] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int shift = kTop; shift >= 0; shift -= 8) {
         for (int i = threadIdx.x; i < n; i += kPick) {
             K k;
-            if (key(i, k) && (shift == (int)sizeof(K) * 8 - 8 || (k >> (shift + 8)) == (prefix >> (shift + 8))))
+            if (key(i, k) && (shift == kTop || (k >> (shift + 8)) == (prefix >> (shift + 8))))
                 atomicAdd(&s.hist[(int)(k >> shift) & 255], 1);
         }
         __syncthreads();
         if (threadIdx.x < 32) {  // lane l: bins 255 - 8 l .. 248 - 8 l, from the top
             const int top = 255 - 8 * threadIdx.x;
-            int mine = 0;
+            int bins[8], mine = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) mine += s.hist[top - i];
+            for (int i = 0; i < 8; ++i) mine += bins[i] = s.hist[top - i];
             int upto = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -487,11 +494,23 @@ __device__ __forceinline__ K radix_pick(PickSpace &s, int n, int rank, int &equa
             }
             const int above = upto - mine;
             if (above < rank && upto >= rank) {
-                int left = rank - above, i = 0;
-                while (i < 7 && s.hist[top - i] < left) left -= s.hist[top - i++];
-                s.pair[0] = top - i;
+                int left = rank - above, bin = top;
+                bool found = false;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (!found) {
+                        if (bins[i] >= left) {
+                            found = true;
+                            bin = top - i;
+                        } else {
+                            left -= bins[i];
+                        }
+                    }
+                s.pair[0] = bin;
                 s.pair[1] = left;
             }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s.hist[top - i] = 0;
         }
         __syncthreads();
         prefix |= (K)s.pair[0] << shift;
@@ -505,7 +524,7 @@ __device__ __forceinline__ K radix_pick(PickSpace &s, int n, int rank, int &equa
 // products have too (4 of a lane, 5 levels); where it is not finite the formula is taken
 // word by word, and NaN counts as infinity, so that it is not overlooked.
 template <typename T, int D>
-__device__ __noinline__ double exact_score(const PagedSelectArgs &a, int b, int kvh, int page, float err) {
+__device__ __forceinline__ double exact_score(const PagedSelectArgs &a, int b, int kvh, int page, float err) {
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
     const T *lo = static_cast<const T *>(a.bounds) + (size_t)page * a.bounds_page_stride + (size_t)kvh * 2 * D + lane * E;
@@ -538,177 +557,210 @@ __device__ __noinline__ double exact_score(const PagedSelectArgs &a, int b, int 
         for (int g = 0; g < a.group; ++g) add(g, false);
         return most;
     }
-    float first = -kInf;  // the largest fp32 sum
-    for (int pass = 0; pass < 2; ++pass)
-        for (int g = 0; g < a.group; ++g) {
-            float s = 0.f;
+    // fp32 sums of 8 heads at a time: lane i gets that of head i % 8
+    auto eight = [&](int g0) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] = 0.f;
+            const int g = min(g0 + i, a.group - 1);  // (the last one again)
 #pragma unroll
             for (int d = 0; d < E; ++d) {
                 const float x = (float)q[g * D + d];
-                s = fmaf(x, x < 0.f ? l[d] : h[d], s);
+                v[i] = fmaf(x, x < 0.f ? l[d] : h[d], v[i]);
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (pass == 0) first = fmaxf(first, s);
-            else if (s >= first - 2.02f * err) add(g, true);
         }
+        int n = 8;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) {
+            n >>= 1;
+            const bool high = lane & o;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k < n) {
+                    const float keep = high ? v[k + n] : v[k], give = high ? v[k] : v[k + n];
+                    v[k] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+        }
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 8);
+        return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+    };
+    float sums = eight(0), first = sums;
+    for (int g0 = 8; g0 < a.group; g0 += 8) first = fmaxf(first, eight(g0));
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) first = fmaxf(first, __shfl_xor_sync(0xffffffffu, first, o));
+    for (int g0 = 0; g0 < a.group; g0 += 8) {
+        if (g0 > 0) sums = eight(g0);
+        uint32_t near = __ballot_sync(0xffffffffu, lane < 8 && g0 + lane < a.group && sums >= first - 2.02f * err);
+        for (; near; near &= near - 1) add(g0 + __ffs(near) - 1, true);
+    }
     return most;
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kPick)
+__global__ void __launch_bounds__(kPick, 4)
 paged_pick_kernel(const __grid_constant__ PagedSelectArgs a, const __grid_constant__ SelectSpace w,
-                  float slack) {
+                  float slack, int cap) {
     __shared__ PickSpace s;
-    ptx::grid_dependency_wait();
-    ptx::grid_launch_dependents();
+    extern __shared__ uint32_t keys[];  // [cap]
     const int unit = blockIdx.x, b = unit / a.num_kv_heads, kvh = unit - b * a.num_kv_heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) s.norm = s.most = 0.f;
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
     const int blocks = unit_blocks(a, b);
     const int32_t *pages = a.block_table + (size_t)b * a.table_stride;
     int32_t *out = a.selected + (size_t)unit * a.count;
-    auto there = [&](int i) {
-        const int p = pages[i];
-        return p >= 0 && p < a.num_pages;
-    };
-    // (as differences: the sums could pass 32 bits)
-    auto kept = [&](int i) { return i < a.keep_first || blocks - 1 - i < a.keep_last; };
-
-    // 0: not chosen, 1: chosen, 2: decided by rank
-    float above = kInf, below = -kInf;  // approximate scores beyond which a block is chosen, or not
-    bool every = true;                  // all blocks that are there are chosen
-    bool ranked = false;
     const char *base = static_cast<const char *>(a.workspace);
     const float *approx = reinterpret_cast<const float *>(base + w.approx) + (size_t)unit * a.table_width;
     double *exact = reinterpret_cast<double *>(static_cast<char *>(a.workspace) + w.exact) +
                     (size_t)unit * a.table_width;
-    if (blocks > a.count) {
-        int present = 0, forced = 0;
-        for (int i = tid; i < blocks; i += kPick)
-            if (there(i)) {
-                ++present;
-                forced += kept(i);
-            }
-        present = block_sum(s, present);
-        forced = block_sum(s, forced);
-        if (present > a.count) {
-            every = false;
-            int need = a.count - forced;  // of the others; at least 0
-            // the scores' error
-            float most = 0.f;
-            const float *mp = reinterpret_cast<const float *>(base + w.most) + (size_t)unit * w.splits;
-            for (int i = tid; i < w.splits; i += kPick) most = max_nan(most, __ldcg(mp + i));
-            float sum = 0.f;
-            for (int h = warp; h < a.group; h += kPickWarps) {
-                const T *q = static_cast<const T *>(a.q) + (size_t)b * a.q_stride +
-                             (size_t)(kvh * a.group + h) * D;
-                float x = 0.f;
-                for (int d = lane; d < D; d += 32) x += fabsf((float)q[d]);
+    const bool scored = blocks > a.count;
+    auto make_key = [&](int i) -> uint32_t {
+        const int p = pages[i];
+        const float x = scored ? __ldcg(approx + i) : 0.f;
+        if (p < 0 || p >= a.num_pages) return kAbsent;
+        // (as differences: the sums could pass 32 bits)
+        if (!scored || i < a.keep_first || blocks - 1 - i < a.keep_last) return kKept;
+        return x == x ? key_of(x) : 1u << 31;  // (no key of NaN may be one of the two above)
+    };
+    auto key_at = [&](int i) { return i < cap ? keys[i] : make_key(i); };
+    int present = 0, forced = 0;
+    constexpr int kFlight = 4;
+    for (int i0 = tid; i0 < blocks; i0 += kFlight * kPick) {
+        uint32_t k[kFlight];
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                sum = max_nan(sum, x);
-            }
-            if (tid == 0) s.real = s.most = 0.f;
-            __syncthreads();
+        for (int f = 0; f < kFlight; ++f) {
+            const int i = i0 + f * kPick;
+            k[f] = i < blocks ? make_key(i) : kAbsent;
+        }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
-            // nonnegative floats (and NaN, the largest) have the order of their bits
-            if (lane == 0) {
-                atomicMax(reinterpret_cast<int *>(&s.most), __float_as_int(most) & 0x7fffffff);
-                atomicMax(reinterpret_cast<int *>(&s.real), __float_as_int(sum) & 0x7fffffff);
-            }
-            __syncthreads();
-            const float err = slack * s.most * s.real;
-            auto free_of = [&](int i) { return there(i) && !kept(i); };
-            if (need == 0) {
-                // above stays infinite, below too
-                below = kInf;
+        for (int f = 0; f < kFlight; ++f) {
+            const int i = i0 + f * kPick;
+            if (i < min(blocks, cap)) keys[i] = k[f];
+            present += k[f] != kAbsent;
+            forced += k[f] == kKept;
+        }
+    }
+    if (scored) {  // the scores' error
+        float most = 0.f, norm = 0.f;
+        const float *mp = reinterpret_cast<const float *>(base + w.most) + (size_t)unit * w.splits;
+        for (int i = tid; i < w.splits; i += kPick) most = max_nan(most, __ldcg(mp + i));
+        for (int h = warp; h < a.group; h += kPickWarps) {
+            const T *q = static_cast<const T *>(a.q) + (size_t)b * a.q_stride + (size_t)(kvh * a.group + h) * D;
+            float x = 0.f;
+#pragma unroll
+            for (int d = 0; d < D; d += 32) x += fabsf((float)q[d + lane]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            norm = max_nan(norm, x);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
+        __syncthreads();
+        // nonnegative floats (and NaN, the largest) have the order of their bits
+        if (lane == 0) {
+            atomicMax(reinterpret_cast<int *>(&s.most), __float_as_int(most) & 0x7fffffff);
+            atomicMax(reinterpret_cast<int *>(&s.norm), __float_as_int(norm) & 0x7fffffff);
+        }
+    }
+    const int2 all = block_sum(s, 0, present, forced);  // (its barrier is the keys' and the error's too)
+    present = all.x;
+    forced = all.y;
+
+    // keys above `above` are chosen, keys below `below` are not; those between by rank, if there are too many
+    uint32_t above = 0u, below = 0u;  // all that are there
+    bool ranked = false;
+    int turn = 1;  // the place for sums over the CTA that is free
+    if (present > a.count) {
+        int need = a.count - forced;  // of the others; at least 0
+        const float err = slack * s.most * s.norm;
+        const bool finite = err < 1e30f;  // false for NaN
+        if (need == 0) {
+            above = below = kKept - 1;
+        } else {
+            if (finite) {
+                int equal;
+                const uint32_t k = radix_pick<uint32_t>(s, blocks, need, equal, [&](int i, uint32_t &key) {
+                    key = key_at(i);
+                    return key != kAbsent && key != kKept;
+                });
+                // (2 e, and room for the rounding of these two sums: e is at least 2^-20 of |t|)
+                const float t = value_of(k);
+                above = key_of(t + 2.25f * err);
+                below = key_of(t - 2.25f * err);
             } else {
-                if (err < 1e30f) {  // false for NaN
+                above = kKept - 1;
+                below = kAbsent + 1;
+            }
+            auto in_band = [&](int i) {
+                const uint32_t k = key_at(i);
+                return k >= below && k <= above && k != kAbsent;
+            };
+            int sure = 0, maybe = 0;
+            for (int i = tid; i < blocks; i += kPick) {
+                const uint32_t k = key_at(i);
+                sure += k > above && k != kKept;
+                maybe += k >= below && k <= above && k != kAbsent;
+            }
+            if (tid == 0) s.found = 0;
+            const int2 sums = block_sum(s, turn, sure, maybe);
+            turn = 0;
+            need -= sums.x;
+            maybe = sums.y;
+            if (maybe > need) {
+                ranked = true;
+                if (maybe <= kRanked) {
+                    for (int i = tid; i < blocks; i += kPick)
+                        if (in_band(i)) s.list[atomicAdd(&s.found, 1)] = i;
+                    __syncthreads();
+                    for (int c = warp; c < maybe; c += kPickWarps) {
+                        const double x = exact_score<T, D>(a, b, kvh, pages[s.list[c]], err);
+                        if (lane == 0) exact[s.list[c]] = x;
+                    }
+                    __syncthreads();
+                    if (tid < maybe) {
+                        const int mine = s.list[tid];
+                        const uint64_t key = key_of(exact[mine]);
+                        int before = 0;
+                        for (int c = 0; c < maybe; ++c) {
+                            const uint64_t other = key_of(exact[s.list[c]]);
+                            before += other > key || (other == key && s.list[c] < mine);
+                        }
+                        if (before == need - 1) {
+                            s.least = key;
+                            s.last = mine;
+                        }
+                    }
+                    __syncthreads();
+                } else {
+                    for (int i = warp; i < blocks; i += kPickWarps)
+                        if (in_band(i)) {
+                            const double x = exact_score<T, D>(a, b, kvh, pages[i], err);
+                            if (lane == 0) exact[i] = x;
+                        }
+                    __syncthreads();
                     int equal;
-                    const uint32_t k = radix_pick<uint32_t>(s, blocks, need, equal, [&](int i, uint32_t &key) {
-                        if (!free_of(i)) return false;
-                        key = key_of(__ldcg(approx + i));
+                    const uint64_t k = radix_pick<uint64_t>(s, blocks, need, equal, [&](int i, uint64_t &key) {
+                        if (!in_band(i)) return false;
+                        key = key_of(exact[i]);
                         return true;
                     });
-                    const float t = value_of(k);
-                    // (2 e, and room for the rounding of these two sums: e is at least 2^-20 of |t|)
-                    above = t + 2.25f * err;
-                    below = t - 2.25f * err;
-                }
-                int sure = 0, maybe = 0;
-                for (int i = tid; i < blocks; i += kPick)
-                    if (free_of(i)) {
-                        const float x = err < 1e30f ? __ldcg(approx + i) : 0.f;
-                        sure += x > above;
-                        maybe += !(x > above) && !(x < below);
+                    // the `equal`-th block that has the least value
+                    if (warp == 0) {
+                        int seen = 0;
+                        for (int i0 = 0; i0 < blocks && seen < equal; i0 += 32) {
+                            const int i = i0 + lane;
+                            const bool is = i < blocks && in_band(i) && key_of(exact[i]) == k;
+                            const uint32_t m = __ballot_sync(0xffffffffu, is);
+                            if (is && seen + __popc(m & ((1u << lane) - 1)) == equal - 1) {
+                                s.least = k;
+                                s.last = i;
+                            }
+                            seen += __popc(m);
+                        }
                     }
-                sure = block_sum(s, sure);
-                maybe = block_sum(s, maybe);
-                need -= sure;
-                if (maybe > need) {
-                    ranked = true;
-                    if (tid == 0) s.found = 0;
                     __syncthreads();
-                    auto in_band = [&](int i) {
-                        if (!free_of(i)) return false;
-                        const float x = err < 1e30f ? __ldcg(approx + i) : 0.f;
-                        return !(x > above) && !(x < below);
-                    };
-                    if (maybe <= kRanked) {
-                        for (int i = tid; i < blocks; i += kPick)
-                            if (in_band(i)) s.list[atomicAdd(&s.found, 1)] = i;
-                        __syncthreads();
-                        for (int c = warp; c < maybe; c += kPickWarps) {
-                            const double x = exact_score<T, D>(a, b, kvh, pages[s.list[c]], err);
-                            if (lane == 0) exact[s.list[c]] = x;
-                        }
-                        __syncthreads();
-                        if (tid < maybe) {
-                            const int mine = s.list[tid];
-                            const uint64_t key = key_of(exact[mine]);
-                            int before = 0;
-                            for (int c = 0; c < maybe; ++c) {
-                                const uint64_t other = key_of(exact[s.list[c]]);
-                                before += other > key || (other == key && s.list[c] < mine);
-                            }
-                            if (before == need - 1) {
-                                s.least = key;
-                                s.last = mine;
-                            }
-                        }
-                        __syncthreads();
-                    } else {
-                        for (int i = warp; i < blocks; i += kPickWarps)
-                            if (in_band(i)) {
-                                const double x = exact_score<T, D>(a, b, kvh, pages[i], err);
-                                if (lane == 0) exact[i] = x;
-                            }
-                        __syncthreads();
-                        int equal;
-                        const uint64_t k = radix_pick<uint64_t>(s, blocks, need, equal, [&](int i, uint64_t &key) {
-                            if (!in_band(i)) return false;
-                            key = key_of(exact[i]);
-                            return true;
-                        });
-                        // the `equal`-th block that has the least value
-                        if (warp == 0) {
-                            int seen = 0;
-                            for (int i0 = 0; i0 < blocks; i0 += 32) {
-                                const int i = i0 + lane;
-                                const bool is = i < blocks && in_band(i) && key_of(exact[i]) == k;
-                                const uint32_t m = __ballot_sync(0xffffffffu, is);
-                                const int below_me = seen + __popc(m & ((1u << lane) - 1));
-                                if (is && below_me == equal - 1) {
-                                    s.least = k;
-                                    s.last = i;
-                                }
-                                seen += __popc(m);
-                                if (seen >= equal) break;
-                            }
-                        }
-                        __syncthreads();
-                    }
                 }
             }
         }
@@ -716,34 +768,23 @@ paged_pick_kernel(const __grid_constant__ PagedSelectArgs a, const __grid_consta
 
     // the chosen blocks in ascending order
     int at = 0;
-    const float *scores = approx;
-    const bool use_scores = !every && (above < kInf || below > -kInf);
-    for (int i0 = 0; i0 < blocks && at < a.count; i0 += kPick) {
+    for (int i0 = 0; i0 < blocks && at < a.count; i0 += kPick, turn ^= 1) {
         const int i = i0 + tid;
-        bool take = false;
-        if (i < blocks && there(i)) {
-            take = every || kept(i);
-            if (!take) {
-                const float x = use_scores && below < kInf ? __ldcg(scores + i) : 0.f;
-                if (x > above) take = true;
-                else if (!(x < below)) {
-                    take = true;
-                    if (ranked) {
-                        const uint64_t key = key_of(exact[i]);
-                        take = key > s.least || (key == s.least && i <= s.last);
-                    }
-                }
-            }
+        const uint32_t k = i < blocks ? key_at(i) : kAbsent;
+        bool take = k != kAbsent && k >= below;
+        if (take && ranked && k <= above) {
+            const uint64_t key = key_of(exact[i]);
+            take = key > s.least || (key == s.least && i <= s.last);
         }
         const uint32_t m = __ballot_sync(0xffffffffu, take);
-        __syncthreads();
-        if (lane == 0) s.warps[warp] = __popc(m);
+        if (lane == 0) s.warps[turn][warp].x = __popc(m);
         __syncthreads();
         int before = at;
 #pragma unroll
         for (int v = 0; v < kPickWarps; ++v) {
-            if (v < warp) before += s.warps[v];
-            at += s.warps[v];
+            const int n = s.warps[turn][v].x;
+            if (v < warp) before += n;
+            at += n;
         }
         const int place = before + __popc(m & ((1u << lane) - 1));
         if (take && place < a.count) out[place] = i;
@@ -766,13 +807,14 @@ template <typename T, int D> cudaError_t launch_bounds_kernel(const PagedBoundsA
 template <typename S, int D> cudaError_t launch_select(const PagedSelectArgs &a) {
     const int64_t units = (int64_t)a.batch * a.num_kv_heads;
     const SelectSpace w = select_space(units, a.table_width);
+    const int cap = a.table_width < kKeys ? a.table_width : kKeys;
     cudaError_t e = cudaSuccess;
     if (a.table_width > a.count)  // else no request has more blocks than are chosen
         e = launch_dependent(paged_score_kernel<S>, (unsigned)(units * (w.splits / kScoreWarps)),
                              kScoreWarps * 32, 0, a.stream, a, w);
     if (e == cudaSuccess)
-        e = launch_dependent(paged_pick_kernel<typename S::T, D>, (unsigned)units, kPick, 0, a.stream, a, w,
-                             S::kSlack);
+        e = launch_dependent(paged_pick_kernel<typename S::T, D>, (unsigned)units, kPick, cap * sizeof(uint32_t),
+                             a.stream, a, w, S::kSlack, cap);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
