@@ -29,13 +29,14 @@
 // Warp roles (640 threads):
 //   warps 0-7    rows of A: two threads a row, each with 64 of a tile's tokens and half of
 //                the columns of o; warps 8-15 those of B
-//   warp 16      MMA issuer: P V of a tile of one group, then that group's next S, then the other
-//                group's (one thread's MMAs run in the order of their issue, so S does not overtake
-//                the P V that reads P in its place).  One issuer keeps the groups half a period apart; with
-//                one each they ran in step, and the tensor core idled while both took exponentials
-//   warp 17      copies of K (18 and 19 only give up registers) and V into a ring of four tiles: TMA boxes of as many rows as divide
+//   warps 16, 17 MMA issuers of A and B: P V of a tile, then the group's next S (one thread's MMAs run in the
+//                order of their issue, so S does not overtake the P V that reads P in its place).  The one
+//                place of X keeps the groups half a period apart; in step, the tensor core would idle while
+//                both take exponentials
+//   warp 18      copies of K and V into a ring of three tiles: TMA boxes of as many rows as divide
 //                both a page and a tile, where those are at least eight; other page sizes and the rows behind
 //                the prefix's end (which may hold anything, and are read as zeros) row by row with cp.async
+//   warp 19      only gives up registers
 // Every wait is bounded; one that gives up sets the CTA's abort flag, all roles leave, copies and MMAs
 // are drained, TMEM is freed and the device error word is raised.
 #include <cuda.h>
@@ -56,7 +57,7 @@ using namespace ptx;
 constexpr int kTokens = kPrefixTile;  // of a tile
 constexpr int kRows = 128;            // of a group
 constexpr int kGroupWarps = 8;
-constexpr int kIssue = 16, kCopy = 17;
+constexpr int kIssue0 = 16, kCopy = 18;
 constexpr int kTcThreads = 640;
 constexpr int kTiles = 3;             // tiles of tokens in shared memory
 constexpr int kRing = 2 * kTiles;     // their K and V
@@ -72,7 +73,7 @@ static_assert(kTokens == 128 && kRows == 128, "operand shapes");
 
 struct TcShared {
     uint64_t full[kTiles], empty[kTiles];
-    uint64_t q_ready[2], s_full[2], p_ready[2], x_full[2], done;
+    uint64_t q_ready[2], s_full[2], p_ready[2], x_full[2], done[2];
     alignas(16) uint32_t have[kTiles][4];  // present tokens of a tile, by its place in the ring
     uint32_t tmem_base;
     int redo[2];                // the group wants S of its tile once more
@@ -220,8 +221,8 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
             mbar_init(bar(cs.s_full[x]), 2);  // the MMAs, and the issuer for the copies' `have`
             mbar_init(bar(cs.p_ready[x]), 1 + kGroupWarps);  // P, and the place of X from the other group
             mbar_init(bar(cs.x_full[x]), 1);
+            mbar_init(bar(cs.done[x]), 1);
         }
-        mbar_init(bar(cs.done), 1);
         cs.abort = 0;
         fence_mbar_init();
     }
@@ -435,106 +436,97 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
                     *reinterpret_cast<float2 *>(slot + (size_t)f.stride * D + 2 * in_unit) = make_float2(m, l);
             }
         }
-    } else if (warp == kIssue) {
-        // ================= MMA issuer =================
-        // Item k is group k & 1's tile number k / 2: tile k / 2 of the CTA where the groups share
-        // them, tile k where they do not.  What the warp does between two items counts twice a tile, so it
-        // waits for as few things as there can be: a tile (K and V together), and a group's weights
+    } else if (warp < kCopy) {
+        // ================= MMA issuers =================
+        // What an issuer does between two of its items (about 60 instructions, each behind the last) is as
+        // long as the items themselves; with one for each group it passes while the other's run.  A waits
+        // for as few things as there can be: a tile (K and V together), and its group's weights
         // together with the other group's word that X has been taken.
-        const int items = walk.left * (kShared ? 2 : 1);
-        int part_end = 0;                          // tiles of the parts entered so far
-        int loaded = 0;                            // tiles that have been waited for
-        bool fresh[2] = {false, false};            // a group's Q has not been waited for
-        uint32_t parts[2] = {0, 0}, weights[2] = {0, 0};  // phases of q_ready and p_ready
-        auto tile_of = [&](int k) { return kShared ? k >> 1 : k; };
-        // Whether item k is the first of its group in a part, whose Q is then to be waited for.
-        auto is_fresh = [&](int k) {
-            while (tile_of(k) >= part_end) {
+        const int x = warp - kIssue0;
+        const uint32_t s_at = x * 128, q_at = kColQ + x * 64;
+        const uint32_t s_full = bar(cs.s_full[x]), x_full = bar(cs.x_full[x]), p_ready = bar(cs.p_ready[x]);
+        // the group's tiles of the CTA: t = first, first + step, ...
+        const int total = walk.left, step = kShared ? 1 : 2, first = kShared ? 0 : x;
+        int part_end = 0;                  // tiles of the parts entered so far
+        bool fresh = false;                // the group's Q has not been waited for
+        uint32_t parts = 0, weights = 0;   // phases of q_ready and p_ready
+        // Whether tile t is the group's first of a part, whose Q is then to be waited for.
+        auto is_fresh = [&](int t) {
+            while (t >= part_end) {
                 walk.next();
                 part_end = walk.at + walk.n;
-                fresh[0] = fresh[1] = true;
+                fresh = true;
             }
-            return k & 1 ? fresh[1] : fresh[0];
-        };
-        auto wait_q = [&](int k) -> bool {
-            const int x = k & 1;
-            if (!warp_wait(bar(cs.q_ready[x]), (x ? parts[1] : parts[0]) & 1, abort_flag)) return false;
-            if (x) {
-                fresh[1] = false;
-                ++parts[1];
-            } else {
-                fresh[0] = false;
-                ++parts[0];
-            }
-            return true;
+            return fresh;
         };
         auto wait_tile = [&](int t) -> bool {
-            if (t < loaded) return true;
-            loaded = t + 1;
             return warp_wait(bar(cs.full[t % kTiles]), (t / kTiles) & 1, abort_flag);
         };
         // (by one lane, with operands that the whole warp has computed: else each MMA becomes a loop)
-        auto issue_s = [&](uint32_t s, uint32_t q, uint64_t dk, uint32_t full) {
+        auto issue_s = [&](uint64_t dk) {
 #pragma unroll
             for (uint32_t i = 0; i < KS; ++i)
-                mma_bf16_tmem_a(s, q + 8 * i, dk + (uint64_t)((i & 3u) * 2 + (i >> 2) * (kAtoms >> 4)), kIdescS,
+                mma_bf16_tmem_a(s_at, q_at + 8 * i, dk + (uint64_t)((i & 3u) * 2 + (i >> 2) * (kAtoms >> 4)), kIdescS,
                                 i ? 1u : 0u);
-            mma_commit(full);
-            mbar_arrive(full);
+            mma_commit(s_full);
+            mbar_arrive(s_full);
         };
-        auto issue_x = [&](uint32_t s, uint64_t dv, uint32_t full, uint32_t empty, bool last) {
+        auto issue_x = [&](uint64_t dv, uint32_t empty) {
 #pragma unroll
             for (uint32_t i = 0; i < 16; ++i)
-                mma_bf16_tmem_a(kColX, s + 8 * i, dv + (uint64_t)(64u * i), kIdescX, i ? 1u : 0u);
-            mma_commit(full);
-            if (last) mma_commit(empty);  // (K could be wanted once more until the weights were there)
+                mma_bf16_tmem_a(kColX, s_at + 8 * i, dv + (uint64_t)(64u * i), kIdescX, i ? 1u : 0u);
+            mma_commit(x_full);
+            // K could be wanted once more until the weights were there; B's P V comes behind A's, whose X
+            // has been taken
+            if (!kShared || x) mma_commit(empty);
         };
-        auto start = [&](int k) -> bool {  // S of an item, waiting for its Q where that is new
-            if ((is_fresh(k) && !wait_q(k)) || !wait_tile(tile_of(k))) return false;
+        auto start = [&](int t) -> bool {  // S of a tile, waiting for Q where that is new
+            if (is_fresh(t)) {
+                if (!warp_wait(bar(cs.q_ready[x]), parts & 1, abort_flag)) return false;
+                ++parts;
+                fresh = false;
+            }
+            if (!wait_tile(t)) return false;
             tc_fence_after();
-            const int x = k & 1;
-            const uint32_t s_at = x * 128, q_at = kColQ + x * 64, full = bar(cs.s_full[x]);
-            const uint64_t dk = sdesc_sw128(ring(tile_of(k) % kTiles * 2), 16, 1024);
-            if (elect_one()) issue_s(s_at, q_at, dk, full);
+            const uint64_t dk = sdesc_sw128(ring(t % kTiles * 2), 16, 1024);
+            if (elect_one()) issue_s(dk);
             __syncwarp();
             return true;
         };
-        if (lane < kGroupWarps) mbar_arrive(bar(cs.p_ready[0]));  // nobody's X is in the first item's way
+        if (x == 0 && lane < kGroupWarps) mbar_arrive(p_ready);  // nobody's X is in the first item's way
         __syncwarp();
-        bool ok = start(0) && (items < 2 || start(1));
-        for (int k = 0; ok && k < items; ++k) {
-            // P V of the item and the group's next S go out together where nothing is to be waited for
-            const bool follows = k + 2 < items && !is_fresh(k + 2);
-            const int x = k & 1, at = tile_of(k) % kTiles, next = tile_of(k + 2) % kTiles;
-            const uint32_t s_at = x * 128, q_at = kColQ + x * 64;
+        bool ok = first >= total || start(first);
+        for (int t = first; ok && t < total; t += step) {
+            // P V of the tile and the group's next S go out together where nothing is to be waited for
+            const int at = t % kTiles, next = (t + step) % kTiles;
+            const bool more = t + step < total, follows = more && !is_fresh(t + step);
             const uint64_t dv = sdesc_sw128(ring(2 * at + 1), kAtoms, 0), dk = sdesc_sw128(ring(2 * next), 16, 1024);
-            const uint32_t s_full = bar(cs.s_full[x]), x_full = bar(cs.x_full[x]), p_ready = bar(cs.p_ready[x]);
             const uint32_t empty = bar(cs.empty[at]);
-            ok = !follows || wait_tile(tile_of(k + 2));
+            ok = !follows || wait_tile(t + step);
             while (ok) {
-                ok = warp_wait(p_ready, (x ? weights[1]++ : weights[0]++) & 1, abort_flag);
+                ok = warp_wait(p_ready, weights++ & 1, abort_flag);
                 if (!ok || !*const_cast<volatile int *>(&cs.redo[x])) break;
                 const uint64_t dk_now = sdesc_sw128(ring(2 * at), 16, 1024);
                 if (lane < kGroupWarps) mbar_arrive(p_ready);  // X has been taken already
                 tc_fence_after();
                 __syncwarp();
-                if (elect_one()) issue_s(s_at, q_at, dk_now, s_full);
+                if (elect_one()) issue_s(dk_now);
                 __syncwarp();
             }
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-                issue_x(s_at, dv, x_full, empty, !kShared || x);
-                if (follows) issue_s(s_at, q_at, dk, s_full);
+                issue_x(dv, empty);
+                if (follows) issue_s(dk);
             }
             __syncwarp();
-            if (!follows && k + 2 < items) ok = start(k + 2);
+            if (!follows && more) ok = start(t + step);
         }
         // all MMAs have to be finished before TMEM is released
-        if (elect_one()) mma_commit(bar(cs.done));
+        if (elect_one()) mma_commit(bar(cs.done[x]));
         __syncwarp();
         int no_abort = 0;
-        warp_wait(bar(cs.done), 0, &no_abort);
+        warp_wait(bar(cs.done[x]), 0, &no_abort);
     } else if (warp == kCopy) {
         // ================= copies =================
         // Row by row: two lanes a row (32 bytes, a sector, at a time), lane l the rows l / 2 + 16 i, from one
