@@ -14,7 +14,8 @@ namespace la {
 // (grid_dependency_wait) before its first global-memory access, so stream
 // order is kept for every memory effect.  Only kernels that begin with that
 // wait are launched this way (the join of the paged attention reads the lengths
-// before it: the kernel in front of it lets it be scheduled only once it has
+// before it, the attention behind a shared prefix all but the prefix's pieces, the choice of pages all
+// but the scores: the kernel in front of each lets it be scheduled only once it has
 // itself waited for whatever wrote them).
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_dependent(void (*kern)(KArgs...), unsigned grid, unsigned block,

@@ -339,6 +339,18 @@ struct Partial {
     }
 };
 
+// Dependent launches: the lengths, the table and the cache may have been written by the kernel
+// before.  Behind a shared prefix that kernel is the prefix's, which lets this one be scheduled only once
+// it has itself waited for whatever wrote them: only its pieces are still to come, and every CTA waits for those
+// before its first row (and before its end, so that the kernel behind this one finds them too).
+template <Kv KV> __device__ __forceinline__ void wait_before_reads() {
+    if constexpr (KV != Kv::kBehind) ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+}
+template <Kv KV> __device__ __forceinline__ void wait_before_rows() {
+    if constexpr (KV == Kv::kBehind) ptx::grid_dependency_wait();
+}
+
 // Zeros (or the prefix's sums) for the requests without tokens, which are nobody's tiles.
 template <typename T, Kv KV>
 __device__ __forceinline__ void write_empty(const PagedDecodeArgs &a) {
@@ -981,11 +993,7 @@ paged_split_kernel(const __grid_constant__ PagedDecodeArgs a) {
     constexpr int kOver = kOverhead<typename Core::T, D>;
     extern __shared__ __align__(128) unsigned char smem[];
 
-    // launched as a dependent launch: the lengths, the table and the cache
-    // may have been written by the kernel before
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
+    wait_before_reads<Core::KV>();
     const int units = a.num_kv_heads * a.head_groups;
     Place at;
     const bool any = find_place<Core::KV, Core::kThreads, kOver>(a, units, blockIdx.x, at);
@@ -1014,6 +1022,7 @@ paged_split_kernel(const __grid_constant__ PagedDecodeArgs a) {
         Core::stream(a, smem, b, kvh, head0, heads, tile0 * kTile, min(len, tile1 * kTile));
         __syncthreads();
         const bool whole = tile0 == 0 && tile1 == tiles;
+        if (whole) wait_before_rows<Core::KV>();
         float *ws = piece_at<D>(a, blockIdx.x, first, ROWS);
         for (int i = threadIdx.x; i < heads * (D / 4); i += Core::kThreads) {
             const int h = i / (D / 4), d = (i % (D / 4)) * 4;
@@ -1028,6 +1037,7 @@ paged_split_kernel(const __grid_constant__ PagedDecodeArgs a) {
         __syncthreads();  // shared memory is the ring again
         first = false;
     }
+    wait_before_rows<Core::KV>();
     write_empty<typename Core::T, Core::KV>(a);
 }
 
@@ -1061,8 +1071,7 @@ __global__ void __launch_bounds__(Core::kThreads, 2)
 paged_cluster_kernel(const __grid_constant__ PagedDecodeArgs a) {
     constexpr int D = Core::D, ROWS = Core::ROWS;
     extern __shared__ __align__(128) unsigned char smem[];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    wait_before_reads<Core::KV>();
 
     // a one-dimensional grid of one-dimensional clusters: the rank in the
     // cluster is the block's index modulo its size
@@ -1076,6 +1085,7 @@ paged_cluster_kernel(const __grid_constant__ PagedDecodeArgs a) {
     const int t0 = rank * share, t1 = min(len, t0 + share);
     const bool any = t0 < t1;
     if (any) Core::stream(a, smem, b, kvh, head0, heads, t0, t1);
+    wait_before_rows<Core::KV>();
     __syncthreads();
     const size_t row0 = (size_t)b * a.num_heads + head0;
     if (S == 1) {

@@ -58,20 +58,14 @@ template <typename Core> cudaError_t launch_prefix(const PagedDecodeArgs &a) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int D> cudaError_t run(PagedDecodeArgs a, const int32_t *prefix_table, bool bf16) {
-    if (a.prefix.max_tokens > 0) {
-        PagedDecodeArgs p = a;
-        p.block_table = prefix_table;
-        cudaError_t e;
-        if (bf16)
-            e = paged_prefix_tc(p);
-        else
-            e = a.prefix.unit_rows == 4   ? launch_prefix<F32Core<Kv::kPrefix, D, 4>>(p)
-                : a.prefix.unit_rows == 8 ? launch_prefix<F32Core<Kv::kPrefix, D, 8>>(p)
-                                          : launch_prefix<F32Core<Kv::kPrefix, D, 16>>(p);
-        if (e != cudaSuccess) return e;
-    }
-    return dispatch<Kv::kBehind, D>(a, bf16);
+template <int D> cudaError_t run(const PagedDecodeArgs &a, const int32_t *prefix_table, bool bf16) {
+    PagedDecodeArgs p = a;
+    p.block_table = prefix_table;
+    const cudaError_t e = bf16                        ? paged_prefix_tc(p)
+                          : a.prefix.unit_rows == 4 ? launch_prefix<F32Core<Kv::kPrefix, D, 4>>(p)
+                          : a.prefix.unit_rows == 8 ? launch_prefix<F32Core<Kv::kPrefix, D, 8>>(p)
+                                                    : launch_prefix<F32Core<Kv::kPrefix, D, 16>>(p);
+    return e != cudaSuccess ? e : dispatch<Kv::kBehind, D>(a, bf16);
 }
 
 }  // namespace
@@ -99,6 +93,8 @@ PrefixPieces paged_prefix_pieces(int64_t batch, int64_t num_heads, int64_t num_k
 }
 
 cudaError_t paged_prefix_decode(const PagedDecodeArgs &a, const int32_t *prefix_table, bool bf16) {
+    // No prefix, no kernel in front of those that are behind one, which rely on it.
+    if (a.prefix.max_tokens == 0) return paged_decode(a, bf16, !bf16);
     if (a.head_dim == 128) return run<128>(a, prefix_table, bf16);
     if (a.head_dim == 64) return run<64>(a, prefix_table, bf16);
     return cudaErrorNotSupported;

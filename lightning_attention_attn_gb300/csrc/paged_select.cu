@@ -147,6 +147,7 @@ constexpr int kScoreTile = 16;   // blocks of a warp's step
 
 struct SelectSpace {
     int splits;        // warps of a unit
+    bool scored;       // some requests may have more blocks than are chosen
     size_t exact, approx, most, bytes;  // offsets
 };
 
@@ -157,6 +158,7 @@ SelectSpace select_space(int64_t units, int64_t width) {
     n = n < tiles ? n : tiles;
     n = (n + kScoreWarps - 1) / kScoreWarps;
     s.splits = (int)(n < 1 ? 1 : n) * kScoreWarps;
+    s.scored = true;
     s.exact = 0;
     s.approx = (size_t)(units * width) * sizeof(double);
     s.most = s.approx + (size_t)(units * width) * sizeof(float);
@@ -606,8 +608,10 @@ paged_pick_kernel(const __grid_constant__ PagedSelectArgs a, const __grid_consta
     const int unit = blockIdx.x, b = unit / a.num_kv_heads, kvh = unit - b * a.num_kv_heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) s.norm = s.most = 0.f;
-    ptx::grid_dependency_wait();
-    ptx::grid_launch_dependents();
+    // Behind the scores' kernel, which lets this one be scheduled only once it has itself waited for whatever
+    // wrote the lengths, the table, the queries and the bounds: only the scores are still to come.
+    if (w.scored) ptx::grid_launch_dependents();
+    else ptx::grid_dependency_wait();
     const int blocks = unit_blocks(a, b);
     const int32_t *pages = a.block_table + (size_t)b * a.table_stride;
     int32_t *out = a.selected + (size_t)unit * a.count;
@@ -616,36 +620,23 @@ paged_pick_kernel(const __grid_constant__ PagedSelectArgs a, const __grid_consta
     double *exact = reinterpret_cast<double *>(static_cast<char *>(a.workspace) + w.exact) +
                     (size_t)unit * a.table_width;
     const bool scored = blocks > a.count;
-    auto make_key = [&](int i) -> uint32_t {
+    auto there = [&](int i) {
         const int p = pages[i];
-        const float x = scored ? __ldcg(approx + i) : 0.f;
-        if (p < 0 || p >= a.num_pages) return kAbsent;
+        return p >= 0 && p < a.num_pages;
+    };
+    auto make_key = [&](int i, bool is, float x) -> uint32_t {
+        if (!is) return kAbsent;
         // (as differences: the sums could pass 32 bits)
         if (!scored || i < a.keep_first || blocks - 1 - i < a.keep_last) return kKept;
         return x == x ? key_of(x) : 1u << 31;  // (no key of NaN may be one of the two above)
     };
-    auto key_at = [&](int i) { return i < cap ? keys[i] : make_key(i); };
-    int present = 0, forced = 0;
-    constexpr int kFlight = 4;
-    for (int i0 = tid; i0 < blocks; i0 += kFlight * kPick) {
-        uint32_t k[kFlight];
-#pragma unroll
-        for (int f = 0; f < kFlight; ++f) {
-            const int i = i0 + f * kPick;
-            k[f] = i < blocks ? make_key(i) : kAbsent;
-        }
-#pragma unroll
-        for (int f = 0; f < kFlight; ++f) {
-            const int i = i0 + f * kPick;
-            if (i < min(blocks, cap)) keys[i] = k[f];
-            present += k[f] != kAbsent;
-            forced += k[f] == kKept;
-        }
-    }
-    if (scored) {  // the scores' error
-        float most = 0.f, norm = 0.f;
-        const float *mp = reinterpret_cast<const float *>(base + w.most) + (size_t)unit * w.splits;
-        for (int i = tid; i < w.splits; i += kPick) most = max_nan(most, __ldcg(mp + i));
+    auto key_at = [&](int i) {
+        return i < cap ? keys[i] : make_key(i, there(i), scored ? __ldcg(approx + i) : 0.f);
+    };
+    // which pages are there, and the queries' part of the scores' error, before the wait
+    for (int i = tid; i < min(blocks, cap); i += kPick) keys[i] = there(i);
+    if (scored) {
+        float norm = 0.f;
         for (int h = warp; h < a.group; h += kPickWarps) {
             const T *q = static_cast<const T *>(a.q) + (size_t)b * a.q_stride + (size_t)(kvh * a.group + h) * D;
             float x = 0.f;
@@ -655,14 +646,38 @@ paged_pick_kernel(const __grid_constant__ PagedSelectArgs a, const __grid_consta
             for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
             norm = max_nan(norm, x);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
         __syncthreads();
         // nonnegative floats (and NaN, the largest) have the order of their bits
-        if (lane == 0) {
-            atomicMax(reinterpret_cast<int *>(&s.most), __float_as_int(most) & 0x7fffffff);
-            atomicMax(reinterpret_cast<int *>(&s.norm), __float_as_int(norm) & 0x7fffffff);
+        if (lane == 0) atomicMax(reinterpret_cast<int *>(&s.norm), __float_as_int(norm) & 0x7fffffff);
+    }
+    if (w.scored) ptx::grid_dependency_wait();
+    else ptx::grid_launch_dependents();
+    int present = 0, forced = 0;
+    constexpr int kFlight = 4;
+    for (int i0 = tid; i0 < blocks; i0 += kFlight * kPick) {
+        float x[kFlight];
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+            const int i = i0 + f * kPick;
+            x[f] = scored && i < blocks ? __ldcg(approx + i) : 0.f;
         }
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+            const int i = i0 + f * kPick;
+            if (i >= blocks) break;
+            const uint32_t k = make_key(i, i < cap ? keys[i] != 0 : there(i), x[f]);
+            if (i < cap) keys[i] = k;
+            present += k != kAbsent;
+            forced += k == kKept;
+        }
+    }
+    if (scored) {
+        float most = 0.f;
+        const float *mp = reinterpret_cast<const float *>(base + w.most) + (size_t)unit * w.splits;
+        for (int i = tid; i < w.splits; i += kPick) most = max_nan(most, __ldcg(mp + i));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
+        if (lane == 0) atomicMax(reinterpret_cast<int *>(&s.most), __float_as_int(most) & 0x7fffffff);
     }
     const int2 all = block_sum(s, 0, present, forced);  // (its barrier is the keys' and the error's too)
     present = all.x;
@@ -806,10 +821,11 @@ template <typename T, int D> cudaError_t launch_bounds_kernel(const PagedBoundsA
 
 template <typename S, int D> cudaError_t launch_select(const PagedSelectArgs &a) {
     const int64_t units = (int64_t)a.batch * a.num_kv_heads;
-    const SelectSpace w = select_space(units, a.table_width);
+    SelectSpace w = select_space(units, a.table_width);
+    w.scored = a.table_width > a.count;
     const int cap = a.table_width < kKeys ? a.table_width : kKeys;
     cudaError_t e = cudaSuccess;
-    if (a.table_width > a.count)  // else no request has more blocks than are chosen
+    if (w.scored)
         e = launch_dependent(paged_score_kernel<S>, (unsigned)(units * (w.splits / kScoreWarps)),
                              kScoreWarps * 32, 0, a.stream, a, w);
     if (e == cudaSuccess)
