@@ -408,6 +408,21 @@ def test_prefix_batches(dtype, h, hk, d, batch):
     check_prefix(randn((batch, h, d), dtype, g), *args)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [4, 8, 24, 128, 200, 256])
+def test_prefix_page_sizes(page, d):
+    """Pages that a tile's copies take as boxes of 8 to 128 rows, or row by row; absent pages of each."""
+    g = gen(page)
+    kc, vc, pt, pl, bt, sl = behind(1500, [30, 0, 7] * 7, page, 2, d, BF16, g)
+    q = randn((21, 8, d), BF16, g)
+    check_prefix(q, kc, vc, pt, pl, bt, sl)
+    for gone in (1, 2, pt.numel() // 2, pt.numel() - 1):
+        if gone < pt.numel():
+            pt[gone] = -1 if gone % 2 else 2 ** 31 - 1
+    check_prefix(q, kc, vc, pt, pl, bt, sl)
+    check_prefix(q[:5], kc, vc, pt, pl, bt[:5], sl[:5])
+
+
 @pytest.mark.parametrize("h, hk, batch, prefix", [(8, 8, 1, 5120), (16, 2, 4, 20000), (24, 12, 70, 2900),
                                                   (160, 160, 2, 100), (200, 200, 130, 300)])
 @pytest.mark.parametrize("d", [64, 128])
@@ -473,6 +488,42 @@ def test_prefix_absent_pages_and_lengths():
     good = behind(600, lens, page, 2, 128, BF16, g)
     pt = good[2][:37]  # the table holds 592 tokens of 2^31 - 1
     check_prefix(q, good[0], good[1], pt, ints([2 ** 31 - 1]), good[4], good[5])
+
+
+@pytest.mark.parametrize("scale", [0.0, -1.0, 3.0])
+def test_prefix_scales(scale):
+    """A scale of 0 (the mean of the values), a negative one, a large one; a whole tile absent too."""
+    g = gen(49)
+    kc, vc, pt, pl, bt, sl = behind(400, [20, 0, 3], 16, 2, 128, BF16, g)
+    pt[8:16] = -1
+    check_prefix(randn((3, 8, 128), BF16, g), kc, vc, pt, pl, bt, sl, scale=scale)
+
+
+@pytest.mark.parametrize("step", [7, 9, 60, 300])
+@pytest.mark.parametrize("batch", [2, 40])
+def test_prefix_maximum_that_jumps(step, batch):
+    """Tiles of 128 tokens whose scores rise by `step` (in log2) over the ones before, for some
+    rows up and for others down."""
+    g = gen(50)
+    kc, vc, pt, pl, bt, sl = behind(1100, [3] * batch, 16, 1, 64, BF16, g, garbage=0.0)
+    t = torch.arange(1100, device="cuda")
+    at = (pt[t // 16].long(), 0, t % 16)
+    x = kc[at] * 0.1
+    x[:, 0] = (t // 128).to(BF16)
+    kc[at] = x
+    q = randn((batch, 4, 64), BF16, g)
+    q[..., 0] = step * torch.tensor([1.0, -1.0, 0.5, 1.0], device="cuda").to(BF16)
+    check_prefix(q, kc, vc, pt, pl, bt, sl, scale=math.log(2))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_prefix_of_an_empty_pool(dtype):
+    empty = torch.empty((0, 2, 16, 64), dtype=dtype, device="cuda")
+    q = randn((3, 4, 64), dtype, gen(51))
+    pt, bt = ints([0, 1, 2]), torch.zeros((3, 2), dtype=torch.int32, device="cuda")
+    lse = torch.empty((3, 4), device="cuda")
+    out = la.paged_prefix_decode(q, empty, empty, pt, ints([40]), bt, ints([5, 0, 32]), lse=lse)
+    assert (out == 0).all() and (lse == -INF).all()
 
 
 @pytest.mark.parametrize("dtype, batch", [(BF16, 3), (BF16, 40), (FP32, 3)])
@@ -601,6 +652,49 @@ def test_prefix_long_sums_do_not_drift():
     assert mean <= bound
 
 
+def test_calls_behind_what_writes_their_arguments():
+    """Every argument written by the call right before, in one stream without a wait between: lengths,
+    table and slots by the reservation, queries and cache by the append, the choice by the selection."""
+    g = gen(52)
+    page, hk, h, d, b, count = 16, 2, 16, 128, 6, 9
+    pages = 700
+    kc, vc = caches(pages, hk, page, d, BF16, g)
+    front = torch.arange(600, 640, dtype=torch.int32, device="cuda")
+    bd = torch.zeros((pages, hk, 2, d), dtype=BF16, device="cuda")
+    table = la.rotary_table(4000, 64, device="cuda")
+    xs = [randn((sum(n), h + 2 * hk, d), BF16, g) for n in ([400, 3, 900, 0, 17, 1], [1] * 6, [1] * 6)]
+
+    def loop(wait):
+        k, v = kc.clone(), vc.clone()
+        bounds = bd.clone()
+        bt = torch.full((b, 80), -1, dtype=torch.int32, device="cuda")
+        lens, free, top = ints([0] * b), torch.arange(600, dtype=torch.int32, device="cuda"), ints([600])
+        got = []
+        for new, x in zip(([400, 3, 900, 0, 17, 1], [1] * 6, [1] * 6), xs):
+            before = lens.clone()
+            slots, pos, cu, _ = la.paged_reserve(bt, lens, ints(new), free, top, page, sum(new))
+            wait()
+            q = la.paged_append(x[:, :h], x[:, h:h + hk], x[:, h + hk:], pos, table, k, v, slots)
+            wait()
+            last = (cu[1:] - 1).clamp(min=0).long()
+            ql = q[last].contiguous()
+            out = la.paged_prefix_decode(ql, k, v, front, ints([630]), bt, lens)
+            wait()
+            la.paged_bounds(k, bounds, bt, before, lens)
+            wait()
+            sel = la.paged_select(ql, bounds, bt, lens, page, count)
+            wait()
+            got += [out, sel, la.paged_sparse_decode(ql, k, v, bt, lens, sel)]
+            wait()
+            got.append(la.paged_prefix_decode(ql, k, v, front[:0], ints([0]), bt, lens))
+            wait()
+        return got
+
+    want = loop(torch.cuda.synchronize)
+    for _ in range(20):
+        assert all(torch.equal(x, y) for x, y in zip(loop(lambda: None), want))
+
+
 # ---------------------------------------------------------------- together
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_serving_loop(dtype):
@@ -684,4 +778,9 @@ def test_offsets_past_32_bits():
     bd2 = torch.zeros((40, hk, 2, d), dtype=BF16, device="cuda")
     sel2, out2 = run_all(q, kc[-40:].contiguous(), vc[-40:].contiguous(), bd2, small, ints([0]), lens, page, 9)
     assert torch.equal(sel, sel2) and torch.equal(out, out2) and torch.equal(bd[-40:], bd2)
+    own, n = bt[:, :2].contiguous(), ints([70])
+    args = [(kc, vc, bt[0, 2:].contiguous(), own), (kc[-40:].contiguous(), vc[-40:].contiguous(),
+                                                    small[0, 2:].contiguous(), small[:, :2].contiguous())]
+    both = [la.paged_prefix_decode(q, x[0], x[1], x[2], ints([38 * page - 9]), x[3], n) for x in args]
+    assert torch.equal(*both)
     assert (bd[:-40] == 0).all()
