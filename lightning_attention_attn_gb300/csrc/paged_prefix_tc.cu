@@ -189,6 +189,10 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
     TcShared &cs = *reinterpret_cast<TcShared *>(base + Z::kCtrl);
     const uint32_t sb = smem_u32(base);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == kCopy && lane == 0 && box) {
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+    }
     grid_dependency_wait();
     grid_launch_dependents();
 

@@ -153,7 +153,7 @@ struct SelectSpace {
 
 SelectSpace select_space(int64_t units, int64_t width) {
     SelectSpace s;
-    int64_t n = (int64_t)kSms * 24 / (units > 0 ? units : 1) + 1;
+    int64_t n = (int64_t)kSms * 48 / (units > 0 ? units : 1) + 1;
     const int64_t tiles = (width + kScoreTile - 1) / kScoreTile;
     n = n < tiles ? n : tiles;
     n = (n + kScoreWarps - 1) / kScoreWarps;
@@ -201,8 +201,8 @@ template <int D, int NT> struct Bf16Scores {
     static constexpr int HEADS = 8 * NT;  // of one pass
     static constexpr float kSlack = 2 * D / 16 * 17 * 0x1p-23f;
 
-    static __device__ __forceinline__ void run(const PagedSelectArgs &a, int b, int kvh, int blocks,
-                                               int split, int splits, float *scores, float &most) {
+    static __device__ __forceinline__ void run(const PagedSelectArgs &a, int b, int kvh, int split, int splits,
+                                               float *scores, float &most) {
         constexpr int CPL = 2 * D / 32;  // chunks of a lane: t, t + 4, ... of a row's minima and maxima
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         const int32_t *pages = a.block_table + (size_t)b * a.table_stride;
@@ -213,7 +213,7 @@ template <int D, int NT> struct Bf16Scores {
             int page[2];  // of rows g and g + 8 of the tile
             auto find = [&](int i0) {
 #pragma unroll
-                for (int r = 0; r < 2; ++r) page[r] = i0 + r * 8 + g < blocks ? pages[i0 + r * 8 + g] : -1;
+                for (int r = 0; r < 2; ++r) page[r] = i0 + r * 8 + g < a.table_width ? pages[i0 + r * 8 + g] : -1;
             };
             find(split * kScoreTile);
             uint32_t q[NT][CPL / 2][4];
@@ -229,12 +229,14 @@ template <int D, int NT> struct Bf16Scores {
                     q[n][c][0] = x.x, q[n][c][1] = x.y, q[n][c][2] = x.z, q[n][c][3] = x.w;
                 }
             }
+            // (the first entries and the queries are on their way beside the length)
+            const int blocks = unit_blocks(a, b);
+            if (blocks <= a.count) return;  // all of them are chosen
             for (int i0 = split * kScoreTile; i0 < blocks; i0 += splits * kScoreTile) {
                 uint4 x[2][CPL];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    // (a page that is none: any row, its score is not used)
-                    const bool there = page[r] >= 0 && page[r] < a.num_pages;
+                    const bool there = i0 + r * 8 + g < blocks && page[r] >= 0 && page[r] < a.num_pages;
                     const uint4 *p = reinterpret_cast<const uint4 *>(
                         bounds + (there ? (size_t)page[r] : 0) * a.bounds_page_stride) + t;
 #pragma unroll
@@ -310,16 +312,21 @@ template <int D> struct F32Scores {
     static constexpr int HEADS = 8;
     static constexpr float kSlack = 0x1p-20f;
 
-    static __device__ __forceinline__ void run(const PagedSelectArgs &a, int b, int kvh, int blocks,
-                                               int split, int splits, float *scores, float &most) {
+    static __device__ __forceinline__ void run(const PagedSelectArgs &a, int b, int kvh, int split, int splits,
+                                               float *scores, float &most) {
         constexpr int LPB = D / 4, BPI = 32 / LPB;  // lanes of a block, blocks of a load
         constexpr int kFlight = 4;
         const int lane = threadIdx.x & 31, sub = lane % LPB;
         const int32_t *pages = a.block_table + (size_t)b * a.table_stride;
         const T *bounds = static_cast<const T *>(a.bounds) + (size_t)kvh * 2 * D;
         most = 0.f;
+        // lane l < 16: the entry of block l of a tile, read a tile ahead
+        auto entry = [&](int i0) {
+            return lane < kScoreTile && i0 + lane < a.table_width ? pages[i0 + lane] : -1;
+        };
         for (int h0 = 0; h0 < a.group; h0 += HEADS) {
             const int heads = min(HEADS, a.group - h0);
+            int page = entry(split * kScoreTile);
             float2 up[HEADS][2], down[HEADS][2];
 #pragma unroll
             for (int h = 0; h < HEADS; ++h) {
@@ -332,19 +339,22 @@ template <int D> struct F32Scores {
                 down[h][0] = make_float2(fminf(x.x, 0.f), fminf(x.y, 0.f));
                 down[h][1] = make_float2(fminf(x.z, 0.f), fminf(x.w, 0.f));
             }
+            // (the first entries and the queries are on their way beside the length)
+            const int blocks = unit_blocks(a, b);
+            if (blocks <= a.count) return;  // all of them are chosen
             for (int i0 = split * kScoreTile; i0 < blocks; i0 += splits * kScoreTile) {
+                const int here = i0 + lane < blocks && page < a.num_pages ? page : -1;
+                page = entry(i0 + splits * kScoreTile);
 #pragma unroll 1
                 for (int j0 = 0; j0 < kScoreTile; j0 += BPI * kFlight) {
                     float4 lo[kFlight], hi[kFlight];
 #pragma unroll
                     for (int f = 0; f < kFlight; ++f) {
-                        const int i = i0 + j0 + f * BPI + lane / LPB;
-                        int page = i < blocks ? pages[i] : -1;
-                        if (page >= a.num_pages) page = -1;
+                        const int from = __shfl_sync(0xffffffffu, here, j0 + f * BPI + lane / LPB);
                         const float4 *p = reinterpret_cast<const float4 *>(
-                            bounds + (size_t)max(page, 0) * a.bounds_page_stride);
+                            bounds + (size_t)max(from, 0) * a.bounds_page_stride);
                         lo[f] = hi[f] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (page >= 0) {
+                        if (from >= 0) {
                             const float4 u = p[sub], v = p[LPB + sub];
                             lo[f] = make_float4(min_nan(u.x, v.x), min_nan(u.y, v.y), min_nan(u.z, v.z), min_nan(u.w, v.w));
                             hi[f] = make_float4(max_nan(u.x, v.x), max_nan(u.y, v.y), max_nan(u.z, v.z), max_nan(u.w, v.w));
@@ -399,20 +409,18 @@ template <int D> struct F32Scores {
 };
 
 template <typename S>
-__global__ void __launch_bounds__(kScoreWarps * 32)
+__global__ void __launch_bounds__(kScoreWarps * 32, 4)
 paged_score_kernel(const __grid_constant__ PagedSelectArgs a, const __grid_constant__ SelectSpace w) {
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const int ctas = w.splits / kScoreWarps;
     const int unit = blockIdx.x / ctas;
     const int b = unit / a.num_kv_heads, kvh = unit - b * a.num_kv_heads;
-    const int blocks = unit_blocks(a, b);
-    if (blocks <= a.count) return;  // all of them are chosen
     const int split = (blockIdx.x - unit * ctas) * kScoreWarps + (threadIdx.x >> 5);
     char *base = static_cast<char *>(a.workspace);
     float *scores = reinterpret_cast<float *>(base + w.approx) + (size_t)unit * a.table_width;
     float most = 0.f;
-    if (split * kScoreTile < blocks) S::run(a, b, kvh, blocks, split, w.splits, scores, most);
+    S::run(a, b, kvh, split, w.splits, scores, most);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
     if ((threadIdx.x & 31) == 0)
@@ -473,7 +481,7 @@ __device__ __forceinline__ K radix_pick(PickSpace &s, int n, int rank, int &equa
     constexpr int kTop = sizeof(K) * 8 - 8;
     K prefix = 0;
     __syncthreads();
-    s.hist[threadIdx.x] = 0;
+    for (int i = threadIdx.x; i < 256; i += kPick) s.hist[i] = 0;
     __syncthreads();
 #pragma unroll 1
     for (int shift = kTop; shift >= 0; shift -= 8) {
