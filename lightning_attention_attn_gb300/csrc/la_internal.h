@@ -181,6 +181,12 @@ struct PrefixPieces {
     int tile = 1, ctas = 1, units = 1, units_per_head = 1, unit_rows = 1;
     int parts = 1, stride = 0;
     float *pieces = nullptr;
+    // A row's sums [B * H][D] and statistics [B * H][2] over its own tokens where one CTA held them all.
+    float *own = nullptr, *own_stat = nullptr;
+    // [1] ranges that the prefix's kernel has cut the tiles into: ctas, or fewer where that leaves SMs to the
+    // own tokens' stream (share).
+    int *ranges = nullptr;
+    bool share = false;
 };
 
 struct PagedDecodeArgs {

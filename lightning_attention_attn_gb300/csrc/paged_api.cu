@@ -207,9 +207,13 @@ la_status check_workspace(const void *workspace, int64_t bytes, int64_t need) {
     return LA_OK;
 }
 
-int64_t prefix_workspace(const la::PrefixPieces &f, int32_t head_dim) {
-    return decode_workspace(head_dim) + ((int64_t)f.ctas + f.units) * f.parts * f.stride *
-                                            (head_dim + 2) * (int64_t)sizeof(float);
+// Behind the attention's own: the prefix's pieces, the rows' own sums and statistics, the ranges.
+int64_t prefix_pieces_floats(const la::PrefixPieces &f, int32_t head_dim) {
+    return ((int64_t)f.ctas + f.units) * f.parts * f.stride * (head_dim + 2);
+}
+int64_t prefix_workspace(const la::PrefixPieces &f, int64_t rows, int32_t head_dim) {
+    return decode_workspace(head_dim) +
+           (prefix_pieces_floats(f, head_dim) + rows * (head_dim + 2) + 4) * (int64_t)sizeof(float);
 }
 
 }  // namespace
@@ -547,7 +551,7 @@ int64_t lightning_attn_paged_prefix_decode_workspace_bytes(int32_t batch, int32_
         (long long)batch * num_heads > 0x7fffffffLL)
         return -1;
     return prefix_workspace(la::paged_prefix_pieces(batch, num_heads, num_kv_heads, dtype == LA_DTYPE_BF16),
-                            head_dim);
+                            (int64_t)batch * num_heads, head_dim);
 }
 
 la_status lightning_attn_paged_prefix_decode(
@@ -569,10 +573,14 @@ la_status lightning_attn_paged_prefix_decode(
         return LA_INVALID("prefix_table and prefix_len must be 4-byte aligned");
     LA_TRY(check_rows("q", q, q_stride, num_heads, head_dim, dtype));
     la::PrefixPieces f = la::paged_prefix_pieces(batch, num_heads, num_kv_heads, dtype == LA_DTYPE_BF16);
-    LA_TRY(check_workspace(workspace, workspace_bytes, prefix_workspace(f, head_dim)));
+    const int64_t rows = (int64_t)batch * num_heads;
+    LA_TRY(check_workspace(workspace, workspace_bytes, prefix_workspace(f, rows, head_dim)));
     f.len = prefix_len;
     f.max_tokens = capacity(prefix_width, page_size);
     f.pieces = reinterpret_cast<float *>(static_cast<char *>(workspace) + decode_workspace(head_dim));
+    f.own = f.pieces + prefix_pieces_floats(f, head_dim);
+    f.own_stat = f.own + rows * head_dim;
+    f.ranges = reinterpret_cast<int *>(f.own_stat + 2 * rows);
     la::PagedDecodeArgs a = decode_args(
         q, q_stride, k_cache, k_page_stride, v_cache, v_page_stride, block_table, table_stride,
         table_width, seq_lens, num_pages, page_size, batch, num_heads, num_kv_heads, head_dim,

@@ -252,14 +252,46 @@ __device__ __forceinline__ float *piece_at(const PagedDecodeArgs &a, int c, bool
 __device__ __forceinline__ int prefix_tiles(const PrefixPieces &f) {
     return (min(max(__ldcg(f.len), 0), f.max_tokens) + f.tile - 1) / f.tile;
 }
-__device__ __forceinline__ long long prefix_chunk(const PrefixPieces &f, int tiles) {
-    return ((long long)f.units * tiles + f.ctas - 1) / f.ctas;
+__device__ __forceinline__ long long prefix_chunk(const PrefixPieces &f, int tiles, int ranges) {
+    return ((long long)f.units * tiles + ranges - 1) / ranges;
 }
 
 // The range of `chunk` that place w is in: 32-bit where it fits.
 __device__ __forceinline__ int range_of(long long w, long long chunk) {
     return ((w | chunk) >> 32) == 0 ? (int)((uint32_t)w / (uint32_t)chunk) : (int)(w / chunk);
 }
+
+// Where columns d .. d + 3 of a row's sums in a piece are, and its maximum and exponential sum.
+struct PieceRow {
+    const float *x, *m;
+};
+// Those of a shared prefix's pieces of a row of the output, in the order of their tokens: the row's unit's
+// part of every CTA that streamed some of the unit's tiles (PrefixPieces).
+struct PrefixRow {
+    const float *x = nullptr, *m = nullptr;
+    size_t size = 0;
+    int n = 0;
+
+    __device__ __forceinline__ PrefixRow(const PagedDecodeArgs &a, size_t row, int d) {
+        const PrefixPieces &f = a.prefix;
+        const int tiles = prefix_tiles(f);
+        if (tiles == 0) return;
+        const int b = (int)(row / a.num_heads), head = (int)(row - (size_t)b * a.num_heads);
+        const int kvh = head / a.group, r = b * a.group + head - kvh * a.group;
+        const int unit = kvh * f.units_per_head + r / f.unit_rows, in = r % f.unit_rows;
+        const long long chunk = prefix_chunk(f, tiles, __ldcg(f.ranges)), w = (long long)unit * tiles;
+        const int c0 = range_of(w, chunk), c1 = range_of(w + tiles - 1, chunk);
+        // (the further parts of a CTA with a single tile are empty, and not written)
+        const int parts = chunk == 1 ? 1 : f.parts;
+        const size_t slot = (size_t)f.stride * (a.head_dim + 2);
+        n = (c1 - c0 + 1) * parts;
+        size = slot * (chunk == 1 ? f.parts : 1);
+        const float *at = f.pieces + (size_t)(c0 + unit) * f.parts * slot;
+        x = at + (size_t)in * a.head_dim + d;
+        m = at + (size_t)f.stride * a.head_dim + 2 * in;
+    }
+    __device__ __forceinline__ PieceRow piece(int i) const { return {x + i * size, m + i * size}; }
+};
 
 // Four columns of one head's softmax in the making: maximum, exponential sum,
 // unnormalised values.
@@ -269,34 +301,21 @@ struct Partial {
 
     __device__ Partial() : m(-kInf), sum(0.f), acc(make_float4(0.f, 0.f, 0.f, 0.f)) {}
 
-    // Adds a shared prefix's pieces of the row, in the order of their tokens: its unit's part of
-    // every CTA that streamed some of the unit's tiles (PrefixPieces).
-    __device__ __forceinline__ void add_prefix(const PagedDecodeArgs &a, size_t row, int d) {
-        const PrefixPieces &f = a.prefix;
-        const int tiles = prefix_tiles(f);
-        if (tiles == 0) return;
-        const int b = (int)(row / a.num_heads), head = (int)(row - (size_t)b * a.num_heads);
-        const int kvh = head / a.group, r = b * a.group + head - kvh * a.group;
-        const int unit = kvh * f.units_per_head + r / f.unit_rows, in = r % f.unit_rows;
-        const long long chunk = prefix_chunk(f, tiles), w = (long long)unit * tiles;
-        const int c0 = range_of(w, chunk), c1 = range_of(w + tiles - 1, chunk);
-        // (the further parts of a CTA with a single tile are empty, and not written)
-        const int parts = chunk == 1 ? 1 : f.parts, n = (c1 - c0 + 1) * parts;
-        const size_t size = (size_t)f.stride * (a.head_dim + 2) * (chunk == 1 ? f.parts : 1);
-        const float *at = f.pieces + (size_t)(c0 + unit) * f.parts * f.stride * (a.head_dim + 2);
-        const float *x_at = at + (size_t)in * a.head_dim + d;
-        const float *m_at = at + (size_t)f.stride * a.head_dim + 2 * in;
+    // Adds pieces from, from + step, ... of a list, kFlight of them in flight together.
+    template <typename F> __device__ __forceinline__ void add_list(int from, int n, int step, F at) {
         constexpr int kFlight = 8;
-        for (int i = 0; i < n; i += kFlight) {
+        for (int i0 = from; i0 < n; i0 += kFlight * step) {
             float4 x[kFlight];
             float2 ms[kFlight];
 #pragma unroll
-            for (int k = 0; k < kFlight; ++k) {
-                x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                ms[k] = make_float2(-kInf, 0.f);
-                if (i + k < n) {
-                    x[k] = __ldcg(reinterpret_cast<const float4 *>(x_at + (i + k) * size));
-                    ms[k] = __ldcg(reinterpret_cast<const float2 *>(m_at + (i + k) * size));
+            for (int f = 0; f < kFlight; ++f) {
+                const int i = i0 + f * step;
+                x[f] = make_float4(0.f, 0.f, 0.f, 0.f);
+                ms[f] = make_float2(-kInf, 0.f);
+                if (i < n) {
+                    const PieceRow p = at(i);
+                    x[f] = __ldcg(reinterpret_cast<const float4 *>(p.x));
+                    ms[f] = __ldcg(reinterpret_cast<const float2 *>(p.m));
                 }
             }
             add<kFlight>(ms, x);
@@ -327,7 +346,10 @@ struct Partial {
     // Writes columns d .. d + 3 of the output's row (and its lse).
     template <typename T, Kv KV>
     __device__ __forceinline__ void write(const PagedDecodeArgs &a, size_t row, int d) {
-        if constexpr (KV == Kv::kBehind) add_prefix(a, row, d);
+        if constexpr (KV == Kv::kBehind) {
+            const PrefixRow f(a, row, d);
+            add_list(0, f.n, 1, [&](int i) { return f.piece(i); });
+        }
         const float r = m == -kInf ? 0.f : 1.f / sum;  // no token; a sum of 0 gives NaN
         T *o = static_cast<T *>(a.out) + row * a.head_dim + d;
         if constexpr (sizeof(T) == 2)
@@ -341,8 +363,9 @@ struct Partial {
 
 // Dependent launches: the lengths, the table and the cache may have been written by the kernel
 // before.  Behind a shared prefix that kernel is the prefix's, which lets this one be scheduled only once
-// it has itself waited for whatever wrote them: only its pieces are still to come, and every CTA waits for those
-// before its first row (and before its end, so that the kernel behind this one finds them too).
+// it has itself waited for whatever wrote them: only its pieces are still to come, and what reads
+// those waits for them (in the cluster kernel every CTA before its rows; the split kernel does not read
+// them, but its last CTA waits, so that whoever waits for this kernel has waited for the prefix's too).
 template <Kv KV> __device__ __forceinline__ void wait_before_reads() {
     if constexpr (KV != Kv::kBehind) ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
@@ -351,22 +374,17 @@ template <Kv KV> __device__ __forceinline__ void wait_before_rows() {
     if constexpr (KV == Kv::kBehind) ptx::grid_dependency_wait();
 }
 
-// Zeros (or the prefix's sums) for the requests without tokens, which are nobody's tiles.
-template <typename T, Kv KV>
+// Zeros for the requests without tokens, which are nobody's tiles.
+template <typename T>
 __device__ __forceinline__ void write_empty(const PagedDecodeArgs &a) {
     const int row = a.num_heads * a.head_dim;
     for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
-        if (request_len<KV>(a, b) != 0) continue;
-        if constexpr (KV == Kv::kBehind) {
-            for (int i = threadIdx.x * 4; i < row; i += blockDim.x * 4)
-                Partial().write<T, KV>(a, (size_t)b * a.num_heads + i / a.head_dim, i % a.head_dim);
-        } else {
-            for (int i = threadIdx.x; i < row; i += blockDim.x)
-                static_cast<T *>(a.out)[(size_t)b * row + i] = T(0.f);
-            if (a.lse)
-                for (int i = threadIdx.x; i < a.num_heads; i += blockDim.x)
-                    a.lse[(size_t)b * a.num_heads + i] = -kInf;
-        }
+        if (own_len(a, b) != 0) continue;
+        for (int i = threadIdx.x; i < row; i += blockDim.x)
+            static_cast<T *>(a.out)[(size_t)b * row + i] = T(0.f);
+        if (a.lse)
+            for (int i = threadIdx.x; i < a.num_heads; i += blockDim.x)
+                a.lse[(size_t)b * a.num_heads + i] = -kInf;
     }
 }
 
@@ -1022,13 +1040,18 @@ paged_split_kernel(const __grid_constant__ PagedDecodeArgs a) {
         Core::stream(a, smem, b, kvh, head0, heads, tile0 * kTile, min(len, tile1 * kTile));
         __syncthreads();
         const bool whole = tile0 == 0 && tile1 == tiles;
-        if (whole) wait_before_rows<Core::KV>();
         float *ws = piece_at<D>(a, blockIdx.x, first, ROWS);
         for (int i = threadIdx.x; i < heads * (D / 4); i += Core::kThreads) {
             const int h = i / (D / 4), d = (i % (D / 4)) * 4;
             Partial p = warps_sum<Core>(smem, h, d);
             if (whole) {
-                p.write<typename Core::T, Core::KV>(a, (size_t)b * a.num_heads + head0 + h, d);
+                const size_t row = (size_t)b * a.num_heads + head0 + h;
+                if constexpr (Core::KV == Kv::kBehind) {  // the join adds the prefix
+                    *reinterpret_cast<float4 *>(a.prefix.own + row * D + d) = p.acc;
+                    if (d == 0) *reinterpret_cast<float2 *>(a.prefix.own_stat + 2 * row) = make_float2(p.m, p.sum);
+                } else {
+                    p.write<typename Core::T, Core::KV>(a, row, d);
+                }
             } else {
                 *reinterpret_cast<float4 *>(ws + h * D + d) = p.acc;
                 if (d == 0) *reinterpret_cast<float2 *>(ws + ROWS * D + 2 * h) = make_float2(p.m, p.sum);
@@ -1037,8 +1060,10 @@ paged_split_kernel(const __grid_constant__ PagedDecodeArgs a) {
         __syncthreads();  // shared memory is the ring again
         first = false;
     }
-    wait_before_rows<Core::KV>();
-    write_empty<typename Core::T, Core::KV>(a);
+    if constexpr (Core::KV != Kv::kBehind)
+        write_empty<typename Core::T>(a);
+    else if (blockIdx.x == gridDim.x - 1)
+        ptx::grid_dependency_wait();  // this kernel ends behind the prefix's
 }
 
 // ---------------------------------------------------------- cluster kernel
@@ -1208,6 +1233,87 @@ paged_join_kernel(const __grid_constant__ PagedDecodeArgs a) {
     p.write<T, KV>(a, (size_t)at.b * a.num_heads + head0 + h, d);
 }
 
+// Behind a shared prefix: a block takes `heads_per_block` heads of a unit, with or without own tokens, and adds
+// the own pieces of the unit (or the sums of one that a CTA held whole) and the prefix's, a slice of
+// threads every slices-th of them.
+constexpr int kBehindJoin = 256;
+
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(kBehindJoin)
+paged_behind_join_kernel(const __grid_constant__ PagedDecodeArgs a, int heads_per_block) {
+    constexpr int kOver = kOverhead<T, D>;
+    __shared__ float4 part[kBehindJoin];
+    __shared__ float2 stat[kBehindJoin];
+    __shared__ long long costs[2][kBehindJoin / 32];
+    const int units = a.num_kv_heads * a.head_groups;
+    const int blocks = (min(ROWS, a.group) + heads_per_block - 1) / heads_per_block;  // of a unit
+    const int hb = blockIdx.x % blocks, u = blockIdx.x / blocks, unit = u % units, b = u / units;
+    const int kvh = unit / a.head_groups, hg = unit % a.head_groups;
+    const int head0 = kvh * a.group + hg * ROWS + hb * heads_per_block;
+    const int n = min(heads_per_block, min(ROWS, a.group - hg * ROWS) - hb * heads_per_block);
+    // costs of the requests before b, and of all; the lengths were complete before the kernel in front
+    // let this one be scheduled
+    const int len = request_len<Kv::kBehind>(a, b);
+    long long below = 0, all = 0;
+    for (int i = threadIdx.x; i < a.batch; i += kBehindJoin) {
+        const int c = unit_cost<kOver>(request_len<Kv::kBehind>(a, i));
+        all += c;
+        if (i < b) below += c;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        below += __shfl_xor_sync(0xffffffffu, below, o);
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+    }
+    if ((threadIdx.x & 31) == 0) {
+        costs[0][threadIdx.x >> 5] = below;
+        costs[1][threadIdx.x >> 5] = all;
+    }
+    __syncthreads();
+    below = all = 0;
+#pragma unroll
+    for (int w = 0; w < kBehindJoin / 32; ++w) {
+        below += costs[0][w];
+        all += costs[1][w];
+    }
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    if (n <= 0) return;  // (the last unit of a head may have fewer rows)
+    const long long chunk = max((all * units + kPagedCtas - 1) / kPagedCtas, 1LL);
+    const int cost = unit_cost<kOver>(len);
+    const long long u0 = below * units + (long long)unit * cost;
+    const int c0 = range_of(u0 + kOver, chunk), c1 = range_of(u0 + max(cost, 1) - 1, chunk);
+    const bool starts = c0 * chunk >= u0;  // CTA c0's range begins with the unit
+    const int own = len > 0 ? c1 - c0 + 1 : 0;
+
+    const int cols = n * (D / 4);  // at most kBehindJoin
+    const int slices = kBehindJoin / cols;
+    const int slice = threadIdx.x / cols, col = threadIdx.x - slice * cols;
+    const int h = col / (D / 4), d = (col % (D / 4)) * 4;
+    const size_t row = (size_t)b * a.num_heads + head0 + h;
+    Partial p;
+    if (slice < slices) {
+        const PrefixRow f(a, row, d);
+        p.add_list(slice, own + f.n, slices, [&](int i) -> PieceRow {
+            if (i >= own) return f.piece(i - own);
+            if (own == 1) return {a.prefix.own + row * D + d, a.prefix.own_stat + 2 * row};
+            const int r = hb * heads_per_block + h;
+            const float *at = piece_at<D>(a, c0 + i, i > 0 || starts, ROWS);
+            return {at + r * D + d, at + ROWS * D + 2 * r};
+        });
+    }
+    part[threadIdx.x] = p.acc;
+    stat[threadIdx.x] = make_float2(p.m, p.sum);
+    __syncthreads();
+    if (slice > 0) return;
+    for (int i = 1; i < slices; ++i) {
+        const float2 ms[1] = {stat[threadIdx.x + i * cols]};
+        const float4 x[1] = {part[threadIdx.x + i * cols]};
+        p.add<1>(ms, x);
+    }
+    p.write<T, Kv::kOwn>(a, row, d);
+}
+
 // Opts a kernel into its dynamic shared memory, once per device (concurrent first
 // calls may both do it, which is harmless).
 template <auto Kern> cudaError_t allow_smem(int smem) {
@@ -1251,30 +1357,47 @@ template <typename Core, int S> cudaError_t launch_cluster(const PagedDecodeArgs
 constexpr int kClusterTiles = 8;
 constexpr int kClusterWaves = 4;
 
-template <typename Core> cudaError_t launch(PagedDecodeArgs a) {
-    a.head_groups = (a.group + Core::ROWS - 1) / Core::ROWS;
+// CTAs of a unit's cluster, 0: the split kernel.
+template <typename Core> int cluster_size(const PagedDecodeArgs &a) {
     // What the table can hold bounds the lengths, which only the GPU knows.
-    const long units = (long)a.batch * a.num_kv_heads * a.head_groups;
+    const long units = (long)a.batch * a.num_kv_heads * ((a.group + Core::ROWS - 1) / Core::ROWS);
     const int most = Core::KV == Kv::kChosen ? min(a.max_tokens, a.chosen_count * a.page_size) : a.max_tokens;
     const int tiles = (most + kTile - 1) / kTile;
     int size = 8;
     while (size > 1 && (size > tiles || units * size > kPagedCtas)) size >>= 1;
-    if (tiles <= kClusterTiles * size && units * size <= kClusterWaves * kPagedCtas) {
-        switch (size) {
-            case 1: return launch_cluster<Core, 1>(a);
-            case 2: return launch_cluster<Core, 2>(a);
-            case 4: return launch_cluster<Core, 4>(a);
-            default: return launch_cluster<Core, 8>(a);
-        }
+    return tiles <= kClusterTiles * size && units * size <= kClusterWaves * kPagedCtas ? size : 0;
+}
+
+template <typename Core> cudaError_t launch(PagedDecodeArgs a) {
+    a.head_groups = (a.group + Core::ROWS - 1) / Core::ROWS;
+    switch (cluster_size<Core>(a)) {
+        case 0: break;
+        case 1: return launch_cluster<Core, 1>(a);
+        case 2: return launch_cluster<Core, 2>(a);
+        case 4: return launch_cluster<Core, 4>(a);
+        default: return launch_cluster<Core, 8>(a);
     }
 
+    using T = typename Core::T;
+    constexpr int D = Core::D, ROWS = Core::ROWS;
     constexpr auto kern = paged_split_kernel<Core>;
     cudaError_t e = allow_smem<kern>(Core::kSmem);
     if (e == cudaSuccess)
         e = launch_dependent(kern, kPagedCtas, Core::kThreads, Core::kSmem, a.stream, a);
-    if (e == cudaSuccess)
-        e = launch_dependent(paged_join_kernel<Core::KV, typename Core::T, Core::D, Core::ROWS>, kPagedCtas - 1,
-                             kJoinThreads<Core::D, Core::ROWS>, 0, a.stream, a);
+    if (e != cudaSuccess) return e;
+    if constexpr (Core::KV == Kv::kBehind) {
+        // one head a block (most slices a row) while that fills the GPU no more than a few times
+        const long units = (long)a.batch * a.num_kv_heads * a.head_groups;
+        const int rows = min(ROWS, a.group);
+        int heads = 1;
+        while (heads < 1024 / D && heads < rows && units * ((rows + heads - 1) / heads) > 8 * kPagedCtas) heads *= 2;
+        const long blocks = units * ((rows + heads - 1) / heads);
+        if (blocks > 0x7fffffffL) return cudaErrorInvalidConfiguration;
+        e = launch_dependent(paged_behind_join_kernel<T, D, ROWS>, (unsigned)blocks, kBehindJoin, 0, a.stream, a, heads);
+    } else {
+        e = launch_dependent(paged_join_kernel<Core::KV, T, D, ROWS>, kPagedCtas - 1, kJoinThreads<D, ROWS>, 0,
+                             a.stream, a);
+    }
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -5,7 +5,7 @@
 //     out = (e^(m' - m) A' + e^(m'' - m) A'') / (e^(m' - m) l' + e^(m'' - m) l''),   m = max(m', m''),
 // from the maximum, exponential sum and weighted sum of either part.  A first kernel leaves those
 // of the prefix for all query heads; the kernels over the requests' own tokens (paged_attention.cuh)
-// add them where they write a row.
+// add them where they write a row, or leave theirs for a join of both.
 //
 // Split.  The query heads of all requests that share a key-value head are its rows; a unit is
 // some of them.  The tiles of all units, one unit after the other, are cut into equal ranges for
@@ -28,7 +28,8 @@ paged_prefix_kernel(const __grid_constant__ PagedDecodeArgs a) {
     const int len = min(max(__ldcg(f.len), 0), f.max_tokens);
     const int tiles = prefix_tiles(f);
     if (tiles == 0) return;
-    const long long chunk = prefix_chunk(f, tiles);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *f.ranges = f.ctas;
+    const long long chunk = prefix_chunk(f, tiles, f.ctas);
     long long w0 = blockIdx.x * chunk;
     const long long w1 = min(w0 + chunk, (long long)f.units * tiles);
     while (w0 < w1) {
@@ -61,10 +62,17 @@ template <typename Core> cudaError_t launch_prefix(const PagedDecodeArgs &a) {
 template <int D> cudaError_t run(const PagedDecodeArgs &a, const int32_t *prefix_table, bool bf16) {
     PagedDecodeArgs p = a;
     p.block_table = prefix_table;
-    const cudaError_t e = bf16                        ? paged_prefix_tc(p)
-                          : a.prefix.unit_rows == 4 ? launch_prefix<F32Core<Kv::kPrefix, D, 4>>(p)
-                          : a.prefix.unit_rows == 8 ? launch_prefix<F32Core<Kv::kPrefix, D, 8>>(p)
-                                                    : launch_prefix<F32Core<Kv::kPrefix, D, 16>>(p);
+    cudaError_t e;
+    if (bf16) {
+        // the split kernel runs beside the prefix's, the cluster kernel's CTAs would wait on their SMs
+        p.prefix.share = (a.group <= 8 ? cluster_size<Bf16Core<Kv::kBehind, D, 1, false>>(a)
+                                       : cluster_size<Bf16Core<Kv::kBehind, D, 2, false>>(a)) == 0;
+        e = paged_prefix_tc(p);
+    } else {
+        e = a.prefix.unit_rows == 4   ? launch_prefix<F32Core<Kv::kPrefix, D, 4>>(p)
+            : a.prefix.unit_rows == 8 ? launch_prefix<F32Core<Kv::kPrefix, D, 8>>(p)
+                                      : launch_prefix<F32Core<Kv::kPrefix, D, 16>>(p);
+    }
     return e != cudaSuccess ? e : dispatch<Kv::kBehind, D>(a, bf16);
 }
 
