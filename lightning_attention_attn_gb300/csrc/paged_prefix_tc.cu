@@ -90,6 +90,13 @@ template <int D> struct TcSizes {
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, kTimeoutNs));
 }
+// Whether the phase is complete, without a wait.
+__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
 // The same for the warps that hold rows, without a call: their registers would have to be stored for it.
 __device__ __forceinline__ bool row_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
     bool ok = mbar_try_wait(bar, parity);
@@ -537,12 +544,10 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
         __syncwarp();
         bool ok = first >= total || start(first);
         for (int t = first; ok && t < total; t += step) {
-            // P V of the tile and the group's next S go out together where nothing is to be waited for
             const int at = t % kTiles, next = (t + step) % kTiles;
-            const bool more = t + step < total, follows = more && !is_fresh(t + step);
+            const bool more = t + step < total, same = more && !is_fresh(t + step);
             const uint64_t dv = sdesc_sw128(ring(2 * at + 1), kAtoms, 0), dk = sdesc_sw128(ring(2 * next), 16, 1024);
             const uint32_t empty = bar(cs.empty[at]);
-            ok = !follows || wait_tile(t + step);
             while (ok) {
                 ok = warp_wait(p_ready, weights++ & 1, abort_flag);
                 if (!ok || !*const_cast<volatile int *>(&cs.redo[x])) break;
@@ -554,6 +559,11 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
                 __syncwarp();
             }
             if (!ok) break;
+            // P V of the tile and the group's next S go out together where nothing is to be waited for.  (Where the
+            // groups do not share the tiles, the next one comes into the place of the one before this, which has
+            // been used up only now that its X is taken: not before, the barrier could not tell the two.)
+            const bool follows =
+                same && __all_sync(0xffffffffu, test_wait(bar(cs.full[next]), ((t + step) / kTiles) & 1));
             tc_fence_after();
             if (elect_one()) {
                 issue_x(dv, empty);
