@@ -15,8 +15,8 @@
 // key-value head, or 16 query heads of one).  The tiles of all units, one after the
 // other, are divided evenly (but for the cost of starting a unit) among a fixed
 // number of CTAs, whatever the lengths are: no host copy of the lengths, no plan, the
-// same launch for one long request and for many ragged ones.  A unit that lies inside one CTA's range is finished
-// there; a piece of a unit leaves its unnormalised sums, maxima and
+// same launch for one long request and for many ragged ones.  A unit that lies inside one
+// CTA's range is finished there; a piece of a unit leaves its unnormalised sums, maxima and
 // exponential sums in the workspace (a CTA has at most two such pieces: the
 // end of one unit and the start of another), and a second kernel joins the
 // pieces of each unit in the order of their tokens.  Where the table bounds the
@@ -1393,7 +1393,8 @@ template <typename Core> cudaError_t launch(PagedDecodeArgs a) {
         while (heads < 1024 / D && heads < rows && units * ((rows + heads - 1) / heads) > 8 * kPagedCtas) heads *= 2;
         const long blocks = units * ((rows + heads - 1) / heads);
         if (blocks > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-        e = launch_dependent(paged_behind_join_kernel<T, D, ROWS>, (unsigned)blocks, kBehindJoin, 0, a.stream, a, heads);
+        e = launch_dependent(paged_behind_join_kernel<T, D, ROWS>, (unsigned)blocks, kBehindJoin, 0,
+                             a.stream, a, heads);
     } else {
         e = launch_dependent(paged_join_kernel<Core::KV, T, D, ROWS>, kPagedCtas - 1, kJoinThreads<D, ROWS>, 0,
                              a.stream, a);

@@ -1,15 +1,22 @@
 // The attention over a shared prefix on the tensor cores (tcgen05 + TMEM), bf16: for the query
 // heads of all requests that share a key-value head (its rows), tile by tile of 128 tokens,
 //     S = Q K^T,   P = e^(scale S - m),   X = P V,   o <- o f + X,   l <- l f + sum P
-// with the running maximum m of each row and f = e^(m before - m).  A CTA leaves m, l and the
+// with a base m of each row near its running maximum and f = e^(m before - m).  A CTA leaves m, l and the
 // unnormalised o of its part of a unit (PrefixPieces); see paged_prefix.cu for the split.
 //
-// Bound: a row does 4 D flops a token, so with many rows the tensor core bounds the kernel, with few
-// (and K and V read once for all of them) HBM.
+// Bound: a row does 4 D flops a token, so with many rows the tensor core bounds the kernel, with few (and
+// K and V read once for all of them) HBM.  Measured, 8 key-value heads of 128, 64 query heads: 32
+// requests behind 64K tokens 110 us with all that follows (0.62 PFLOP/s of the formula's products, 0.93
+// of those that are done; the tensor pipe is busy 52 % of this kernel's cycles), 16 requests behind 128K
+// 129 us (4.2 TB/s), one 109 us (4.9 TB/s).  What bounds it then is the chain of a group's tile, about
+// 5000 cycles by cycle stamps: P V and the next S (1536 on the tensor core), the weights, and 500 to 800
+// from each of them to the threads that wait for it; two chains in turn keep the tensor core busy for
+// 3072 of the 5000.  Half the exponentials moved to FMAs, or none of the low parts, change the time by 0
+// to 4 %.  A third group finds no room in tensor memory.
 //
 // P is passed as two bf16 parts (parts_of: off by at most 2^-16 of each weight, as in the attention
 // of one request), which makes P V two products instead of one: 1536 tensor cycles a 128 x 128
-// tile instead of 1024.  One part would double the error that the output's own rounding leaves.
+// tile instead of 1024.  One part would add as much error again as the output's own rounding.
 // X is taken anew for every tile and added to o in registers: rounded to nearest, where the tensor
 // core's own accumulation over a long prefix drops the bits that do not fit, and a maximum
 // that moves costs a product in registers instead of a pass through tensor memory.
@@ -19,12 +26,13 @@
 // exponentials.  Where a key-value head has no more than 128 rows, both groups have the same
 // rows and every other tile each, and leave a part each.
 //
-// TMEM (512 columns): S of A and B 128 columns each, X 128, Q of A and B 64 each.  P takes the place of S:
-// 8 tokens' scores are 8 columns, their weights 4 columns of high and 4 of low parts, which together are one
-// K step of 16; its operand V is the 8 tokens' rows twice (a stride of 0 between groups of 8 rows).  Q is there because a
-// 128 x 128 product of two operands in shared memory runs at half the rate (1024 cycles for S instead
-// of 512); the room for it comes from X, which the two groups share: a group takes its X to registers
-// while its own next S runs, before the other group's P V needs the place.
+// TMEM (512 columns): S of A and B 128 columns each, X 128, Q of A and B 64 each.  P takes the place of
+// S: 8 tokens' scores are 8 columns, their weights 4 columns of high and 4 of low parts, which together
+// are one K step of 16; its operand V is the 8 tokens' rows twice (a stride of 0 between groups of 8
+// rows).  Q is there because a 128 x 128 product of two operands in shared memory was issued at half the
+// rate (about 1100 cycles for S instead of 512); the room for it comes from X, which the two groups
+// share: a group takes its X to registers while its own next S runs, before the other group's P V needs
+// the place.
 //
 // Warp roles (640 threads):
 //   warps 0-7    rows of A: two threads a row, each with 64 of a tile's tokens and half of
@@ -64,7 +72,8 @@ constexpr int kRing = 2 * kTiles;     // their K and V
 constexpr uint32_t kAtoms = kTokens * 128;  // 128 rows of 64 bf16
 // Weights are taken against a base that may lie below the row's maximum: the maximum of the tiles
 // before, so that a tile's weights need not wait for its own.  Weights of up to 2^kRedo lose nothing in
-// floating point; a tile whose maximum is further above is taken again (S once more, then its maximum first).
+// floating point (but sums of values near the type's largest reach it 2^kRedo earlier); a tile whose maximum is
+// further above is taken again (S once more, then its maximum first).
 // A base that is kMove below is moved after the tile.  (log2)
 constexpr float kRedo = 8.f, kMove = 4.f;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
@@ -141,7 +150,8 @@ __device__ __forceinline__ void weights_of(float (&v)[8], float scale, float bas
     uint32_t lo[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 t = f2_fma(make_float2(v[2 * i], v[2 * i + 1]), make_float2(scale, scale), make_float2(base, base));
+        const float2 t = f2_fma(make_float2(v[2 * i], v[2 * i + 1]), make_float2(scale, scale),
+                                make_float2(base, base));
         const float2 p = make_float2(ex2(t.x), ex2(t.y));
         l = f2_add(l, p);
         const uint32_t x = __float_as_uint(p.x), y = __float_as_uint(p.y);
@@ -179,7 +189,9 @@ struct Walk {
 };
 
 // SMs for the prefix where the own tokens' split kernel can run on the others meanwhile: the number for which
-// both are done first.  A tile takes an SM about kTileUs (two where the groups share it); own bytes
+// both are done first.  128 requests of 1 to 2048 own tokens behind 8K: 48, 64, 72, 80, 96, 112 and all 152
+// SMs give 173, 158, 162, 171, 165, 163 and 174 us (the own kernel's 304 ranges go in waves of what
+// is free); the rule's choice 159.  A tile takes an SM about kTileUs (two where the groups share it); own bytes
 // stream at kHbm, from fewer than kFullSms SMs at that share of it, from all once the prefix is done.
 constexpr float kTileUs = 1.5f, kHbm = 6.7e6f /* bytes a us */, kFullSms = 110.f;
 
@@ -391,12 +403,14 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
                     if (ok) ok = row_wait(bar(cs.s_full[x]), steps & 1, abort_flag);
                     ++steps;
                     tc_fence_after();
-                    const uint4 mask = *reinterpret_cast<const uint4 *>(cs.have[(kShared ? walk.at + j : 2 * (int)tiles + x) % kTiles]);
+                    const int at = (kShared ? walk.at + j : 2 * (int)tiles + x) % kTiles;
+                    const uint4 mask = *reinterpret_cast<const uint4 *>(cs.have[at]);
                     if (ok && (mask.x & mask.y & mask.z & mask.w) != 0xffffffffu) {
                         // tokens that are not there: S is -infinity
 #pragma unroll 1
                         for (int c = 0; c < 64; c += 16) {
-                            const uint32_t here = (half ? c & 32 ? mask.w : mask.z : c & 32 ? mask.y : mask.x) >> (c & 16);
+                            const uint32_t word = half ? c & 32 ? mask.w : mask.z : c & 32 ? mask.y : mask.x;
+                            const uint32_t here = word >> (c & 16);
                             float v[16];
                             tmem_ld16(ts + c, v);
                             tmem_wait_ld();
@@ -747,8 +761,8 @@ template <int D, bool kShared> cudaError_t launch_tc(const PagedDecodeArgs &a) {
     int box = a.page_size & -a.page_size;
     box = box > kTokens ? kTokens : box;
     CUtensorMap map_k = {}, map_v = {};
-    if (box < 8 || a.num_pages == 0 || (int64_t)a.num_kv_heads * a.page_size > 0x7fffffffLL || !make_map(&map_k, a.k, a.k_page_stride, a, box) ||
-        !make_map(&map_v, a.v, a.v_page_stride, a, box))
+    if (box < 8 || a.num_pages == 0 || (int64_t)a.num_kv_heads * a.page_size > 0x7fffffffLL ||
+        !make_map(&map_k, a.k, a.k_page_stride, a, box) || !make_map(&map_v, a.v, a.v_page_stride, a, box))
         box = 0;
     cudaError_t e = allow_smem<kern>(smem);
     if (e == cudaSuccess)
