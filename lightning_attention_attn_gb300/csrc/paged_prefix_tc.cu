@@ -11,7 +11,7 @@
 // 129 us (4.2 TB/s), one 109 us (4.9 TB/s).  What bounds it then is the chain of a group's tile, about
 // 5000 cycles by cycle stamps: P V and the next S (1536 on the tensor core), the weights, and 500 to 800
 // from each of them to the threads that wait for it; two chains in turn keep the tensor core busy for
-// 3072 of the 5000.  Half the exponentials moved to FMAs, or none of the low parts, change the time by 0
+// three fifths of it.  Half the exponentials moved to FMAs, or none of the low parts, change the time by 0
 // to 4 %.  A third group finds no room in tensor memory.
 //
 // P is passed as two bf16 parts (parts_of: off by at most 2^-16 of each weight, as in the attention
