@@ -12,7 +12,8 @@
 // The choice is that of scores in 64 bits: two blocks whose scores differ by less than fp32 (or the
 // tensor core) resolves would otherwise be chosen by the order of the additions.  So the scores are
 // first taken in fp32 with a bound on their error, e = kSlack sum|q| max|bound| (the largest of the
-// heads and of the unit's pages), and with T the count-th largest of them
+// heads and of the unit's pages) + 2^-118 (2 D results of less than 2^-126, which are not off in proportion to
+// themselves), and with T the count-th largest of them
 //     s > T + 2 e  is chosen,   s < T - 2 e  is not,
 // whatever the true scores are; those in between (a few) are taken again in 64 bits and ranked, and of their
 // heads only those that fp32 cannot tell from the largest (the fp64 pipe does two lanes a cycle: all
@@ -705,7 +706,7 @@ paged_pick_kernel(const __grid_constant__ PagedSelectArgs a, const __grid_consta
     int turn = 1;  // the place for sums over the CTA that is free
     if (present > a.count) {
         int need = a.count - forced;  // of the others; at least 0
-        const float err = slack * s.most * s.norm;
+        const float err = fmaf(slack, s.most * s.norm, 0x1p-118f);
         const bool finite = err < 1e30f;  // false for NaN
         if (need == 0) {
             above = below = kKept - 1;

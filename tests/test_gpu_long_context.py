@@ -193,6 +193,20 @@ def test_select_cancelling_sums():
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("of_q, of_k", [(-70, -72), (-60, -60), (-74, -74), (0, -131), (-131, 0), (60, -138)])
+def test_select_tiny_numbers(dtype, of_q, of_k):
+    """Scores (or queries, or bounds) in and below the subnormal range of fp32, where an error is not
+    relative to its terms: exact in 64 bits, and so is the choice."""
+    g = gen(9)
+    page, n = 16, 300
+    bt, pages = tables([n] * 4, g)
+    bd = (some_bounds(pages, 2, 64, FP32, g).double() * 2.0 ** of_k).to(dtype)
+    q = (torch.randn((4, 6, 64), generator=g, device="cuda").double() * 2.0 ** of_q).to(dtype)
+    for count in (1, 20, 100):
+        check_select(q, bd, bt, ints([n * page] * 4), page, count, 0, 0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_select_infinities_nan_and_absent_pages(dtype):
     g = gen(9)
     d, page, n = 64, 16, 200
