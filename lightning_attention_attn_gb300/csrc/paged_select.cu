@@ -146,7 +146,7 @@ paged_bounds_kernel(const __grid_constant__ PagedBoundsArgs a, int splits) {
 // A unit is a request's key-value head.  `splits` warps share its blocks, 16 at a time; each leaves
 // the fp32 scores and its largest |bound|.  Units whose blocks are all chosen have no scores.
 // Bound: every bound is read once (G query heads do G flops a byte).  128 requests of 1K to 32K tokens, pages of
-// 64, 64 and 8 heads of 128: 47 us with the choice, this kernel two thirds of it (138 MB at 4.2 TB/s under a
+// 64, 64 and 8 heads of 128: 45 us with the choice, this kernel two thirds of it (138 MB at 4.2 TB/s under a
 // profiler: three dependent latencies before a warp's first bounds, and requests of 16 to 512 blocks).
 constexpr int kScoreWarps = 4;   // of a CTA, all of one unit
 constexpr int kScoreTile = 16;   // blocks of a warp's step
@@ -483,8 +483,8 @@ __device__ __forceinline__ int2 block_sum(PickSpace &s, int turn, int x, int y) 
 }
 
 // The rank-th largest (from 1) of the keys that key(i, k) gives for i < n, and how many of those
-// that equal it are among the rank largest.  Eight bits a pass.
-template <typename K, typename F>
+// that equal it are among the rank largest, of the bits from kLow up.  Eight bits a pass.
+template <int kLow, typename K, typename F>
 __device__ __forceinline__ K radix_pick(PickSpace &s, int n, int rank, int &equal, F key) {
     constexpr int kTop = sizeof(K) * 8 - 8;
     K prefix = 0;
@@ -492,7 +492,7 @@ __device__ __forceinline__ K radix_pick(PickSpace &s, int n, int rank, int &equa
     for (int i = threadIdx.x; i < 256; i += kPick) s.hist[i] = 0;
     __syncthreads();
 #pragma unroll 1
-    for (int shift = kTop; shift >= 0; shift -= 8) {
+    for (int shift = kTop; shift >= kLow; shift -= 8) {
         for (int i = threadIdx.x; i < n; i += kPick) {
             K k;
             if (key(i, k) && (shift == kTop || (k >> (shift + 8)) == (prefix >> (shift + 8))))
@@ -713,14 +713,14 @@ paged_pick_kernel(const __grid_constant__ PagedSelectArgs a, const __grid_consta
         } else {
             if (finite) {
                 int equal;
-                const uint32_t k = radix_pick<uint32_t>(s, blocks, need, equal, [&](int i, uint32_t &key) {
+                const uint32_t k = radix_pick<8, uint32_t>(s, blocks, need, equal, [&](int i, uint32_t &key) {
                     key = key_at(i);
                     return key != kAbsent && key != kKept;
                 });
-                // (2 e, and room for the rounding of these two sums: e is at least 2^-20 of |t|)
-                const float t = value_of(k);
-                above = key_of(t + 2.25f * err);
-                below = key_of(t - 2.25f * err);
+                // T to 2^-15 of itself, which is near enough to e that a fourth pass would not pay.  (2 e, and
+                // room for the rounding of these two sums: e is at least 2^-20 of |T|)
+                above = key_of(value_of(k | 255u) + 2.25f * err);
+                below = key_of(value_of(k) - 2.25f * err);
             } else {
                 above = kKept - 1;
                 below = kAbsent + 1;
@@ -773,7 +773,7 @@ paged_pick_kernel(const __grid_constant__ PagedSelectArgs a, const __grid_consta
                         }
                     __syncthreads();
                     int equal;
-                    const uint64_t k = radix_pick<uint64_t>(s, blocks, need, equal, [&](int i, uint64_t &key) {
+                    const uint64_t k = radix_pick<0, uint64_t>(s, blocks, need, equal, [&](int i, uint64_t &key) {
                         if (!in_band(i)) return false;
                         key = key_of(exact[i]);
                         return true;
