@@ -183,8 +183,8 @@ struct PrefixPieces {
     float *pieces = nullptr;
     // A row's sums [B * H][D] and statistics [B * H][2] over its own tokens where one CTA held them all.
     float *own = nullptr, *own_stat = nullptr;
-    // [1] ranges that the prefix's kernel has cut the tiles into: ctas, or fewer where that leaves SMs to the
-    // own tokens' stream (share).
+    // [2] ranges that the prefix's kernel has cut its tiles into: ctas, or fewer where that leaves SMs to the
+    // own tokens' split kernel (share); and the latter's.
     int *ranges = nullptr;
     bool share = false;
 };

@@ -68,6 +68,19 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool v
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
                  : "memory");
 }
+// The same, of what is read once: it leaves L2 before what is not (the attention of 128 requests of up to 2048 own
+// tokens beside a prefix of 8K, which each of four units reads: 144 -> 142 us, with other splits 160 -> 150).
+__device__ __forceinline__ uint64_t once_policy() {
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid, uint64_t policy) {
+    const int n = valid ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+                 "r"(n), "l"(policy)
+                 : "memory");
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -141,7 +154,7 @@ template <int OVERHEAD> __device__ __forceinline__ int unit_cost(int len) {
 }
 
 // Where CTA `cta`'s range begins.  The costs of all units, request by request,
-// are cut into ranges of `chunk`, CTA c taking [c chunk, (c + 1) chunk).
+// are cut into ranges of `chunk`, CTA c taking [c chunk, (c + 1) chunk): ranges(all) of them.
 struct Place {
     long long all, chunk, w;  // cost of all units, of a range, start of this one
     long long unit0;          // start of request b's units
@@ -150,8 +163,8 @@ struct Place {
 
 // Whole block (kThr threads): false where the CTA has no range.  The lengths are
 // read once for up to kThr requests.
-template <Kv KV, int kThr, int OVERHEAD>
-__device__ __forceinline__ bool find_place(const PagedDecodeArgs &a, int units, int cta, Place &p) {
+template <Kv KV, int kThr, int OVERHEAD, typename F>
+__device__ __forceinline__ bool find_place(const PagedDecodeArgs &a, int units, int cta, Place &p, F ranges) {
     constexpr int kW = kThr / 32;
     __shared__ long long sums[kW];
     __shared__ long long found[2];
@@ -188,7 +201,8 @@ __device__ __forceinline__ bool find_place(const PagedDecodeArgs &a, int units, 
         sum += total;
     }
     p.all = sum * units;
-    p.chunk = max((p.all + kPagedCtas - 1) / kPagedCtas, 1LL);
+    const int r = ranges(p.all);
+    p.chunk = max((p.all + r - 1) / r, 1LL);
     p.w = cta * p.chunk;
     if (p.w >= p.all) return false;
     long long base = 0;
@@ -254,6 +268,31 @@ __device__ __forceinline__ int prefix_tiles(const PrefixPieces &f) {
 }
 __device__ __forceinline__ long long prefix_chunk(const PrefixPieces &f, int tiles, int ranges) {
     return ((long long)f.units * tiles + ranges - 1) / ranges;
+}
+
+// SMs for the prefix on the tensor cores where the own tokens' split kernel can run on the others meanwhile
+// (and has as many ranges as those hold at once): the number for which both are done first, or all SMs, one
+// kernel behind the other, which costs kBehindUs more.  A tile takes an SM about kTileUs (two where the groups
+// share it), kBesideUs beside the other kernel; own tokens, `cost` tiles of them, stream at kHbm, from
+// fewer than kFullSms SMs at that share of it.  Measured, 64 and 8 heads of 128, for the rule's choice / the best
+// of ten numbers / all SMs: 128 requests of up to 2048 own tokens behind 8K 149 / 148 / 177 us, of up to
+// 8192 behind 2K 329 / 329 / 363, 64 of up to 2048 behind 32K 155 / 154 / 173, 256 of up to 1024 behind 4K
+// 163 / 158 / 178, 32 of up to 8192 behind 16K 141 / 130 / 165, 16 of up to 16K behind 128K 209 / 194 / 215.
+// With 304 ranges, in waves of what is free, the first takes 162.
+template <int D> constexpr float kTileUs = D == 128 ? 1.5f : 1.1f;
+template <int D> constexpr float kBesideUs = D == 128 ? 2.f : 1.4f;
+constexpr float kHbm = 6.7e6f /* bytes a us */, kFullSms = 110.f, kBehindUs = 20.f;
+
+// (Whole warps; a lane a number.)
+template <int D> __device__ __forceinline__ int ranges_beside(const PrefixPieces &f, int tiles, long long cost) {
+    const int lane = threadIdx.x & 31, n = f.ctas - 4 * lane;
+    const float work = (float)prefix_chunk(f, tiles, n) * (f.parts == 1 ? 2.f : 1.f);  // tiles of an SM
+    const float stream = (float)cost * (kTile * D * 4) / kHbm;
+    const float beside = stream / fminf(1.f, (f.ctas - n) / kFullSms);
+    const uint32_t us = __float_as_uint(lane ? fmaxf(work * kBesideUs<D>, beside)
+                                                  : work * kTileUs<D> + stream + kBehindUs);
+    const uint32_t least = __reduce_min_sync(0xffffffffu, us);
+    return f.ctas - 4 * (__ffs(__ballot_sync(0xffffffffu, us == least)) - 1);
 }
 
 // The range of `chunk` that place w is in: 32-bit where it fits.
@@ -538,6 +577,9 @@ struct Bf16Core {
         // r of a group: its offset inside a key (value) head's page, or -1.
         Finder<KV, kStages - 1> find(a, b, kvh);
         const int mine = t0 + (lane & 15);  // token of group 0
+        // the prefix's kernel runs beside this one and reads its keys and values again for every unit
+        uint64_t policy = 0;
+        if constexpr (KV == Kv::kBehind) policy = once_policy();
         // Issues the copies of one group; returns the mask of its present rows.
         auto issue = [&](int stage, int page, int row) -> uint32_t {
             if (page >= a.num_pages) page = -1;  // first use of the table's entry, a group after its load
@@ -552,8 +594,15 @@ struct Bf16Core {
                 const size_t in = ((size_t)kvh * a.page_size + rw) * D + cch * 8;
                 const size_t p = ok ? pg : 0;
                 const uint32_t off = r * kRow + ((cch ^ (r & 7)) << 4);
-                cp_async16(dk + off, static_cast<const __nv_bfloat16 *>(a.k) + p * a.k_page_stride + in, ok);
-                cp_async16(dv + off, static_cast<const __nv_bfloat16 *>(a.v) + p * a.v_page_stride + in, ok);
+                const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k) + p * a.k_page_stride + in;
+                const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + p * a.v_page_stride + in;
+                if constexpr (KV == Kv::kBehind) {
+                    cp_async16(dk + off, k, ok, policy);
+                    cp_async16(dv + off, v, ok, policy);
+                } else {
+                    cp_async16(dk + off, k, ok);
+                    cp_async16(dv + off, v, ok);
+                }
             }
             return have;
         };
@@ -1014,7 +1063,17 @@ paged_split_kernel(const __grid_constant__ PagedDecodeArgs a) {
     wait_before_reads<Core::KV>();
     const int units = a.num_kv_heads * a.head_groups;
     Place at;
-    const bool any = find_place<Core::KV, Core::kThreads, kOver>(a, units, blockIdx.x, at);
+    const bool any = find_place<Core::KV, Core::kThreads, kOver>(a, units, blockIdx.x, at, [&](long long all) {
+        int ranges = kPagedCtas;
+        if constexpr (Core::KV == Kv::kBehind) {
+            const PrefixPieces &f = a.prefix;
+            const int tiles = f.share ? prefix_tiles(f) : 0;
+            const int sms = tiles > 0 ? f.ctas - ranges_beside<D>(f, tiles, all) : 0;
+            if (sms > 0) ranges = 2 * sms;
+            if (blockIdx.x == 0 && threadIdx.x == 0) f.ranges[1] = ranges;
+        }
+        return ranges;
+    });
     long long w0 = any ? at.w : 0, unit0 = any ? at.unit0 : 0;
     const long long w1 = any ? min(at.all, w0 + at.chunk) : 0;
     int b = any ? at.b : 0;
@@ -1171,7 +1230,7 @@ paged_join_kernel(const __grid_constant__ PagedDecodeArgs a) {
     Place at;
     const int c = blockIdx.x + 1;
     constexpr int kOver = kOverhead<T, D>;
-    const bool any = find_place<KV, kJoin, kOver>(a, units, c, at);
+    const bool any = find_place<KV, kJoin, kOver>(a, units, c, at, [](long long) { return kPagedCtas; });
     int unit = 0, c0 = 0, c1 = 0;
     long long u0 = 0;
     if (any) {
@@ -1279,7 +1338,8 @@ paged_behind_join_kernel(const __grid_constant__ PagedDecodeArgs a, int heads_pe
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     if (n <= 0) return;  // (the last unit of a head may have fewer rows)
-    const long long chunk = max((all * units + kPagedCtas - 1) / kPagedCtas, 1LL);
+    const int ranges = __ldcg(a.prefix.ranges + 1);
+    const long long chunk = max((all * units + ranges - 1) / ranges, 1LL);
     const int cost = unit_cost<kOver>(len);
     const long long u0 = below * units + (long long)unit * cost;
     const int c0 = range_of(u0 + kOver, chunk), c1 = range_of(u0 + max(cost, 1) - 1, chunk);

@@ -61,14 +61,15 @@ template <typename Core> cudaError_t launch_prefix(const PagedDecodeArgs &a) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int D> cudaError_t run(const PagedDecodeArgs &a, const int32_t *prefix_table, bool bf16) {
+template <int D> cudaError_t run(PagedDecodeArgs a, const int32_t *prefix_table, bool bf16) {
+    // the split kernel runs beside the prefix's, the cluster kernel's CTAs would wait on their SMs
+    if (bf16)
+        a.prefix.share = (a.group <= 8 ? cluster_size<Bf16Core<Kv::kBehind, D, 1, false>>(a)
+                                       : cluster_size<Bf16Core<Kv::kBehind, D, 2, false>>(a)) == 0;
     PagedDecodeArgs p = a;
     p.block_table = prefix_table;
     cudaError_t e;
     if (bf16) {
-        // the split kernel runs beside the prefix's, the cluster kernel's CTAs would wait on their SMs
-        p.prefix.share = (a.group <= 8 ? cluster_size<Bf16Core<Kv::kBehind, D, 1, false>>(a)
-                                       : cluster_size<Bf16Core<Kv::kBehind, D, 2, false>>(a)) == 0;
         e = paged_prefix_tc(p);
     } else {
         e = a.prefix.unit_rows == 4   ? launch_prefix<F32Core<Kv::kPrefix, D, 4>>(p)

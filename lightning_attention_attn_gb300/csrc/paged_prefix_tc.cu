@@ -188,28 +188,6 @@ struct Walk {
     }
 };
 
-// SMs for the prefix where the own tokens' split kernel can run on the others meanwhile: the number for which
-// both are done first.  128 requests of 1 to 2048 own tokens behind 8K: 48, 64, 72, 80, 96, 112 and all 152
-// SMs give 173, 158, 162, 171, 165, 163 and 174 us (the own kernel's 304 ranges go in waves of what
-// is free); the rule's choice 159.  A tile takes an SM about kTileUs (two where the groups share it); own bytes
-// stream at kHbm, from fewer than kFullSms SMs at that share of it, from all once the prefix is done.
-constexpr float kTileUs = 1.5f, kHbm = 6.7e6f /* bytes a us */, kFullSms = 110.f;
-
-__device__ __forceinline__ int ranges_beside(const PrefixPieces &f, int tiles, float bytes) {
-    const float work = (float)f.units * tiles * (f.parts == 1 ? 2.f : 1.f) * kTileUs, stream = bytes / kHbm;
-    int best = f.ctas;
-    float least = work / best + stream;
-    for (int n = f.ctas - 8; n >= 40; n -= 8) {
-        const float first = work / n, rate = fminf(1.f, (f.ctas - n) / kFullSms);
-        const float all = first + fmaxf(stream - first * rate, 0.f);
-        if (all < least) {
-            least = all;
-            best = n;
-        }
-    }
-    return best;
-}
-
 // kShared: the two groups have rows of their own and share the tiles; otherwise they have the same
 // rows, A the CTA's tiles 0, 2, ... and B 1, 3, ...
 template <int D, bool kShared>
@@ -245,7 +223,8 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
     if (f.share) {
         __shared__ long long sums[kTcThreads / 32];
         long long own = 0;
-        for (int i = threadIdx.x; i < a.batch; i += kTcThreads) own += own_len(a, i);
+        for (int i = threadIdx.x; i < a.batch; i += kTcThreads)
+            own += unit_cost<kOverhead<__nv_bfloat16, D>>(own_len(a, i));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
         if (lane == 0) sums[warp] = own;
@@ -253,7 +232,8 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
         own = 0;
 #pragma unroll
         for (int i = 0; i < kTcThreads / 32; ++i) own += sums[i];
-        ranges = ranges_beside(f, walk.tiles, (float)own * a.num_kv_heads * (D * 4));
+        // (a request's units: its key-value heads, and up to 16 query heads of each)
+        ranges = ranges_beside<D>(f, walk.tiles, own * a.num_kv_heads * ((a.group + 15) / 16));
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) *f.ranges = ranges;
     if ((int)blockIdx.x >= ranges) return;

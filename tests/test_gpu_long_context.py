@@ -455,6 +455,25 @@ def test_prefix_parts_of_several_units(h, hk, batch, prefix, d):
     la.device_status()
 
 
+@pytest.mark.parametrize("h, hk, d", [(16, 2, 128), (12, 1, 64), (40, 1, 128), (8, 4, 64)])
+@pytest.mark.parametrize("prefix", [100, 3000, 30000])
+def test_prefix_beside_ragged_own_tokens(prefix, h, hk, d):
+    """Few and many SMs for the prefix beside own tokens of every length, in one call after another
+    over one workspace: whole requests, requests in many pieces, and none."""
+    g = gen(prefix + h)
+    lens = [(997 * i) % 600 if i % 5 else 0 for i in range(60)]
+    lens[7], lens[31] = 9000, 5000
+    kc, vc, pt, pl, bt, sl = behind(prefix, lens, 64, hk, d, BF16, g)
+    q = randn((60, h, d), BF16, g)
+    ws = torch.empty(la.paged_prefix_decode_workspace_bytes(60, h, hk, d), dtype=torch.uint8, device="cuda")
+    some = [0, 1, 7, 13, 31, 59]
+    for own in (sl, sl // 50, sl):  # (the second time the prefix gets nearly all SMs)
+        out = la.paged_prefix_decode(q, kc, vc, pt, pl, bt, own, workspace=ws)
+        parts = lref.Behind((c(kc), c(vc)), c(pt), c(pl), c(bt[some]), c(own[some]))
+        want, _, bound, _ = lref.over(c(q[some]), parts, d ** -0.5, tile=128)
+        ref.within(out[some], want, bound, ref.u_of(BF16), "out")
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_prefix_long_and_wide(dtype):
     """A prefix of many tiles a CTA, own tokens for the split over all CTAs, a table much wider
