@@ -13,10 +13,10 @@ namespace la {
 // while the kernel before it in the stream is finishing, and waits
 // (grid_dependency_wait) before its first global-memory access, so stream
 // order is kept for every memory effect.  Only kernels that begin with that
-// wait are launched this way (the join of the paged attention reads the lengths
-// before it, the attention behind a shared prefix all but the prefix's pieces, the choice of pages all
-// but the scores: the kernel in front of each lets it be scheduled only once it has
-// itself waited for whatever wrote them).
+// wait are launched this way, but for three that read some of the call's arguments before it: the join of the
+// paged attention the lengths, through L2, and, behind an acquire, the choice of pages all but the scores and the
+// attention behind a shared prefix all but the prefix's pieces.  The first kernel of each of these calls has
+// waited, in every CTA, for whatever wrote the arguments, and none of the others is scheduled before that.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_dependent(void (*kern)(KArgs...), unsigned grid, unsigned block,
                                     size_t smem, cudaStream_t stream, Args &&...args) {
@@ -183,8 +183,9 @@ struct PrefixPieces {
     float *pieces = nullptr;
     // A row's sums [B * H][D] and statistics [B * H][2] over its own tokens where one CTA held them all.
     float *own = nullptr, *own_stat = nullptr;
-    // [2] ranges that the prefix's kernel has cut its tiles into: ctas, or fewer where that leaves SMs to the
-    // own tokens' split kernel (share); and the latter's.
+    // [3] ranges that the prefix's kernel has cut its tiles into: ctas, or fewer where that leaves SMs to the
+    // own tokens' split kernel (share); the latter's; released by the prefix's kernel once it has waited for
+    // whatever wrote the call's arguments, acquired by the own tokens' (its value means nothing).
     int *ranges = nullptr;
     bool share = false;
 };

@@ -133,8 +133,9 @@ __device__ __forceinline__ Parts parts_of(float x, float y) {
 // ------------------------------------------------------------ work split
 // What the kernel before may have written (it can still be running when this one is
 // scheduled) is never read as constant data: the lengths, which the join reads before
-// its wait, through L2, the rest with plain loads behind the wait (a table entry serves
-// several groups: reading it through L2 each time cost 4 to 15 %).
+// its wait, through L2 (an SM's L1 may hold what an earlier call read at the same place), the rest with
+// plain loads behind the wait, or what stands for it (wait_before_reads).  (A table entry serves
+// several groups: reading it through L2 each time cost 4 to 15 %.)
 // Length of request b as the kernels use it: inside [0, table capacity].
 __device__ __forceinline__ int own_len(const PagedDecodeArgs &a, int b) {
     return min(max(__ldcg(a.seq_lens + b), 0), a.max_tokens);
@@ -401,12 +402,18 @@ struct Partial {
 };
 
 // Dependent launches: the lengths, the table and the cache may have been written by the kernel
-// before.  Behind a shared prefix that kernel is the prefix's, which lets this one be scheduled only once
-// it has itself waited for whatever wrote them: only its pieces are still to come, and what reads
+// before.  Behind a shared prefix that kernel is the prefix's, all of whose CTAs have waited for whatever wrote
+// them before this one is scheduled.  That orders the two but makes nothing visible here: for that the prefix's
+// kernel then releases f.ranges[2], and every thread here acquires it (which also lets go of L1's lines) in place of
+// a wait.  Only the prefix's pieces are still to come, and what reads
 // those waits for them (in the cluster kernel every CTA before its rows; the split kernel does not read
-// them, but its last CTA waits, so that whoever waits for this kernel has waited for the prefix's too).
-template <Kv KV> __device__ __forceinline__ void wait_before_reads() {
+// them, but its last CTA waits, so that whoever waits for this kernel has waited for the prefix's too).  The
+// join behind the split kernel reads the lengths before its wait, through L2: the split kernel has not waited,
+// but does not run before the prefix's has.  (128 requests of up to 2048 own tokens behind 8K: 142 us; with the
+// table through L2 in place of the acquire 154.)
+template <Kv KV> __device__ __forceinline__ void wait_before_reads(const PagedDecodeArgs &a) {
     if constexpr (KV != Kv::kBehind) ptx::grid_dependency_wait();
+    else ptx::load_acquire(a.prefix.ranges + 2);
     ptx::grid_launch_dependents();
 }
 template <Kv KV> __device__ __forceinline__ void wait_before_rows() {
@@ -1060,7 +1067,7 @@ paged_split_kernel(const __grid_constant__ PagedDecodeArgs a) {
     constexpr int kOver = kOverhead<typename Core::T, D>;
     extern __shared__ __align__(128) unsigned char smem[];
 
-    wait_before_reads<Core::KV>();
+    wait_before_reads<Core::KV>(a);
     const int units = a.num_kv_heads * a.head_groups;
     Place at;
     const bool any = find_place<Core::KV, Core::kThreads, kOver>(a, units, blockIdx.x, at, [&](long long all) {
@@ -1155,7 +1162,7 @@ __global__ void __launch_bounds__(Core::kThreads, 2)
 paged_cluster_kernel(const __grid_constant__ PagedDecodeArgs a) {
     constexpr int D = Core::D, ROWS = Core::ROWS;
     extern __shared__ __align__(128) unsigned char smem[];
-    wait_before_reads<Core::KV>();
+    wait_before_reads<Core::KV>(a);
 
     // a one-dimensional grid of one-dimensional clusters: the rank in the
     // cluster is the block's index modulo its size
@@ -1310,8 +1317,7 @@ paged_behind_join_kernel(const __grid_constant__ PagedDecodeArgs a, int heads_pe
     const int kvh = unit / a.head_groups, hg = unit % a.head_groups;
     const int head0 = kvh * a.group + hg * ROWS + hb * heads_per_block;
     const int n = min(heads_per_block, min(ROWS, a.group - hg * ROWS) - hb * heads_per_block);
-    // costs of the requests before b, and of all; the lengths were complete before the kernel in front
-    // let this one be scheduled
+    // costs of the requests before b, and of all (the lengths before the wait: wait_before_reads)
     const int len = request_len<Kv::kBehind>(a, b);
     long long below = 0, all = 0;
     for (int i = threadIdx.x; i < a.batch; i += kBehindJoin) {

@@ -154,7 +154,7 @@ constexpr int kScoreTile = 16;   // blocks of a warp's step
 struct SelectSpace {
     int splits;        // warps of a unit
     bool scored;       // some requests may have more blocks than are chosen
-    size_t exact, approx, most, bytes;  // offsets
+    size_t exact, approx, most, ready, bytes;  // offsets
 };
 
 SelectSpace select_space(int64_t units, int64_t width) {
@@ -168,7 +168,8 @@ SelectSpace select_space(int64_t units, int64_t width) {
     s.exact = 0;
     s.approx = (size_t)(units * width) * sizeof(double);
     s.most = s.approx + (size_t)(units * width) * sizeof(float);
-    s.bytes = s.most + (size_t)units * s.splits * sizeof(float);
+    s.ready = s.most + (size_t)units * s.splits * sizeof(float);
+    s.bytes = s.ready + sizeof(int);
     return s;
 }
 
@@ -420,6 +421,8 @@ template <typename S>
 __global__ void __launch_bounds__(kScoreWarps * 32, 4)
 paged_score_kernel(const __grid_constant__ PagedSelectArgs a, const __grid_constant__ SelectSpace w) {
     ptx::grid_dependency_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0)  // for the choice, which has no wait for what wrote the arguments
+        ptx::store_release(reinterpret_cast<int *>(static_cast<char *>(a.workspace) + w.ready), 1);
     ptx::grid_launch_dependents();
     const int ctas = w.splits / kScoreWarps;
     const int unit = blockIdx.x / ctas;
@@ -625,10 +628,17 @@ paged_pick_kernel(const __grid_constant__ PagedSelectArgs a, const __grid_consta
     const int unit = blockIdx.x, b = unit / a.num_kv_heads, kvh = unit - b * a.num_kv_heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) s.norm = s.most = 0.f;
-    // Behind the scores' kernel, which lets this one be scheduled only once it has itself waited for whatever
-    // wrote the lengths, the table, the queries and the bounds: only the scores are still to come.
-    if (w.scored) ptx::grid_launch_dependents();
-    else ptx::grid_dependency_wait();
+    // Behind the scores' kernel, all of whose CTAs have waited for whatever wrote the lengths, the table, the
+    // queries and the bounds before this one is scheduled.  That orders the two but makes nothing visible here: for
+    // that the scores' kernel then releases w.ready (its value means nothing), and every thread here acquires
+    // it (which also lets go of L1's lines).  Only the scores are still to come: what else is wanted is read before
+    // the wait for them.
+    if (w.scored) {
+        ptx::load_acquire(reinterpret_cast<const int *>(static_cast<char *>(a.workspace) + w.ready));
+        ptx::grid_launch_dependents();
+    } else {
+        ptx::grid_dependency_wait();
+    }
     const int blocks = unit_blocks(a, b);
     const int32_t *pages = a.block_table + (size_t)b * a.table_stride;
     int32_t *out = a.selected + (size_t)unit * a.count;

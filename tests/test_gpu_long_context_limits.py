@@ -1,0 +1,152 @@
+"""Long-context operators of the softmax layers at the limits of their contract: calls right behind what
+writes their arguments, lengths and values near the types' ends, paths of large calls alone."""
+import math
+
+import pytest
+import torch
+
+import long_context_reference as lref
+import softmax_reference as ref
+import lightning_attention_attn_gb300 as la
+from lightning_attention_attn_gb300 import build as labuild
+
+pytestmark = pytest.mark.gpu
+BF16, FP32 = torch.bfloat16, torch.float32
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    la.load(labuild.build())
+    yield
+    torch.cuda.synchronize()
+    la.device_status()
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(shape, dtype, g):
+    return torch.randn(shape, generator=g, device="cuda").to(dtype)
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def c(x):
+    return x.cpu()
+
+
+# ------------------------------- calls right behind what writes their arguments
+def same_behind_their_writers(loop):
+    """loop(wait) returns tensors; wait() stands between its kernels.  The same bits with a wait for the GPU
+    there, without one, and from a graph that is replayed (no host between two kernels)."""
+    want = [x.clone() for x in loop(torch.cuda.synchronize)]
+    for _ in range(5):
+        got = loop(lambda: None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = loop(lambda: None)
+    for _ in range(10):
+        for x in got:
+            x.fill_(3)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype, page, width, n", [(BF16, 16, 12, 130), (BF16, 64, 300, 9000), (FP32, 16, 12, 130),
+                                                   (FP32, 64, 160, 3000)])
+def test_arguments_that_the_kernel_in_front_has_written(dtype, page, width, n):
+    """Table, lengths and queries of the choice and of the attention behind a prefix, at one place each, with other
+    contents before every call (so that what an earlier call read there is stale), each of them
+    in turn the one written last.  Narrow tables (a cluster a unit) and wide ones (split and join)."""
+    g = gen(60)
+    b, hk, h, d, steps = 5, 2, 16, 128, 6
+    pages = 1200
+    kc, vc = (randn((pages, hk, page, d), dtype, g) for _ in range(2))
+    bd = torch.stack([kc.amin(2), kc.amax(2)], 2)
+    sets = []
+    for j in range(steps):
+        order = torch.randperm(pages, generator=g, device="cuda").int()
+        lens = torch.randint(0, n + 1, (b,), generator=g, device="cuda").int()
+        lens[j % b] = 0
+        sets.append(dict(bt=order[:b * width // 4].repeat(4).reshape(b, width), lens=lens, q=randn((b, h, d), dtype, g),
+                         pt=order[-40:].clone(), pl=ints([j * 100 + 37])))
+    live = {k: torch.zeros_like(v) for k, v in sets[0].items()}
+    names = list(live)
+
+    def loop(wait):
+        got = []
+        for j, s in enumerate(sets):
+            for call in range(2):
+                for k in names[j % 5:] + names[:j % 5]:
+                    live[k].copy_(s[k])
+                wait()
+                if call:
+                    out = la.paged_select(live["q"], bd, live["bt"], live["lens"], page, 5)
+                else:
+                    out = la.paged_prefix_decode(live["q"], kc, vc, live["pt"], live["pl"], live["bt"], live["lens"])
+                wait()
+                got.append(out)
+                for k in names:
+                    live[k].zero_()
+                wait()
+        return got
+
+    same_behind_their_writers(loop)
+
+
+@pytest.mark.parametrize("width", [40, 400])
+def test_right_behind_the_reservation_and_the_append(width):
+    """The choice and the attention behind a prefix with nothing between them and the reservation (table, lengths) or
+    the append (queries, cache); requests end and others take their place, on other pages."""
+    g = gen(61)
+    page, hk, h, d, b, pages = 16, 2, 16, 128, 6, 500
+    kc, vc = (randn((pages, hk, page, d), BF16, g) for _ in range(2))
+    bd = torch.stack([kc.amin(2), kc.amax(2)], 2)
+    order = torch.randperm(pages - 40, generator=g, device="cuda").int()
+    front, length = torch.arange(pages - 40, pages, dtype=torch.int32, device="cuda"), ints([630])
+    steps = [([400, 3, 600, 1, 17, 1], [0] * 6), ([1] * 6, [0] * 6), ([1, 30, 1, 200, 1, 1], [0, 1, 1, 0, 0, 0]),
+             ([1] * 6, [0] * 6), ([600, 1, 1, 1, 1, 5], [1, 0, 0, 1, 0, 1])]
+    steps = [(ints(n), torch.tensor(f, dtype=torch.bool, device="cuda"), sum(n)) for n, f in steps]
+    xs = [randn((b, h + 2 * hk, d), BF16, g) for _ in steps]
+    q, table = randn((b, h, d), BF16, g), la.rotary_table(1000, 64, device="cuda")
+    bt, lens, free, top = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in ((b, width), b, pages - 40, 1))
+    height, k, v, qo = ints([pages - 40]), kc.clone(), vc.clone(), torch.empty_like(q)
+    pos = ints([5, 900, 17, 0, 33, 64])
+    slots = [(order[-6:] * page + j).contiguous() for j in range(len(steps))]  # pages that are never reserved
+
+    def loop(wait):
+        got = []
+        bt.fill_(-1), lens.zero_(), free.copy_(order), top.copy_(height)
+        k.copy_(kc), v.copy_(vc)
+        wait()
+        top.sub_(6)
+        for (new, over, total), x, at in zip(steps, xs, slots):
+            la.paged_reserve(bt, lens, new, free, top, page, total, finished=over)
+            wait()
+            got.append(la.paged_prefix_decode(q, k, v, front, length, bt, lens))
+            wait()
+            la.paged_reserve(bt, lens, new, free, top, page, total)
+            wait()
+            got.append(la.paged_select(q, bd, bt, lens, page, 4))
+            wait()
+            la.paged_append(x[:, :h], x[:, h:h + hk], x[:, h + hk:], pos, table, k, v, at, q_out=qo)
+            wait()
+            got.append(la.paged_prefix_decode(qo, k, v, front, length, bt, lens))
+            wait()
+            la.paged_append(x[:, :h], x[:, h:h + hk], x[:, h + hk:], pos, table, k, v, at, q_out=qo)
+            wait()
+            got.append(la.paged_select(qo, bd, bt, lens, page, 4))
+            wait()
+            got += [bt.clone(), lens.clone()]
+        return got
+
+    same_behind_their_writers(loop)
