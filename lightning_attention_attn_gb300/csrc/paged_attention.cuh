@@ -140,12 +140,14 @@ __device__ __forceinline__ Parts parts_of(float x, float y) {
 __device__ __forceinline__ int own_len(const PagedDecodeArgs &a, int b) {
     return min(max(__ldcg(a.seq_lens + b), 0), a.max_tokens);
 }
+// Blocks of n tokens (n + page_size could pass 32 bits).
+__device__ __forceinline__ int blocks_of(int n, int page_size) { return n > 0 ? (n - 1) / page_size + 1 : 0; }
 // Tokens that the kernels pass for it: with chosen pages, those of its entries that count,
 // as if every page were full.
 template <Kv KV> __device__ __forceinline__ int request_len(const PagedDecodeArgs &a, int b) {
     const int n = own_len(a, b);
     if constexpr (KV == Kv::kChosen)
-        return min((n + a.page_size - 1) / a.page_size, a.chosen_count) * a.page_size;
+        return min(blocks_of(n, a.page_size), a.chosen_count) * a.page_size;
     return n;
 }
 // Cost of a unit of `len` tokens, in tiles: the overhead of starting it, then its
@@ -464,7 +466,7 @@ template <Kv KV> struct Tokens {
         if constexpr (KV == Kv::kChosen) {
             chosen = a.chosen + ((size_t)b * a.num_kv_heads + kvh) * a.chosen_count;
             len = own_len(a, b);
-            blocks = (len + a.page_size - 1) / a.page_size;
+            blocks = blocks_of(len, a.page_size);
         }
     }
     // The block and row of token t (-1: behind t1).

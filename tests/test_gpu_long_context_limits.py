@@ -150,3 +150,32 @@ def test_right_behind_the_reservation_and_the_append(width):
         return got
 
     same_behind_their_writers(loop)
+
+
+# ------------------------------------------------------------ lengths near 2^31
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("page, count", [(1 << 17, 3), (1 << 20, 40)])
+def test_chosen_pages_of_the_longest_table(dtype, page, count):
+    """A table that holds 2^31 tokens in pages of more than 2^16, most of them absent, and lengths
+    that are clamped to what it holds: blocks are counted without passing 32 bits."""
+    g = gen(62)
+    width, hk, h, d = (1 << 31) // page, 1, 2, 64
+    kc, vc = (torch.zeros((2, hk, page, d), dtype=dtype, device="cuda") for _ in range(2))
+    for x in (kc, vc):
+        x[:, :, :300] = randn((2, hk, 300, d), dtype, g)
+        x[:, :, 300:] = NAN
+    bt = torch.full((3, width), -1, dtype=torch.int32, device="cuda")
+    lens = ints([2 ** 31 - 1, 0, 300])
+    bt[0, 5], bt[2, 0] = 0, 1  # a full page, whose tokens are all attended to
+    kc[0, :, 300:], vc[0, :, 300:] = 0, 0
+    sel = torch.full((3, hk, count), -1, dtype=torch.int32, device="cuda")
+    sel[0, 0, :3], sel[2, 0, 0] = ints([width - 1, 5, 7]), 0
+    q = randn((3, h, d), dtype, g)
+    out, lse = torch.full((3, h, d), 7.0, dtype=dtype, device="cuda"), torch.full((3, h), 7.0, device="cuda")
+    la.paged_sparse_decode(q, kc, vc, bt, lens, sel, out=out, lse=lse)
+    for b, n in ((0, page), (2, 300)):
+        at = 0 if b == 0 else 1
+        want, wlse, bound, lbound = lref.attend(c(q[b]), c(kc[at, 0, :n]), c(vc[at, 0, :n]), d ** -0.5)
+        ref.within(out[b], want, bound, ref.u_of(dtype), "out")
+        ref.within(lse[b], wlse, lbound, ref.u_of(FP32), "lse")
+    assert (out[1] == 0).all() and (lse[1] == -INF).all()
