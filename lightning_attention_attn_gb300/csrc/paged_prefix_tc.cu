@@ -71,9 +71,11 @@ constexpr int kTiles = 3;             // tiles of tokens in shared memory
 constexpr int kRing = 2 * kTiles;     // their K and V
 constexpr uint32_t kAtoms = kTokens * 128;  // 128 rows of 64 bf16
 // Weights are taken against a base that may lie below the row's maximum: the maximum of the tiles
-// before, so that a tile's weights need not wait for its own.  Weights of up to 2^kRedo lose nothing in
-// floating point (but sums of values near the type's largest reach it 2^kRedo earlier); a tile whose maximum is
-// further above is taken again (S once more, then its maximum first).
+// before, so that a tile's weights need not wait for its own.  A tile whose maximum is more than kRedo above is
+// taken again (S once more, then its maximum first), and the weights are e^(s - base) 2^-kRedo, so at most 1, and
+// sums of the largest values pass the type's range no earlier than against the maximum itself.  (The
+// factor is part of the base where the sums are written.  What it takes from the other end, weights of less than
+// 2^-102 of the largest whose low part may be 0, is below the 2^-100 that infinite values are promised.)
 // A base that is kMove below is moved after the tile.  (log2)
 constexpr float kRedo = 8.f, kMove = 4.f;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
@@ -421,7 +423,7 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
                         rescale(fmaxf(m, fmaxf(top, based ? kLowest : -kInf)));
                         top = -kInf;
                     }
-                    const float b = m == -kInf ? 0.f : -m;
+                    const float b = m == -kInf ? 0.f : -(m + kRedo);
                     float2 sum = make_float2(0.f, 0.f);
                     if (ok) {
                         float v[2][8];
@@ -475,7 +477,7 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
                 for (int c = 0; c < D / 4; c += 2)
                     *reinterpret_cast<float4 *>(at + 2 * c) = make_float4(o[c].x, o[c].y, o[c + 1].x, o[c + 1].y);
                 if (half == 0)
-                    *reinterpret_cast<float2 *>(slot + (size_t)f.stride * D + 2 * in_unit) = make_float2(m, l);
+                    *reinterpret_cast<float2 *>(slot + (size_t)f.stride * D + 2 * in_unit) = make_float2(m + kRedo, l);
             }
         }
     } else if (warp < kCopy) {

@@ -179,3 +179,39 @@ def test_chosen_pages_of_the_longest_table(dtype, page, count):
         ref.within(out[b], want, bound, ref.u_of(dtype), "out")
         ref.within(lse[b], wlse, lbound, ref.u_of(FP32), "lse")
     assert (out[1] == 0).all() and (lse[1] == -INF).all()
+
+
+# ------------------------------------------------- values near the type's largest
+@pytest.mark.parametrize("dtype, batch", [(BF16, 2), (BF16, 40), (FP32, 2)])
+@pytest.mark.parametrize("step", [3, 3.75, 5, 7.5])
+@pytest.mark.parametrize("spike", [True, False])
+def test_prefix_large_values_and_scores_that_rise(dtype, batch, step, spike):
+    """Scores that rise by `step` (in log2) from one tile of 128 tokens to the next, for one token of it or all, over
+    values whose weighted sums against the running maximum are just within the type's range (1.1e38, or
+    128 * 1.1e36, and at most 0.6 of it more from other tiles): finite, as the attention without a prefix has it.
+    As many key-value heads as there are CTAs, so that each passes about a head's tiles."""
+    g = gen(63)
+    page, n, hk, group, d = 16, 128 * 12, 152, 4, 64
+    t = torch.arange(n, device="cuda")
+    score = (t // 128) * step
+    v = (0.9 + 0.2 * torch.rand((n, d), generator=g, device="cuda")) * (1e38 if spike else 1e36)
+    if spike:  # others are far below the tile's one, and small
+        score = torch.where(t % 128 == 77, score, -200.0)
+        v[t % 128 != 77] *= 1e-38
+    kc, vc = (torch.zeros((n // page + 1, hk, page, d), dtype=dtype, device="cuda") for _ in range(2))
+    pt = torch.randperm(n // page, generator=g, device="cuda").int()
+    kc[pt[t // page].long(), :, t % page, 0] = score.to(dtype)[:, None]
+    vc[pt[t // page].long(), :, t % page] = v.to(dtype)[:, None]
+    q = torch.zeros((batch, hk * group, d), dtype=dtype, device="cuda")
+    q[..., 0] = torch.tensor([1.0, 1.0, -1.0, 0.5] * hk, device="cuda").to(dtype)
+    bt, none = torch.full((batch, 1), n // page, dtype=torch.int32, device="cuda"), ints([0] * batch)
+    lse = torch.empty((batch, hk * group), device="cuda")
+    out = la.paged_prefix_decode(q, kc, vc, pt, ints([n]), bt, none, scale=math.log(2), lse=lse)
+    parts = lref.Behind((c(kc[:, :1]), c(vc[:, :1])), c(pt), n, c(bt[:1]), c(none[:1]))
+    want, wlse, bound, lbound = lref.over(c(q[:1, :group]), parts, math.log(2), tile=128)
+    assert torch.isfinite(out).all()
+    out, lse = out.reshape(batch, hk, group, d), lse.reshape(batch, hk, group)
+    for x, y, e, u, name in ((out, want, bound, ref.u_of(dtype), "out"), (lse, wlse, lbound, ref.u_of(FP32), "lse")):
+        ref.within(x, y[:, None].expand(x.shape), e[:, None].expand(x.shape), u, name)
+    rows = pt[None].expand(batch, -1).contiguous()
+    assert torch.isfinite(la.paged_decode(q, kc, vc, rows, none + n, scale=math.log(2))).all()
