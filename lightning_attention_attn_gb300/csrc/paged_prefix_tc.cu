@@ -296,9 +296,14 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
         const uint32_t tx = tmem + lanes + kColX + half * (D / 2);
         const int group = 1 + x;
         // A negative scale goes into the signs of Q, so that the largest score is the largest S, and a
-        // scale of 0 into Q as a whole, so that an S of -infinity has weight 0 whatever the scale.
+        // scale of 0 into Q as a whole, so that an S of -infinity has weight 0 whatever the scale (0 times
+        // an infinite or NaN query is NaN).
         const float scale = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
-        const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u, keep = a.scale_log2 == 0.f ? 0u : ~0u;
+        const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+        auto scaled = [&](uint32_t x) {
+            if (a.scale_log2 != 0.f) return x ^ flip;
+            return ((x & 0x7f80u) == 0x7f80u ? 0x7fffu : 0u) | ((x & 0x7f800000u) == 0x7f800000u ? 0x7fff0000u : 0u);
+        };
         // where the two threads of a row exchange a number: halves and tiles apart by powers of two
         constexpr uint32_t kOther = kRows * 4, kNext = 2 * kOther;
         const uint32_t mine = smem_u32(&cs.part[x][0][half][r]);
@@ -323,10 +328,10 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
                     for (int i = 0; i < 4; ++i) {
                         uint4 v = make_uint4(0, 0, 0, 0);
                         if (row < all_rows) v = __ldcg(qp + c + i);
-                        w[4 * i] = (v.x ^ flip) & keep;
-                        w[4 * i + 1] = (v.y ^ flip) & keep;
-                        w[4 * i + 2] = (v.z ^ flip) & keep;
-                        w[4 * i + 3] = (v.w ^ flip) & keep;
+                        w[4 * i] = scaled(v.x);
+                        w[4 * i + 1] = scaled(v.y);
+                        w[4 * i + 2] = scaled(v.z);
+                        w[4 * i + 3] = scaled(v.w);
                     }
                     tmem_st16(q_at + 4 * c, w);
                 }

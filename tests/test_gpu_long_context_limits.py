@@ -215,3 +215,29 @@ def test_prefix_large_values_and_scores_that_rise(dtype, batch, step, spike):
         ref.within(x, y[:, None].expand(x.shape), e[:, None].expand(x.shape), u, name)
     rows = pt[None].expand(batch, -1).contiguous()
     assert torch.isfinite(la.paged_decode(q, kc, vc, rows, none + n, scale=math.log(2))).all()
+
+
+# --------------------------------------------------------------- a scale of 0
+@pytest.mark.parametrize("dtype, batch, d", [(BF16, 3, 128), (BF16, 3, 64), (BF16, 40, 128), (FP32, 3, 64)])
+def test_prefix_scale_of_zero_with_infinite_and_nan_queries(dtype, batch, d):
+    """0 times an infinite or NaN product is NaN, with own tokens and without; other heads get the mean."""
+    g = gen(64)
+    page, n, hk, h = 16, 300, 2, 8
+    kc, vc = (randn((30, hk, page, d), dtype, g) for _ in range(2))
+    pt, bt = torch.arange(20, dtype=torch.int32, device="cuda"), torch.full((batch, 2), 25, dtype=torch.int32, device="cuda")
+    own = torch.tensor([0, 7, 0] * batch, dtype=torch.int32, device="cuda")[:batch].contiguous()
+    q = randn((batch, h, d), dtype, g)
+    bad = torch.zeros((batch, h), dtype=torch.bool, device="cuda")
+    for b, head, at, x in ((0, 1, 0, NAN), (0, 5, d - 1, INF), (1, 2, 3, -INF), (2, 7, d // 2, NAN), (batch - 1, 0, 2, INF)):
+        q[b, head, at], bad[b, head] = x, True
+    lse = torch.empty((batch, h), device="cuda")
+    out = la.paged_prefix_decode(q, kc, vc, pt, ints([n]), bt, own, scale=0.0, lse=lse)
+    assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
+    parts = lref.Behind((c(kc), c(vc)), c(pt), n, c(bt), c(own))
+    want, wlse, bound, lbound = lref.over(c(q.masked_fill(bad[..., None], 1.0)), parts, 0.0, tile=128)
+    good = ~c(bad)
+    ref.within(c(out)[good], want[good], bound[good], ref.u_of(dtype), "out")
+    ref.within(c(lse)[good], wlse[good], lbound[good], ref.u_of(FP32), "lse")
+    rows = pt[None].expand(batch, -1).contiguous()
+    dense = la.paged_decode(q, kc, vc, rows, own * 0 + n, scale=0.0)
+    assert torch.isnan(dense[bad]).all() and torch.isfinite(dense[~bad]).all()
