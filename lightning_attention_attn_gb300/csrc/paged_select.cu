@@ -162,6 +162,10 @@ SelectSpace select_space(int64_t units, int64_t width) {
     int64_t n = (int64_t)kSms * 48 / (units > 0 ? units : 1) + 1;
     const int64_t tiles = (width + kScoreTile - 1) / kScoreTile;
     n = n < tiles ? n : tiles;
+    // no more than keep a warp's step below 2^16 blocks, which indices have room for behind the last block (at most
+    // 2^31 - 2^16 are scored); 2432 warps run at once
+    constexpr int64_t kMost = (0x7fffffff - kMaxTokens) / kScoreTile / kScoreWarps * kScoreWarps - kScoreWarps;
+    n = n < kMost ? n : kMost;
     n = (n + kScoreWarps - 1) / kScoreWarps;
     s.splits = (int)(n < 1 ? 1 : n) * kScoreWarps;
     s.scored = true;
