@@ -445,7 +445,7 @@ la_status lightning_attn_paged_append(
  *              zeros, and -infinity as its lse; one whose scores are all -infinity
  *              NaN, with the same lse.
  * scale        softmax scale (e.g. head_dim^-1/2).
- * out          [batch, num_heads, head_dim], contiguous.
+ * out          [batch, num_heads, head_dim], contiguous; may be q where that is, too.
  * lse          nullable; [batch, num_heads] fp32: log sum_t e^(scale q . k_t).
  * workspace    lightning_attn_paged_decode_workspace_bytes(head_dim) bytes,
  *              16-byte aligned; scratch, not shared by calls that may overlap
@@ -522,7 +522,8 @@ la_status lightning_attn_paged_bounds(
  * keep_first, keep_last  the first and the last blocks of a request that are chosen whatever their
  *              scores; together at most count.
  * selected     [batch, num_kv_heads, count] int32: the chosen blocks (indices into the request's
- *              row of block_table) in ascending order, then -1 where the request has fewer.
+ *              row of block_table) in ascending order, then -1 where the request has fewer.  No other
+ *              argument's array.
  *              Blocks whose page is outside [0, num_pages) are not chosen.
  * workspace    lightning_attn_paged_select_workspace_bytes(...) bytes, 16-byte aligned; scratch, not
  *              shared by calls that may overlap.

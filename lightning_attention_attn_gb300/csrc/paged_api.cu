@@ -159,6 +159,15 @@ la_status check_decode(const int32_t *block_table, int32_t table_stride, int32_t
     return LA_OK;
 }
 
+// Queries of an attention, and the output over them.
+la_status check_queries(const void *q, int64_t q_stride, int32_t batch, int32_t num_heads, int32_t head_dim,
+                        la_dtype dtype, const void *out) {
+    LA_TRY(check_rows("q", q, q_stride, num_heads, head_dim, dtype));
+    if (out == q && batch > 1 && q_stride != (int64_t)num_heads * head_dim)
+        return LA_INVALID("an output in place of its input needs the input's stride");
+    return LA_OK;
+}
+
 // Tokens that a row of a table can hold.
 int capacity(int32_t table_width, int32_t page_size) {
     const long long most = (long long)table_width * page_size;
@@ -367,7 +376,7 @@ la_status lightning_attn_paged_decode(
                         v_cache, v_page_stride, num_pages, page_size, batch, num_heads,
                         num_kv_heads, head_dim, dtype, scale, out, lse));
     if (batch == 0) return LA_OK;
-    LA_TRY(check_rows("q", q, q_stride, num_heads, head_dim, dtype));
+    LA_TRY(check_queries(q, q_stride, batch, num_heads, head_dim, dtype, out));
     LA_TRY(check_workspace(workspace, workspace_bytes, decode_workspace(head_dim)));
     const la::PagedDecodeArgs a = decode_args(
         q, q_stride, k_cache, k_page_stride, v_cache, v_page_stride, block_table, table_stride,
@@ -487,6 +496,8 @@ la_status lightning_attn_paged_select(
         LA_TRY(check_cache("bounds", bounds, bounds_page_stride, num_kv_heads, 2, head_dim, dtype));
     if (!selected || !aligned(selected, 4))
         return LA_INVALID("selected must be a 4-byte aligned device array");
+    if (selected == block_table || selected == seq_lens)
+        return LA_INVALID("selected and block_table or seq_lens are one array");
     const int64_t need = la::paged_select_workspace(batch, num_kv_heads, table_width);
     if (need < 0) return LA_INVALID("too many blocks");
     LA_TRY(check_workspace(workspace, workspace_bytes, need));
@@ -532,7 +543,7 @@ la_status lightning_attn_paged_sparse_decode(
         return LA_INVALID("selected must be a 4-byte aligned device array");
     if ((long long)count * page_size > la::kMaxTokens)
         return LA_FAIL(LA_ERR_UNSUPPORTED, "count * page_size must be at most %d", la::kMaxTokens);
-    LA_TRY(check_rows("q", q, q_stride, num_heads, head_dim, dtype));
+    LA_TRY(check_queries(q, q_stride, batch, num_heads, head_dim, dtype, out));
     LA_TRY(check_workspace(workspace, workspace_bytes, decode_workspace(head_dim)));
     la::PagedDecodeArgs a = decode_args(
         q, q_stride, k_cache, k_page_stride, v_cache, v_page_stride, block_table, table_stride,
@@ -571,7 +582,7 @@ la_status lightning_attn_paged_prefix_decode(
         return LA_INVALID("null prefix_table or prefix_len");
     if (!aligned(prefix_table, 4) || !aligned(prefix_len, 4))
         return LA_INVALID("prefix_table and prefix_len must be 4-byte aligned");
-    LA_TRY(check_rows("q", q, q_stride, num_heads, head_dim, dtype));
+    LA_TRY(check_queries(q, q_stride, batch, num_heads, head_dim, dtype, out));
     la::PrefixPieces f = la::paged_prefix_pieces(batch, num_heads, num_kv_heads, dtype == LA_DTYPE_BF16);
     const int64_t rows = (int64_t)batch * num_heads;
     LA_TRY(check_workspace(workspace, workspace_bytes, prefix_workspace(f, rows, head_dim)));

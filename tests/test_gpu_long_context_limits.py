@@ -241,3 +241,27 @@ def test_prefix_scale_of_zero_with_infinite_and_nan_queries(dtype, batch, d):
     rows = pt[None].expand(batch, -1).contiguous()
     dense = la.paged_decode(q, kc, vc, rows, own * 0 + n, scale=0.0)
     assert torch.isnan(dense[bad]).all() and torch.isfinite(dense[~bad]).all()
+
+
+# --------------------------------------------------- outputs in place of queries
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("width", [30, 300])
+def test_outputs_in_place_of_contiguous_queries(dtype, width):
+    """The same bits as in an array of their own; clusters and split with join, several requests in pieces."""
+    g = gen(65)
+    page, hk, h, d, b = 16, 2, 32, 128, 5
+    kc, vc = (randn((900, hk, page, d), dtype, g) for _ in range(2))
+    bt = torch.randperm(900, generator=g, device="cuda").int()[:b * width // 3].repeat(3).reshape(b, width)
+    lens, pt, pl = ints([width * page, 0, 1, width * 7, width * page - 5]), bt[3, :30].contiguous(), ints([450])
+    sel = torch.arange(20, dtype=torch.int32, device="cuda").expand(b, hk, 20).contiguous()
+    q = randn((b, h, d), dtype, g)
+    for call in (lambda x, **kw: la.paged_decode(x, kc, vc, bt, lens, **kw),
+                 lambda x, **kw: la.paged_sparse_decode(x, kc, vc, bt, lens, sel, **kw),
+                 lambda x, **kw: la.paged_prefix_decode(x, kc, vc, pt, pl, bt, lens, **kw)):
+        want = call(q)
+        for _ in range(3):
+            x = q.clone()
+            assert torch.equal(call(x, out=x), want)
+        wide = randn((b, h + 1, d), dtype, g)
+        with pytest.raises(la.LightningAttnError, match="in place"):
+            call(wide[:, :h], out=wide.flatten()[:b * h * d].view(b, h, d))
