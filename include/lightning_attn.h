@@ -568,6 +568,7 @@ la_status lightning_attn_paged_sparse_decode(
  * workspace    lightning_attn_paged_prefix_decode_workspace_bytes(...) bytes, 16-byte aligned;
  *              scratch, not shared by calls that may overlap.
  * The rest, infinities included, is as for lightning_attn_paged_decode; lse is that of all tokens.
+ * In bf16 the waits of its pipeline are bounded: lightning_attn_device_status reports one that gave up.
  */
 la_status lightning_attn_paged_prefix_decode(
     const void *q, int64_t q_stride, const void *k_cache, int64_t k_page_stride,
@@ -626,7 +627,8 @@ la_status lightning_attn_paged_reserve(
 /*
  * Synchronises `stream`, then reports whether a kernel of this library raised
  * its device error word since the last call (and clears it).  The
- * tensor-core prefill bounds every wait of its pipeline (about 2 s); a wait
+ * tensor-core kernels (prefill, attention behind a shared prefix) bound every wait of
+ * their pipelines (about 2 s); a wait
  * that gives up ends the kernel cleanly (the context stays usable), leaves the
  * outputs of that launch unspecified and makes this call return
  * LA_ERR_TIMEOUT.  Returns LA_ERR_CUDA if the synchronisation fails.

@@ -259,7 +259,8 @@ def paged_prefix_decode(q, k_cache, v_cache, prefix_table, prefix_len, block_tab
 
     prefix_table: int32 [blocks], prefix_len: int32 [1], the prefix's pages and its tokens; block_table,
     seq_lens: the requests' own tokens behind it, on pages of their own (0 tokens are allowed).
-    lse is that of all tokens; other arguments as for :func:`paged_decode`.
+    lse is that of all tokens; other arguments as for :func:`paged_decode`.  In bf16 the waits of its
+    pipeline are bounded: ``device_status`` reports one that gave up.
     """
     return (_binding or _calls()).paged_prefix_decode(q, k_cache, v_cache, prefix_table, prefix_len,
                                                       block_table, seq_lens, scale, out, lse, workspace,

@@ -1,4 +1,6 @@
 """The long-context operators of the softmax layers at the limits of their contract, without a GPU."""
+import os
+
 import pytest
 
 import lightning_attention_attn_gb300 as la
@@ -54,3 +56,18 @@ def test_an_output_in_place_of_strided_queries_is_refused(lib, name):
     for ok in (_call(lib, name, dict(out="q")), _call(lib, name, dict(out="q"), stride=520, batch=1),
                _call(lib, name, {}, stride=520)):
         assert "workspace too small" in ok
+
+
+# ------------------------------------------------------------------- contract
+def test_contract_names_every_kernel_whose_waits_may_give_up():
+    """The calls whose device error words device_status takes are named there, and send their caller to it."""
+    with open(os.path.join(labuild.ROOT, "include", "lightning_attn.h")) as f:
+        header = f.read()
+
+    def before(entry):  # the comment in front of a declaration
+        at = header.index("la_status lightning_attn_" + entry + "(")
+        return header[header.rindex("/*", 0, at):at]
+
+    assert "prefill" in before("device_status") and "prefix" in before("device_status")
+    assert "lightning_attn_device_status" in before("paged_prefix_decode")
+    assert "device_status" in la.paged_prefix_decode.__doc__
