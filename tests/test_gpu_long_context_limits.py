@@ -265,3 +265,57 @@ def test_outputs_in_place_of_contiguous_queries(dtype, width):
         wide = randn((b, h + 1, d), dtype, g)
         with pytest.raises(la.LightningAttnError, match="in place"):
             call(wide[:, :h], out=wide.flatten()[:b * h * d].view(b, h, d))
+
+
+# ------------------------------------------------- paths of large calls alone
+@pytest.mark.parametrize("dtype, h, hk, d", [(BF16, 8, 2, 64), (BF16, 16, 1, 128), (FP32, 3, 1, 64)])
+def test_select_among_more_blocks_than_keys_are_kept(dtype, h, hk, d):
+    """8192 blocks' keys stay in shared memory, further ones are made again at every pass: requests on both sides of
+    that and far behind it, absent pages among them, few and many equal scores, infinities and NaN."""
+    g = gen(66)
+    blocks, page = [8192, 8193, 20000, 12288, 9000], 16
+    pages = sum(blocks)
+    bt = torch.full((5, max(blocks) + 3), -1, dtype=torch.int32, device="cuda")
+    order = torch.randperm(pages, generator=g, device="cuda").int()
+    for b, n in enumerate(blocks):
+        bt[b, :n] = order[sum(blocks[:b]):sum(blocks[:b]) + n]
+    mid = torch.randn((pages, hk, d), generator=g, device="cuda")
+    reach = 0.5 + 2 * torch.rand((pages, hk, d), generator=g, device="cuda")
+    bd = torch.stack([mid * 0.5 - reach, mid * 0.5 + reach], 2).to(dtype)
+    q = randn((5, h, d), dtype, g)
+    lens = ints([n * page - i for i, n in enumerate(blocks)])
+    bt[1, 8192], bt[2, 8000:8400], bt[2, 19999] = -1, 10 ** 9, -5
+    same = bt[3, 100:12000].long()      # 11900 equal scores, the border among them
+    bd[same] = bd[same[:1]]
+    bd[bt[4, 8500].long(), 0, 1, 3], bd[bt[4, 8999].long(), 0, 0, 2] = INF, NAN
+
+    def check(count, first, last):
+        out = la.paged_select(q, bd, bt, lens, page, count, keep_first=first, keep_last=last)
+        assert torch.equal(out.cpu(), lref.select(c(q), c(bd), c(bt), c(lens), page, count, first, last))
+
+    for count, first, last in ((1, 0, 0), (64, 1, 1), (5000, 0, 3), (8192, 1, 0), (12200, 4, 2)):
+        check(count, first, last)
+
+
+@pytest.mark.parametrize("page", [3, 12, 20])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("batch", [40, 3])
+def test_prefix_rows_one_by_one_over_many_tiles(page, d, batch):
+    """Pages that no box of eight rows divides, several tiles a CTA and units that begin and end inside its
+    range, rows for two groups that share the tiles and for two that do not."""
+    g = gen(67)
+    n, hk, group = 2900, 24, 8
+    pages = -(-n // page) + batch
+    kc, vc = (randn((pages, hk, page, d), BF16, g) for _ in range(2))
+    pt = torch.randperm(pages - batch, generator=g, device="cuda").int()
+    bt = torch.arange(pages - batch, pages, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    own = (torch.arange(batch, device="cuda") % (page + 1)).int()
+    q = randn((batch, hk * group, d), BF16, g)
+    some = [0, 1, 2, 17, 39] if batch == 40 else [0, 1, 2]
+    for gone in ([], [0, 7, pt.numel() - 1], list(range(50, 50 + 300 // page))):
+        for i in gone:
+            pt[i] = -1 if i % 2 else 2 ** 31 - 1
+        out = la.paged_prefix_decode(q, kc, vc, pt, ints([n]), bt, own)
+        parts = lref.Behind((c(kc), c(vc)), c(pt), n, c(bt[some]), c(own[some]))
+        want, _, bound, _ = lref.over(c(q[some]), parts, d ** -0.5, tile=128)
+        ref.within(out[some], want, bound, ref.u_of(BF16), "out")
