@@ -319,3 +319,125 @@ def test_prefix_rows_one_by_one_over_many_tiles(page, d, batch):
         parts = lref.Behind((c(kc), c(vc)), c(pt), n, c(bt[some]), c(own[some]))
         want, _, bound, _ = lref.over(c(q[some]), parts, d ** -0.5, tile=128)
         ref.within(out[some], want, bound, ref.u_of(BF16), "out")
+
+
+# ------------------------------------------------------ threads, streams, widths
+def all_calls(kc, vc, bd, bt, lens, pt, pl, q, page):
+    """Every call once, those of a few units and of many; the outputs."""
+    b2 = la.paged_bounds(kc, bd.clone(), bt, lens * 0, lens)
+    sel = la.paged_select(q, b2, bt, lens, page, 6)
+    few = torch.cat([bt, bt[:, :1].expand(-1, 3000) * 0 - 1], 1).contiguous()
+    return [b2, sel, la.paged_sparse_decode(q, kc, vc, bt, lens, sel),
+            la.paged_prefix_decode(q, kc, vc, pt, pl, bt, lens), la.paged_prefix_decode(q, kc, vc, pt, pl, few, lens),
+            la.paged_prefix_decode(q[:1], kc, vc, pt, pl, bt[:1], lens[:1])]
+
+
+def some_calls(dtype, g, b=20):
+    page, hk, h, d = 16, 2, 16, 128
+    kc, vc = (randn((400, hk, page, d), dtype, g) for _ in range(2))
+    bd = torch.zeros((400, hk, 2, d), dtype=dtype, device="cuda")
+    bt = torch.randperm(300, generator=g, device="cuda").int().reshape(b, 300 // b)
+    lens, pt, pl = (torch.arange(b, device="cuda") * 11 % 230).int(), torch.arange(300, 400, device="cuda").int(), ints([1590])
+    return kc, vc, bd, bt, lens, pt, pl, randn((b, h, d), dtype, g), page
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_two_host_threads(dtype):
+    """Calls from two threads, each on its own stream and then both on one: results as alone."""
+    import threading
+    case = some_calls(dtype, gen(68))
+    want = all_calls(*case)
+    torch.cuda.synchronize()
+    bad, shared = [], torch.cuda.Stream()
+
+    def run(stream):
+        try:
+            with torch.cuda.stream(stream):
+                for _ in range(20):
+                    got = all_calls(*case)
+                    stream.synchronize()
+                    if not all(torch.equal(x, y) for x, y in zip(got, want)):
+                        bad.append("differs")
+        except Exception as e:
+            bad.append(repr(e))
+
+    for streams in ((torch.cuda.Stream(), torch.cuda.Stream()), (shared, shared)):
+        threads = [threading.Thread(target=run, args=(s,)) for s in streams]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    assert not bad, bad
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_streams_inside_a_graph_and_the_default_stream(dtype):
+    """Captured calls on two streams that were forked from the capturing one, at once, joined and used; and calls on
+    the default stream while another is current."""
+    case = some_calls(dtype, gen(69))
+    want = [x.clone() for x in all_calls(*case)]
+    kc, vc, bd, bt, lens, pt, pl, q, page = case
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = []
+        for s in sides:
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got.append(all_calls(*case))
+        for s in sides:
+            torch.cuda.current_stream().wait_stream(s)
+        last = la.paged_prefix_decode(q, kc, vc, pt, pl, bt, lens)
+    for _ in range(5):
+        for x in got[0] + got[1]:
+            x.fill_(1)
+        graph.replay()
+        torch.cuda.synchronize()
+        for outs in got:
+            assert all(torch.equal(x, y) for x, y in zip(outs, want))
+        assert torch.equal(last, want[3])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(sides[0]):
+        default = torch.cuda.default_stream()
+        out = la.paged_prefix_decode(q, kc, vc, pt, pl, bt, lens, stream=default)
+        sel = la.paged_select(q, want[0], bt, lens, page, 6, stream=default)
+        few = la.paged_sparse_decode(q, kc, vc, bt, lens, sel, stream=default)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[3]) and torch.equal(sel, want[1]) and torch.equal(few, want[2])
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_tables_without_a_column(dtype):
+    """Requests that can have no token of their own, whatever their lengths say."""
+    g = gen(70)
+    kc, vc = (randn((40, 2, 16, 64), dtype, g) for _ in range(2))
+    bd = torch.zeros((40, 2, 2, 64), dtype=dtype, device="cuda")
+    q, lens, none = randn((30, 16, 64), dtype, g), ints([5, 0, -1] * 10), torch.empty((30, 0), dtype=torch.int32, device="cuda")
+    assert (la.paged_bounds(kc, bd, none, lens * 0, lens) == 0).all()
+    sel = la.paged_select(q, bd, none, lens, 16, 3)
+    assert (sel == -1).all()
+    lse = torch.zeros((30, 16), device="cuda")
+    assert (la.paged_sparse_decode(q, kc, vc, none, lens, sel, lse=lse) == 0).all() and (lse == -INF).all()
+    pt, pl = torch.arange(40, dtype=torch.int32, device="cuda"), ints([600])
+    out = la.paged_prefix_decode(q, kc, vc, pt, pl, none, lens, lse=lse)
+    parts = lref.Behind((c(kc), c(vc)), c(pt), 600, c(none), c(lens))
+    want, wlse, bound, lbound = lref.over(c(q), parts, 64 ** -0.5, tile=128)
+    ref.within(out, want, bound, ref.u_of(dtype), "out")
+    ref.within(lse, wlse, lbound, ref.u_of(FP32), "lse")
+    assert (la.paged_prefix_decode(q, kc, vc, none[0], pl, none, lens, lse=lse) == 0).all() and (lse == -INF).all()
+
+
+def test_writes_are_seen_by_autograd():
+    """Calls raise the version of what they write, and of nothing else."""
+    kc, vc, bd, bt, lens, pt, pl, q, page = some_calls(BF16, gen(71))
+    sel, out = torch.empty((20, 2, 6), dtype=torch.int32, device="cuda"), torch.empty_like(q)
+    lse = torch.empty((20, 16), device="cuda")
+    every = (kc, vc, bd, bt, lens, pt, pl, q, sel, out, lse)
+    for call, written in ((lambda: la.paged_bounds(kc, bd, bt, lens, lens), (bd,)),
+                          (lambda: la.paged_select(q, bd, bt, lens, page, 6, out=sel), (sel,)),
+                          (lambda: la.paged_sparse_decode(q, kc, vc, bt, lens, sel, out=out, lse=lse), (out, lse)),
+                          (lambda: la.paged_prefix_decode(q, kc, vc, pt, pl, bt, lens, out=out, lse=lse), (out, lse))):
+        before = [x._version for x in every]
+        call()
+        for x, v in zip(every, before):
+            assert (x._version > v) == any(x is y for y in written)
