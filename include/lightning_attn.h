@@ -560,6 +560,9 @@ la_status lightning_attn_paged_sparse_decode(
  * lightning_attn_paged_decode where the requests share a prefix (a system prompt, a document):
  * request b attends to the first prefix_len[0] tokens of the prefix's pages and to the first
  * seq_lens[b] tokens of its own, and the prefix's keys and values are read for the batch as a whole.
+ * With 64 query and 8 key-value heads of 128 in bf16 that is faster than lightning_attn_paged_decode over tables
+ * that name the prefix's pages (its length a multiple of page_size) from 16 requests behind 2K tokens, 8 behind
+ * 8K, 4 behind 32K or 2 behind 128K; for fewer it is slower (4 behind 2K 17 us instead of 10).
  *
  * prefix_table [prefix_width] int32, prefix_len [1] int32: as a row of block_table and its length.
  * block_table, seq_lens  the requests' own tokens behind the prefix, which begin with a

@@ -277,11 +277,13 @@ __device__ __forceinline__ long long prefix_chunk(const PrefixPieces &f, int til
 // (and has as many ranges as those hold at once): the number for which both are done first, or all SMs, one
 // kernel behind the other, which costs kBehindUs more.  A tile takes an SM about kTileUs (two where the groups
 // share it), kBesideUs beside the other kernel; own tokens, `cost` tiles of them, stream at kHbm, from
-// fewer than kFullSms SMs at that share of it.  Measured, 64 and 8 heads of 128, for the rule's choice / the best
-// of ten numbers / all SMs: 128 requests of up to 2048 own tokens behind 8K 149 / 148 / 177 us, of up to
-// 8192 behind 2K 329 / 329 / 363, 64 of up to 2048 behind 32K 155 / 154 / 173, 256 of up to 1024 behind 4K
-// 163 / 158 / 178, 32 of up to 8192 behind 16K 141 / 130 / 165, 16 of up to 16K behind 128K 209 / 194 / 215.
-// With 304 ranges, in waves of what is free, the first takes 162.
+// fewer than kFullSms SMs at that share of it.  A tile's times, from the prefix alone and from what bounds the calls
+// below: 128 wide 1.2 (shared) to 1.5 us and 2.0 beside, 64 wide 0.9 to 1.1 and 1.2 to 1.5.  Measured,
+// 64 and 8 heads of 128 (of 64), for the rule's choice / the best of ten numbers / all SMs: 128
+// requests of up to 2048 own tokens behind 8K 145 / 144 / 175 us (104 / 103 / 116), of up to 8192 behind 2K 335 / 335 /
+// 362 (192 / 192 / 203), 64 of up to 2048 behind 32K 153 / 153 / 168 (117 / 114 / 121), 256 of up to 1024 behind 4K
+// 160 / 154 / 176, 32 of up to 8192 behind 16K 135 / 131 / 158 (87 / 85 / 101), 16 of up to 16K behind 128K 207 / 195 /
+// 210 (123 / 123 / 136).  With 304 ranges, in waves of what is free, the first took 162 (149 then).
 template <int D> constexpr float kTileUs = D == 128 ? 1.5f : 1.1f;
 template <int D> constexpr float kBesideUs = D == 128 ? 2.f : 1.4f;
 constexpr float kHbm = 6.7e6f /* bytes a us */, kFullSms = 110.f, kBehindUs = 20.f;

@@ -6,13 +6,14 @@
 //
 // Bound: a row does 4 D flops a token, so with many rows the tensor core bounds the kernel, with few (and
 // K and V read once for all of them) HBM.  Measured, 8 key-value heads of 128, 64 query heads: 32
-// requests behind 64K tokens 110 us with all that follows (0.62 PFLOP/s of the formula's products, 0.93
+// requests behind 64K tokens 106 us with all that follows (0.65 PFLOP/s of the formula's products, 0.97
 // of those that are done; the tensor pipe is busy 52 % of this kernel's cycles), 16 requests behind 128K
-// 129 us (4.2 TB/s), one 109 us (4.9 TB/s).  What bounds it then is the chain of a group's tile, about
+// 127 us (4.2 TB/s), one 109 us (4.9 TB/s).  What bounds it then is the chain of a group's tile, about
 // 5000 cycles by cycle stamps: P V and the next S (1536 on the tensor core), the weights, and 500 to 800
 // from each of them to the threads that wait for it; two chains in turn keep the tensor core busy for
 // three fifths of it.  Half the exponentials moved to FMAs, or none of the low parts, change the time by 0
-// to 4 %.  A third group finds no room in tensor memory.
+// to 4 %.  A third group finds no room in tensor memory.  At its 96 registers the kernel spills: 128 and 168
+// bytes at 128 wide (tiles shared by the groups, and not), 84 and 68 at 64; which role does has not been told apart.
 //
 // P is passed as two bf16 parts (parts_of: off by at most 2^-16 of each weight, as in the attention
 // of one request), which makes P V two products instead of one: 1536 tensor cycles a 128 x 128

@@ -147,7 +147,9 @@ paged_bounds_kernel(const __grid_constant__ PagedBoundsArgs a, int splits) {
 // the fp32 scores and its largest |bound|.  Units whose blocks are all chosen have no scores.
 // Bound: every bound is read once (G query heads do G flops a byte).  128 requests of 1K to 32K tokens, pages of
 // 64, 64 and 8 heads of 128: 45 us with the choice, this kernel two thirds of it (138 MB at 4.2 TB/s under a
-// profiler: three dependent latencies before a warp's first bounds, and requests of 16 to 512 blocks).
+// profiler: three dependent latencies before a warp's first bounds, the next tile's loads behind this one's products,
+// and requests of 16 to 512 blocks).  Spills at its 128 registers: 16 bytes (bf16, up to 8 heads of 128 a key-value
+// head), 124 (bf16, more heads), 8 and 16 (fp32).
 constexpr int kScoreWarps = 4;   // of a CTA, all of one unit
 constexpr int kScoreTile = 16;   // blocks of a warp's step
 
