@@ -25,7 +25,7 @@ paged_prefix_kernel(const __grid_constant__ PagedDecodeArgs a) {
     constexpr int D = Core::D, ROWS = Core::ROWS;
     extern __shared__ __align__(128) unsigned char smem[];
     ptx::grid_dependency_wait();
-    if (blockIdx.x == 0 && threadIdx.x == 0) ptx::store_release(a.prefix.ranges + 2, 1);
+    ptx::release_to_next(a.prefix.ranges + 2);
     ptx::grid_launch_dependents();
     const PrefixPieces &f = a.prefix;
     const int len = min(max(__ldcg(f.len), 0), f.max_tokens);

@@ -214,7 +214,7 @@ paged_prefix_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_c
         tma_prefetch_desc(&map_v);
     }
     grid_dependency_wait();
-    if (blockIdx.x == 0 && threadIdx.x == 0) store_release(a.prefix.ranges + 2, 1);
+    release_to_next(a.prefix.ranges + 2);
     grid_launch_dependents();
 
     const PrefixPieces &f = a.prefix;

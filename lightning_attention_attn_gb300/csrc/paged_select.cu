@@ -427,8 +427,8 @@ template <typename S>
 __global__ void __launch_bounds__(kScoreWarps * 32, 4)
 paged_score_kernel(const __grid_constant__ PagedSelectArgs a, const __grid_constant__ SelectSpace w) {
     ptx::grid_dependency_wait();
-    if (blockIdx.x == 0 && threadIdx.x == 0)  // for the choice, which has no wait for what wrote the arguments
-        ptx::store_release(reinterpret_cast<int *>(static_cast<char *>(a.workspace) + w.ready), 1);
+    // for the choice, which has no wait for what wrote the arguments
+    ptx::release_to_next(reinterpret_cast<int *>(static_cast<char *>(a.workspace) + w.ready));
     ptx::grid_launch_dependents();
     const int ctas = w.splits / kScoreWarps;
     const int unit = blockIdx.x / ctas;

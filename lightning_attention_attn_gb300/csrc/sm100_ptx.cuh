@@ -155,7 +155,10 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, uint
         : "memory");
 }
 
-// Handing on what a thread has seen, between two kernels of which the second does not wait for the first.
+// Handing on what a kernel has waited for to one that does not wait for it: the first calls release_to_next, all of
+// the block, between its wait and its trigger, and the second's threads load_acquire the word before they read (its value
+// means nothing).  The word is in its place before any of the block's threads triggers, and so before the second
+// kernel runs.
 __device__ __forceinline__ int load_acquire(const int *p) {
     int x;
     asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
@@ -163,6 +166,14 @@ __device__ __forceinline__ int load_acquire(const int *p) {
 }
 __device__ __forceinline__ void store_release(int *p, int x) {
     asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(x) : "memory");
+}
+__device__ __forceinline__ void release_to_next(int *word) {
+    if (blockIdx.x > 0) return;
+    if (threadIdx.x == 0) {
+        store_release(word, 1);
+        __threadfence();
+    }
+    __syncthreads();
 }
 
 // Barrier among `count` threads (a multiple of 32) of the CTA, id 1..15.
