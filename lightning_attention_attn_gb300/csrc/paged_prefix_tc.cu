@@ -6,7 +6,7 @@
 //
 // Bound: a row does 4 D flops a token, so with many rows the tensor core bounds the kernel, with few (and
 // K and V read once for all of them) HBM.  Measured, 8 key-value heads of 128, 64 query heads: 32
-// requests behind 64K tokens 106 us with all that follows (0.65 PFLOP/s of the formula's products, 0.97
+// requests behind 64K tokens 107 us with all that follows (0.64 PFLOP/s of the formula's products, 0.96
 // of those that are done; the tensor pipe is busy 52 % of this kernel's cycles), 16 requests behind 128K
 // 127 us (4.2 TB/s), one 109 us (4.9 TB/s).  What bounds it then is the chain of a group's tile, about
 // 5000 cycles by cycle stamps: P V and the next S (1536 on the tensor core), the weights, and 500 to 800
